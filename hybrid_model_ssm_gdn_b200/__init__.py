@@ -8,6 +8,9 @@ device memory (the context's arena, outputs) and the current CUDA stream.
                       A=A, D=D, in_dtype=torch.bfloat16)
     layer.load_checkpoint(S0)            # fp32 [Bt][H][P][N]
     y = layer.mamba2_step(x, B, C, dt)   # fp32 [Bt][H][P]
+
+Prompts and drafts around it: ``ReplaySSM.prefill`` / ``mamba2_scan``, ``shortconv_prefill`` / ``_step`` / ``_verify`` /
+``_commit`` and ``accept_drafts``.
 """
 
 from __future__ import annotations
@@ -20,7 +23,8 @@ from . import abi
 from .abi import RSSMError
 
 __all__ = ["ReplaySSM", "RSSMError", "conv_mamba2_step", "conv_gdn_step", "snap_verify", "snap_commit", "sched_probe",
-           "make_config", "abi"]
+           "make_config", "abi", "mamba2_scan", "shortconv_prefill", "shortconv_step", "shortconv_verify",
+           "shortconv_commit", "accept_drafts"]
 
 _DT = {torch.float32: abi.F32, torch.bfloat16: abi.BF16}
 _HP = {"f32": abi.HP_F32, "f16sr": abi.HP_F16_SR, "f8sr": abi.HP_F8_SR}
@@ -152,6 +156,16 @@ class ReplaySSM:
         a = _dev(accepted, torch.int32, "accepted", self.batch)
         abi.check(self.lib.rssm_commit(self.handle, _ptr(a), _stream()), "rssm_commit")
 
+    def prefill(self, x, B, C_, dt, offsets, slots=None, resume=None, y=None, workspace=None):
+        """Run packed prompts (rssm_mamba2_prefill): x [total][H][P], B, C [total][G][128], dt [total][H];
+        offsets int32 [n+1]; slots int32 [n] (sequence of each prompt), resume uint8 [n] -> y fp32 [total][H][P]."""
+        H, P, G = self.nheads, self.rows, self.ngroups
+        total, pr, tok, y = _scan_args(x, B, C_, dt, offsets, slots, resume, y, H, P, G, self.in_dtype)
+        work = _scan_work(self.lib, self.cfg, total, pr.nseq, workspace)
+        abi.check(self.lib.rssm_mamba2_prefill(self.handle, C.byref(pr), C.byref(tok), _ptr(y), _ptr(work),
+                                               0 if work is None else work.numel(), _stream()), "rssm_mamba2_prefill")
+        return y
+
     def flush(self, mask=None):
         m = _dev(mask, torch.uint8, "mask", self.batch)
         abi.check(self.lib.rssm_flush(self.handle, _ptr(m), _stream()), "rssm_flush")
@@ -214,6 +228,204 @@ class ReplaySSM:
         if st not in (0, 6):
             abi.check(st, "rssm_get_error")
         return code.value, seq.value
+
+
+# ---------------------------------------------------------------------- prompts and drafts
+
+def _arr(t, dtype, name, shape, optional=False):
+    """``t`` after checking that it is a contiguous tensor of ``dtype`` and exactly ``shape`` on the current device."""
+    if t is None and optional:
+        return None
+    if tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{name}: expected shape {tuple(shape)}, got {tuple(t.shape)}")
+    if t.dtype != dtype or not t.is_cuda or not t.is_contiguous():
+        raise ValueError(f"{name}: expected a contiguous CUDA tensor of {dtype}, got {t.dtype} on {t.device}")
+    if t.get_device() != torch.cuda.current_device():
+        raise ValueError(f"{name}: on {t.device}, but the current device is cuda:{torch.cuda.current_device()}")
+    return t
+
+
+def _prompts(total, offsets, slots, resume):
+    n = offsets.numel() - 1
+    if n < 1:
+        raise ValueError(f"offsets: needs at least 2 elements, got {n + 1}")
+    _arr(offsets, torch.int32, "offsets", (n + 1,))
+    _arr(slots, torch.int32, "slots", (n,), optional=True)
+    _arr(resume, torch.uint8, "resume", (n,), optional=True)
+    return abi.Prompts(total, n, offsets.data_ptr(), None if slots is None else slots.data_ptr(),
+                       None if resume is None else resume.data_ptr())
+
+
+def _in_dtype(t, name):
+    if t.dtype not in _DT:
+        raise ValueError(f"{name}: expected torch.float32 or torch.bfloat16, got {t.dtype}")
+    return t.dtype
+
+
+def _scan_args(x, B, C_, dt, offsets, slots, resume, y, H, P, G, dtype):
+    total = x.shape[0]
+    _arr(x, dtype, "x", (total, H, P))
+    _arr(B, dtype, "B", (total, G, 128))
+    _arr(C_, dtype, "C", (total, G, 128))
+    _arr(dt, dtype, "dt", (total, H))
+    pr = _prompts(total, offsets, slots, resume)
+    if y is None:
+        y = torch.empty(total, H, P, dtype=torch.float32, device=x.device)
+    _arr(y, torch.float32, "y", (total, H, P))
+    tok = abi.Tokens(x=x.data_ptr(), B=B.data_ptr(), C=C_.data_ptr(), dt=dt.data_ptr())
+    return total, pr, tok, y
+
+
+def _scan_work(lib, cfg, total, nseq, workspace):
+    """The scratch tensor of a scan: the caller's, or a new one from the caching allocator (None if none is needed)."""
+    n = C.c_size_t()
+    abi.check(lib.rssm_mamba2_scan_workspace(C.byref(cfg), total, nseq, C.byref(n)), "rssm_mamba2_scan_workspace")
+    if n.value == 0:
+        return None
+    if workspace is not None:
+        if not workspace.is_cuda or workspace.dtype != torch.uint8 or not workspace.is_contiguous() or \
+                workspace.numel() < n.value:
+            raise ValueError(f"workspace: expected a contiguous CUDA tensor of uint8 with at least {n.value} elements")
+        return workspace
+    return torch.empty(n.value, dtype=torch.uint8, device="cuda")
+
+
+def mamba2_scan(S, x, B, C_, dt, A, D, offsets, slots=None, resume=None, y=None, workspace=None):
+    """Mamba-2 over packed prompts on the caller's states (rssm_mamba2_scan): S fp32 [batch][H][P][128], the prompts'
+    sequences rewritten in place; x [total][H][P], B, C [total][G][128], dt [total][H] (bf16 or fp32), A, D fp32 [H];
+    prompt i is rows offsets[i] .. offsets[i+1]-1 and belongs to S[slots[i]] (S[i] without slots), from which it
+    continues where resume[i] is set -> y fp32 [total][H][P]."""
+    if x.dim() != 3 or B.dim() != 3 or S.dim() != 4:
+        raise ValueError("x, B and S: expected 3, 3 and 4 dimensions")
+    total, H, P = x.shape
+    dtype = _in_dtype(x, "x")
+    _arr(S, torch.float32, "S", (S.shape[0], H, P, 128))
+    _arr(A, torch.float32, "A", (H,))
+    _arr(D, torch.float32, "D", (H,))
+    total, pr, tok, y = _scan_args(x, B, C_, dt, offsets, slots, resume, y, H, P, B.shape[1], dtype)
+    cfg = abi.Config(kind=abi.MAMBA2, batch=S.shape[0], nheads=H, headdim=P, dstate=128, ngroups=B.shape[1], window=1,
+                     in_dtype=_DT[dtype], A=A.data_ptr(), D=D.data_ptr())
+    lib = abi.load()
+    work = _scan_work(lib, cfg, total, pr.nseq, workspace)
+    abi.check(lib.rssm_mamba2_scan(C.byref(cfg), C.byref(pr), C.byref(tok), _ptr(S), _ptr(y), _ptr(work),
+                                   0 if work is None else work.numel(), _stream()), "rssm_mamba2_scan")
+    return y
+
+
+def _shortconv(hist, cur, x, weight, bias, splits, activation, out, lead):
+    """Config, outputs and row stride of a short-convolution call; ``lead``: the leading dimensions of x."""
+    if hist.dim() != 3 or weight.dim() != 2:
+        raise ValueError("hist and weight: expected 3 and 2 dimensions")
+    dtype = _in_dtype(x, "x")
+    batch, ring, ch = hist.shape
+    _arr(hist, dtype, "hist", (batch, ring, ch))
+    _arr(cur, torch.int32, "cur", (batch,))
+    _arr(weight, dtype, "weight", (ch, weight.shape[1]))
+    _arr(bias, dtype, "bias", (ch,), optional=True)
+    splits = (ch,) if splits is None else tuple(splits)
+    if len(splits) > 3 or sum(splits) != ch or min(splits) < 1:
+        raise ValueError(f"splits: expected up to three positive sizes that sum to {ch}, got {splits}")
+    if activation not in (None, "silu"):
+        raise ValueError(f"activation: expected None or 'silu', got {activation!r}")
+    if tuple(x.shape) != (*lead, ch) or not x.is_cuda or x.get_device() != torch.cuda.current_device():
+        raise ValueError(f"x: expected shape {(*lead, ch)} on the current CUDA device, got {tuple(x.shape)} on {x.device}")
+    # rows may lie apart (a slice of a wider projection) but evenly, with contiguous channels
+    stride = x.stride(-2) if x.numel() and x.shape[-2] > 1 else ch
+    if x.numel():
+        if len(lead) == 2 and lead[0] > 1:
+            if lead[1] == 1:
+                stride = x.stride(0)
+            elif x.stride(0) != lead[1] * stride:
+                raise ValueError("x: the rows of all sequences must lie evenly apart")
+        if x.stride(-1) != 1 or stride < ch or stride % 8:
+            raise ValueError(f"x: expected contiguous channels and a row stride that is a multiple of 8, got {x.stride()}")
+    if out is None:
+        out = tuple(torch.empty(*lead, n, dtype=dtype, device=x.device) for n in splits)
+    if len(out) != len(splits):
+        raise ValueError(f"out: expected {len(splits)} tensors, got {len(out)}")
+    for i, (o, n) in enumerate(zip(out, splits)):
+        _arr(o, dtype, f"out[{i}]", (*lead, n))
+    pad = (0,) * (3 - len(splits))
+    cfg = abi.ShortConvConfig(batch, ch, weight.shape[1], ring, _DT[dtype], activation == "silu",
+                              (C.c_int * 3)(*splits, *pad), weight.data_ptr(),
+                              None if bias is None else bias.data_ptr())
+    ptrs = (C.c_void_p * 3)(*[o.data_ptr() for o in out], *[None for _ in pad])
+    return cfg, ptrs, out, stride
+
+
+def shortconv_prefill(hist, cur, x, weight, bias, offsets, slots=None, resume=None, splits=None, activation="silu",
+                      out=None):
+    """Short causal convolution over packed prompts (rssm_shortconv_prefill): x [total][channels]; hist
+    [batch][ring][channels] and cur int32 [batch] are the sequences' histories -> one tensor [total][n] a split."""
+    cfg, ptrs, out, stride = _shortconv(hist, cur, x, weight, bias, splits, activation, out, (x.shape[0],))
+    pr = _prompts(x.shape[0], offsets, slots, resume)
+    abi.check(abi.load().rssm_shortconv_prefill(C.byref(cfg), C.byref(pr), _ptr(hist), _ptr(cur), _ptr(x), stride,
+                                                C.byref(ptrs), _stream()), "rssm_shortconv_prefill")
+    return out
+
+
+def shortconv_step(hist, cur, x, weight, bias=None, splits=None, activation="silu", out=None):
+    """One token a sequence: x [batch][channels] -> one tensor [batch][n] a split; cur advances."""
+    cfg, ptrs, out, stride = _shortconv(hist, cur, x, weight, bias, splits, activation, out, (hist.shape[0],))
+    abi.check(abi.load().rssm_shortconv_step(C.byref(cfg), _ptr(hist), _ptr(cur), _ptr(x), stride, C.byref(ptrs),
+                                             _stream()), "rssm_shortconv_step")
+    return out
+
+
+def shortconv_verify(hist, cur, x, weight, bias=None, splits=None, activation="silu", out=None):
+    """T tentative tokens a sequence: x [batch][T][channels] -> one tensor [batch][T][n] a split; cur stays until
+    ``shortconv_commit``."""
+    if x.dim() != 3:
+        raise ValueError(f"x: expected 3 dimensions, got {x.dim()}")
+    T = x.shape[1]
+    cfg, ptrs, out, stride = _shortconv(hist, cur, x, weight, bias, splits, activation, out, (hist.shape[0], T))
+    abi.check(abi.load().rssm_shortconv_verify(C.byref(cfg), T, _ptr(hist), _ptr(cur), _ptr(x), stride, C.byref(ptrs),
+                                               _stream()), "rssm_shortconv_verify")
+    return out
+
+
+def shortconv_commit(hist, cur, accepted, width):
+    """Advance the cursors by the accepted prefixes, int32 [batch]; ``width`` is the filter's."""
+    batch, ring = hist.shape[:2]
+    _arr(cur, torch.int32, "cur", (batch,))
+    _arr(accepted, torch.int32, "accepted", (batch,))
+    cfg = abi.ShortConvConfig(batch=batch, width=width, ring=ring)
+    abi.check(abi.load().rssm_shortconv_commit(C.byref(cfg), _ptr(cur), _ptr(accepted), _stream()),
+              "rssm_shortconv_commit")
+
+
+def _rows(t, name, batch, rows, vocab):
+    """The row stride of [batch][rows][vocab] probabilities whose rows lie evenly apart."""
+    if tuple(t.shape) != (batch, rows, vocab) or t.dtype != torch.float32 or not t.is_cuda or \
+            t.get_device() != torch.cuda.current_device():
+        raise ValueError(f"{name}: expected fp32 of shape {(batch, rows, vocab)} on the current CUDA device, got {t.dtype} "
+                         f"of {tuple(t.shape)} on {t.device}")
+    if t.numel() == 0:
+        return vocab
+    ld = t.stride(1) if rows > 1 else (t.stride(0) if batch > 1 else vocab)
+    if t.stride(2) != 1 and vocab > 1 or ld < vocab or (rows > 1 and batch > 1 and t.stride(0) != rows * ld):
+        raise ValueError(f"{name}: expected contiguous rows that lie evenly apart, got strides {t.stride()}")
+    return ld
+
+
+def accept_drafts(target, tokens, u, draft=None, count=None):
+    """Verify drafts against target probabilities (rssm_accept_drafts): target fp32 [batch][T+1][vocab], tokens int32
+    [batch][T], u fp32 [batch][T+1] in [0, 1), draft fp32 [batch][T][vocab] or None (drafts that were looked up), count
+    int32 [batch] (drafts of each sequence) -> (accepted, accepted + 1, next token), int32 [batch] each."""
+    if target.dim() != 3:
+        raise ValueError(f"target: expected 3 dimensions, got {target.dim()}")
+    batch, T, vocab = target.shape[0], target.shape[1] - 1, target.shape[2]
+    ld_t = _rows(target, "target", batch, T + 1, vocab)
+    ld_d = 0 if draft is None else _rows(draft, "draft", batch, T, vocab)
+    _arr(tokens, torch.int32, "tokens", (batch, T))
+    _arr(u, torch.float32, "u", (batch, T + 1))
+    _arr(count, torch.int32, "count", (batch,), optional=True)
+    got = torch.empty(3, batch, dtype=torch.int32, device=target.device)
+    accepted, committed, nxt = got[0], got[1], got[2]
+    abi.check(abi.load().rssm_accept_drafts(batch, T, vocab, _ptr(target), ld_t, _ptr(draft), ld_d, _ptr(tokens),
+                                            _ptr(count), _ptr(u), _ptr(accepted), _ptr(committed), _ptr(nxt),
+                                            _stream()), "rssm_accept_drafts")
+    return accepted, committed, nxt
 
 
 # ---------------------------------------------------------------------- comparison kernels

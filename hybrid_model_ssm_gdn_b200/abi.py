@@ -19,7 +19,7 @@ HP_F32, HP_F16_SR, HP_F8_SR = 0, 1, 2
 READ_SAME, READ_NVFP4, READ_SHARED_NVFP4, READ_NVFP4D = 0, 1, 2, 3
 STATUS = {0: "RSSM_OK", 1: "RSSM_ERR_ARG", 2: "RSSM_ERR_SHAPE", 3: "RSSM_ERR_UNSUPPORTED",
           4: "RSSM_ERR_ARENA_TOO_SMALL", 5: "RSSM_ERR_CUDA", 6: "RSSM_ERR_DEVICE"}
-DEV_OK, DEV_PENDING, DEV_NO_VERIFY, DEV_ACCEPTED, DEV_TIMEOUT = 0, 1, 2, 3, 4
+DEV_OK, DEV_PENDING, DEV_NO_VERIFY, DEV_ACCEPTED, DEV_TIMEOUT, DEV_PROMPT, DEV_BUFFERED = 0, 1, 2, 3, 4, 5, 6
 
 
 class Config(C.Structure):
@@ -33,6 +33,17 @@ class Tokens(C.Structure):
     _fields_ = [("x", C.c_void_p), ("B", C.c_void_p), ("C", C.c_void_p), ("dt", C.c_void_p),
                 ("q", C.c_void_p), ("k", C.c_void_p), ("v", C.c_void_p), ("alpha", C.c_void_p),
                 ("beta", C.c_void_p)]
+
+
+class Prompts(C.Structure):
+    _fields_ = [("total", C.c_int), ("nseq", C.c_int), ("offsets", C.c_void_p), ("slots", C.c_void_p),
+                ("resume", C.c_void_p)]
+
+
+class ShortConvConfig(C.Structure):
+    _fields_ = [("batch", C.c_int), ("channels", C.c_int), ("width", C.c_int), ("ring", C.c_int),
+                ("in_dtype", C.c_int), ("silu", C.c_int), ("split", C.c_int * 3), ("weight", C.c_void_p),
+                ("bias", C.c_void_p)]
 
 
 class RSSMError(RuntimeError):
@@ -62,6 +73,15 @@ _SIGS = {
     "rssm_conv_gdn_step": [C.POINTER(Config), _P, _P, _P, _P, _P, _P, _P, _P],
     "rssm_snap_verify": [C.POINTER(Config), _P, _P, C.c_int, C.POINTER(Tokens), _P, _P],
     "rssm_snap_commit": [C.POINTER(Config), _P, _P, _P],
+    "rssm_mamba2_scan_workspace": [C.POINTER(Config), C.c_int, C.c_int, C.POINTER(C.c_size_t)],
+    "rssm_mamba2_scan": [C.POINTER(Config), C.POINTER(Prompts), C.POINTER(Tokens), _P, _P, _P, C.c_size_t, _P],
+    "rssm_mamba2_prefill": [_P, C.POINTER(Prompts), C.POINTER(Tokens), _P, _P, C.c_size_t, _P],
+    "rssm_shortconv_prefill": [C.POINTER(ShortConvConfig), C.POINTER(Prompts), _P, _P, _P, C.c_longlong,
+                               C.POINTER(_P * 3), _P],
+    "rssm_shortconv_step": [C.POINTER(ShortConvConfig), _P, _P, _P, C.c_longlong, C.POINTER(_P * 3), _P],
+    "rssm_shortconv_verify": [C.POINTER(ShortConvConfig), C.c_int, _P, _P, _P, C.c_longlong, C.POINTER(_P * 3), _P],
+    "rssm_shortconv_commit": [C.POINTER(ShortConvConfig), _P, _P, _P],
+    "rssm_accept_drafts": [C.c_int, C.c_int, C.c_int, _P, C.c_longlong, _P, C.c_longlong, _P, _P, _P, _P, _P, _P, _P],
     "rssm_sched_probe": [C.c_int, C.c_int, _P, _P, _P],
 }
 

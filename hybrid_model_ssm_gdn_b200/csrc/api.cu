@@ -395,6 +395,206 @@ rssm_status rssm_get_error(rssm_ctx *x, int *code, int *seq, rssm_stream stream)
   return RSSM_ERR_DEVICE;
 }
 
+// ------------------------------------------------------------------ prompts
+
+static rssm_status sm_count(int *sms) {
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e == cudaSuccess) e = cudaDeviceGetAttribute(sms, cudaDevAttrMultiProcessorCount, dev);
+  return e == cudaSuccess ? RSSM_OK : cuda_fail(e);
+}
+
+// the shape rules of a Mamba-2 state that is not a context's
+static rssm_status scan_validate(const rssm_config *cfg) {
+  if (!cfg) return RSSM_ERR_ARG;
+  rssm_config c = *cfg;
+  c.hp = RSSM_HP_F32;
+  c.read = RSSM_READ_SAME;
+  c.skip_tau = 0.f;
+  rssm_status s = validate(&c);
+  if (s != RSSM_OK) return s;
+  return c.kind == RSSM_MAMBA2 ? RSSM_OK : RSSM_ERR_UNSUPPORTED;
+}
+
+static rssm_status prompts_validate(const rssm_prompts *pr, int batch) {
+  if (!pr || !pr->offsets) return RSSM_ERR_ARG;
+  if (pr->total < 0 || pr->nseq < 1 || pr->nseq > batch) return RSSM_ERR_SHAPE;
+  if ((long long)pr->total + pr->nseq > 0x7fffffffLL) return RSSM_ERR_SHAPE;
+  return RSSM_OK;
+}
+
+static Prompts device_prompts(const rssm_prompts *pr, int nslots, const int4 *meta) {
+  Prompts p{};
+  p.total = pr->total; p.nseq = pr->nseq; p.nslots = nslots;
+  p.off = pr->offsets; p.slots = pr->slots; p.resume = pr->resume; p.meta = meta;
+  return p;
+}
+
+static rssm_status run_scan(const rssm_config &c, const Prompts &p, const rssm_tokens *tok, float *S, float *y,
+                            int num_sms, cudaStream_t st) {
+  if (c.nheads > 65535) return RSSM_ERR_SHAPE;  // one grid row a head
+  ScanArgs a{};
+  a.H = c.nheads; a.P = c.headdim; a.G = c.ngroups;
+  a.piece_len = p.total + 1;
+  a.x = tok->x; a.Bin = tok->B; a.C = tok->C; a.dt = tok->dt; a.A = c.A; a.D = c.D; a.S = S; a.y = y;
+  const cudaError_t e = launch_scan(a, p, esize(c), num_sms, st);
+  return e == cudaSuccess ? RSSM_OK : cuda_fail(e);
+}
+
+// token pointers of a scan: with no tokens in all they may be null
+static bool scan_pointers(const rssm_prompts *pr, const rssm_tokens *tok, const float *y) {
+  if (!tok) return false;
+  if (pr->total == 0) return true;
+  return tok->x && tok->B && tok->C && tok->dt && y && aligned16(tok->x) && aligned16(tok->B) && aligned16(tok->C) &&
+         aligned16(y);
+}
+
+rssm_status rssm_mamba2_scan_workspace(const rssm_config *cfg, int total, int nseq, size_t *bytes) {
+  rssm_status s = scan_validate(cfg);
+  if (s != RSSM_OK) return s;
+  if (!bytes) return RSSM_ERR_ARG;
+  if (total < 0 || nseq < 1 || nseq > cfg->batch) return RSSM_ERR_SHAPE;
+  *bytes = 0;
+  return RSSM_OK;
+}
+
+rssm_status rssm_mamba2_scan(const rssm_config *cfg, const rssm_prompts *pr, const rssm_tokens *tok, float *S, float *y,
+                             void *work, size_t work_bytes, rssm_stream stream) {
+  rssm_status s = scan_validate(cfg);
+  if (s == RSSM_OK) s = prompts_validate(pr, cfg->batch);
+  if (s != RSSM_OK) return s;
+  if (!S || !aligned16(S) || !scan_pointers(pr, tok, y)) return RSSM_ERR_ARG;
+  (void)work; (void)work_bytes;
+  int sms = 0;
+  s = sm_count(&sms);
+  if (s != RSSM_OK) return s;
+  return run_scan(*cfg, device_prompts(pr, cfg->batch, nullptr), tok, S, y, sms, reinterpret_cast<cudaStream_t>(stream));
+}
+
+rssm_status rssm_mamba2_prefill(rssm_ctx *x, const rssm_prompts *pr, const rssm_tokens *tok, float *y, void *work,
+                                size_t work_bytes, rssm_stream stream) {
+  if (!x) return RSSM_ERR_ARG;
+  if (x->cfg.kind != RSSM_MAMBA2 || !x->loaded) return RSSM_ERR_UNSUPPORTED;
+  rssm_status s = prompts_validate(pr, x->cfg.batch);
+  if (s != RSSM_OK) return s;
+  if (!scan_pointers(pr, tok, y)) return RSSM_ERR_ARG;
+  (void)work; (void)work_bytes;
+  cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+  const Prompts p = device_prompts(pr, x->cfg.batch, meta_cur(x));
+  s = run_scan(x->cfg, p, tok, reinterpret_cast<float *>(x->arena + x->lay.hp), y, x->num_sms, st);
+  if (s != RSSM_OK) return s;
+  unsigned char *skip = x->cfg.skip_tau > 0.f ? x->arena + x->lay.skip : nullptr;
+  const cudaError_t e = launch_prefill_meta(p, meta_cur(x), meta_next(x), skip, x->cfg.nheads, err_word(x), st);
+  if (e != cudaSuccess) return cuda_fail(e);
+  x->parity ^= 1;
+  // all counts stay known as 0 where they were, or where every sequence starts again
+  if (!(x->pos == 0 || (!pr->slots && pr->nseq == x->cfg.batch))) x->pos = -1;
+  else x->pos = 0;
+  return RSSM_OK;
+}
+
+// ------------------------------------------------------------------ short convolution
+
+static rssm_status shortconv_validate(const rssm_shortconv_config *c, int tokens) {
+  if (!c) return RSSM_ERR_ARG;
+  if (c->in_dtype != RSSM_F32 && c->in_dtype != RSSM_BF16) return RSSM_ERR_ARG;
+  if (c->batch < 1 || c->channels < 8 || c->channels % 8 != 0 || c->channels > (1 << 24)) return RSSM_ERR_SHAPE;
+  if (c->width < 2 || c->width > 4 || tokens < 0 || c->ring < c->width - 1 + tokens || c->ring > (1 << 20))
+    return RSSM_ERR_SHAPE;
+  long long sum = 0;
+  for (int s = 0; s < 3; ++s) {
+    if (c->split[s] < 0 || c->split[s] % 8 != 0 || (s > 0 && c->split[s] > 0 && c->split[s - 1] == 0)) return RSSM_ERR_SHAPE;
+    sum += c->split[s];
+  }
+  if (sum != c->channels) return RSSM_ERR_SHAPE;
+  if (!c->weight || !aligned16(c->weight) || (c->bias && !aligned16(c->bias))) return RSSM_ERR_ARG;
+  return RSSM_OK;
+}
+
+static rssm_status shortconv_args(const rssm_shortconv_config *c, void *hist, const int *cur, const void *in,
+                                  long long in_stride, void *const out[3], bool rows, ShortConvArgs &a) {
+  if (!hist || !aligned16(hist) || !cur || !out) return RSSM_ERR_ARG;
+  if (rows) {
+    if (!in || !aligned16(in)) return RSSM_ERR_ARG;
+    for (int s = 0; s < 3; ++s)
+      if (c->split[s] > 0 && (!out[s] || !aligned16(out[s]))) return RSSM_ERR_ARG;
+    if (in_stride < c->channels || in_stride % 8 != 0) return RSSM_ERR_SHAPE;
+  }
+  a.batch = c->batch; a.channels = c->channels; a.width = c->width; a.ring = c->ring; a.silu = c->silu != 0;
+  a.weight = c->weight; a.bias = c->bias; a.hist = hist; a.cur = cur; a.in = in; a.in_stride = in_stride;
+  for (int s = 0; s < 3; ++s) {
+    a.split[s] = c->split[s];
+    a.out[s] = out[s];
+  }
+  return RSSM_OK;
+}
+
+static int shortconv_esize(const rssm_shortconv_config *c) { return c->in_dtype == RSSM_BF16 ? 2 : 4; }
+
+rssm_status rssm_shortconv_prefill(const rssm_shortconv_config *cfg, const rssm_prompts *pr, void *hist, const int *cur,
+                                   const void *in, long long in_stride, void *const out[3], rssm_stream stream) {
+  rssm_status s = shortconv_validate(cfg, 0);
+  if (s == RSSM_OK) s = prompts_validate(pr, cfg->batch);
+  if (s != RSSM_OK) return s;
+  ShortConvArgs a{};
+  s = shortconv_args(cfg, hist, cur, in, in_stride, out, pr->total > 0, a);
+  if (s != RSSM_OK) return s;
+  const cudaError_t e = launch_shortconv_prompt(a, device_prompts(pr, cfg->batch, nullptr), shortconv_esize(cfg),
+                                                reinterpret_cast<cudaStream_t>(stream));
+  return e == cudaSuccess ? RSSM_OK : cuda_fail(e);
+}
+
+rssm_status rssm_shortconv_step(const rssm_shortconv_config *cfg, void *hist, int *cur, const void *in,
+                                long long in_stride, void *const out[3], rssm_stream stream) {
+  rssm_status s = shortconv_validate(cfg, 1);
+  if (s != RSSM_OK) return s;
+  ShortConvArgs a{};
+  s = shortconv_args(cfg, hist, cur, in, in_stride, out, true, a);
+  if (s != RSSM_OK) return s;
+  a.cur_out = cur;
+  const cudaError_t e = launch_shortconv_tokens(a, 1, 1, shortconv_esize(cfg), reinterpret_cast<cudaStream_t>(stream));
+  return e == cudaSuccess ? RSSM_OK : cuda_fail(e);
+}
+
+rssm_status rssm_shortconv_verify(const rssm_shortconv_config *cfg, int T, void *hist, const int *cur, const void *in,
+                                  long long in_stride, void *const out[3], rssm_stream stream) {
+  if (T < 1) return RSSM_ERR_ARG;
+  rssm_status s = shortconv_validate(cfg, T);
+  if (s != RSSM_OK) return s;
+  ShortConvArgs a{};
+  s = shortconv_args(cfg, hist, cur, in, in_stride, out, true, a);
+  if (s != RSSM_OK) return s;
+  const cudaError_t e = launch_shortconv_tokens(a, T, 0, shortconv_esize(cfg), reinterpret_cast<cudaStream_t>(stream));
+  return e == cudaSuccess ? RSSM_OK : cuda_fail(e);
+}
+
+rssm_status rssm_shortconv_commit(const rssm_shortconv_config *cfg, int *cur, const int *accepted, rssm_stream stream) {
+  if (!cfg || !cur || !accepted) return RSSM_ERR_ARG;
+  if (cfg->batch < 1 || cfg->width < 2 || cfg->width > 4 || cfg->ring < cfg->width - 1) return RSSM_ERR_SHAPE;
+  const cudaError_t e = launch_shortconv_commit(cur, accepted, cfg->batch, cfg->ring, cfg->ring - (cfg->width - 1),
+                                                reinterpret_cast<cudaStream_t>(stream));
+  return e == cudaSuccess ? RSSM_OK : cuda_fail(e);
+}
+
+// ------------------------------------------------------------------ draft verification
+
+rssm_status rssm_accept_drafts(int batch, int T, int vocab, const float *target, long long ld_target, const float *draft,
+                               long long ld_draft, const int *tokens, const int *count, const float *u, int *accepted,
+                               int *committed, int *next, rssm_stream stream) {
+  if (!target || !u || !accepted || !next || (T > 0 && !tokens)) return RSSM_ERR_ARG;
+  if (batch < 1 || batch > (1 << 24) || T < 0 || T > kMaxAccept || vocab < 1 || vocab > (1 << 30)) return RSSM_ERR_SHAPE;
+  if (ld_target < vocab || (draft && ld_draft < vocab)) return RSSM_ERR_SHAPE;
+  int sms = 0;
+  const rssm_status s = sm_count(&sms);
+  if (s != RSSM_OK) return s;
+  AcceptArgs a{};
+  a.batch = batch; a.T = T; a.vocab = vocab; a.target = target; a.ld_target = ld_target;
+  a.draft = draft; a.ld_draft = ld_draft; a.tokens = tokens; a.count = count; a.u = u;
+  a.accepted = accepted; a.committed = committed; a.next = next;
+  const cudaError_t e = launch_accept(a, sms, reinterpret_cast<cudaStream_t>(stream));
+  return e == cudaSuccess ? RSSM_OK : cuda_fail(e);
+}
+
 // ------------------------------------------------------------------ comparison kernels
 
 static rssm_status conv_common(const rssm_config *cfg, ConvArgs &a) {

@@ -1,0 +1,70 @@
+// prompts.cuh -- packed prompts: which piece of which prompt a block works on.
+//
+// Prompt i holds tokens off[i] .. off[i+1]-1.  Work is handed out in pieces of `len` tokens that start at the
+// prompt's own first token.  The host knows the total and the number of prompts but not the offsets, so a piece
+// number maps to a prompt on the device: prompt i owns the numbers off[i]/len + i .. off[i+1]/len + i, which are
+// disjoint, at least one for every prompt (empty ones too) and at least ceil(length/len).  total/len + nseq numbers
+// cover them all.  One coalesced pass of the block over the offsets finds the owner and checks every offset and slot
+// on the way; for a few hundred prompts that is one load a thread.
+#pragma once
+
+#include "common.cuh"
+
+namespace rssm {
+
+struct Prompts {
+  int total, nseq, nslots;
+  const int *off;
+  const int *slots;             // may be null
+  const unsigned char *resume;  // may be null
+  const int4 *meta;             // bookkeeping of a context (a resumed sequence needs an empty buffer), or null
+};
+
+struct Piece {
+  int seq, slot;
+  int begin, end;  // the prompt's tokens
+  int first;       // first token of this piece, relative to begin (may lie at or past the end)
+  int index;       // number of this piece within the prompt
+  bool resume;
+};
+
+__host__ __device__ inline int prompt_pieces(int total, int nseq, int len) { return total / len + nseq; }
+
+__device__ __forceinline__ bool prompt_bad(const Prompts &p, int i) {
+  const int o0 = p.off[i], o1 = p.off[i + 1];
+  const int s = p.slots ? p.slots[i] : i;
+  return o0 < 0 || o1 < o0 || o1 > p.total || s < 0 || s >= p.nslots;
+}
+
+// Collective over the block; false: nothing to do for this piece (bad prompts, refused slot, number without owner).
+__device__ __forceinline__ bool find_piece(const Prompts &p, int number, int len, Piece &out) {
+  __shared__ int found;
+  if (threadIdx.x == 0) found = -1;
+  __syncthreads();
+  bool bad = false;
+  for (int i = threadIdx.x; i < p.nseq; i += blockDim.x) {
+    const int o0 = p.off[i], o1 = p.off[i + 1];
+    const int s = p.slots ? p.slots[i] : i;
+    bad |= o0 < 0 || o1 < o0 || o1 > p.total || s < 0 || s >= p.nslots;
+    if (!bad && o0 / len + i <= number && number <= o1 / len + i) found = i;
+  }
+  bad = __syncthreads_or(bad);
+  const int i = found;
+  if (bad || i < 0) return false;
+  out.seq = i;
+  out.begin = p.off[i];
+  out.end = p.off[i + 1];
+  out.slot = p.slots ? p.slots[i] : i;
+  out.index = number - (out.begin / len + i);
+  out.first = out.index * len;
+  out.resume = p.resume && p.resume[i];
+  if (out.resume && p.meta && (p.meta[out.slot].x != 0 || p.meta[out.slot].z != 0)) return false;
+  if (p.slots) {  // a slot named twice
+    bool twice = false;
+    for (int j = threadIdx.x; j < p.nseq; j += blockDim.x) twice |= j != i && p.slots[j] == out.slot;
+    if (__syncthreads_or(twice)) return false;
+  }
+  return true;
+}
+
+}  // namespace rssm

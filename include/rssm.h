@@ -70,7 +70,10 @@ enum {
   RSSM_DEV_PENDING = 1,     /* step / verify / flush on a sequence with a verify pending */
   RSSM_DEV_NO_VERIFY = 2,   /* commit on a sequence without a pending verify */
   RSSM_DEV_ACCEPTED = 3,    /* accepted length outside 0..pending */
-  RSSM_DEV_TIMEOUT = 4      /* a bounded wait on an asynchronous copy gave up */
+  RSSM_DEV_TIMEOUT = 4,     /* a bounded wait on an asynchronous copy gave up */
+  RSSM_DEV_PROMPT = 5,      /* prefill: offsets not 0 <= off[i] <= off[i+1] <= total, or a slot outside the batch or
+                             * named twice; the index reported is the prompt's place in its call */
+  RSSM_DEV_BUFFERED = 6     /* prefill that resumes a sequence with buffered records (flush it first) */
 };
 
 typedef enum { RSSM_MAMBA2 = 0, RSSM_GDN = 1 } rssm_kind;
@@ -186,6 +189,90 @@ rssm_status rssm_commit(rssm_ctx *ctx, const int *accepted, rssm_stream stream);
 /* Fold the committed records of the selected sequences into the checkpoint (count = 0,
  * epoch += 1 where count > 0).  mask device uint8 [Bt] (nonzero = selected) or NULL = all. */
 rssm_status rssm_flush(rssm_ctx *ctx, const unsigned char *mask, rssm_stream stream);
+
+/* ---------------------------------------------------------------- prompts
+ * The pages start from a checkpoint and leave open what makes one; these calls do, from the published Mamba-2
+ * recurrence.  Prompts come packed: prompt i holds tokens offsets[i] .. offsets[i+1]-1 of `total`, so the token
+ * inputs have the leading dimension [total] and no padding.  A prompt may be empty.  Rows of no prompt are neither
+ * read into a result nor written.  Prompt i belongs to sequence slots[i] of the state (i itself without slots); other
+ * sequences keep theirs.
+ * If any offset or slot is out of range nothing is written at all; prompts that share a slot are left out. */
+typedef struct {
+  int total, nseq;              /* tokens in all, prompts; total >= 0, nseq >= 1 */
+  const int *offsets;           /* device [nseq + 1], non-decreasing within 0..total */
+  const int *slots;             /* device [nseq] or NULL */
+  const unsigned char *resume;  /* device [nseq] or NULL: nonzero = continue from the sequence's state, else from zero */
+} rssm_prompts;
+
+/* Bytes of device scratch that rssm_mamba2_scan and rssm_mamba2_prefill want for prompts of this size (0 is
+ * possible): segment states, so that few long prompts fill the GPU.  Depends on the arguments alone. */
+rssm_status rssm_mamba2_scan_workspace(const rssm_config *cfg, int total, int nseq, size_t *bytes);
+
+/* Mamba-2 over whole prompts, on a state that the caller keeps (cfg as for rssm_conv_mamba2_step; cfg.batch is the
+ * number of sequences of S).  tok: x [total][H][P], B, C [total][G][N], dt [total][H] in cfg.in_dtype;
+ *   S device fp32 [batch][H][P][N], the prompts' sequences rewritten;  y device fp32 [total][H][P];
+ *   work device, 256-byte aligned, >= rssm_mamba2_scan_workspace bytes (NULL if that is 0), free again when the
+ *   call's work on the stream is done. */
+rssm_status rssm_mamba2_scan(const rssm_config *cfg, const rssm_prompts *pr, const rssm_tokens *tok, float *S, float *y,
+                             void *work, size_t work_bytes, rssm_stream stream);
+
+/* The same on a context: the states become the sequences' checkpoints (count = pending = 0, epoch += 1, skip flags
+ * cleared), so that decoding goes on from them.  A prompt that starts from zero replaces whatever its sequence held; one
+ * that resumes needs an empty buffer (RSSM_DEV_PENDING, RSSM_DEV_BUFFERED: that prompt is left out).  The context must
+ * have been loaded once (rssm_load_checkpoint). */
+rssm_status rssm_mamba2_prefill(rssm_ctx *ctx, const rssm_prompts *pr, const rssm_tokens *tok, float *y, void *work,
+                                size_t work_bytes, rssm_stream stream);
+
+/* ---------------------------------------------------------------- short convolution
+ * The causal depthwise filter in front of a layer's inputs (x, B, C of Mamba-2; q, k, v of GDN):
+ *   out[t][c] = act(bias[c] + sum_{k < K} weight[c][k] in[t - (K-1) + k][c]),
+ * summed in fp32 and rounded once to the input type.  Its state follows the scheme of the replay buffer: a ring of
+ * the last raw inputs, hist [batch][ring][channels] in the input type, with a cursor cur [batch] (the slot of the next
+ * token, 0..ring-1; any other value is taken modulo ring).  A draft is a tentative row and commit moves the cursor.
+ * Row r of `in` starts at in + r * in_stride elements.  Outputs are up to three contiguous tensors out[s]
+ * [rows][split[s]], the channels cut in order, so that a step or verify call can take them as they are. */
+typedef struct {
+  int batch;         /* sequences of hist, >= 1 */
+  int channels;      /* multiple of 8 */
+  int width;         /* K, 2..4 */
+  int ring;          /* rows of hist, >= K - 1 + tokens of a call (K - 1 for prompts) */
+  int in_dtype;      /* rssm_dtype of in, weight, bias, hist and out */
+  int silu;          /* 1: act(v) = v / (1 + exp(-v)), 0: none */
+  int split[3];      /* channels of each output, multiples of 8 that sum to channels; unused ones 0 */
+  const void *weight; /* device [channels][K] */
+  const void *bias;   /* device [channels] or NULL */
+} rssm_shortconv_config;
+
+/* Prompts (see rssm_prompts; slots index hist): in [total] rows.  The K-1 newest inputs of each prompt become its
+ * sequence's history; its cursor stays. */
+rssm_status rssm_shortconv_prefill(const rssm_shortconv_config *cfg, const rssm_prompts *pr, void *hist, const int *cur,
+                                   const void *in, long long in_stride, void *const out[3], rssm_stream stream);
+/* One token a sequence: in [batch] rows; the cursor advances. */
+rssm_status rssm_shortconv_step(const rssm_shortconv_config *cfg, void *hist, int *cur, const void *in,
+                                long long in_stride, void *const out[3], rssm_stream stream);
+/* T tentative tokens a sequence, 1 <= T <= ring - (K-1): in [batch * T] rows; the cursor stays. */
+rssm_status rssm_shortconv_verify(const rssm_shortconv_config *cfg, int T, void *hist, const int *cur, const void *in,
+                                  long long in_stride, void *const out[3], rssm_stream stream);
+/* cur[b] moves by accepted[b] (device int32 [batch]; clamped to 0..ring-(K-1)).  Uses cfg's batch, width and ring. */
+rssm_status rssm_shortconv_commit(const rssm_shortconv_config *cfg, int *cur, const int *accepted, rssm_stream stream);
+
+/* ---------------------------------------------------------------- draft verification
+ * Which drafts of a speculative round stand ([HMD] Interpretation 3rd paragraph leaves the test itself open; this is
+ * the published rejection rule, after which tokens are distributed as the target's): with target probabilities p_j
+ * and draft probabilities q_j after j drafts, draft d_j stands while u_j q_j(d_j) < p_j(d_j).  At the first that does
+ * not (n), the next token is drawn from max(p_n - q_n, 0); if all of them stand (n = T_b), from p_n.  It is the lowest v
+ * whose inclusive sum exceeds u_T times the sum over all v (the last v with mass if none does).  Without q (drafts
+ * that were looked up, not sampled) q_j is 1 at d_j and 0 elsewhere.  Masses and their sums are 64-bit, and the product
+ * above is exact.  Entries that are not positive finite numbers carry no mass; if max(p_n - q_n, 0) has none, p_n is
+ * used, and if that has none next is -1.  A draft outside 0..vocab-1 never stands.
+ *   target device fp32, row (b, j), j = 0..T, at target + (b (T+1) + j) ld_target;  draft likewise with T rows a
+ *   sequence, or NULL;  tokens device int32 [batch][T];  count device int32 [batch] (drafts of sequence b, clamped to
+ *   0..T) or NULL = T;  u device fp32 [batch][T+1] in [0, 1): u_0 .. u_{T-1} for the drafts, u_T for the draw;
+ *   accepted = n, committed = n + 1 (may be NULL: what rssm_commit wants where a round's first verified token was
+ *   the one drawn before), next: device int32 [batch].  0 <= T <= 16. */
+rssm_status rssm_accept_drafts(int batch, int T, int vocab, const float *target, long long ld_target, const float *draft,
+                               long long ld_draft, const int *tokens, const int *count, const float *u, int *accepted,
+                               int *committed, int *next, rssm_stream stream);
 
 /* ---------------------------------------------------------------- inspection */
 

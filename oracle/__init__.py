@@ -33,6 +33,8 @@ Modules:
 * ``philox`` -- Philox4x32-10.
 * ``decoder`` -- the checkpoint + input-buffer bookkeeping (step, verify,
   commit, flush) and the separate-precision modes.
+* ``prompts`` -- packed prompts through the recurrence, the short convolution
+  with its history ring, and the verification of drafted tokens.
 
 Pins: every function is checked by tests marked ``not gpu`` against closed
 forms, invariants stated by the pages, brute force on tiny shapes, library
