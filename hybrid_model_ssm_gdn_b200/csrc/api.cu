@@ -430,14 +430,28 @@ static Prompts device_prompts(const rssm_prompts *pr, int nslots, const int4 *me
   return p;
 }
 
+// Tokens of a piece of a prompt (total + 1: prompts are not cut).
+static int scan_piece_len(const rssm_config &c, int total, int nseq) {
+  const char *pl = getenv("RSSM_PIECE_LEN");
+  if (pl && c.in_dtype == RSSM_BF16 && total > 0) return atoi(pl) < total + 1 ? atoi(pl) : total + 1;
+  (void)nseq;
+  return total + 1;
+}
+
 static rssm_status run_scan(const rssm_config &c, const Prompts &p, const rssm_tokens *tok, float *S, float *y,
-                            int num_sms, cudaStream_t st) {
+                            void *work, size_t work_bytes, int *err, long long wait_cycles, int num_sms, cudaStream_t st) {
   if (c.nheads > 65535) return RSSM_ERR_SHAPE;  // one grid row a head
   ScanArgs a{};
   a.H = c.nheads; a.P = c.headdim; a.G = c.ngroups;
-  a.piece_len = p.total + 1;
+  a.piece_len = scan_piece_len(c, p.total, p.nseq);
   a.x = tok->x; a.Bin = tok->B; a.C = tok->C; a.dt = tok->dt; a.A = c.A; a.D = c.D; a.S = S; a.y = y;
-  const cudaError_t e = launch_scan(a, p, esize(c), num_sms, st);
+  a.work = work; a.err = err; a.wait_cycles = wait_cycles;
+  if (a.piece_len <= p.total) {
+    if (!work || ((uintptr_t)work & 255u)) return RSSM_ERR_ARG;
+    if (work_bytes < scan_tc_workspace(a.H, a.P, prompt_pieces(p.total, p.nseq, a.piece_len), nullptr))
+      return RSSM_ERR_ARENA_TOO_SMALL;
+  }
+  const cudaError_t e = c.in_dtype == RSSM_BF16 && p.total > 0 ? launch_scan_tc(a, p, st) : launch_scan(a, p, esize(c), num_sms, st);
   return e == cudaSuccess ? RSSM_OK : cuda_fail(e);
 }
 
@@ -454,7 +468,8 @@ rssm_status rssm_mamba2_scan_workspace(const rssm_config *cfg, int total, int ns
   if (s != RSSM_OK) return s;
   if (!bytes) return RSSM_ERR_ARG;
   if (total < 0 || nseq < 1 || nseq > cfg->batch) return RSSM_ERR_SHAPE;
-  *bytes = 0;
+  const int len = scan_piece_len(*cfg, total, nseq);
+  *bytes = len <= total ? scan_tc_workspace(cfg->nheads, cfg->headdim, prompt_pieces(total, nseq, len), nullptr) : 0;
   return RSSM_OK;
 }
 
@@ -464,11 +479,11 @@ rssm_status rssm_mamba2_scan(const rssm_config *cfg, const rssm_prompts *pr, con
   if (s == RSSM_OK) s = prompts_validate(pr, cfg->batch);
   if (s != RSSM_OK) return s;
   if (!S || !aligned16(S) || !scan_pointers(pr, tok, y)) return RSSM_ERR_ARG;
-  (void)work; (void)work_bytes;
   int sms = 0;
   s = sm_count(&sms);
   if (s != RSSM_OK) return s;
-  return run_scan(*cfg, device_prompts(pr, cfg->batch, nullptr), tok, S, y, sms, reinterpret_cast<cudaStream_t>(stream));
+  return run_scan(*cfg, device_prompts(pr, cfg->batch, nullptr), tok, S, y, work, work_bytes, nullptr, kWaitCycles, sms,
+                  reinterpret_cast<cudaStream_t>(stream));
 }
 
 rssm_status rssm_mamba2_prefill(rssm_ctx *x, const rssm_prompts *pr, const rssm_tokens *tok, float *y, void *work,
@@ -478,10 +493,10 @@ rssm_status rssm_mamba2_prefill(rssm_ctx *x, const rssm_prompts *pr, const rssm_
   rssm_status s = prompts_validate(pr, x->cfg.batch);
   if (s != RSSM_OK) return s;
   if (!scan_pointers(pr, tok, y)) return RSSM_ERR_ARG;
-  (void)work; (void)work_bytes;
   cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
   const Prompts p = device_prompts(pr, x->cfg.batch, meta_cur(x));
-  s = run_scan(x->cfg, p, tok, reinterpret_cast<float *>(x->arena + x->lay.hp), y, x->num_sms, st);
+  s = run_scan(x->cfg, p, tok, reinterpret_cast<float *>(x->arena + x->lay.hp), y, work, work_bytes, err_word(x),
+               x->wait_cycles, x->num_sms, st);
   if (s != RSSM_OK) return s;
   unsigned char *skip = x->cfg.skip_tau > 0.f ? x->arena + x->lay.skip : nullptr;
   const cudaError_t e = launch_prefill_meta(p, meta_cur(x), meta_next(x), skip, x->cfg.nheads, err_word(x), st);

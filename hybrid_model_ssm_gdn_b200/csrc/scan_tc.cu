@@ -1,0 +1,694 @@
+// scan_tc.cu -- the Mamba-2 scan over packed prompts on the tensor cores (bf16 inputs).
+//
+// Chunks of Q = 128 tokens turn the recurrence into matrix products.  With c_j the sum of dt over the chunk's tokens up
+// to j (included), per head:
+//   G   = C B^T                                          tokens x tokens, one for all heads of a group
+//   M   = [j >= i] G_ji exp(A (c_j - c_i)) dt_i + D [j = i]
+//   Y   = M X + diag(exp(A c)) C S^T                      tokens x P
+//   S  <- exp(A c_Q) S + (diag(exp(A (c_Q - c)) dt) X)^T B   P x 128
+// A block carries two heads of one group (2 x 64 rows of state fill the 128 lanes of tensor memory) along one piece of a
+// prompt, chunk after chunk, so the state never leaves the chip.
+//
+// Precision: C, B and X are bf16 and enter exactly; sums are fp32.  The three fp32 operands M, S and the weighted X are
+// cut into two bf16 pieces (hi = RN(v), lo = RN(v - hi): what is lost is below 2^-17 of v) and multiplied twice, which
+// keeps the library's fp32 outputs and checkpoints at the accuracy its other kernels have; one bf16 piece would leave
+// them at 2^-9.  That doubles three of the four products: 14.7 M multiply-adds for a chunk of two heads, 3600 cycles of
+// the tensor core, against the 2.3 us that its bytes take at the measured bandwidth (x, y and the group's share of B
+// and C): both limits lie close together, and tcgen05 is needed for either (mma.sync measured a quarter of its rate).
+//
+// Tensor memory (512 columns): S 128 (row = head and p, column = n), Y 128 (row = token, column = head and p), G 128, and
+// M as hi | lo pairs 128, for one head after the other; M is the left operand straight from tensor memory.  Shared
+// memory: C, X, two stages of B, and one 64 KB buffer that holds the pieces of S until C S^T is done and then the pieces
+// of the weighted X; 192 KB in all, so one block an SM.
+//
+// Decays never divide and never exceed what they stand for: a token's weight is a product of exp of sums of dt over
+// tokens between, by blocks of 32: within the row's block exp(A (c_j - c_i)), else exp(A (c_j - end)) exp(A (end - c_i))
+// with `end` the end of i's block, both at most 1, so only 32 exponentials a row and head are left.
+//
+// Twenty warps: 0-7 make M from G, scale C S^T and write Y; 8-15 weigh X and cut S; then one for the loads, one for the
+// products along the state (C S^T, S), one for those along the tokens (G, M X), one for the decay tables.  The loop that
+// bounds a chunk is  cut S -> C S^T -> weigh X -> S product -> cut S; all else runs beside it.
+// Every wait is bounded; after one runs out the others stop waiting and the block goes through its remaining steps, so
+// all barriers and the release of tensor memory are still reached.
+#include <cuda.h>
+
+#include "kernels.h"
+#include "tcgen05.cuh"
+
+namespace rssm {
+
+namespace {
+
+constexpr int Q = 128;
+constexpr int kTile = Q * 128;  // bytes of a tile: 128 rows of 64 bf16
+constexpr uint32_t kColS = 0, kColY = 128, kColG = 256, kColM = 384;
+constexpr int kWarpLoad = 16, kWarpState = 17, kWarpToken = 18, kWarpTable = 19;
+constexpr int kTcThreads = 640;
+
+struct TcShared {
+  unsigned char C[2][kTile];     // K-major, halves of n
+  unsigned char X[2][kTile];     // token rows, per head; afterwards Y on its way out, 4 KB a warp
+  unsigned char B[2][2][kTile];  // stages, halves of n
+  unsigned char U[4][kTile];     // S pieces: hi, lo x halves of n; weighted X pieces: hi, lo x heads
+  float cl[2][2][Q];             // sum of dt within the token's block of 32, included  (chunk parity, head, token)
+  float dt[2][2][Q];
+  float e[2][2][Q];              // exp(A (end of block - c_i)) dt_i
+  float w[2][2][Q];              // exp(A (c_Q - c_i)) dt_i
+  float tot[2][2][4];            // sums of the blocks of 32
+  uint64_t full_C, full_X, full_B[2], x_free, tab_full[2], tab_free[2];
+  uint64_t g_done, y1_done, y20_done, y2_done, y_free, s_done[2], sp_ready, m_ready[2], xs_ready, drained[2];
+  uint32_t tmem;
+  int abort;
+};
+constexpr int kTcSmem = (int)sizeof(TcShared) + 1024;
+
+struct TcArgs {
+  int H, P, G, pairs;       // pairs of heads in a group
+  int piece_len;
+  const float *A, *D;
+  const __nv_bfloat16 *dt;  // [total][H]
+  float *S;                 // [nslots][H][P][128]
+  float *y;                 // [total][H][P]
+  float *seg;               // piece states [pieces][H][P][128], or null: prompts are not cut
+  float *seg_dt;            // their sums of dt [pieces][H]
+  int *err;                 // may be null
+  long long wait_cycles;
+};
+
+constexpr float kLog2e = 1.4426950408889634f;
+
+struct Waiter {
+  TcShared *sh;
+  int *err;
+  int seq;
+  WaitSpec ws;
+  __device__ __forceinline__ void operator()(uint64_t &bar, int phase) const {
+    if (!mbar_wait_or_abort(&bar, phase & 1, &sh->abort, ws)) {
+      *(volatile int *)&sh->abort = 1;
+      if (err) record_error(err, seq, RSSM_DEV_TIMEOUT);
+    }
+  }
+};
+
+// after a warp's writes to shared or tensor memory, or its reads of what is to be overwritten
+__device__ __forceinline__ void warp_arrive(uint64_t &bar, int lane) {
+  tm_fence_before();
+  fence_async_smem();
+  __syncwarp();
+  if (lane == 0) mbar_arrive(&bar);
+}
+
+// kState: only the state at the piece's end, from zero (first pass of prompts that are cut into pieces)
+template <bool kState>
+__global__ void __launch_bounds__(kTcThreads, 1)
+    scan_tc_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_constant__ CUtensorMap map_B,
+                   const __grid_constant__ CUtensorMap map_C, const __grid_constant__ CUtensorMap map_y, TcArgs a,
+                   Prompts pr) {
+  extern __shared__ unsigned char raw[];
+  TcShared &sh = *reinterpret_cast<TcShared *>((reinterpret_cast<uintptr_t>(raw) + 1023) & ~(uintptr_t)1023);
+  const int units = a.G * a.pairs;
+  const int number = blockIdx.x / units, unit = blockIdx.x % units;
+  Piece pc;
+  if (!find_piece(pr, number, a.piece_len, pc)) return;
+  const int r = a.H / a.G, group = unit / a.pairs;
+  const int h0 = group * r + 2 * (unit % a.pairs);
+  const bool two = h0 + 1 < (group + 1) * r;  // without a second head the first is computed twice and stored once
+  const int h1 = two ? h0 + 1 : h0;
+  const int len = pc.end - pc.begin, ntok = min(a.piece_len, len - pc.first);
+  const bool cut_up = len > a.piece_len, last_piece = pc.first + ntok >= len;
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const size_t head_elems = (size_t)a.P * kCols;
+
+  if (ntok <= 0 || (kState && last_piece)) {
+    if (!kState && pc.index == 0 && !pc.resume) {  // an empty prompt from zero
+      float *S0 = a.S + ((size_t)pc.slot * a.H + h0) * head_elems;
+      for (size_t i = tid; i < head_elems * (two ? 2 : 1) / 4; i += kTcThreads) reinterpret_cast<float4 *>(S0)[i] = f4zero();
+    }
+    return;
+  }
+  const float *init = nullptr;  // state at the piece's start: [H][P][128] from its first head
+  if (!kState) {
+    if (cut_up) init = a.seg + (size_t)number * a.H * head_elems;
+    else if (pc.resume) init = a.S + (size_t)pc.slot * a.H * head_elems;
+  }
+  float *final = nullptr;
+  if (kState) final = a.seg + (size_t)number * a.H * head_elems;
+  else if (last_piece) final = a.S + (size_t)pc.slot * a.H * head_elems;
+  const int chunks = (ntok + Q - 1) / Q;
+  const int t0 = pc.begin + pc.first;
+
+  if (tid == 0) {
+    uint64_t *one[] = {&sh.full_C, &sh.full_X, &sh.full_B[0], &sh.full_B[1], &sh.tab_full[0], &sh.tab_full[1], &sh.g_done,
+                       &sh.y1_done, &sh.y20_done, &sh.y2_done, &sh.s_done[0], &sh.s_done[1], &sh.drained[0],
+                       &sh.drained[1]};
+    for (uint64_t *b : one) mbar_init(b, 1);
+    uint64_t *team[] = {&sh.x_free, &sh.y_free, &sh.sp_ready, &sh.m_ready[0], &sh.m_ready[1], &sh.xs_ready};
+    for (uint64_t *b : team) mbar_init(b, 8);
+    for (int i = 0; i < 2; ++i) mbar_init(&sh.tab_free[i], kState ? 8 : 16);
+    sh.abort = 0;
+    fence_barrier_init();
+  }
+  if (warp == kWarpLoad) tm_alloc(&sh.tmem, 512);
+  tm_fence_before();
+  __syncthreads();
+  tm_fence_after();
+  const uint32_t tm = sh.tmem;
+  const Waiter wait{&sh, a.err, pc.seq, {a.wait_cycles, 0}};
+
+  if (warp == kWarpLoad) {
+    if (lane == 0) {
+      for (int c = 0; c < chunks; ++c) {
+        const int t = t0 + c * Q;
+        if (c > 1) wait(sh.s_done[c & 1], (c - 2) >> 1);
+        mbar_arrive_expect_tx(&sh.full_B[c & 1], 2 * kTile);
+        tma_load_2d(sh.B[c & 1][0], &map_B, group * kCols, t, &sh.full_B[c & 1]);
+        tma_load_2d(sh.B[c & 1][1], &map_B, group * kCols + 64, t, &sh.full_B[c & 1]);
+        if (!kState) {
+          if (c > 0) {
+            wait(sh.y1_done, c - 1);
+            wait(sh.g_done, c - 1);
+          }
+          mbar_arrive_expect_tx(&sh.full_C, 2 * kTile);
+          tma_load_2d(sh.C[0], &map_C, group * kCols, t, &sh.full_C);
+          tma_load_2d(sh.C[1], &map_C, group * kCols + 64, t, &sh.full_C);
+        }
+        if (c > 0) {
+          if (kState) wait(sh.xs_ready, c - 1);
+          else wait(sh.x_free, c - 1);
+        }
+        mbar_arrive_expect_tx(&sh.full_X, 2 * kTile);
+        tma_load_3d(sh.X[0], &map_x, 0, h0, t, &sh.full_X);
+        tma_load_3d(sh.X[1], &map_x, 0, h1, t, &sh.full_X);
+      }
+      if (*(volatile int *)&sh.abort) {  // otherwise every load has been consumed when the block ends
+        if (!kState) mbar_wait(&sh.full_C, (chunks - 1) & 1, wait.ws);
+        mbar_wait(&sh.full_X, (chunks - 1) & 1, wait.ws);
+        mbar_wait(&sh.full_B[(chunks - 1) & 1], ((chunks - 1) >> 1) & 1, wait.ws);
+        if (chunks > 1) mbar_wait(&sh.full_B[chunks & 1], ((chunks - 2) >> 1) & 1, wait.ws);
+      }
+    }
+    __syncwarp();
+  } else if (warp == kWarpState) {
+    if (lane == 0) {
+      constexpr uint32_t shape_y = mma_shape(128, 128, false, false), shape_s = mma_shape(128, 128, true, true);
+      const uint64_t dC = tile_desc(sh.C[0], 16), dSp = tile_desc(sh.U[0], 16);        // K-major
+      const uint64_t dXs = tile_desc(sh.U[0], kTile), dB = tile_desc(sh.B[0][0], kTile);  // MN-major, two tiles
+      constexpr int step = kTile >> 4;
+      for (int c = 0; c < chunks; ++c) {
+        const int s = c & 1;
+        const bool carried = c > 0 || init != nullptr;
+        if (!kState) {
+          wait(sh.full_C, c);
+          wait(sh.sp_ready, c);
+          if (c > 0) wait(sh.y_free, c - 1);
+          tm_fence_after();
+          if (carried) {
+#pragma unroll
+            for (int p = 0; p < 2; ++p)
+#pragma unroll
+              for (int k = 0; k < 8; ++k)
+                mma_ss(tm + kColY, dC + (k >> 2) * step + 2 * (k & 3), dSp + (2 * p + (k >> 2)) * step + 2 * (k & 3),
+                       shape_y, p > 0 || k > 0);
+          }
+          mma_commit(&sh.y1_done);
+        } else {
+          wait(sh.sp_ready, c);
+        }
+        wait(sh.full_B[s], c >> 1);
+        wait(sh.xs_ready, c);
+        tm_fence_after();
+        if (c + 1 < chunks || final) {
+#pragma unroll
+          for (int p = 0; p < 2; ++p)
+#pragma unroll
+            for (int k = 0; k < 8; ++k)  // 16 token rows are 2048 bytes
+              mma_ss(tm + kColS, dXs + 2 * p * step + 128 * k, dB + 2 * s * step + 128 * k, shape_s,
+                     carried || p > 0 || k > 0);
+        }
+        mma_commit(&sh.s_done[s]);
+      }
+      mma_commit(&sh.drained[0]);
+      mbar_wait(&sh.drained[0], 0, wait.ws);
+    }
+    __syncwarp();
+  } else if (warp == kWarpToken) {
+    if (!kState && lane == 0) {
+      constexpr uint32_t shape_g = mma_shape(128, 128, false, false), shape_y = mma_shape(128, 64, false, true);
+      const uint64_t dC = tile_desc(sh.C[0], 16), dB = tile_desc(sh.B[0][0], 16), dX = tile_desc(sh.X[0], 16);
+      constexpr int step = kTile >> 4;
+      for (int c = 0; c < chunks; ++c) {
+        const int s = c & 1;
+        const bool carried = c > 0 || init != nullptr;
+        wait(sh.full_B[s], c >> 1);
+        wait(sh.full_C, c);
+        tm_fence_after();
+#pragma unroll
+        for (int k = 0; k < 8; ++k)
+          mma_ss(tm + kColG, dC + (k >> 2) * step + 2 * (k & 3), dB + (2 * s + (k >> 2)) * step + 2 * (k & 3), shape_g,
+                 k > 0);
+        mma_commit(&sh.g_done);
+        wait(sh.full_X, c);
+        if (ntok - c * Q < Q) wait(sh.xs_ready, c);  // the rows behind the prompt's end have been cleared
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          wait(sh.m_ready[h], c);
+          tm_fence_after();
+#pragma unroll
+          for (int p = 0; p < 2; ++p)
+#pragma unroll
+            for (int k = 0; k < 8; ++k)
+              mma_ts(tm + kColY + 64 * h, tm + kColM + 64 * p + 8 * k, dX + h * step + 128 * k, shape_y,
+                     carried || p > 0 || k > 0);
+          mma_commit(h ? &sh.y2_done : &sh.y20_done);
+        }
+      }
+      mma_commit(&sh.drained[1]);
+      mbar_wait(&sh.drained[1], 0, wait.ws);
+    }
+    __syncwarp();
+  } else if (warp == kWarpTable) {
+    // decay tables, a chunk ahead: lane = token of a block of 32, four blocks a head
+    const __nv_bfloat16 *dtp[2] = {a.dt + (size_t)t0 * a.H + h0, a.dt + (size_t)t0 * a.H + h1};
+    const float lA[2] = {a.A[h0] * kLog2e, a.A[h1] * kLog2e};
+    float total_dt[2] = {0.f, 0.f};
+    __nv_bfloat16 next[2][4];
+    auto fetch = [&](int c) {
+#pragma unroll
+      for (int h = 0; h < 2; ++h)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const int t = c * Q + 32 * i + lane;
+          next[h][i] = t < ntok ? dtp[h][(size_t)t * a.H] : __ushort_as_bfloat16(0);
+        }
+    };
+    fetch(0);
+    for (int c = 0; c < chunks; ++c) {
+      const int b = c & 1;
+      float d[2][4];
+#pragma unroll
+      for (int h = 0; h < 2; ++h)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) d[h][i] = __bfloat162float(next[h][i]);
+      if (c + 1 < chunks) fetch(c + 1);
+      if (c > 1) wait(sh.tab_free[b], (c - 2) >> 1);
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        float after = 0.f;
+#pragma unroll
+        for (int i = 3; i >= 0; --i) {
+          float s = d[h][i];
+#pragma unroll
+          for (int off = 1; off < 32; off <<= 1) {
+            const float t = __shfl_up_sync(0xffffffffu, s, off);
+            if (lane >= off) s += t;
+          }
+          const float tot = __shfl_sync(0xffffffffu, s, 31);
+          const float e = exp2_approx(lA[h] * (tot - s)) * d[h][i];
+          sh.cl[b][h][32 * i + lane] = s;
+          sh.dt[b][h][32 * i + lane] = d[h][i];
+          sh.e[b][h][32 * i + lane] = e;
+          sh.w[b][h][32 * i + lane] = e * exp2_approx(lA[h] * after);
+          if (lane == 0) sh.tot[b][h][i] = tot;
+          after += tot;
+        }
+        total_dt[h] += after;
+      }
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&sh.tab_full[b]);
+    }
+    if (kState && lane == 0) {
+      a.seg_dt[(size_t)number * a.H + h0] = total_dt[0];
+      if (two) a.seg_dt[(size_t)number * a.H + h1] = total_dt[1];
+    }
+  } else if (warp < 8) {
+    // token rows: M from G, Y
+    if (!kState) {
+      const int g = warp >> 2, q = warp & 3, row = 32 * q + lane;
+      const uint32_t lanes = (uint32_t)(32 * q) << 16;
+      const float lA[2] = {a.A[h0] * kLog2e, a.A[h1] * kLog2e}, D[2] = {a.D[h0], a.D[h1]};
+      const int hg = g ? h1 : h0;
+      unsigned char *stage = sh.X[0] + warp * 4096;
+      for (int c = 0; c < chunks; ++c) {
+        const int b = c & 1, valid = min(Q, ntok - c * Q);
+        const bool carried = c > 0 || init != nullptr;
+        wait(sh.tab_full[b], c >> 1);
+        wait(sh.g_done, c);
+        tm_fence_after();
+        float sum = sh.cl[b][g][row];  // c_j, for the head of this thread's Y columns
+#pragma unroll
+        for (int i = 0; i < 3; ++i) sum += i < q ? sh.tot[b][g][i] : 0.f;
+        const float rise = exp2_approx(lA[g] * sum);
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          // both warps of a quarter take its rows, each 16 of a block's 32 columns
+          const float cl = sh.cl[b][h][row];
+          float since = cl;  // sum of dt from the end of block i to this token
+#pragma unroll
+          for (int half = 1; half >= 0; --half) {
+            uint32_t G[2][16];
+#pragma unroll
+            for (int i = 0; i < 2; ++i)
+              if (2 * half + i <= q) tm_ld16(tm + lanes + kColG + 32 * (2 * half + i) + 16 * g, G[i]);
+            tm_wait_ld();
+            if (h == 1 && half == 1) {  // M of the first head has been used
+              wait(sh.y20_done, c);
+              tm_fence_after();
+            }
+#pragma unroll
+            for (int ii = 1; ii >= 0; --ii) {
+              const int i = 2 * half + ii;
+              uint32_t hi[8], lo[8];
+              if (i > q) {
+#pragma unroll
+                for (int k = 0; k < 8; ++k) hi[k] = lo[k] = 0;
+              } else if (i == q) {
+#pragma unroll
+                for (int k = 0; k < 16; k += 4) {
+                  const float4 ci = *reinterpret_cast<const float4 *>(&sh.cl[b][h][32 * i + 16 * g + k]);
+                  const float4 di = *reinterpret_cast<const float4 *>(&sh.dt[b][h][32 * i + 16 * g + k]);
+                  const float cs[4] = {ci.x, ci.y, ci.z, ci.w}, ds[4] = {di.x, di.y, di.z, di.w};
+                  float m[4];
+#pragma unroll
+                  for (int j = 0; j < 4; ++j) {
+                    const int col = 16 * g + k + j;
+                    const float v = __uint_as_float(G[ii][k + j]) * (exp2_approx(lA[h] * (cl - cs[j])) * ds[j]);
+                    m[j] = col < lane ? v : col == lane ? v + D[h] : 0.f;
+                  }
+                  split_bf16x2(m[0], m[1], hi[k / 2], lo[k / 2]);
+                  split_bf16x2(m[2], m[3], hi[k / 2 + 1], lo[k / 2 + 1]);
+                }
+              } else {
+                const float f = exp2_approx(lA[h] * since);
+                since += sh.tot[b][h][i];
+#pragma unroll
+                for (int k = 0; k < 16; k += 4) {
+                  const float4 e = *reinterpret_cast<const float4 *>(&sh.e[b][h][32 * i + 16 * g + k]);
+                  split_bf16x2(__uint_as_float(G[ii][k]) * (f * e.x), __uint_as_float(G[ii][k + 1]) * (f * e.y),
+                               hi[k / 2], lo[k / 2]);
+                  split_bf16x2(__uint_as_float(G[ii][k + 2]) * (f * e.z), __uint_as_float(G[ii][k + 3]) * (f * e.w),
+                               hi[k / 2 + 1], lo[k / 2 + 1]);
+                }
+              }
+              tm_st8(tm + lanes + kColM + 16 * i + 8 * g, hi);
+              tm_st8(tm + lanes + kColM + 64 + 16 * i + 8 * g, lo);
+            }
+          }
+          if (h == 0) {
+            // diag(exp(A c)) C S^T in place, before M X is added; this warp's half of the columns is head g
+            wait(sh.y1_done, c);
+            tm_fence_after();
+            if (carried) {
+#pragma unroll
+              for (int part = 0; part < 2; ++part) {
+                uint32_t v[32];
+                tm_ld32(tm + lanes + kColY + 64 * g + 32 * part, v);
+                tm_wait_ld();
+#pragma unroll
+                for (int i = 0; i < 32; ++i) v[i] = __float_as_uint(__uint_as_float(v[i]) * rise);
+                tm_st32(tm + lanes + kColY + 64 * g + 32 * part, v);
+              }
+            }
+          }
+          tm_wait_st();
+          warp_arrive(sh.m_ready[h], lane);
+        }
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&sh.tab_free[b]);
+        // Y: through this warp's 4 KB of the X buffer, which both heads' products and the weighing are done with
+        wait(sh.y2_done, c);
+        wait(sh.xs_ready, c);
+        tm_fence_after();
+        const bool whole = 32 * q + 32 <= valid, store = g == 0 || two;
+        const int t = t0 + c * Q + 32 * q;
+#pragma unroll
+        for (int part = 0; part < 2; ++part) {
+          uint32_t v[32];
+          tm_ld32(tm + lanes + kColY + 64 * g + 32 * part, v);
+          tm_wait_ld();
+          if (part == 1) {  // all of Y has been read
+            tm_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&sh.y_free);
+          }
+          if (!store || 32 * part >= a.P) continue;
+          if (whole) {
+            if (part == 1) {
+              if (lane == 0) bulk_wait_read();
+              __syncwarp();
+            }
+#pragma unroll
+            for (int i = 0; i < 8; ++i)
+              *reinterpret_cast<uint4 *>(stage + lane * 128 + (i ^ (lane & 7)) * 16) =
+                  make_uint4(v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]);
+            fence_async_smem();
+            __syncwarp();
+            if (lane == 0) {
+              tma_store_3d(&map_y, stage, 32 * part, hg, t);
+              bulk_commit();
+            }
+          } else if (row < valid) {
+            float *yp = a.y + ((size_t)(t + lane) * a.H + hg) * a.P + 32 * part;
+#pragma unroll
+            for (int i = 0; i < 8; ++i)
+              if (32 * part + 4 * i < a.P)
+                *reinterpret_cast<uint4 *>(yp + 4 * i) = make_uint4(v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]);
+          }
+        }
+        if (lane == 0) {
+          bulk_wait_read();
+          mbar_arrive(&sh.x_free);
+        }
+        __syncwarp();
+      }
+    }
+  } else {
+    // state rows: weighted X, S
+    const int g = (warp >> 2) & 1, q = warp & 3, t128 = tid & 127, row = t128;
+    const uint32_t lanes = (uint32_t)(32 * q) << 16;
+    const int hs = q >> 1;  // head of this thread's state row
+    const float lAs = a.A[hs ? h1 : h0] * kLog2e;
+    const int sp = row & 63;  // its p
+    // decay of this thread's state row over chunk c
+    auto row_decay = [&](int c) {
+      const float *t = sh.tot[c & 1][hs];
+      return exp2_approx(lAs * ((t[0] + t[1]) + (t[2] + t[3])));
+    };
+    // 32 columns of the state row from 64 g + 32 part: pieces to U, the decayed row to tensor memory
+    auto put_state = [&](uint32_t (&v)[32], int part, float decay) {
+      if (!kState) {
+        unsigned char *hi = sh.U[g] + row * 128, *lo = sh.U[2 + g] + row * 128;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          uint4 h, l;
+          split_bf16x2(__uint_as_float(v[8 * i]), __uint_as_float(v[8 * i + 1]), h.x, l.x);
+          split_bf16x2(__uint_as_float(v[8 * i + 2]), __uint_as_float(v[8 * i + 3]), h.y, l.y);
+          split_bf16x2(__uint_as_float(v[8 * i + 4]), __uint_as_float(v[8 * i + 5]), h.z, l.z);
+          split_bf16x2(__uint_as_float(v[8 * i + 6]), __uint_as_float(v[8 * i + 7]), h.w, l.w);
+          const int off = ((4 * part + i) ^ (row & 7)) * 16;
+          *reinterpret_cast<uint4 *>(hi + off) = h;
+          *reinterpret_cast<uint4 *>(lo + off) = l;
+        }
+      }
+#pragma unroll
+      for (int i = 0; i < 32; ++i) v[i] = __float_as_uint(__uint_as_float(v[i]) * decay);
+      tm_st32(tm + lanes + kColS + 64 * g + 32 * part, v);
+    };
+
+    if (init) {
+      wait(sh.tab_full[0], 0);
+      const float decay = row_decay(0);
+      const float *src = init + (size_t)(hs ? h1 : h0) * head_elems + (size_t)sp * kCols + 64 * g;
+#pragma unroll
+      for (int part = 0; part < 2; ++part) {
+        uint32_t v[32];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          const float4 f = sp < a.P ? *reinterpret_cast<const float4 *>(src + 32 * part + 4 * i) : f4zero();
+          v[4 * i] = __float_as_uint(f.x);
+          v[4 * i + 1] = __float_as_uint(f.y);
+          v[4 * i + 2] = __float_as_uint(f.z);
+          v[4 * i + 3] = __float_as_uint(f.w);
+        }
+        put_state(v, part, decay);
+      }
+      tm_wait_st();
+    }
+    warp_arrive(sh.sp_ready, lane);
+
+    for (int c = 0; c < chunks; ++c) {
+      const int b = c & 1, valid = min(Q, ntok - c * Q);
+      wait(sh.tab_full[b], c >> 1);
+      wait(sh.full_X, c);
+      if (valid < Q) {  // rows of the chunk that belong to other prompts must not reach a sum, whatever they hold
+        wait(sh.full_B[b], c >> 1);
+        for (int i = t128 + valid * 8; i < Q * 8; i += 128) {
+          *reinterpret_cast<uint4 *>(sh.X[g] + 16 * i) = make_uint4(0, 0, 0, 0);
+          *reinterpret_cast<uint4 *>(sh.B[b][g] + 16 * i) = make_uint4(0, 0, 0, 0);
+        }
+      }
+      if (!kState) wait(sh.y1_done, c);  // the pieces of S have been used
+      // weighted X in two pieces, element by element in the layout of X
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        const int rr = 16 * i + (t128 >> 3), off = rr * 128 + (t128 & 7) * 16;
+        const uint4 x = *reinterpret_cast<const uint4 *>(sh.X[g] + off);
+        const float w = sh.w[b][g][rr];
+        uint4 h = make_uint4(0, 0, 0, 0), l = h;
+        if (rr < valid) {
+          split_bf16x2(__uint_as_float(x.x << 16) * w, __uint_as_float(x.x & 0xffff0000u) * w, h.x, l.x);
+          split_bf16x2(__uint_as_float(x.y << 16) * w, __uint_as_float(x.y & 0xffff0000u) * w, h.y, l.y);
+          split_bf16x2(__uint_as_float(x.z << 16) * w, __uint_as_float(x.z & 0xffff0000u) * w, h.z, l.z);
+          split_bf16x2(__uint_as_float(x.w << 16) * w, __uint_as_float(x.w & 0xffff0000u) * w, h.w, l.w);
+        }
+        *reinterpret_cast<uint4 *>(sh.U[g] + off) = h;
+        *reinterpret_cast<uint4 *>(sh.U[2 + g] + off) = l;
+      }
+      warp_arrive(sh.xs_ready, lane);
+      if (lane == 0) mbar_arrive(&sh.tab_free[b]);
+      // the state: next chunk's operand, or the piece's result
+      if (c + 1 < chunks) {
+        wait(sh.tab_full[1 - b], (c + 1) >> 1);
+        const float decay = row_decay(c + 1);
+        wait(sh.s_done[b], c >> 1);
+        tm_fence_after();
+#pragma unroll
+        for (int part = 0; part < 2; ++part) {
+          uint32_t v[32];
+          tm_ld32(tm + lanes + kColS + 64 * g + 32 * part, v);
+          tm_wait_ld();
+          put_state(v, part, decay);
+        }
+        tm_wait_st();
+        warp_arrive(sh.sp_ready, lane);
+      } else if (final) {
+        wait(sh.s_done[b], c >> 1);
+        tm_fence_after();
+        float *dst = final + (size_t)(hs ? h1 : h0) * head_elems + (size_t)sp * kCols + 64 * g;
+#pragma unroll
+        for (int part = 0; part < 2; ++part) {
+          uint32_t v[32];
+          tm_ld32(tm + lanes + kColS + 64 * g + 32 * part, v);
+          tm_wait_ld();
+          if (sp < a.P && (hs == 0 || two)) {
+#pragma unroll
+            for (int i = 0; i < 8; ++i)
+              *reinterpret_cast<uint4 *>(dst + 32 * part + 4 * i) =
+                  make_uint4(v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]);
+          }
+        }
+      }
+    }
+    tm_fence_before();
+  }
+  __syncthreads();
+  if (warp == kWarpLoad) {
+    tm_fence_after();
+    tm_free(tm, 512);
+  }
+}
+
+// States at the starts of the pieces of prompts that are cut: seg[s] <- state before piece s, from the pieces' own end
+// states and decays, one thread four elements.  Small against the pieces' tokens, and its loads mostly hit L2.
+__global__ void __launch_bounds__(256) join_kernel(TcArgs a, Prompts pr) {
+  Piece pc;
+  if (!find_piece(pr, pr.off[blockIdx.x] / a.piece_len + (int)blockIdx.x, a.piece_len, pc)) return;
+  const int len = pc.end - pc.begin, h = blockIdx.y;
+  if (len <= a.piece_len) return;
+  const int elem = 4 * (blockIdx.z * 256 + threadIdx.x);
+  const size_t head_elems = (size_t)a.P * kCols;
+  if (elem >= (int)head_elems) return;
+  const int pieces = (len + a.piece_len - 1) / a.piece_len;
+  const int number = pc.begin / a.piece_len + pc.seq;
+  float4 carry = f4zero();
+  if (pc.resume) carry = *reinterpret_cast<const float4 *>(a.S + ((size_t)pc.slot * a.H + h) * head_elems + elem);
+  for (int s = 0; s < pieces; ++s) {
+    const size_t at = (size_t)(number + s) * a.H + h;
+    float4 *p = reinterpret_cast<float4 *>(a.seg + at * head_elems + elem);
+    const float4 prev = carry;
+    if (s + 1 < pieces) {
+      const float4 v = *p;
+      const float d = expf(a.A[h] * a.seg_dt[at]);
+      carry = make_float4(fmaf(d, carry.x, v.x), fmaf(d, carry.y, v.y), fmaf(d, carry.z, v.z), fmaf(d, carry.w, v.w));
+    }
+    *p = prev;
+  }
+}
+
+using EncodeTiled = CUresult (*)(CUtensorMap *, CUtensorMapDataType, cuuint32_t, void *, const cuuint64_t *,
+                                 const cuuint64_t *, const cuuint32_t *, const cuuint32_t *, CUtensorMapInterleave,
+                                 CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+
+// cuTensorMapEncodeTiled from the driver that is loaded (the library links the runtime alone)
+cudaError_t encoder(EncodeTiled *fn) {
+  void *p = nullptr;
+  cudaDriverEntryPointQueryResult found;
+  const cudaError_t e = cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &p, 12000, cudaEnableDefault, &found);
+  if (e != cudaSuccess) return e;
+  if (found != cudaDriverEntryPointSuccess || !p) return cudaErrorNotSupported;
+  *fn = reinterpret_cast<EncodeTiled>(p);
+  return cudaSuccess;
+}
+
+// rows of 128 bytes with the 128-byte swizzle; what lies outside the tensor reads as zero and is not written
+cudaError_t make_map(EncodeTiled fn, CUtensorMap *map, CUtensorMapDataType type, const void *p, int dims,
+                     const cuuint64_t *size, const cuuint64_t *stride, const cuuint32_t *box) {
+  const cuuint32_t one[3] = {1, 1, 1};
+  const CUresult r = fn(map, type, dims, const_cast<void *>(p), size, stride, box, one,
+                        CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_128B,
+                        CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  return r == CUDA_SUCCESS ? cudaSuccess : cudaErrorInvalidValue;
+}
+
+}  // namespace
+
+size_t scan_tc_workspace(int H, int P, int pieces, size_t *seg_dt) {
+  const size_t states = align_up((size_t)pieces * H * P * kCols * 4, 256);
+  if (seg_dt) *seg_dt = states;
+  return states + align_up((size_t)pieces * H * 4, 256);
+}
+
+cudaError_t launch_scan_tc(const ScanArgs &s, const Prompts &pr, cudaStream_t stream) {
+  TcArgs a{};
+  a.H = s.H; a.P = s.P; a.G = s.G;
+  a.pairs = (s.H / s.G + 1) / 2;
+  a.piece_len = s.piece_len;
+  a.A = s.A; a.D = s.D; a.dt = static_cast<const __nv_bfloat16 *>(s.dt); a.S = s.S; a.y = s.y;
+  a.err = s.err; a.wait_cycles = s.wait_cycles;
+  const int pieces = prompt_pieces(pr.total, pr.nseq, s.piece_len);
+  const bool cut_up = s.piece_len <= pr.total;
+  if (cut_up) {
+    size_t off;
+    scan_tc_workspace(s.H, s.P, pieces, &off);
+    a.seg = static_cast<float *>(s.work);
+    a.seg_dt = reinterpret_cast<float *>(static_cast<unsigned char *>(s.work) + off);
+  }
+  EncodeTiled fn;
+  cudaError_t e = encoder(&fn);
+  if (e != cudaSuccess) return e;
+  CUtensorMap mx, mB, mC, my;
+  const CUtensorMapDataType bf16 = CU_TENSOR_MAP_DATA_TYPE_BFLOAT16;
+  const cuuint64_t sx[3] = {(cuuint64_t)s.P, (cuuint64_t)s.H, (cuuint64_t)pr.total};
+  const cuuint64_t tx[2] = {(cuuint64_t)s.P * 2, (cuuint64_t)s.H * s.P * 2};
+  const cuuint32_t bx[3] = {64, 1, Q};
+  e = make_map(fn, &mx, bf16, s.x, 3, sx, tx, bx);
+  const cuuint64_t sB[2] = {(cuuint64_t)s.G * kCols, (cuuint64_t)pr.total};
+  const cuuint64_t tB[1] = {(cuuint64_t)s.G * kCols * 2};
+  const cuuint32_t bB[2] = {64, Q};
+  if (e == cudaSuccess) e = make_map(fn, &mB, bf16, s.Bin, 2, sB, tB, bB);
+  if (e == cudaSuccess) e = make_map(fn, &mC, bf16, s.C, 2, sB, tB, bB);
+  const cuuint64_t ty[2] = {(cuuint64_t)s.P * 4, (cuuint64_t)s.H * s.P * 4};
+  const cuuint32_t by[3] = {32, 1, 32};
+  if (e == cudaSuccess) e = make_map(fn, &my, CU_TENSOR_MAP_DATA_TYPE_FLOAT32, s.y, 3, sx, ty, by);
+  if (e == cudaSuccess) e = cudaFuncSetAttribute(scan_tc_kernel<false>, cudaFuncAttributeMaxDynamicSharedMemorySize, kTcSmem);
+  if (e == cudaSuccess) e = cudaFuncSetAttribute(scan_tc_kernel<true>, cudaFuncAttributeMaxDynamicSharedMemorySize, kTcSmem);
+  if (e != cudaSuccess) return e;
+  const unsigned grid = (unsigned)pieces * a.G * a.pairs;
+  if (cut_up) {
+    scan_tc_kernel<true><<<grid, kTcThreads, kTcSmem, stream>>>(mx, mB, mC, my, a, pr);
+    join_kernel<<<dim3(pr.nseq, s.H, (s.P * kCols / 4 + 255) / 256), 256, 0, stream>>>(a, pr);
+  }
+  scan_tc_kernel<false><<<grid, kTcThreads, kTcSmem, stream>>>(mx, mB, mC, my, a, pr);
+  return cudaGetLastError();
+}
+
+}  // namespace rssm
