@@ -37,19 +37,19 @@ __device__ __forceinline__ bool prompt_bad(const Prompts &p, int i) {
 }
 
 // Collective over the block; false: nothing to do for this piece (bad prompts, refused slot, number without owner).
-__device__ __forceinline__ bool find_piece(const Prompts &p, int number, int len, Piece &out) {
-  __shared__ int found;
-  if (threadIdx.x == 0) found = -1;
+// found: a word of shared memory.
+__device__ __forceinline__ bool find_piece(const Prompts &p, int number, int len, Piece &out, int *found) {
+  if (threadIdx.x == 0) *found = -1;
   __syncthreads();
   bool bad = false;
   for (int i = threadIdx.x; i < p.nseq; i += blockDim.x) {
     const int o0 = p.off[i], o1 = p.off[i + 1];
     const int s = p.slots ? p.slots[i] : i;
     bad |= o0 < 0 || o1 < o0 || o1 > p.total || s < 0 || s >= p.nslots;
-    if (!bad && o0 / len + i <= number && number <= o1 / len + i) found = i;
+    if (!bad && o0 / len + i <= number && number <= o1 / len + i) *found = i;
   }
   bad = __syncthreads_or(bad);
-  const int i = found;
+  const int i = *found;
   if (bad || i < 0) return false;
   out.seq = i;
   out.begin = p.off[i];

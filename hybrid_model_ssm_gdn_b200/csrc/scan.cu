@@ -43,9 +43,10 @@ struct Stage {
 template <typename TI, int R>
 __global__ void __launch_bounds__(4 * R) scan_kernel(ScanArgs a, Prompts pr) {
   __shared__ __align__(16) Stage<R> st;
+  __shared__ int found;
   Piece pc;
   const int h = blockIdx.y, row0 = blockIdx.z * R;
-  if (!find_piece(pr, blockIdx.x, a.piece_len, pc)) return;
+  if (!find_piece(pr, blockIdx.x, a.piece_len, pc, &found)) return;
   const int len = pc.end - pc.begin;
   if (pc.first >= len && pc.index > 0) return;
   const int tid = threadIdx.x, q = tid & 3, row = row0 + (tid >> 2);

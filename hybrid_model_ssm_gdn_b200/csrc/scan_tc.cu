@@ -45,22 +45,25 @@ constexpr uint32_t kColS = 0, kColY = 128, kColG = 256, kColM = 384;
 constexpr int kWarpLoad = 16, kWarpState = 17, kWarpToken = 18, kWarpTable = 19;
 constexpr int kTcThreads = 640;
 
+// 227 KB to the last few bytes, and tiles start on 1024-byte boundaries: there is no static shared memory in this
+// file's kernels, so the block's dynamic part starts aligned (checked).
 struct TcShared {
-  unsigned char C[2][kTile];     // K-major, halves of n
-  unsigned char X[2][kTile];     // token rows, per head; afterwards Y on its way out, 4 KB a warp
-  unsigned char B[2][2][kTile];  // stages, halves of n
-  unsigned char U[4][kTile];     // S pieces: hi, lo x halves of n; weighted X pieces: hi, lo x heads
-  float cl[2][2][Q];             // sum of dt within the token's block of 32, included  (chunk parity, head, token)
-  float dt[2][2][Q];
-  float e[2][2][Q];              // exp(A (end of block - c_i)) dt_i
-  float w[2][2][Q];              // exp(A (c_Q - c_i)) dt_i
-  float tot[2][2][4];            // sums of the blocks of 32
-  uint64_t full_C, full_X, full_B[2], x_free, tab_full[2], tab_free[2];
+  unsigned char C[2][kTile];        // K-major, halves of n
+  unsigned char X[2][kTile];        // token rows, per head
+  unsigned char B[2][2][kTile];     // stages, halves of n
+  unsigned char U[4][kTile];        // S pieces: hi, lo x halves of n; weighted X pieces: hi, lo x heads
+  unsigned char Y[8][4096];         // Y on its way out: 32 tokens by 32 columns a warp
+  float cl[2][Q];                   // sum of dt within the token's block of 32, included  (head, token)
+  float e[2][Q];                    // exp(A (end of block - c_i)) dt_i
+  __nv_bfloat16 dt[2][Q];
+  float tot[2][2][4];               // sums of the blocks of 32 (chunk parity, head, block)
+  uint64_t full_C, full_X, full_B[2], tab_full, tab_free;
   uint64_t g_done, y1_done, y20_done, y2_done, y_free, s_done[2], sp_ready, m_ready[2], xs_ready, drained[2];
   uint32_t tmem;
-  int abort;
+  int abort, found;
 };
-constexpr int kTcSmem = (int)sizeof(TcShared) + 1024;
+constexpr int kTcSmem = (int)sizeof(TcShared);
+static_assert(kTcSmem <= 227 * 1024, "shared memory of a block");
 
 struct TcArgs {
   int H, P, G, pairs;       // pairs of heads in a group
@@ -104,12 +107,16 @@ __global__ void __launch_bounds__(kTcThreads, 1)
     scan_tc_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_constant__ CUtensorMap map_B,
                    const __grid_constant__ CUtensorMap map_C, const __grid_constant__ CUtensorMap map_y, TcArgs a,
                    Prompts pr) {
-  extern __shared__ unsigned char raw[];
-  TcShared &sh = *reinterpret_cast<TcShared *>((reinterpret_cast<uintptr_t>(raw) + 1023) & ~(uintptr_t)1023);
+  extern __shared__ __align__(1024) unsigned char raw[];
+  TcShared &sh = *reinterpret_cast<TcShared *>(raw);
+  if (smem_u32(raw) & 1023u) {
+    if (threadIdx.x == 0 && a.err) record_error(a.err, 0, RSSM_DEV_TIMEOUT);
+    return;
+  }
   const int units = a.G * a.pairs;
   const int number = blockIdx.x / units, unit = blockIdx.x % units;
   Piece pc;
-  if (!find_piece(pr, number, a.piece_len, pc)) return;
+  if (!find_piece(pr, number, a.piece_len, pc, &sh.found)) return;
   const int r = a.H / a.G, group = unit / a.pairs;
   const int h0 = group * r + 2 * (unit % a.pairs);
   const bool two = h0 + 1 < (group + 1) * r;  // without a second head the first is computed twice and stored once
@@ -138,13 +145,13 @@ __global__ void __launch_bounds__(kTcThreads, 1)
   const int t0 = pc.begin + pc.first;
 
   if (tid == 0) {
-    uint64_t *one[] = {&sh.full_C, &sh.full_X, &sh.full_B[0], &sh.full_B[1], &sh.tab_full[0], &sh.tab_full[1], &sh.g_done,
-                       &sh.y1_done, &sh.y20_done, &sh.y2_done, &sh.s_done[0], &sh.s_done[1], &sh.drained[0],
+    uint64_t *one[] = {&sh.full_C, &sh.full_X, &sh.full_B[0], &sh.full_B[1], &sh.tab_full, &sh.g_done, &sh.y1_done,
+                       &sh.y20_done, &sh.y2_done, &sh.s_done[0], &sh.s_done[1], &sh.drained[0],
                        &sh.drained[1]};
     for (uint64_t *b : one) mbar_init(b, 1);
-    uint64_t *team[] = {&sh.x_free, &sh.y_free, &sh.sp_ready, &sh.m_ready[0], &sh.m_ready[1], &sh.xs_ready};
+    uint64_t *team[] = {&sh.y_free, &sh.sp_ready, &sh.m_ready[0], &sh.m_ready[1], &sh.xs_ready};
     for (uint64_t *b : team) mbar_init(b, 8);
-    for (int i = 0; i < 2; ++i) mbar_init(&sh.tab_free[i], kState ? 8 : 16);
+    mbar_init(&sh.tab_free, kState ? 8 : 16);
     sh.abort = 0;
     fence_barrier_init();
   }
@@ -173,8 +180,8 @@ __global__ void __launch_bounds__(kTcThreads, 1)
           tma_load_2d(sh.C[1], &map_C, group * kCols + 64, t, &sh.full_C);
         }
         if (c > 0) {
-          if (kState) wait(sh.xs_ready, c - 1);
-          else wait(sh.x_free, c - 1);
+          wait(sh.xs_ready, c - 1);
+          if (!kState) wait(sh.y2_done, c - 1);
         }
         mbar_arrive_expect_tx(&sh.full_X, 2 * kTile);
         tma_load_3d(sh.X[0], &map_x, 0, h0, t, &sh.full_X);
@@ -290,12 +297,11 @@ __global__ void __launch_bounds__(kTcThreads, 1)
 #pragma unroll
         for (int i = 0; i < 4; ++i) d[h][i] = __bfloat162float(next[h][i]);
       if (c + 1 < chunks) fetch(c + 1);
-      if (c > 1) wait(sh.tab_free[b], (c - 2) >> 1);
+      float cl[2][4], e[2][4];
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
-        float after = 0.f;
 #pragma unroll
-        for (int i = 3; i >= 0; --i) {
+        for (int i = 0; i < 4; ++i) {
           float s = d[h][i];
 #pragma unroll
           for (int off = 1; off < 32; off <<= 1) {
@@ -303,18 +309,23 @@ __global__ void __launch_bounds__(kTcThreads, 1)
             if (lane >= off) s += t;
           }
           const float tot = __shfl_sync(0xffffffffu, s, 31);
-          const float e = exp2_approx(lA[h] * (tot - s)) * d[h][i];
-          sh.cl[b][h][32 * i + lane] = s;
-          sh.dt[b][h][32 * i + lane] = d[h][i];
-          sh.e[b][h][32 * i + lane] = e;
-          sh.w[b][h][32 * i + lane] = e * exp2_approx(lA[h] * after);
-          if (lane == 0) sh.tot[b][h][i] = tot;
-          after += tot;
+          cl[h][i] = s;
+          e[h][i] = exp2_approx(lA[h] * (tot - s)) * d[h][i];
+          if (lane == 0) sh.tot[b][h][i] = tot;  // chunk c - 2's readers have freed their tables
+          total_dt[h] += tot;
         }
-        total_dt[h] += after;
       }
+      if (c > 0) wait(sh.tab_free, c - 1);
+#pragma unroll
+      for (int h = 0; h < 2; ++h)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          sh.cl[h][32 * i + lane] = cl[h][i];
+          sh.e[h][32 * i + lane] = e[h][i];
+          sh.dt[h][32 * i + lane] = __float2bfloat16(d[h][i]);
+        }
       __syncwarp();
-      if (lane == 0) mbar_arrive(&sh.tab_full[b]);
+      if (lane == 0) mbar_arrive(&sh.tab_full);
     }
     if (kState && lane == 0) {
       a.seg_dt[(size_t)number * a.H + h0] = total_dt[0];
@@ -325,80 +336,80 @@ __global__ void __launch_bounds__(kTcThreads, 1)
     if (!kState) {
       const int g = warp >> 2, q = warp & 3, row = 32 * q + lane;
       const uint32_t lanes = (uint32_t)(32 * q) << 16;
-      const float lA[2] = {a.A[h0] * kLog2e, a.A[h1] * kLog2e}, D[2] = {a.D[h0], a.D[h1]};
       const int hg = g ? h1 : h0;
-      unsigned char *stage = sh.X[0] + warp * 4096;
+      const float lAg = a.A[hg] * kLog2e;
+      {  // blocks above the diagonal stay zero
+        const uint32_t zero[8] = {};
+        for (int i = q + 1; i < 4; ++i) {
+          tm_st8(tm + lanes + kColM + 16 * i + 8 * g, zero);
+          tm_st8(tm + lanes + kColM + 64 + 16 * i + 8 * g, zero);
+        }
+      }
       for (int c = 0; c < chunks; ++c) {
         const int b = c & 1, valid = min(Q, ntok - c * Q);
         const bool carried = c > 0 || init != nullptr;
-        wait(sh.tab_full[b], c >> 1);
+        wait(sh.tab_full, c);
         wait(sh.g_done, c);
         tm_fence_after();
-        float sum = sh.cl[b][g][row];  // c_j, for the head of this thread's Y columns
-#pragma unroll
-        for (int i = 0; i < 3; ++i) sum += i < q ? sh.tot[b][g][i] : 0.f;
-        const float rise = exp2_approx(lA[g] * sum);
-#pragma unroll
+#pragma unroll 1
         for (int h = 0; h < 2; ++h) {
           // both warps of a quarter take its rows, each 16 of a block's 32 columns
-          const float cl = sh.cl[b][h][row];
-          float since = cl;  // sum of dt from the end of block i to this token
+          const float lA = a.A[h ? h1 : h0] * kLog2e;
+          const float cl = sh.cl[h][row];
+          uint32_t G[16], hi[8], lo[8];
+          tm_ld16(tm + lanes + kColG + 32 * q + 16 * g, G);
+          if (h == 1) {  // M of the first head has been used
+            wait(sh.y20_done, c);
+            tm_fence_after();
+          }
+          tm_wait_ld();
+          {
+            const float D = a.D[h ? h1 : h0];
 #pragma unroll
-          for (int half = 1; half >= 0; --half) {
-            uint32_t G[2][16];
+            for (int k = 0; k < 16; k += 4) {
+              const float4 ci = *reinterpret_cast<const float4 *>(&sh.cl[h][32 * q + 16 * g + k]);
+              const float4 di = load4(&sh.dt[h][32 * q + 16 * g + k]);
+              const float cs[4] = {ci.x, ci.y, ci.z, ci.w}, ds[4] = {di.x, di.y, di.z, di.w};
+              float m[4];
 #pragma unroll
-            for (int i = 0; i < 2; ++i)
-              if (2 * half + i <= q) tm_ld16(tm + lanes + kColG + 32 * (2 * half + i) + 16 * g, G[i]);
-            tm_wait_ld();
-            if (h == 1 && half == 1) {  // M of the first head has been used
-              wait(sh.y20_done, c);
-              tm_fence_after();
-            }
-#pragma unroll
-            for (int ii = 1; ii >= 0; --ii) {
-              const int i = 2 * half + ii;
-              uint32_t hi[8], lo[8];
-              if (i > q) {
-#pragma unroll
-                for (int k = 0; k < 8; ++k) hi[k] = lo[k] = 0;
-              } else if (i == q) {
-#pragma unroll
-                for (int k = 0; k < 16; k += 4) {
-                  const float4 ci = *reinterpret_cast<const float4 *>(&sh.cl[b][h][32 * i + 16 * g + k]);
-                  const float4 di = *reinterpret_cast<const float4 *>(&sh.dt[b][h][32 * i + 16 * g + k]);
-                  const float cs[4] = {ci.x, ci.y, ci.z, ci.w}, ds[4] = {di.x, di.y, di.z, di.w};
-                  float m[4];
-#pragma unroll
-                  for (int j = 0; j < 4; ++j) {
-                    const int col = 16 * g + k + j;
-                    const float v = __uint_as_float(G[ii][k + j]) * (exp2_approx(lA[h] * (cl - cs[j])) * ds[j]);
-                    m[j] = col < lane ? v : col == lane ? v + D[h] : 0.f;
-                  }
-                  split_bf16x2(m[0], m[1], hi[k / 2], lo[k / 2]);
-                  split_bf16x2(m[2], m[3], hi[k / 2 + 1], lo[k / 2 + 1]);
-                }
-              } else {
-                const float f = exp2_approx(lA[h] * since);
-                since += sh.tot[b][h][i];
-#pragma unroll
-                for (int k = 0; k < 16; k += 4) {
-                  const float4 e = *reinterpret_cast<const float4 *>(&sh.e[b][h][32 * i + 16 * g + k]);
-                  split_bf16x2(__uint_as_float(G[ii][k]) * (f * e.x), __uint_as_float(G[ii][k + 1]) * (f * e.y),
-                               hi[k / 2], lo[k / 2]);
-                  split_bf16x2(__uint_as_float(G[ii][k + 2]) * (f * e.z), __uint_as_float(G[ii][k + 3]) * (f * e.w),
-                               hi[k / 2 + 1], lo[k / 2 + 1]);
-                }
+              for (int j = 0; j < 4; ++j) {
+                const int col = 16 * g + k + j;
+                const float v = __uint_as_float(G[k + j]) * (exp2_approx(lA * (cl - cs[j])) * ds[j]);
+                m[j] = col < lane ? v : col == lane ? v + D : 0.f;
               }
-              tm_st8(tm + lanes + kColM + 16 * i + 8 * g, hi);
-              tm_st8(tm + lanes + kColM + 64 + 16 * i + 8 * g, lo);
+              split_bf16x2(m[0], m[1], hi[k / 2], lo[k / 2]);
+              split_bf16x2(m[2], m[3], hi[k / 2 + 1], lo[k / 2 + 1]);
+            }
+          }
+          float since = cl;  // sum of dt from the end of block i to this token
+#pragma unroll 1
+          for (int i = q;; --i) {
+            if (i > 0) tm_ld16(tm + lanes + kColG + 32 * (i - 1) + 16 * g, G);
+            tm_st8(tm + lanes + kColM + 16 * i + 8 * g, hi);
+            tm_st8(tm + lanes + kColM + 64 + 16 * i + 8 * g, lo);
+            if (i == 0) break;
+            const float f = exp2_approx(lA * since);
+            since += sh.tot[b][h][i - 1];
+            tm_wait_ld();
+#pragma unroll
+            for (int k = 0; k < 16; k += 4) {
+              const float4 e = *reinterpret_cast<const float4 *>(&sh.e[h][32 * (i - 1) + 16 * g + k]);
+              split_bf16x2(__uint_as_float(G[k]) * (f * e.x), __uint_as_float(G[k + 1]) * (f * e.y), hi[k / 2],
+                           lo[k / 2]);
+              split_bf16x2(__uint_as_float(G[k + 2]) * (f * e.z), __uint_as_float(G[k + 3]) * (f * e.w),
+                           hi[k / 2 + 1], lo[k / 2 + 1]);
             }
           }
           if (h == 0) {
             // diag(exp(A c)) C S^T in place, before M X is added; this warp's half of the columns is head g
+            float sum = sh.cl[g][row];
+#pragma unroll
+            for (int i = 0; i < 3; ++i) sum += i < q ? sh.tot[b][g][i] : 0.f;
+            const float rise = exp2_approx(lAg * sum);
             wait(sh.y1_done, c);
             tm_fence_after();
             if (carried) {
-#pragma unroll
+#pragma unroll 1
               for (int part = 0; part < 2; ++part) {
                 uint32_t v[32];
                 tm_ld32(tm + lanes + kColY + 64 * g + 32 * part, v);
@@ -410,32 +421,27 @@ __global__ void __launch_bounds__(kTcThreads, 1)
             }
           }
           tm_wait_st();
-          warp_arrive(sh.m_ready[h], lane);
+          tm_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&sh.m_ready[h]);
         }
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&sh.tab_free[b]);
-        // Y: through this warp's 4 KB of the X buffer, which both heads' products and the weighing are done with
+        if (lane == 0) mbar_arrive(&sh.tab_free);
         wait(sh.y2_done, c);
-        wait(sh.xs_ready, c);
         tm_fence_after();
         const bool whole = 32 * q + 32 <= valid, store = g == 0 || two;
         const int t = t0 + c * Q + 32 * q;
-#pragma unroll
+        unsigned char *stage = sh.Y[warp];
+#pragma unroll 1
         for (int part = 0; part < 2; ++part) {
           uint32_t v[32];
           tm_ld32(tm + lanes + kColY + 64 * g + 32 * part, v);
+          if (lane == 0) bulk_wait_read();  // the stage's last store has left it
           tm_wait_ld();
-          if (part == 1) {  // all of Y has been read
-            tm_fence_before();
-            __syncwarp();
-            if (lane == 0) mbar_arrive(&sh.y_free);
-          }
+          tm_fence_before();
+          __syncwarp();
+          if (part == 1 && lane == 0) mbar_arrive(&sh.y_free);
           if (!store || 32 * part >= a.P) continue;
           if (whole) {
-            if (part == 1) {
-              if (lane == 0) bulk_wait_read();
-              __syncwarp();
-            }
 #pragma unroll
             for (int i = 0; i < 8; ++i)
               *reinterpret_cast<uint4 *>(stage + lane * 128 + (i ^ (lane & 7)) * 16) =
@@ -454,19 +460,15 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                 *reinterpret_cast<uint4 *>(yp + 4 * i) = make_uint4(v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]);
           }
         }
-        if (lane == 0) {
-          bulk_wait_read();
-          mbar_arrive(&sh.x_free);
-        }
-        __syncwarp();
       }
+      if (lane == 0) bulk_wait_read();
     }
   } else {
     // state rows: weighted X, S
     const int g = (warp >> 2) & 1, q = warp & 3, t128 = tid & 127, row = t128;
     const uint32_t lanes = (uint32_t)(32 * q) << 16;
     const int hs = q >> 1;  // head of this thread's state row
-    const float lAs = a.A[hs ? h1 : h0] * kLog2e;
+    const float lAs = a.A[hs ? h1 : h0] * kLog2e, lAg = a.A[g ? h1 : h0] * kLog2e;
     const int sp = row & 63;  // its p
     // decay of this thread's state row over chunk c
     auto row_decay = [&](int c) {
@@ -495,7 +497,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
     };
 
     if (init) {
-      wait(sh.tab_full[0], 0);
+      wait(sh.tab_full, 0);
       const float decay = row_decay(0);
       const float *src = init + (size_t)(hs ? h1 : h0) * head_elems + (size_t)sp * kCols + 64 * g;
 #pragma unroll
@@ -517,7 +519,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
 
     for (int c = 0; c < chunks; ++c) {
       const int b = c & 1, valid = min(Q, ntok - c * Q);
-      wait(sh.tab_full[b], c >> 1);
+      wait(sh.tab_full, c);
       wait(sh.full_X, c);
       if (valid < Q) {  // rows of the chunk that belong to other prompts must not reach a sum, whatever they hold
         wait(sh.full_B[b], c >> 1);
@@ -528,11 +530,19 @@ __global__ void __launch_bounds__(kTcThreads, 1)
       }
       if (!kState) wait(sh.y1_done, c);  // the pieces of S have been used
       // weighted X in two pieces, element by element in the layout of X
+      float after[4];  // decay from the end of a block of 32 to the chunk's end
+      {
+        const float *tt = sh.tot[b][g];
+        after[3] = 1.f;
+        after[2] = exp2_approx(lAg * tt[3]);
+        after[1] = exp2_approx(lAg * (tt[3] + tt[2]));
+        after[0] = exp2_approx(lAg * (tt[3] + tt[2] + tt[1]));
+      }
 #pragma unroll
       for (int i = 0; i < 8; ++i) {
         const int rr = 16 * i + (t128 >> 3), off = rr * 128 + (t128 & 7) * 16;
         const uint4 x = *reinterpret_cast<const uint4 *>(sh.X[g] + off);
-        const float w = sh.w[b][g][rr];
+        const float w = sh.e[g][rr] * after[i >> 1];
         uint4 h = make_uint4(0, 0, 0, 0), l = h;
         if (rr < valid) {
           split_bf16x2(__uint_as_float(x.x << 16) * w, __uint_as_float(x.x & 0xffff0000u) * w, h.x, l.x);
@@ -544,12 +554,12 @@ __global__ void __launch_bounds__(kTcThreads, 1)
         *reinterpret_cast<uint4 *>(sh.U[2 + g] + off) = l;
       }
       warp_arrive(sh.xs_ready, lane);
-      if (lane == 0) mbar_arrive(&sh.tab_free[b]);
+      if (lane == 0) mbar_arrive(&sh.tab_free);
       // the state: next chunk's operand, or the piece's result
       if (c + 1 < chunks) {
-        wait(sh.tab_full[1 - b], (c + 1) >> 1);
-        const float decay = row_decay(c + 1);
         wait(sh.s_done[b], c >> 1);
+        wait(sh.tab_full, c + 1);
+        const float decay = row_decay(c + 1);
         tm_fence_after();
 #pragma unroll
         for (int part = 0; part < 2; ++part) {
@@ -590,8 +600,9 @@ __global__ void __launch_bounds__(kTcThreads, 1)
 // States at the starts of the pieces of prompts that are cut: seg[s] <- state before piece s, from the pieces' own end
 // states and decays, one thread four elements.  Small against the pieces' tokens, and its loads mostly hit L2.
 __global__ void __launch_bounds__(256) join_kernel(TcArgs a, Prompts pr) {
+  __shared__ int found;
   Piece pc;
-  if (!find_piece(pr, pr.off[blockIdx.x] / a.piece_len + (int)blockIdx.x, a.piece_len, pc)) return;
+  if (!find_piece(pr, pr.off[blockIdx.x] / a.piece_len + (int)blockIdx.x, a.piece_len, pc, &found)) return;
   const int len = pc.end - pc.begin, h = blockIdx.y;
   if (len <= a.piece_len) return;
   const int elem = 4 * (blockIdx.z * 256 + threadIdx.x);

@@ -99,8 +99,9 @@ __device__ __forceinline__ TI *split_out(const ShortConvArgs &a, int c, int &row
 // reads and rewrites the sequence's history, each thread its own channels, so the rewrite is safe in place.
 template <typename TI, int K>
 __global__ void __launch_bounds__(kPromptThreads) prompt_kernel(ShortConvArgs a, Prompts pr) {
+  __shared__ int found;
   Piece pc;
-  if (!find_piece(pr, blockIdx.x, kTile, pc)) return;
+  if (!find_piece(pr, blockIdx.x, kTile, pc, &found)) return;
   const int c = (blockIdx.y * kPromptThreads + threadIdx.x) * 8;
   const int len = pc.end - pc.begin;
   if (c >= a.channels || (pc.first >= len && pc.index > 0)) return;
