@@ -6,32 +6,13 @@
 // registers as packed fp32 pairs, so a token costs a thread 48 packed multiply-adds and the columns' sum two shuffles.
 // Tokens are staged in shared memory 16 at a time.
 #include "kernels.h"
+#include "packed.cuh"
 
 namespace rssm {
 
 namespace {
 
 constexpr int kTok = 16;   // tokens staged at a time
-
-struct f2 {
-  unsigned long long v;
-};
-__device__ __forceinline__ f2 pack2(float a, float b) {
-  f2 r;
-  asm("mov.b64 %0, {%1, %2};" : "=l"(r.v) : "f"(a), "f"(b));
-  return r;
-}
-__device__ __forceinline__ void unpack2(f2 p, float &a, float &b) { asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(p.v)); }
-__device__ __forceinline__ f2 mul2(f2 a, f2 b) {
-  f2 r;
-  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r.v) : "l"(a.v), "l"(b.v));
-  return r;
-}
-__device__ __forceinline__ f2 fma2(f2 a, f2 b, f2 c) {
-  f2 r;
-  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r.v) : "l"(a.v), "l"(b.v), "l"(c.v));
-  return r;
-}
 
 template <int R>
 struct Stage {

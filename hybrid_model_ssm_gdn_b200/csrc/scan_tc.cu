@@ -33,6 +33,7 @@
 #include <cuda.h>
 
 #include "kernels.h"
+#include "packed.cuh"
 #include "tcgen05.cuh"
 
 namespace rssm {
@@ -57,8 +58,8 @@ struct TcShared {
   float e[2][Q];                    // exp(A (end of block - c_i)) dt_i
   __nv_bfloat16 dt[2][Q];
   float tot[2][2][4];               // sums of the blocks of 32 (chunk parity, head, block)
-  uint64_t full_C, full_X, full_B[2], tab_full, tab_free;
-  uint64_t g_done, y1_done, y20_done, y2_done, y_free, s_done[2], sp_ready, m_ready[2], xs_ready, drained[2];
+  uint64_t full_C, full_X, full_B[2], tab_full, tab_free, tot_full;
+  uint64_t g_done, y1_done, y20_done, y2_done, y_free, s_done[2], sp_ready[2], m_ready[2], xs_ready[2], drained[2];
   uint32_t tmem;
   int abort, found;
 };
@@ -77,6 +78,13 @@ struct TcArgs {
   int *err;                 // may be null
   long long wait_cycles;
 };
+
+__device__ __forceinline__ void scale2(uint32_t &a, uint32_t &b, f2 by) {
+  float x, y;
+  unpack2(mul2(pack2(a, b), by), x, y);
+  a = __float_as_uint(x);
+  b = __float_as_uint(y);
+}
 
 constexpr float kLog2e = 1.4426950408889634f;
 
@@ -145,11 +153,12 @@ __global__ void __launch_bounds__(kTcThreads, 1)
   const int t0 = pc.begin + pc.first;
 
   if (tid == 0) {
-    uint64_t *one[] = {&sh.full_C, &sh.full_X, &sh.full_B[0], &sh.full_B[1], &sh.tab_full, &sh.g_done, &sh.y1_done,
+    uint64_t *one[] = {&sh.full_C, &sh.full_X, &sh.full_B[0], &sh.full_B[1], &sh.tab_full, &sh.tot_full, &sh.g_done, &sh.y1_done,
                        &sh.y20_done, &sh.y2_done, &sh.s_done[0], &sh.s_done[1], &sh.drained[0],
                        &sh.drained[1]};
     for (uint64_t *b : one) mbar_init(b, 1);
-    uint64_t *team[] = {&sh.y_free, &sh.sp_ready, &sh.m_ready[0], &sh.m_ready[1], &sh.xs_ready};
+    uint64_t *team[] = {&sh.y_free, &sh.sp_ready[0], &sh.sp_ready[1], &sh.m_ready[0],
+                        &sh.m_ready[1], &sh.xs_ready[0], &sh.xs_ready[1]};
     for (uint64_t *b : team) mbar_init(b, 8);
     mbar_init(&sh.tab_free, kState ? 8 : 16);
     sh.abort = 0;
@@ -180,12 +189,16 @@ __global__ void __launch_bounds__(kTcThreads, 1)
           tma_load_2d(sh.C[1], &map_C, group * kCols + 64, t, &sh.full_C);
         }
         if (c > 0) {
-          wait(sh.xs_ready, c - 1);
+          wait(sh.xs_ready[1], c - 1);
           if (!kState) wait(sh.y2_done, c - 1);
         }
         mbar_arrive_expect_tx(&sh.full_X, 2 * kTile);
         tma_load_3d(sh.X[0], &map_x, 0, h0, t, &sh.full_X);
         tma_load_3d(sh.X[1], &map_x, 0, h1, t, &sh.full_X);
+        if (c + 1 < chunks) {  // X has one buffer: have the next chunk's in L2
+          tma_prefetch_3d(&map_x, 0, h0, t + Q);
+          tma_prefetch_3d(&map_x, 0, h1, t + Q);
+        }
       }
       if (*(volatile int *)&sh.abort) {  // otherwise every load has been consumed when the block ends
         if (!kState) mbar_wait(&sh.full_C, (chunks - 1) & 1, wait.ws);
@@ -198,39 +211,49 @@ __global__ void __launch_bounds__(kTcThreads, 1)
   } else if (warp == kWarpState) {
     if (lane == 0) {
       constexpr uint32_t shape_y = mma_shape(128, 128, false, false), shape_s = mma_shape(128, 128, true, true);
-      const uint64_t dC = tile_desc(sh.C[0], 16), dSp = tile_desc(sh.U[0], 16);        // K-major
-      const uint64_t dXs = tile_desc(sh.U[0], kTile), dB = tile_desc(sh.B[0][0], kTile);  // MN-major, two tiles
+      const uint32_t dC = tile_desc(sh.C[0], 16), dSp = tile_desc(sh.U[0], 16);        // K-major
+      const uint32_t dXs = tile_desc(sh.U[0], kTile), dB = tile_desc(sh.B[0][0], kTile);  // MN-major, two tiles
       constexpr int step = kTile >> 4;
       for (int c = 0; c < chunks; ++c) {
         const int s = c & 1;
         const bool carried = c > 0 || init != nullptr;
         if (!kState) {
           wait(sh.full_C, c);
-          wait(sh.sp_ready, c);
           if (c > 0) wait(sh.y_free, c - 1);
-          tm_fence_after();
-          if (carried) {
+#pragma unroll 1
+          for (int part = 0; part < 2; ++part) {  // columns n of S as their pieces arrive: 32 of each half
+            wait(sh.sp_ready[part], c);
+            tm_fence_after();
+            if (carried) {
+#pragma unroll 1
+              for (int p = 0; p < 2; ++p)
 #pragma unroll
-            for (int p = 0; p < 2; ++p)
-#pragma unroll
-              for (int k = 0; k < 8; ++k)
-                mma_ss(tm + kColY, dC + (k >> 2) * step + 2 * (k & 3), dSp + (2 * p + (k >> 2)) * step + 2 * (k & 3),
-                       shape_y, p > 0 || k > 0);
+                for (int k = 0; k < 4; ++k) {
+                  const int at = (k >> 1) * step + 2 * (k & 1) + 4 * part;
+                  mma_ss(tm + kColY, dC + at, dSp + 2 * p * step + at, shape_y, part > 0 || p > 0 || k > 0);
+                }
+            }
           }
           mma_commit(&sh.y1_done);
         } else {
-          wait(sh.sp_ready, c);
+          wait(sh.sp_ready[0], c);
+          wait(sh.sp_ready[1], c);
         }
         wait(sh.full_B[s], c >> 1);
-        wait(sh.xs_ready, c);
-        tm_fence_after();
-        if (c + 1 < chunks || final) {
+#pragma unroll 1
+        for (int part = 0; part < 2; ++part) {  // tokens as their weighted X arrives
+          wait(sh.xs_ready[part], c);
+          tm_fence_after();
+          if (c + 1 < chunks || final) {
+#pragma unroll 1
+            for (int p = 0; p < 2; ++p)
 #pragma unroll
-          for (int p = 0; p < 2; ++p)
-#pragma unroll
-            for (int k = 0; k < 8; ++k)  // 16 token rows are 2048 bytes
-              mma_ss(tm + kColS, dXs + 2 * p * step + 128 * k, dB + 2 * s * step + 128 * k, shape_s,
-                     carried || p > 0 || k > 0);
+              for (int k = 0; k < 4; ++k) {  // 16 token rows are 2048 bytes
+                const int at = 128 * (4 * part + k);
+                mma_ss(tm + kColS, dXs + 2 * p * step + at, dB + 2 * s * step + at, shape_s,
+                       carried || part > 0 || p > 0 || k > 0);
+              }
+          }
         }
         mma_commit(&sh.s_done[s]);
       }
@@ -241,7 +264,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
   } else if (warp == kWarpToken) {
     if (!kState && lane == 0) {
       constexpr uint32_t shape_g = mma_shape(128, 128, false, false), shape_y = mma_shape(128, 64, false, true);
-      const uint64_t dC = tile_desc(sh.C[0], 16), dB = tile_desc(sh.B[0][0], 16), dX = tile_desc(sh.X[0], 16);
+      const uint32_t dC = tile_desc(sh.C[0], 16), dB = tile_desc(sh.B[0][0], 16), dX = tile_desc(sh.X[0], 16);
       constexpr int step = kTile >> 4;
       for (int c = 0; c < chunks; ++c) {
         const int s = c & 1;
@@ -255,12 +278,12 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                  k > 0);
         mma_commit(&sh.g_done);
         wait(sh.full_X, c);
-        if (ntok - c * Q < Q) wait(sh.xs_ready, c);  // the rows behind the prompt's end have been cleared
-#pragma unroll
+        if (ntok - c * Q < Q) wait(sh.xs_ready[0], c);  // the rows behind the prompt's end have been cleared
+#pragma unroll 1
         for (int h = 0; h < 2; ++h) {
           wait(sh.m_ready[h], c);
           tm_fence_after();
-#pragma unroll
+#pragma unroll 1
           for (int p = 0; p < 2; ++p)
 #pragma unroll
             for (int k = 0; k < 8; ++k)
@@ -297,6 +320,8 @@ __global__ void __launch_bounds__(kTcThreads, 1)
 #pragma unroll
         for (int i = 0; i < 4; ++i) d[h][i] = __bfloat162float(next[h][i]);
       if (c + 1 < chunks) fetch(c + 1);
+      // the state warps have read the sums of chunk c - 1 (and so waited for them), all warps those of chunk c - 2
+      if (c > 0) wait(sh.sp_ready[1], c - 1);
       float cl[2][4], e[2][4];
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
@@ -311,10 +336,12 @@ __global__ void __launch_bounds__(kTcThreads, 1)
           const float tot = __shfl_sync(0xffffffffu, s, 31);
           cl[h][i] = s;
           e[h][i] = exp2_approx(lA[h] * (tot - s)) * d[h][i];
-          if (lane == 0) sh.tot[b][h][i] = tot;  // chunk c - 2's readers have freed their tables
+          if (lane == 0) sh.tot[b][h][i] = tot;
           total_dt[h] += tot;
         }
       }
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&sh.tot_full);
       if (c > 0) wait(sh.tab_free, c - 1);
 #pragma unroll
       for (int h = 0; h < 2; ++h)
@@ -337,7 +364,9 @@ __global__ void __launch_bounds__(kTcThreads, 1)
       const int g = warp >> 2, q = warp & 3, row = 32 * q + lane;
       const uint32_t lanes = (uint32_t)(32 * q) << 16;
       const int hg = g ? h1 : h0;
-      const float lAg = a.A[hg] * kLog2e;
+      const float lA0 = a.A[h0] * kLog2e, lA1 = a.A[h1] * kLog2e, D0 = a.D[h0], D1 = a.D[h1];
+      const bool store = g == 0 || two;
+      unsigned char *stage = sh.Y[warp];
       {  // blocks above the diagonal stay zero
         const uint32_t zero[8] = {};
         for (int i = q + 1; i < 4; ++i) {
@@ -345,77 +374,100 @@ __global__ void __launch_bounds__(kTcThreads, 1)
           tm_st8(tm + lanes + kColM + 64 + 16 * i + 8 * g, zero);
         }
       }
+      // 32 columns of Y of chunk c to global memory: whole quarters through the stage, others row by row
+      auto put_y = [&](const uint32_t (&v)[32], int part, int c) {
+        if (!store || 32 * part >= a.P) return;
+        if (lane == 0) bulk_wait_read();  // the stage's last store has left it
+        __syncwarp();
+        const int t = t0 + c * Q + 32 * q, valid = ntok - c * Q;
+        if (32 * q + 32 <= valid) {
+#pragma unroll
+          for (int i = 0; i < 8; ++i)
+            *reinterpret_cast<uint4 *>(stage + lane * 128 + (i ^ (lane & 7)) * 16) =
+                make_uint4(v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]);
+          fence_async_smem();
+          __syncwarp();
+          if (lane == 0) {
+            tma_store_3d(&map_y, stage, 32 * part, hg, t);
+            bulk_commit();
+          }
+        } else if (row < valid) {
+          float *yp = a.y + ((size_t)(t + lane) * a.H + hg) * a.P + 32 * part;
+#pragma unroll
+          for (int i = 0; i < 8; ++i)
+            if (32 * part + 4 * i < a.P)
+              *reinterpret_cast<uint4 *>(yp + 4 * i) = make_uint4(v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]);
+        }
+      };
       for (int c = 0; c < chunks; ++c) {
-        const int b = c & 1, valid = min(Q, ntok - c * Q);
-        const bool carried = c > 0 || init != nullptr;
+        const int b = c & 1;
         wait(sh.tab_full, c);
         wait(sh.g_done, c);
         tm_fence_after();
 #pragma unroll 1
         for (int h = 0; h < 2; ++h) {
           // both warps of a quarter take its rows, each 16 of a block's 32 columns
-          const float lA = a.A[h ? h1 : h0] * kLog2e;
+          const float lA = h ? lA1 : lA0;
           const float cl = sh.cl[h][row];
-          uint32_t G[16], hi[8], lo[8];
-          tm_ld16(tm + lanes + kColG + 32 * q + 16 * g, G);
           if (h == 1) {  // M of the first head has been used
             wait(sh.y20_done, c);
             tm_fence_after();
           }
-          tm_wait_ld();
-          {
-            const float D = a.D[h ? h1 : h0];
-#pragma unroll
-            for (int k = 0; k < 16; k += 4) {
-              const float4 ci = *reinterpret_cast<const float4 *>(&sh.cl[h][32 * q + 16 * g + k]);
-              const float4 di = load4(&sh.dt[h][32 * q + 16 * g + k]);
-              const float cs[4] = {ci.x, ci.y, ci.z, ci.w}, ds[4] = {di.x, di.y, di.z, di.w};
-              float m[4];
-#pragma unroll
-              for (int j = 0; j < 4; ++j) {
-                const int col = 16 * g + k + j;
-                const float v = __uint_as_float(G[k + j]) * (exp2_approx(lA * (cl - cs[j])) * ds[j]);
-                m[j] = col < lane ? v : col == lane ? v + D : 0.f;
-              }
-              split_bf16x2(m[0], m[1], hi[k / 2], lo[k / 2]);
-              split_bf16x2(m[2], m[3], hi[k / 2 + 1], lo[k / 2 + 1]);
-            }
-          }
           float since = cl;  // sum of dt from the end of block i to this token
 #pragma unroll 1
-          for (int i = q;; --i) {
-            if (i > 0) tm_ld16(tm + lanes + kColG + 32 * (i - 1) + 16 * g, G);
+          for (int i = q; i >= 0; --i) {
+            uint32_t G[16], hi[8], lo[8];
+            tm_ld16(tm + lanes + kColG + 32 * i + 16 * g, G);
+            tm_wait_ld();
+            if (i < q) {
+              const float f = exp2_approx(lA * since);
+              const f2 ff = pack2(f, f);
+              since += sh.tot[b][h][i];
+#pragma unroll
+              for (int k = 0; k < 16; k += 4) {
+                const float4 e = *reinterpret_cast<const float4 *>(&sh.e[h][32 * i + 16 * g + k]);
+                cut2(mul2(pack2(G[k], G[k + 1]), mul2(ff, pack2(e.x, e.y))), hi[k / 2], lo[k / 2]);
+                cut2(mul2(pack2(G[k + 2], G[k + 3]), mul2(ff, pack2(e.z, e.w))), hi[k / 2 + 1], lo[k / 2 + 1]);
+              }
+            } else {
+              // the block on the diagonal: its columns' tokens are this warp's rows
+              const float D = h ? D1 : D0;
+#pragma unroll
+              for (int k = 0; k < 16; k += 4) {
+                const float4 ci = *reinterpret_cast<const float4 *>(&sh.cl[h][32 * i + 16 * g + k]);
+                const float4 di = load4(&sh.dt[h][32 * i + 16 * g + k]);
+                const float cs[4] = {ci.x, ci.y, ci.z, ci.w}, ds[4] = {di.x, di.y, di.z, di.w};
+                float m[4];
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                  const int col = 16 * g + k + j;
+                  const float v = __uint_as_float(G[k + j]) * (exp2_approx(lA * (cl - cs[j])) * ds[j]);
+                  m[j] = col < lane ? v : col == lane ? v + D : 0.f;
+                }
+                cut2(pack2(m[0], m[1]), hi[k / 2], lo[k / 2]);
+                cut2(pack2(m[2], m[3]), hi[k / 2 + 1], lo[k / 2 + 1]);
+              }
+            }
             tm_st8(tm + lanes + kColM + 16 * i + 8 * g, hi);
             tm_st8(tm + lanes + kColM + 64 + 16 * i + 8 * g, lo);
-            if (i == 0) break;
-            const float f = exp2_approx(lA * since);
-            since += sh.tot[b][h][i - 1];
-            tm_wait_ld();
-#pragma unroll
-            for (int k = 0; k < 16; k += 4) {
-              const float4 e = *reinterpret_cast<const float4 *>(&sh.e[h][32 * (i - 1) + 16 * g + k]);
-              split_bf16x2(__uint_as_float(G[k]) * (f * e.x), __uint_as_float(G[k + 1]) * (f * e.y), hi[k / 2],
-                           lo[k / 2]);
-              split_bf16x2(__uint_as_float(G[k + 2]) * (f * e.z), __uint_as_float(G[k + 3]) * (f * e.w),
-                           hi[k / 2 + 1], lo[k / 2 + 1]);
-            }
           }
           if (h == 0) {
             // diag(exp(A c)) C S^T in place, before M X is added; this warp's half of the columns is head g
             float sum = sh.cl[g][row];
 #pragma unroll
             for (int i = 0; i < 3; ++i) sum += i < q ? sh.tot[b][g][i] : 0.f;
-            const float rise = exp2_approx(lAg * sum);
+            const float rise = exp2_approx((g ? lA1 : lA0) * sum);
+            const f2 rise2 = pack2(rise, rise);
             wait(sh.y1_done, c);
             tm_fence_after();
-            if (carried) {
+            if (c > 0 || init != nullptr) {
 #pragma unroll 1
               for (int part = 0; part < 2; ++part) {
                 uint32_t v[32];
                 tm_ld32(tm + lanes + kColY + 64 * g + 32 * part, v);
                 tm_wait_ld();
 #pragma unroll
-                for (int i = 0; i < 32; ++i) v[i] = __float_as_uint(__uint_as_float(v[i]) * rise);
+                for (int i = 0; i < 32; i += 2) scale2(v[i], v[i + 1], rise2);
                 tm_st32(tm + lanes + kColY + 64 * g + 32 * part, v);
               }
             }
@@ -428,38 +480,15 @@ __global__ void __launch_bounds__(kTcThreads, 1)
         if (lane == 0) mbar_arrive(&sh.tab_free);
         wait(sh.y2_done, c);
         tm_fence_after();
-        const bool whole = 32 * q + 32 <= valid, store = g == 0 || two;
-        const int t = t0 + c * Q + 32 * q;
-        unsigned char *stage = sh.Y[warp];
-#pragma unroll 1
-        for (int part = 0; part < 2; ++part) {
-          uint32_t v[32];
-          tm_ld32(tm + lanes + kColY + 64 * g + 32 * part, v);
-          if (lane == 0) bulk_wait_read();  // the stage's last store has left it
-          tm_wait_ld();
-          tm_fence_before();
-          __syncwarp();
-          if (part == 1 && lane == 0) mbar_arrive(&sh.y_free);
-          if (!store || 32 * part >= a.P) continue;
-          if (whole) {
-#pragma unroll
-            for (int i = 0; i < 8; ++i)
-              *reinterpret_cast<uint4 *>(stage + lane * 128 + (i ^ (lane & 7)) * 16) =
-                  make_uint4(v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]);
-            fence_async_smem();
-            __syncwarp();
-            if (lane == 0) {
-              tma_store_3d(&map_y, stage, 32 * part, hg, t);
-              bulk_commit();
-            }
-          } else if (row < valid) {
-            float *yp = a.y + ((size_t)(t + lane) * a.H + hg) * a.P + 32 * part;
-#pragma unroll
-            for (int i = 0; i < 8; ++i)
-              if (32 * part + 4 * i < a.P)
-                *reinterpret_cast<uint4 *>(yp + 4 * i) = make_uint4(v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]);
-          }
-        }
+        uint32_t Y[2][32];
+        tm_ld32(tm + lanes + kColY + 64 * g, Y[0]);
+        tm_ld32(tm + lanes + kColY + 64 * g + 32, Y[1]);
+        tm_wait_ld();
+        tm_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&sh.y_free);
+        put_y(Y[0], 0, c);
+        put_y(Y[1], 1, c);
       }
       if (lane == 0) bulk_wait_read();
     }
@@ -482,22 +511,22 @@ __global__ void __launch_bounds__(kTcThreads, 1)
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
           uint4 h, l;
-          split_bf16x2(__uint_as_float(v[8 * i]), __uint_as_float(v[8 * i + 1]), h.x, l.x);
-          split_bf16x2(__uint_as_float(v[8 * i + 2]), __uint_as_float(v[8 * i + 3]), h.y, l.y);
-          split_bf16x2(__uint_as_float(v[8 * i + 4]), __uint_as_float(v[8 * i + 5]), h.z, l.z);
-          split_bf16x2(__uint_as_float(v[8 * i + 6]), __uint_as_float(v[8 * i + 7]), h.w, l.w);
+          cut2(pack2(v[8 * i], v[8 * i + 1]), h.x, l.x);
+          cut2(pack2(v[8 * i + 2], v[8 * i + 3]), h.y, l.y);
+          cut2(pack2(v[8 * i + 4], v[8 * i + 5]), h.z, l.z);
+          cut2(pack2(v[8 * i + 6], v[8 * i + 7]), h.w, l.w);
           const int off = ((4 * part + i) ^ (row & 7)) * 16;
           *reinterpret_cast<uint4 *>(hi + off) = h;
           *reinterpret_cast<uint4 *>(lo + off) = l;
         }
       }
 #pragma unroll
-      for (int i = 0; i < 32; ++i) v[i] = __float_as_uint(__uint_as_float(v[i]) * decay);
+      for (int i = 0; i < 32; i += 2) scale2(v[i], v[i + 1], pack2(decay, decay));
       tm_st32(tm + lanes + kColS + 64 * g + 32 * part, v);
     };
 
     if (init) {
-      wait(sh.tab_full, 0);
+      wait(sh.tot_full, 0);
       const float decay = row_decay(0);
       const float *src = init + (size_t)(hs ? h1 : h0) * head_elems + (size_t)sp * kCols + 64 * g;
 #pragma unroll
@@ -515,7 +544,8 @@ __global__ void __launch_bounds__(kTcThreads, 1)
       }
       tm_wait_st();
     }
-    warp_arrive(sh.sp_ready, lane);
+    warp_arrive(sh.sp_ready[0], lane);
+    if (lane == 0) mbar_arrive(&sh.sp_ready[1]);
 
     for (int c = 0; c < chunks; ++c) {
       const int b = c & 1, valid = min(Q, ntok - c * Q);
@@ -538,27 +568,32 @@ __global__ void __launch_bounds__(kTcThreads, 1)
         after[1] = exp2_approx(lAg * (tt[3] + tt[2]));
         after[0] = exp2_approx(lAg * (tt[3] + tt[2] + tt[1]));
       }
+#pragma unroll 1
+      for (int part = 0; part < 2; ++part) {
+      const float w0 = part ? after[2] : after[0], w1 = part ? after[3] : after[1];
 #pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        const int rr = 16 * i + (t128 >> 3), off = rr * 128 + (t128 & 7) * 16;
+      for (int i = 0; i < 4; ++i) {
+        const int rr = 64 * part + 16 * i + (t128 >> 3), off = rr * 128 + (t128 & 7) * 16;
         const uint4 x = *reinterpret_cast<const uint4 *>(sh.X[g] + off);
-        const float w = sh.e[g][rr] * after[i >> 1];
+        const float w = sh.e[g][rr] * (i < 2 ? w0 : w1);
         uint4 h = make_uint4(0, 0, 0, 0), l = h;
         if (rr < valid) {
-          split_bf16x2(__uint_as_float(x.x << 16) * w, __uint_as_float(x.x & 0xffff0000u) * w, h.x, l.x);
-          split_bf16x2(__uint_as_float(x.y << 16) * w, __uint_as_float(x.y & 0xffff0000u) * w, h.y, l.y);
-          split_bf16x2(__uint_as_float(x.z << 16) * w, __uint_as_float(x.z & 0xffff0000u) * w, h.z, l.z);
-          split_bf16x2(__uint_as_float(x.w << 16) * w, __uint_as_float(x.w & 0xffff0000u) * w, h.w, l.w);
+          const f2 ww = pack2(w, w);
+          cut2(mul2(pack2(x.x << 16, x.x & 0xffff0000u), ww), h.x, l.x);
+          cut2(mul2(pack2(x.y << 16, x.y & 0xffff0000u), ww), h.y, l.y);
+          cut2(mul2(pack2(x.z << 16, x.z & 0xffff0000u), ww), h.z, l.z);
+          cut2(mul2(pack2(x.w << 16, x.w & 0xffff0000u), ww), h.w, l.w);
         }
         *reinterpret_cast<uint4 *>(sh.U[g] + off) = h;
         *reinterpret_cast<uint4 *>(sh.U[2 + g] + off) = l;
       }
-      warp_arrive(sh.xs_ready, lane);
+      warp_arrive(sh.xs_ready[part], lane);
+      }
       if (lane == 0) mbar_arrive(&sh.tab_free);
       // the state: next chunk's operand, or the piece's result
       if (c + 1 < chunks) {
         wait(sh.s_done[b], c >> 1);
-        wait(sh.tab_full, c + 1);
+        wait(sh.tot_full, c + 1);
         const float decay = row_decay(c + 1);
         tm_fence_after();
 #pragma unroll
@@ -567,9 +602,9 @@ __global__ void __launch_bounds__(kTcThreads, 1)
           tm_ld32(tm + lanes + kColS + 64 * g + 32 * part, v);
           tm_wait_ld();
           put_state(v, part, decay);
+          tm_wait_st();
+          warp_arrive(sh.sp_ready[part], lane);
         }
-        tm_wait_st();
-        warp_arrive(sh.sp_ready, lane);
       } else if (final) {
         wait(sh.s_done[b], c >> 1);
         tm_fence_after();

@@ -64,31 +64,34 @@ __device__ __forceinline__ void tm_st8(uint32_t taddr, const uint32_t (&r)[8]) {
                "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7])
                : "memory");
 }
-// Descriptor of an operand tile with the 128-byte swizzle.  stride: bytes between groups of 8 rows (1024 here);
-// lead: MN-major only, bytes between tiles of 64 indices of M or N.
-__device__ __forceinline__ uint64_t tile_desc(const void *p, uint32_t lead, uint32_t stride = 1024) {
-  return (uint64_t)((smem_u32(p) & 0x3ffffu) >> 4) | ((uint64_t)(lead >> 4) << 16) | ((uint64_t)(stride >> 4) << 32) |
-         (1ull << 46) | (2ull << 61);
+// Descriptor of an operand tile with the 128-byte swizzle, in two words: the low one holds the address in units of 16
+// bytes (so that moving along a tile is a 32-bit add) and `lead`: MN-major only, bytes between tiles of 64 indices of M
+// or N; the high one is the same for all (1024 bytes between groups of 8 rows).
+__device__ __forceinline__ uint32_t tile_desc(const void *p, uint32_t lead) {
+  return ((smem_u32(p) & 0x3ffffu) >> 4) | ((lead >> 4) << 16);
 }
+constexpr uint32_t kTileDescHigh = (1024u >> 4) | (1u << 14) | (2u << 29);
 // instruction descriptor: bf16 operands, fp32 accumulators, M x N
 __host__ __device__ constexpr uint32_t mma_shape(int M, int N, bool a_mn_major, bool b_mn_major) {
   return (1u << 4) | (1u << 7) | (1u << 10) | ((a_mn_major ? 1u : 0u) << 15) | ((b_mn_major ? 1u : 0u) << 16) |
          ((uint32_t)(N >> 3) << 17) | ((uint32_t)(M >> 4) << 24);
 }
 // d[M x N] (+)= a b over K = 16; one thread issues
-__device__ __forceinline__ void mma_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t shape, bool accumulate) {
+__device__ __forceinline__ void mma_ss(uint32_t d, uint32_t a, uint32_t b, uint32_t shape, bool accumulate) {
   asm volatile(
-      "{\n\t.reg .pred p;\n\tsetp.ne.u32 p, %4, 0;\n\t"
-      "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
-      "l"(a), "l"(b), "r"(shape), "r"((uint32_t)accumulate)
+      "{\n\t.reg .pred p;\n\t.reg .b64 da, db;\n\tsetp.ne.u32 p, %4, 0;\n\t"
+      "mov.b64 da, {%1, %5};\n\tmov.b64 db, {%2, %5};\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], da, db, %3, p;\n\t}" ::"r"(d),
+      "r"(a), "r"(b), "r"(shape), "r"((uint32_t)accumulate), "r"(kTileDescHigh)
       : "memory");
 }
 // the same with a in tensor memory: lane = row, 8 columns of bf16 pairs
-__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t shape, bool accumulate) {
+__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint32_t b, uint32_t shape, bool accumulate) {
   asm volatile(
-      "{\n\t.reg .pred p;\n\tsetp.ne.u32 p, %4, 0;\n\t"
-      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d),
-      "r"(a), "l"(b), "r"(shape), "r"((uint32_t)accumulate)
+      "{\n\t.reg .pred p;\n\t.reg .b64 db;\n\tsetp.ne.u32 p, %4, 0;\n\t"
+      "mov.b64 db, {%2, %5};\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], db, %3, p;\n\t}" ::"r"(d),
+      "r"(a), "r"(b), "r"(shape), "r"((uint32_t)accumulate), "r"(kTileDescHigh)
       : "memory");
 }
 
@@ -106,6 +109,12 @@ __device__ __forceinline__ void tma_load_3d(void *dst, const void *map, int x, i
           smem_u32(dst)),
       "l"(map), "r"(x), "r"(y), "r"(z), "r"(smem_u32(bar))
       : "memory");
+}
+
+// bring a box into L2 ahead of its load
+__device__ __forceinline__ void tma_prefetch_3d(const void *map, int x, int y, int z) {
+  asm volatile("cp.async.bulk.prefetch.tensor.3d.L2.global.tile [%0, {%1, %2, %3}];" ::"l"(map), "r"(x), "r"(y), "r"(z)
+               : "memory");
 }
 
 // tiled TMA store, tracked by the issuing thread's bulk async-group; coordinates are not negative
