@@ -430,12 +430,21 @@ static Prompts device_prompts(const rssm_prompts *pr, int nslots, const int4 *me
   return p;
 }
 
-// Tokens of a piece of a prompt (total + 1: prompts are not cut).
-static int scan_piece_len(const rssm_config &c, int total, int nseq) {
-  const char *pl = getenv("RSSM_PIECE_LEN");
-  if (pl && c.in_dtype == RSSM_BF16 && total > 0) return atoi(pl) < total + 1 ? atoi(pl) : total + 1;
-  (void)nseq;
-  return total + 1;
+// Tokens of a piece of a prompt on the tensor cores (total + 1: prompts are not cut).  A block carries two heads along
+// one piece, so prompts x pairs of heads below the number of SMs leave some idle, however long the prompts are.  Cut
+// into pieces a prompt costs a first pass over all but its last one for their end states (some 0.45 of the full pass a
+// chunk) and a start per piece (about two chunks), so it pays where one prompt's chain is what takes the time: one prompt
+// of 8191 tokens and 64 pairs on 148 SMs takes 0.38 ms whole, 0.28 ms in two pieces of 4096 and 0.34 ms in eight of 1024.
+static int scan_piece_len(const rssm_config &c, int total, int nseq, int num_sms) {
+  const int whole = total + 1;
+  if (c.in_dtype != RSSM_BF16) return whole;
+  const int pairs = c.ngroups * ((c.nheads / c.ngroups + 1) / 2);
+  const int pieces = num_sms / pairs - (nseq - 1);  // of the longest prompt, if the others are one each
+  if (pieces < 2) return whole;
+  const long long len = ((long long)total / pieces + kScanChunk) / kScanChunk * kScanChunk;
+  const long long piece = len < 2 * kScanChunk ? 2 * kScanChunk : len;
+  const long long chain = nseq == 1 ? total : (long long)total * 5 / (4 * nseq);  // of the longest, if they are uneven
+  return piece * 3 / 2 + 4 * kScanChunk < chain ? (int)piece : whole;
 }
 
 static rssm_status run_scan(const rssm_config &c, const Prompts &p, const rssm_tokens *tok, float *S, float *y,
@@ -443,7 +452,7 @@ static rssm_status run_scan(const rssm_config &c, const Prompts &p, const rssm_t
   if (c.nheads > 65535) return RSSM_ERR_SHAPE;  // one grid row a head
   ScanArgs a{};
   a.H = c.nheads; a.P = c.headdim; a.G = c.ngroups;
-  a.piece_len = scan_piece_len(c, p.total, p.nseq);
+  a.piece_len = scan_piece_len(c, p.total, p.nseq, num_sms);
   a.x = tok->x; a.Bin = tok->B; a.C = tok->C; a.dt = tok->dt; a.A = c.A; a.D = c.D; a.S = S; a.y = y;
   a.work = work; a.err = err; a.wait_cycles = wait_cycles;
   if (a.piece_len <= p.total) {
@@ -468,7 +477,10 @@ rssm_status rssm_mamba2_scan_workspace(const rssm_config *cfg, int total, int ns
   if (s != RSSM_OK) return s;
   if (!bytes) return RSSM_ERR_ARG;
   if (total < 0 || nseq < 1 || nseq > cfg->batch) return RSSM_ERR_SHAPE;
-  const int len = scan_piece_len(*cfg, total, nseq);
+  int sms = 0;
+  s = sm_count(&sms);
+  if (s != RSSM_OK) return s;
+  const int len = scan_piece_len(*cfg, total, nseq, sms);
   *bytes = len <= total ? scan_tc_workspace(cfg->nheads, cfg->headdim, prompt_pieces(total, nseq, len), nullptr) : 0;
   return RSSM_OK;
 }

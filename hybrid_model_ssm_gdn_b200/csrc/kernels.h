@@ -103,6 +103,7 @@ cudaError_t launch_conv(ConvArgs a, int esz, cudaStream_t stream);
 cudaError_t launch_snap_commit(int *cur, const int *accepted, int Bt, int nslots, cudaStream_t stream);
 
 // Mamba-2 scan over packed prompts
+constexpr int kScanChunk = 128;      // tokens of a chunk on the tensor cores
 struct ScanArgs {
   int H, P, G;
   int piece_len;                    // tokens of a piece (total + 1: every prompt is one piece)

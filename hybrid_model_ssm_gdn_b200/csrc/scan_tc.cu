@@ -40,11 +40,12 @@ namespace rssm {
 
 namespace {
 
-constexpr int Q = 128;
+constexpr int Q = kScanChunk;
 constexpr int kTile = Q * 128;  // bytes of a tile: 128 rows of 64 bf16
 constexpr uint32_t kColS = 0, kColY = 128, kColG = 256, kColM = 384;
 constexpr int kWarpLoad = 16, kWarpState = 17, kWarpToken = 18, kWarpTable = 19;
 constexpr int kTcThreads = 640;
+constexpr int kByLength = 64;
 
 // 227 KB to the last few bytes, and tiles start on 1024-byte boundaries: there is no static shared memory in this
 // file's kernels, so the block's dynamic part starts aligned (checked).
@@ -69,6 +70,7 @@ static_assert(kTcSmem <= 227 * 1024, "shared memory of a block");
 struct TcArgs {
   int H, P, G, pairs;       // pairs of heads in a group
   int piece_len;
+  int by_length;            // hand out the prompts by length (at most kByLength of them, not cut)
   const float *A, *D;
   const __nv_bfloat16 *dt;  // [total][H]
   float *S;                 // [nslots][H][P][128]
@@ -122,7 +124,22 @@ __global__ void __launch_bounds__(kTcThreads, 1)
     return;
   }
   const int units = a.G * a.pairs;
-  const int number = blockIdx.x / units, unit = blockIdx.x % units;
+  int number = blockIdx.x / units;
+  const int unit = blockIdx.x % units;
+  if (a.by_length) {  // prompts that are not cut, the longest first: the last blocks to finish are short ones
+    int *lens = reinterpret_cast<int *>(sh.cl);
+    if (threadIdx.x < pr.nseq) lens[threadIdx.x] = pr.off[threadIdx.x + 1] - pr.off[threadIdx.x];
+    __syncthreads();
+    if (threadIdx.x < pr.nseq) {
+      const int mine = lens[threadIdx.x];
+      int rank = 0;
+      for (int j = 0; j < pr.nseq; ++j) rank += lens[j] > mine || (lens[j] == mine && j < (int)threadIdx.x);
+      if (rank == number) sh.found = threadIdx.x;
+    }
+    __syncthreads();
+    number = sh.found;
+    __syncthreads();
+  }
   Piece pc;
   if (!find_piece(pr, number, a.piece_len, pc, &sh.found)) return;
   const int r = a.H / a.G, group = unit / a.pairs;
@@ -188,9 +205,17 @@ __global__ void __launch_bounds__(kTcThreads, 1)
           tma_load_2d(sh.C[0], &map_C, group * kCols, t, &sh.full_C);
           tma_load_2d(sh.C[1], &map_C, group * kCols + 64, t, &sh.full_C);
         }
+        if (kState) {  // C's buffer is the second one for X; the wait above has freed either
+          uint64_t &full = c & 1 ? sh.full_C : sh.full_X;
+          unsigned char *x = c & 1 ? sh.C[0] : sh.X[0];
+          mbar_arrive_expect_tx(&full, 2 * kTile);
+          tma_load_3d(x, &map_x, 0, h0, t, &full);
+          tma_load_3d(x + kTile, &map_x, 0, h1, t, &full);
+          continue;
+        }
         if (c > 0) {
           wait(sh.xs_ready[1], c - 1);
-          if (!kState) wait(sh.y2_done, c - 1);
+          wait(sh.y2_done, c - 1);
         }
         mbar_arrive_expect_tx(&sh.full_X, 2 * kTile);
         tma_load_3d(sh.X[0], &map_x, 0, h0, t, &sh.full_X);
@@ -201,8 +226,13 @@ __global__ void __launch_bounds__(kTcThreads, 1)
         }
       }
       if (*(volatile int *)&sh.abort) {  // otherwise every load has been consumed when the block ends
-        if (!kState) mbar_wait(&sh.full_C, (chunks - 1) & 1, wait.ws);
-        mbar_wait(&sh.full_X, (chunks - 1) & 1, wait.ws);
+        if (kState) {
+          mbar_wait(chunks & 1 ? &sh.full_X : &sh.full_C, ((chunks - 1) >> 1) & 1, wait.ws);
+          if (chunks > 1) mbar_wait(chunks & 1 ? &sh.full_C : &sh.full_X, ((chunks - 2) >> 1) & 1, wait.ws);
+        } else {
+          mbar_wait(&sh.full_C, (chunks - 1) & 1, wait.ws);
+          mbar_wait(&sh.full_X, (chunks - 1) & 1, wait.ws);
+        }
         mbar_wait(&sh.full_B[(chunks - 1) & 1], ((chunks - 1) >> 1) & 1, wait.ws);
         if (chunks > 1) mbar_wait(&sh.full_B[chunks & 1], ((chunks - 2) >> 1) & 1, wait.ws);
       }
@@ -550,11 +580,12 @@ __global__ void __launch_bounds__(kTcThreads, 1)
     for (int c = 0; c < chunks; ++c) {
       const int b = c & 1, valid = min(Q, ntok - c * Q);
       wait(sh.tab_full, c);
-      wait(sh.full_X, c);
+      wait(kState && b ? sh.full_C : sh.full_X, kState ? c >> 1 : c);
+      unsigned char *const X = (kState && b ? sh.C[0] : sh.X[0]) + g * kTile;
       if (valid < Q) {  // rows of the chunk that belong to other prompts must not reach a sum, whatever they hold
         wait(sh.full_B[b], c >> 1);
         for (int i = t128 + valid * 8; i < Q * 8; i += 128) {
-          *reinterpret_cast<uint4 *>(sh.X[g] + 16 * i) = make_uint4(0, 0, 0, 0);
+          *reinterpret_cast<uint4 *>(X + 16 * i) = make_uint4(0, 0, 0, 0);
           *reinterpret_cast<uint4 *>(sh.B[b][g] + 16 * i) = make_uint4(0, 0, 0, 0);
         }
       }
@@ -574,7 +605,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
         const int rr = 64 * part + 16 * i + (t128 >> 3), off = rr * 128 + (t128 & 7) * 16;
-        const uint4 x = *reinterpret_cast<const uint4 *>(sh.X[g] + off);
+        const uint4 x = *reinterpret_cast<const uint4 *>(X + off);
         const float w = sh.e[g][rr] * (i < 2 ? w0 : w1);
         uint4 h = make_uint4(0, 0, 0, 0), l = h;
         if (rr < valid) {
@@ -708,6 +739,8 @@ cudaError_t launch_scan_tc(const ScanArgs &s, const Prompts &pr, cudaStream_t st
     a.seg = static_cast<float *>(s.work);
     a.seg_dt = reinterpret_cast<float *>(static_cast<unsigned char *>(s.work) + off);
   }
+  // finding the order costs each block some 500 cycles, worth it where a prompt has a few chunks
+  a.by_length = !cut_up && pr.nseq > 1 && pr.nseq <= kByLength && pr.total / pr.nseq >= 4 * Q;
   EncodeTiled fn;
   cudaError_t e = encoder(&fn);
   if (e != cudaSuccess) return e;

@@ -6,11 +6,13 @@ a product of exact inputs and one fp32 weight that reaches the tensor cores in t
 sums are fp32 (2^-24 a level): together below 2^-16.
 """
 
+import ctypes as C
+
 import numpy as np
 import pytest
 import torch
 
-from hybrid_model_ssm_gdn_b200 import ReplaySSM, mamba2_scan
+from hybrid_model_ssm_gdn_b200 import ReplaySSM, abi, make_config, mamba2_scan
 from oracle.prompts import mamba2_scan as oracle_scan
 from synth import round_to_dtype
 
@@ -241,3 +243,30 @@ def test_prefill_in_a_graph_and_on_a_stream(cuda_ok):
         graph.replay()
         torch.cuda.synchronize()
         compare(d2, [0, 90, 200], None, None, g["S"].cpu().numpy(), y.cpu().numpy())
+
+
+@pytest.mark.parametrize("H,P,G,lens,resume", [(2, 64, 1, [1900], [1]), (3, 40, 1, [2049], [0]), (4, 64, 4, [1, 2600, 0], [0, 1, 1]),
+                                               (2, 64, 2, [1792, 1535], [1, 0])])
+def test_long_prompts_in_pieces(cuda_ok, H, P, G, lens, resume):
+    """Few heads and long prompts: the prompts are cut into pieces that run side by side."""
+    offsets = np.concatenate([[0], np.cumsum(lens)]).tolist()
+    d = make(H + len(lens), torch.bfloat16, offsets[-1], H, P, G, len(lens) + 1, decay=0.05)
+    cfg = make_config("mamba2", len(lens) + 1, H, P, 128, G, 1, 0, torch.bfloat16, A=torch.empty(H), D=torch.empty(H))
+    n = C.c_size_t()
+    assert abi.load().rssm_mamba2_scan_workspace(C.byref(cfg), offsets[-1], len(lens), C.byref(n)) == 0 and n.value > 0
+    check(d, torch.bfloat16, offsets, slots=list(range(len(lens), 0, -1)), resume=resume)
+
+
+def test_workspace_of_the_caller(cuda_ok):
+    """Scratch from the caller, with whatever it holds; too small or misplaced scratch is refused before any launch."""
+    d = make(20, torch.bfloat16, 2000, 2, 64, 1, 1, decay=0.05)
+    g = on_gpu(d, torch.bfloat16)
+    args = (g["S"], g["x"], g["B"], g["C"], g["dt"], g["A"], g["D"], idx([0, 2000]))
+    y = torch.full((2000, 2, 64), 7.0, device="cuda")
+    work = torch.full((8 << 20,), 255, dtype=torch.uint8, device="cuda")
+    mamba2_scan(*args, y=y, workspace=work)
+    compare(d, [0, 2000], None, None, g["S"].cpu().numpy(), y.cpu().numpy())
+    with pytest.raises(ValueError, match="workspace"):
+        mamba2_scan(*args, y=y, workspace=work[:1024])
+    with pytest.raises(RuntimeError, match="RSSM_ERR_ARG"):
+        mamba2_scan(*args, y=y, workspace=work[16:])
