@@ -162,8 +162,8 @@ class ReplaySSM:
         H, P, G = self.nheads, self.rows, self.ngroups
         total, pr, tok, y = _scan_args(x, B, C_, dt, offsets, slots, resume, y, H, P, G, self.in_dtype)
         work = _scan_work(self.lib, self.cfg, total, pr.nseq, workspace)
-        abi.check(self.lib.rssm_mamba2_prefill(self.handle, C.byref(pr), C.byref(tok), _ptr(y), _ptr(work),
-                                               0 if work is None else work.numel(), _stream()), "rssm_mamba2_prefill")
+        abi.check(self.lib.rssm_mamba2_prefill(self.handle, C.byref(pr), C.byref(tok), _addr(y), _addr(work),
+                                               0 if work is None else work.numel(), _raw_stream()), "rssm_mamba2_prefill")
         return y
 
     def flush(self, mask=None):
@@ -236,13 +236,22 @@ def _arr(t, dtype, name, shape, optional=False):
     """``t`` after checking that it is a contiguous tensor of ``dtype`` and exactly ``shape`` on the current device."""
     if t is None and optional:
         return None
-    if tuple(t.shape) != tuple(shape):
+    if t.shape != shape:
         raise ValueError(f"{name}: expected shape {tuple(shape)}, got {tuple(t.shape)}")
-    if t.dtype != dtype or not t.is_cuda or not t.is_contiguous():
+    if t.dtype is not dtype or not t.is_cuda or not t.is_contiguous():
         raise ValueError(f"{name}: expected a contiguous CUDA tensor of {dtype}, got {t.dtype} on {t.device}")
-    if t.get_device() != torch.cuda.current_device():
+    if t.get_device() != torch._C._cuda_getDevice():
         raise ValueError(f"{name}: on {t.device}, but the current device is cuda:{torch.cuda.current_device()}")
     return t
+
+
+def _raw_stream():
+    """The current stream's handle, without building a stream object (these calls are short)."""
+    return torch._C._cuda_getCurrentRawStream(torch._C._cuda_getDevice())
+
+
+def _addr(t):
+    return None if t is None else t.data_ptr()
 
 
 def _prompts(total, offsets, slots, resume):
@@ -307,9 +316,28 @@ def mamba2_scan(S, x, B, C_, dt, A, D, offsets, slots=None, resume=None, y=None,
                      in_dtype=_DT[dtype], A=A.data_ptr(), D=D.data_ptr())
     lib = abi.load()
     work = _scan_work(lib, cfg, total, pr.nseq, workspace)
-    abi.check(lib.rssm_mamba2_scan(C.byref(cfg), C.byref(pr), C.byref(tok), _ptr(S), _ptr(y), _ptr(work),
-                                   0 if work is None else work.numel(), _stream()), "rssm_mamba2_scan")
+    abi.check(lib.rssm_mamba2_scan(C.byref(cfg), C.byref(pr), C.byref(tok), _addr(S), _addr(y), _addr(work),
+                                   0 if work is None else work.numel(), _raw_stream()), "rssm_mamba2_scan")
     return y
+
+
+_I3, _P3 = C.c_int * 3, C.c_void_p * 3
+
+
+def _row_stride(x, lead, ch):
+    """Elements from one row of x [*lead][ch] to the next: rows may lie apart (a slice of a wider projection) but
+    evenly, with contiguous channels."""
+    if x.is_contiguous():
+        return ch
+    stride = x.stride(-2) if x.shape[-2] > 1 else ch
+    if len(lead) == 2 and lead[0] > 1:
+        if lead[1] == 1:
+            stride = x.stride(0)
+        elif x.stride(0) != lead[1] * stride:
+            raise ValueError("x: the rows of all sequences must lie evenly apart")
+    if x.stride(-1) != 1 or stride < ch or stride % 8:
+        raise ValueError(f"x: expected contiguous channels and a row stride that is a multiple of 8, got {x.stride()}")
+    return stride
 
 
 def _shortconv(hist, cur, x, weight, bias, splits, activation, out, lead):
@@ -318,39 +346,31 @@ def _shortconv(hist, cur, x, weight, bias, splits, activation, out, lead):
         raise ValueError("hist and weight: expected 3 and 2 dimensions")
     dtype = _in_dtype(x, "x")
     batch, ring, ch = hist.shape
+    width = weight.shape[1]
     _arr(hist, dtype, "hist", (batch, ring, ch))
     _arr(cur, torch.int32, "cur", (batch,))
-    _arr(weight, dtype, "weight", (ch, weight.shape[1]))
+    _arr(weight, dtype, "weight", (ch, width))
     _arr(bias, dtype, "bias", (ch,), optional=True)
     splits = (ch,) if splits is None else tuple(splits)
-    if len(splits) > 3 or sum(splits) != ch or min(splits) < 1:
+    n = len(splits)
+    if n > 3 or sum(splits) != ch or min(splits) < 1:
         raise ValueError(f"splits: expected up to three positive sizes that sum to {ch}, got {splits}")
-    if activation not in (None, "silu"):
+    if activation is not None and activation != "silu":
         raise ValueError(f"activation: expected None or 'silu', got {activation!r}")
-    if tuple(x.shape) != (*lead, ch) or not x.is_cuda or x.get_device() != torch.cuda.current_device():
+    if x.shape != (*lead, ch) or not x.is_cuda or x.get_device() != hist.get_device():
         raise ValueError(f"x: expected shape {(*lead, ch)} on the current CUDA device, got {tuple(x.shape)} on {x.device}")
-    # rows may lie apart (a slice of a wider projection) but evenly, with contiguous channels
-    stride = x.stride(-2) if x.numel() and x.shape[-2] > 1 else ch
-    if x.numel():
-        if len(lead) == 2 and lead[0] > 1:
-            if lead[1] == 1:
-                stride = x.stride(0)
-            elif x.stride(0) != lead[1] * stride:
-                raise ValueError("x: the rows of all sequences must lie evenly apart")
-        if x.stride(-1) != 1 or stride < ch or stride % 8:
-            raise ValueError(f"x: expected contiguous channels and a row stride that is a multiple of 8, got {x.stride()}")
+    stride = _row_stride(x, lead, ch)
     if out is None:
-        out = tuple(torch.empty(*lead, n, dtype=dtype, device=x.device) for n in splits)
-    if len(out) != len(splits):
-        raise ValueError(f"out: expected {len(splits)} tensors, got {len(out)}")
-    for i, (o, n) in enumerate(zip(out, splits)):
-        _arr(o, dtype, f"out[{i}]", (*lead, n))
-    pad = (0,) * (3 - len(splits))
-    cfg = abi.ShortConvConfig(batch, ch, weight.shape[1], ring, _DT[dtype], activation == "silu",
-                              (C.c_int * 3)(*splits, *pad), weight.data_ptr(),
-                              None if bias is None else bias.data_ptr())
-    ptrs = (C.c_void_p * 3)(*[o.data_ptr() for o in out], *[None for _ in pad])
-    return cfg, ptrs, out, stride
+        device = x.device
+        out = tuple([torch.empty((*lead, c), dtype=dtype, device=device) for c in splits])
+    else:
+        if len(out) != n:
+            raise ValueError(f"out: expected {n} tensors, got {len(out)}")
+        for o, c in zip(out, splits):
+            _arr(o, dtype, "out", (*lead, c))
+    cfg = abi.ShortConvConfig(batch, ch, width, ring, _DT[dtype], activation is not None, _I3(*splits),
+                              weight.data_ptr(), None if bias is None else bias.data_ptr())
+    return cfg, _P3(*[o.data_ptr() for o in out]), out, stride
 
 
 def shortconv_prefill(hist, cur, x, weight, bias, offsets, slots=None, resume=None, splits=None, activation="silu",
@@ -359,16 +379,16 @@ def shortconv_prefill(hist, cur, x, weight, bias, offsets, slots=None, resume=No
     [batch][ring][channels] and cur int32 [batch] are the sequences' histories -> one tensor [total][n] a split."""
     cfg, ptrs, out, stride = _shortconv(hist, cur, x, weight, bias, splits, activation, out, (x.shape[0],))
     pr = _prompts(x.shape[0], offsets, slots, resume)
-    abi.check(abi.load().rssm_shortconv_prefill(C.byref(cfg), C.byref(pr), _ptr(hist), _ptr(cur), _ptr(x), stride,
-                                                C.byref(ptrs), _stream()), "rssm_shortconv_prefill")
+    abi.check(abi.load().rssm_shortconv_prefill(C.byref(cfg), C.byref(pr), _addr(hist), _addr(cur), _addr(x), stride,
+                                                C.byref(ptrs), _raw_stream()), "rssm_shortconv_prefill")
     return out
 
 
 def shortconv_step(hist, cur, x, weight, bias=None, splits=None, activation="silu", out=None):
     """One token a sequence: x [batch][channels] -> one tensor [batch][n] a split; cur advances."""
     cfg, ptrs, out, stride = _shortconv(hist, cur, x, weight, bias, splits, activation, out, (hist.shape[0],))
-    abi.check(abi.load().rssm_shortconv_step(C.byref(cfg), _ptr(hist), _ptr(cur), _ptr(x), stride, C.byref(ptrs),
-                                             _stream()), "rssm_shortconv_step")
+    abi.check(abi.load().rssm_shortconv_step(C.byref(cfg), _addr(hist), _addr(cur), _addr(x), stride, C.byref(ptrs),
+                                             _raw_stream()), "rssm_shortconv_step")
     return out
 
 
@@ -379,8 +399,8 @@ def shortconv_verify(hist, cur, x, weight, bias=None, splits=None, activation="s
         raise ValueError(f"x: expected 3 dimensions, got {x.dim()}")
     T = x.shape[1]
     cfg, ptrs, out, stride = _shortconv(hist, cur, x, weight, bias, splits, activation, out, (hist.shape[0], T))
-    abi.check(abi.load().rssm_shortconv_verify(C.byref(cfg), T, _ptr(hist), _ptr(cur), _ptr(x), stride, C.byref(ptrs),
-                                               _stream()), "rssm_shortconv_verify")
+    abi.check(abi.load().rssm_shortconv_verify(C.byref(cfg), T, _addr(hist), _addr(cur), _addr(x), stride, C.byref(ptrs),
+                                               _raw_stream()), "rssm_shortconv_verify")
     return out
 
 
@@ -390,14 +410,14 @@ def shortconv_commit(hist, cur, accepted, width):
     _arr(cur, torch.int32, "cur", (batch,))
     _arr(accepted, torch.int32, "accepted", (batch,))
     cfg = abi.ShortConvConfig(batch=batch, width=width, ring=ring)
-    abi.check(abi.load().rssm_shortconv_commit(C.byref(cfg), _ptr(cur), _ptr(accepted), _stream()),
+    abi.check(abi.load().rssm_shortconv_commit(C.byref(cfg), _addr(cur), _addr(accepted), _raw_stream()),
               "rssm_shortconv_commit")
 
 
 def _rows(t, name, batch, rows, vocab):
     """The row stride of [batch][rows][vocab] probabilities whose rows lie evenly apart."""
-    if tuple(t.shape) != (batch, rows, vocab) or t.dtype != torch.float32 or not t.is_cuda or \
-            t.get_device() != torch.cuda.current_device():
+    if t.shape != (batch, rows, vocab) or t.dtype is not torch.float32 or not t.is_cuda or \
+            t.get_device() != torch._C._cuda_getDevice():
         raise ValueError(f"{name}: expected fp32 of shape {(batch, rows, vocab)} on the current CUDA device, got {t.dtype} "
                          f"of {tuple(t.shape)} on {t.device}")
     if t.numel() == 0:
@@ -422,9 +442,9 @@ def accept_drafts(target, tokens, u, draft=None, count=None):
     _arr(count, torch.int32, "count", (batch,), optional=True)
     got = torch.empty(3, batch, dtype=torch.int32, device=target.device)
     accepted, committed, nxt = got[0], got[1], got[2]
-    abi.check(abi.load().rssm_accept_drafts(batch, T, vocab, _ptr(target), ld_t, _ptr(draft), ld_d, _ptr(tokens),
-                                            _ptr(count), _ptr(u), _ptr(accepted), _ptr(committed), _ptr(nxt),
-                                            _stream()), "rssm_accept_drafts")
+    abi.check(abi.load().rssm_accept_drafts(batch, T, vocab, _addr(target), ld_t, _addr(draft), ld_d, _addr(tokens),
+                                            _addr(count), _addr(u), _addr(accepted), _addr(committed), _addr(nxt),
+                                            _raw_stream()), "rssm_accept_drafts")
     return accepted, committed, nxt
 
 

@@ -566,7 +566,10 @@ rssm_status rssm_shortconv_prefill(const rssm_shortconv_config *cfg, const rssm_
   ShortConvArgs a{};
   s = shortconv_args(cfg, hist, cur, in, in_stride, out, pr->total > 0, a);
   if (s != RSSM_OK) return s;
-  const cudaError_t e = launch_shortconv_prompt(a, device_prompts(pr, cfg->batch, nullptr), shortconv_esize(cfg),
+  int sms = 0;
+  s = sm_count(&sms);
+  if (s != RSSM_OK) return s;
+  const cudaError_t e = launch_shortconv_prompt(a, device_prompts(pr, cfg->batch, nullptr), shortconv_esize(cfg), sms,
                                                 reinterpret_cast<cudaStream_t>(stream));
   return e == cudaSuccess ? RSSM_OK : cuda_fail(e);
 }
@@ -579,7 +582,11 @@ rssm_status rssm_shortconv_step(const rssm_shortconv_config *cfg, void *hist, in
   s = shortconv_args(cfg, hist, cur, in, in_stride, out, true, a);
   if (s != RSSM_OK) return s;
   a.cur_out = cur;
-  const cudaError_t e = launch_shortconv_tokens(a, 1, 1, shortconv_esize(cfg), reinterpret_cast<cudaStream_t>(stream));
+  int sms = 0;
+  s = sm_count(&sms);
+  if (s != RSSM_OK) return s;
+  const cudaError_t e = launch_shortconv_tokens(a, 1, 1, shortconv_esize(cfg), sms,
+                                                reinterpret_cast<cudaStream_t>(stream));
   return e == cudaSuccess ? RSSM_OK : cuda_fail(e);
 }
 
@@ -591,7 +598,11 @@ rssm_status rssm_shortconv_verify(const rssm_shortconv_config *cfg, int T, void 
   ShortConvArgs a{};
   s = shortconv_args(cfg, hist, cur, in, in_stride, out, true, a);
   if (s != RSSM_OK) return s;
-  const cudaError_t e = launch_shortconv_tokens(a, T, 0, shortconv_esize(cfg), reinterpret_cast<cudaStream_t>(stream));
+  int sms = 0;
+  s = sm_count(&sms);
+  if (s != RSSM_OK) return s;
+  const cudaError_t e = launch_shortconv_tokens(a, T, 0, shortconv_esize(cfg), sms,
+                                                reinterpret_cast<cudaStream_t>(stream));
   return e == cudaSuccess ? RSSM_OK : cuda_fail(e);
 }
 

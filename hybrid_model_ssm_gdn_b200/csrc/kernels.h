@@ -134,8 +134,10 @@ struct ShortConvArgs {
   long long in_stride;
   void *out[3];
 };
-cudaError_t launch_shortconv_prompt(const ShortConvArgs &a, const Prompts &pr, int esz, cudaStream_t stream);
-cudaError_t launch_shortconv_tokens(const ShortConvArgs &a, int T, int advance, int esz, cudaStream_t stream);
+cudaError_t launch_shortconv_prompt(const ShortConvArgs &a, const Prompts &pr, int esz, int num_sms,
+                                    cudaStream_t stream);
+cudaError_t launch_shortconv_tokens(const ShortConvArgs &a, int T, int advance, int esz, int num_sms,
+                                    cudaStream_t stream);
 cudaError_t launch_shortconv_commit(int *cur, const int *accepted, int batch, int ring, int most, cudaStream_t stream);
 
 // draft verification

@@ -4,15 +4,50 @@
 //
 // A few multiply-adds per value against one read and one write of it: the bound is memory.  A thread owns 8
 // consecutive channels (16 bytes of bf16), keeps their K taps and the last K-1 inputs in registers as fp32 and walks
-// along the tokens, so every input is loaded once (plus K-1 rows where a prompt is cut into tiles).
+// along the tokens, so every input is loaded once (plus K-1 rows where a prompt is cut into tiles), a group of tokens
+// ahead of its use.  SiLU is one exponential and one reciprocal of the special-function unit, which alone would take
+// three quarters of the memory's time; the exact division and expf took twice that.
+#include <cooperative_groups.h>
+
 #include "kernels.h"
+
+namespace cg = cooperative_groups;
 
 namespace rssm {
 
 namespace {
 
-constexpr int kTile = 32;         // tokens of a prompt tile: K-1 = 3 rows read twice in 32 is 9%, served by L2
-constexpr int kPromptThreads = 128;
+constexpr int kPromptThreads = 128, kTokenThreads = 256;
+// tokens loaded together, one group ahead: with bf16 64 bytes in flight a thread of a prompt; two where registers are short
+constexpr int kPromptGroup = 4, kTokenGroup = 2;
+
+// 8 values as they lie in memory
+template <typename TI>
+struct Raw8;
+template <>
+struct Raw8<__nv_bfloat16> {
+  uint4 u;
+  __device__ __forceinline__ void load(const __nv_bfloat16 *p) { u = *reinterpret_cast<const uint4 *>(p); }
+  __device__ __forceinline__ void widen(float (&o)[8]) const {
+    const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      o[2 * i] = __uint_as_float(w[i] << 16);
+      o[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
+    }
+  }
+};
+template <>
+struct Raw8<float> {
+  float4 a, b;
+  __device__ __forceinline__ void load(const float *p) {
+    a = *reinterpret_cast<const float4 *>(p);
+    b = *reinterpret_cast<const float4 *>(p + 4);
+  }
+  __device__ __forceinline__ void widen(float (&o)[8]) const {
+    o[0] = a.x; o[1] = a.y; o[2] = a.z; o[3] = a.w; o[4] = b.x; o[5] = b.y; o[6] = b.z; o[7] = b.w;
+  }
+};
 
 template <typename TI>
 __device__ __forceinline__ void store8(TI *p, const float (&v)[8]);
@@ -57,8 +92,13 @@ struct Filter {
     if (a.bias) load8(reinterpret_cast<const TI *>(a.bias) + c, b);
     silu = a.silu;
   }
-  // v / (1 + exp(-v)); where exp overflows the quotient is -0
-  __device__ __forceinline__ float act(float v) const { return silu ? v / (1.f + expf(-v)) : v; }
+  // v / (1 + exp(-v)), to about 2^-21 of it; where exp overflows the quotient is -0
+  __device__ __forceinline__ float act(float v) const {
+    float e, r;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e) : "f"(v * -1.4426950408889634f));
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(1.f + e));
+    return silu ? v * r : v;
+  }
   __device__ __forceinline__ void apply(const float (&win)[K - 1][8], const float (&x)[8], float (&o)[8]) const {
 #pragma unroll
     for (int j = 0; j < 8; ++j) {
@@ -85,23 +125,49 @@ __device__ __forceinline__ int wrap(int v, int ring) {
   return v < 0 ? v + ring : v;
 }
 
-// where the channels from c go: the output that holds them, its row length and the offset in a row
+// where the channels from c go: the output that holds them (at its first row) and its row length
 template <typename TI>
 __device__ __forceinline__ TI *split_out(const ShortConvArgs &a, int c, int &row) {
-  int s = 0, c0 = 0;
-  if (c >= a.split[0]) { c0 = a.split[0]; s = 1; }
-  if (s == 1 && c >= c0 + a.split[1]) { c0 += a.split[1]; s = 2; }
-  row = a.split[s];
-  return reinterpret_cast<TI *>(a.out[s]) + (c - c0);
+  const int c1 = a.split[0], c2 = c1 + a.split[1];
+  row = c < c1 ? a.split[0] : c < c2 ? a.split[1] : a.split[2];
+  void *const p = c < c1 ? a.out[0] : c < c2 ? a.out[1] : a.out[2];
+  return reinterpret_cast<TI *>(p) + (c < c1 ? c : c < c2 ? c - c1 : c - c2);
+}
+
+// n tokens from `in` through the filter, loaded a group ahead; `keep(t, raw)` sees every raw input
+template <typename TI, int K, int kGroup, typename Keep>
+__device__ __forceinline__ void walk(const Filter<TI, K> &f, float (&win)[K - 1][8], const TI *in, size_t in_stride,
+                                     TI *out, int row, int n, Keep keep) {
+  Raw8<TI> now[kGroup], next[kGroup];
+#pragma unroll
+  for (int i = 0; i < kGroup; ++i)
+    if (i < n) now[i].load(in + i * in_stride);
+  for (int t = 0; t < n; t += kGroup) {
+#pragma unroll
+    for (int i = 0; i < kGroup; ++i)
+      if (t + kGroup + i < n) next[i].load(in + (t + kGroup + i) * in_stride);
+#pragma unroll
+    for (int i = 0; i < kGroup; ++i) {
+      if (t + i < n) {
+        float x[8], o[8];
+        now[i].widen(x);
+        f.apply(win, x, o);
+        push<K>(win, x);
+        store8<TI>(out + (size_t)(t + i) * row, o);
+        keep(t + i, x);
+      }
+      now[i] = next[i];
+    }
+  }
 }
 
 // Prompts.  blockIdx.x: tile of a prompt; blockIdx.y: block of channels.  The block of a prompt's first tile alone
 // reads and rewrites the sequence's history, each thread its own channels, so the rewrite is safe in place.
 template <typename TI, int K>
-__global__ void __launch_bounds__(kPromptThreads) prompt_kernel(ShortConvArgs a, Prompts pr) {
+__global__ void __launch_bounds__(kPromptThreads) prompt_kernel(ShortConvArgs a, Prompts pr, int tile) {
   __shared__ int found;
   Piece pc;
-  if (!find_piece(pr, blockIdx.x, kTile, pc, &found)) return;
+  if (!find_piece(pr, blockIdx.x, tile, pc, &found)) return;
   const int c = (blockIdx.y * kPromptThreads + threadIdx.x) * 8;
   const int len = pc.end - pc.begin;
   if (c >= a.channels || (pc.first >= len && pc.index > 0)) return;
@@ -147,46 +213,79 @@ __global__ void __launch_bounds__(kPromptThreads) prompt_kernel(ShortConvArgs a,
     for (int k = 0; k < K - 1; ++k) load8(in + (size_t)(pc.first - (K - 1) + k) * a.in_stride, win[k]);
   }
   int row;
-  TI *out = split_out<TI>(a, c, row) + (size_t)(pc.begin + pc.first) * row;
-  const int n = min(kTile, len - pc.first);
-  in += (size_t)pc.first * a.in_stride;
-  for (int t = 0; t < n; ++t) {
-    float x[8], o[8];
-    load8(in + (size_t)t * a.in_stride, x);
-    f.apply(win, x, o);
-    push<K>(win, x);
-    store8<TI>(out + (size_t)t * row, o);
-  }
+  TI *out = split_out<TI>(a, c, row);
+  out += (size_t)(pc.begin + pc.first) * row;
+  walk<TI, K, kPromptGroup>(f, win, in + (size_t)pc.first * a.in_stride, a.in_stride, out, row, min(tile, len - pc.first),
+              [](int, const float(&)[8]) {});
 }
 
-// T tokens a sequence on top of its history.  One block a sequence, so that the cursor can advance in place once
-// every thread has read it (`advance`: one token that stands; otherwise the rows stay tentative).
-template <typename TI, int K>
-__global__ void __launch_bounds__(1024) token_kernel(ShortConvArgs a, int T, int advance) {
-  const int b = blockIdx.x;
-  const int cur = wrap(a.cur[b], a.ring);
-  for (int c = threadIdx.x * 8; c < a.channels; c += blockDim.x * 8) {
-    Filter<TI, K> f;
-    f.load(a, c);
-    TI *hist = reinterpret_cast<TI *>(a.hist) + (size_t)b * a.ring * a.channels + c;
-    const TI *in = reinterpret_cast<const TI *>(a.in) + (size_t)b * T * a.in_stride + c;
-    float win[K - 1][8];
-#pragma unroll
-    for (int k = 0; k < K - 1; ++k) load8(hist + (size_t)wrap(cur - (K - 1) + k, a.ring) * a.channels, win[k]);
+// T tokens a sequence on top of its history.  A thread keeps the taps of its channels and takes the sequences of its
+// cluster one after the other, with one token (kOne) the next sequence's rows on their way.  The blocks of a cluster
+// share out the channels, so that the cursors can advance in place once all of them have read them (`advance`: one token
+// that stands; otherwise the rows stay tentative).
+template <typename TI, int K, bool kOne>
+__global__ void __launch_bounds__(kTokenThreads, 2) token_kernel(ShortConvArgs a, int T, int advance) {
+  cg::cluster_group cluster = cg::this_cluster();
+  const int blocks = cluster.num_blocks(), rank = cluster.block_rank();
+  const int first = blockIdx.x / blocks, stride = gridDim.x / blocks;
+  const size_t row_hist = a.channels;
+  for (int c = (rank * blockDim.x + threadIdx.x) * 8; c < a.channels; c += blocks * blockDim.x * 8) {
+    TI *hist0 = reinterpret_cast<TI *>(a.hist) + c;
+    const TI *in0 = reinterpret_cast<const TI *>(a.in) + c;
     int row;
-    TI *out = split_out<TI>(a, c, row) + (size_t)b * T * row;
-    for (int t = 0; t < T; ++t) {
-      float x[8], o[8];
-      load8(in + (size_t)t * a.in_stride, x);
-      f.apply(win, x, o);
-      push<K>(win, x);
-      store8<TI>(hist + (size_t)wrap(cur + t, a.ring) * a.channels, x);
-      store8<TI>(out + (size_t)t * row, o);
+    TI *out0 = split_out<TI>(a, c, row);
+    if (kOne) {
+      Raw8<TI> now[K], next[K];  // K-1 rows of history, then the token
+      auto load = [&](int b, int cur, Raw8<TI> (&r)[K]) {
+#pragma unroll
+        for (int k = 0; k < K - 1; ++k)
+          r[k].load(hist0 + ((size_t)b * a.ring + wrap(cur - (K - 1) + k, a.ring)) * row_hist);
+        r[K - 1].load(in0 + (size_t)b * a.in_stride);
+      };
+      int cur = wrap(a.cur[first], a.ring);
+      load(first, cur, now);
+      Filter<TI, K> f;
+      f.load(a, c);
+      int cur_next = first + stride < a.batch ? wrap(a.cur[first + stride], a.ring) : 0;
+      for (int b = first; b < a.batch; b += stride) {
+        const int after = b + 2 * stride < a.batch ? a.cur[b + 2 * stride] : 0;
+        if (b + stride < a.batch) load(b + stride, cur_next, next);
+        float win[K - 1][8], x[8], o[8];
+#pragma unroll
+        for (int k = 0; k < K - 1; ++k) now[k].widen(win[k]);
+        now[K - 1].widen(x);
+        f.apply(win, x, o);
+        store8<TI>(hist0 + ((size_t)b * a.ring + cur) * row_hist, x);
+        store8<TI>(out0 + (size_t)b * row, o);
+        cur = cur_next;
+        cur_next = wrap(after, a.ring);
+#pragma unroll
+        for (int k = 0; k < K; ++k) now[k] = next[k];
+      }
+    } else {
+      Filter<TI, K> f;
+      f.load(a, c);
+      for (int b = first; b < a.batch; b += stride) {
+        int slot = wrap(a.cur[b], a.ring);
+        TI *hist = hist0 + (size_t)b * a.ring * row_hist;
+        float win[K - 1][8];
+#pragma unroll
+        for (int k = 0; k < K - 1; ++k) load8(hist + (size_t)wrap(slot - (K - 1) + k, a.ring) * row_hist, win[k]);
+        walk<TI, K, kTokenGroup>(f, win, in0 + (size_t)b * T * a.in_stride, a.in_stride, out0 + (size_t)b * T * row, row, T,
+                    [&](int, const float(&x)[8]) {
+                      store8<TI>(hist + (size_t)slot * row_hist, x);
+                      slot = slot + 1 == a.ring ? 0 : slot + 1;
+                    });
+      }
     }
   }
   if (advance) {
-    __syncthreads();
-    if (threadIdx.x == 0) a.cur_out[b] = wrap(cur + 1, a.ring);
+    cluster.sync();
+    if (rank == 0)
+      for (int b = first + threadIdx.x * stride; b < a.batch; b += blockDim.x * stride) {
+        const int cur = wrap(a.cur[b], a.ring);
+        a.cur_out[b] = cur + 1 == a.ring ? 0 : cur + 1;
+      }
   }
 }
 
@@ -198,32 +297,62 @@ __global__ void commit_kernel(int *cur, const int *accepted, int batch, int ring
 }
 
 template <typename TI>
-cudaError_t launch_prompt(const ShortConvArgs &a, const Prompts &pr, cudaStream_t stream) {
-  const dim3 grid(prompt_pieces(pr.total, pr.nseq, kTile), (a.channels / 8 + kPromptThreads - 1) / kPromptThreads);
-  if (a.width == 2) prompt_kernel<TI, 2><<<grid, kPromptThreads, 0, stream>>>(a, pr);
-  else if (a.width == 3) prompt_kernel<TI, 3><<<grid, kPromptThreads, 0, stream>>>(a, pr);
-  else prompt_kernel<TI, 4><<<grid, kPromptThreads, 0, stream>>>(a, pr);
+cudaError_t launch_prompt(const ShortConvArgs &a, const Prompts &pr, int num_sms, cudaStream_t stream) {
+  // Tiles as long as they still give two blocks an SM: K-1 rows are read twice a tile (from L2) and the taps once, and a
+  // short tile is soon done, which is what counts when there are few.
+  const int columns = (a.channels / 8 + kPromptThreads - 1) / kPromptThreads;
+  int tile = 8;
+  while (tile < 64 && (long long)(pr.total / (2 * tile) + 1) * columns >= 2LL * num_sms) tile *= 2;
+  const dim3 grid(prompt_pieces(pr.total, pr.nseq, tile), columns);
+  if (a.width == 2) prompt_kernel<TI, 2><<<grid, kPromptThreads, 0, stream>>>(a, pr, tile);
+  else if (a.width == 3) prompt_kernel<TI, 3><<<grid, kPromptThreads, 0, stream>>>(a, pr, tile);
+  else prompt_kernel<TI, 4><<<grid, kPromptThreads, 0, stream>>>(a, pr, tile);
   return cudaGetLastError();
 }
 
+template <typename TI, int K>
+cudaError_t launch_tokens(const ShortConvArgs &a, int T, int advance, int num_sms, cudaStream_t stream) {
+  const int vectors = a.channels / 8;
+  int threads = (vectors + 31) / 32 * 32;
+  threads = threads > kTokenThreads ? kTokenThreads : threads;
+  int blocks = (vectors + threads - 1) / threads;
+  blocks = blocks > 8 ? 8 : blocks;  // the portable cluster
+  // as many clusters as fit the SMs at once (two blocks an SM): the taps are read once a cluster
+  int clusters = 2 * num_sms / blocks;
+  clusters = a.batch < clusters ? a.batch : clusters;
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3((unsigned)clusters * blocks);
+  cfg.blockDim = dim3(threads);
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = blocks;
+  attr[0].val.clusterDim.y = 1;
+  attr[0].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return T == 1 ? cudaLaunchKernelEx(&cfg, token_kernel<TI, K, true>, a, T, advance)
+                : cudaLaunchKernelEx(&cfg, token_kernel<TI, K, false>, a, T, advance);
+}
+
 template <typename TI>
-cudaError_t launch_tokens(const ShortConvArgs &a, int T, int advance, cudaStream_t stream) {
-  int threads = (a.channels / 8 + 31) / 32 * 32;
-  threads = threads > 256 ? 256 : threads;
-  if (a.width == 2) token_kernel<TI, 2><<<a.batch, threads, 0, stream>>>(a, T, advance);
-  else if (a.width == 3) token_kernel<TI, 3><<<a.batch, threads, 0, stream>>>(a, T, advance);
-  else token_kernel<TI, 4><<<a.batch, threads, 0, stream>>>(a, T, advance);
-  return cudaGetLastError();
+cudaError_t launch_tokens(const ShortConvArgs &a, int T, int advance, int num_sms, cudaStream_t stream) {
+  if (a.width == 2) return launch_tokens<TI, 2>(a, T, advance, num_sms, stream);
+  if (a.width == 3) return launch_tokens<TI, 3>(a, T, advance, num_sms, stream);
+  return launch_tokens<TI, 4>(a, T, advance, num_sms, stream);
 }
 
 }  // namespace
 
-cudaError_t launch_shortconv_prompt(const ShortConvArgs &a, const Prompts &pr, int esz, cudaStream_t stream) {
-  return esz == 2 ? launch_prompt<__nv_bfloat16>(a, pr, stream) : launch_prompt<float>(a, pr, stream);
+cudaError_t launch_shortconv_prompt(const ShortConvArgs &a, const Prompts &pr, int esz, int num_sms,
+                                    cudaStream_t stream) {
+  return esz == 2 ? launch_prompt<__nv_bfloat16>(a, pr, num_sms, stream) : launch_prompt<float>(a, pr, num_sms, stream);
 }
 
-cudaError_t launch_shortconv_tokens(const ShortConvArgs &a, int T, int advance, int esz, cudaStream_t stream) {
-  return esz == 2 ? launch_tokens<__nv_bfloat16>(a, T, advance, stream) : launch_tokens<float>(a, T, advance, stream);
+cudaError_t launch_shortconv_tokens(const ShortConvArgs &a, int T, int advance, int esz, int num_sms,
+                                    cudaStream_t stream) {
+  return esz == 2 ? launch_tokens<__nv_bfloat16>(a, T, advance, num_sms, stream)
+                  : launch_tokens<float>(a, T, advance, num_sms, stream);
 }
 
 cudaError_t launch_shortconv_commit(int *cur, const int *accepted, int batch, int ring, int most, cudaStream_t stream) {
