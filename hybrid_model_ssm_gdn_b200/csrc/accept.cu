@@ -6,7 +6,10 @@
 // chunk in which the sum passes the goal is read again, from L2.
 //
 // The drawn token is a whole number next to a border of the sums, so masses (p - q is exact in fp64) and sums are
-// fp64: fp32 sums of a vocabulary's values would move the border by more than many tokens' mass.
+// fp64: fp32 sums of a vocabulary's values would move the border by more than many tokens' mass.  Conversions to fp64
+// run at an eighth of the fp32 rate, so the long pass makes one an element instead of two: the fp32 difference goes to the
+// fp64 sum, and its rounding error, which fp32 arithmetic gives exactly, to an fp32 sum of its own (errors are below 2^-24
+// of their values and lose 2^-24 of that in turn).
 //
 // A cluster of blocks shares a sequence (when there are few, so that one row is read by several SMs); the blocks'
 // totals are exchanged through distributed shared memory.
@@ -20,8 +23,9 @@ namespace rssm {
 
 namespace {
 
-constexpr int kWarps = 16;
-constexpr int kFine = 1024;  // longest run that one warp scans element by element
+constexpr int kWarps = 8;
+constexpr int kUnroll = 8;
+constexpr int kFine = 256;  // longest run that one warp searches by itself: 8 consecutive elements a lane
 
 struct Row {
   const float *p, *q;  // q null: no draft row
@@ -41,39 +45,79 @@ __device__ __forceinline__ double warp_sum_f64(double v) {
 }
 
 // sum of the masses of [lo, hi), the whole warp
+template <bool kDraft>
 __device__ __forceinline__ double warp_mass(const Row &r, int lo, int hi, int lane) {
-  double s0 = 0.0, s1 = 0.0;
-  int v = lo + lane;
-  for (; v + 7 * 32 < hi; v += 8 * 32) {
-#pragma unroll
-    for (int i = 0; i < 8; i += 2) {
-      s0 += r.mass(v + i * 32);
-      s1 += r.mass(v + (i + 1) * 32);
+  const float inf = __int_as_float(0x7f800000);
+  double s = 0.0;
+  float lost = 0.f;
+  auto add = [&](float p, float q, int v) {
+    if (kDraft) {
+      const bool some = p > q && p < inf && q > -inf;
+      p = some ? p : 0.f;
+      q = some ? q : 0.f;
+      const float d = p - q, back = d - p;
+      s += (double)d;
+      lost += (p - (d - back)) - (q + back);  // p - q = d + this
+    } else {
+      s += (double)(p > 0.f && p < inf && v != r.hot ? p : 0.f);
     }
+  };
+  int v = lo + lane;
+  for (; v + (kUnroll - 1) * 32 < hi; v += kUnroll * 32) {
+    float p[kUnroll], q[kUnroll];
+#pragma unroll
+    for (int i = 0; i < kUnroll; ++i) {
+      p[i] = r.p[v + 32 * i];
+      q[i] = kDraft ? r.q[v + 32 * i] : 0.f;
+    }
+#pragma unroll
+    for (int i = 0; i < kUnroll; ++i) add(p[i], q[i], v + 32 * i);
   }
-  for (; v < hi; v += 32) s0 += r.mass(v);
-  return warp_sum_f64(s0 + s1);
+  for (; v < hi; v += 32) add(r.p[v], kDraft ? r.q[v] : 0.f, v);
+  s = warp_sum_f64(s + (double)lost);
+  if (kDraft && !(s < (double)inf)) {  // a difference beyond fp32's range: once more in fp64
+    s = 0.0;
+    for (v = lo + lane; v < hi; v += 32) s += r.mass(v);
+    s = warp_sum_f64(s);
+  }
+  return s;
+}
+__device__ __forceinline__ double warp_mass(const Row &r, int lo, int hi, int lane) {
+  return r.q ? warp_mass<true>(r, lo, hi, lane) : warp_mass<false>(r, lo, hi, lane);
 }
 
-// lowest v of [lo, hi) where base + the inclusive sum passes goal; else the last one with mass; else -1.  Whole warp.
+// lowest v of [lo, hi), at most kFine long, where base + the inclusive sum passes goal; else the last one with mass;
+// else -1.  Whole warp.
 __device__ __forceinline__ int warp_find(const Row &r, int lo, int hi, double base, double goal, int lane) {
-  int last = -1;
-  for (int v0 = lo; v0 < hi; v0 += 32) {
-    const int v = v0 + lane;
-    const double m = v < hi ? r.mass(v) : 0.0;
-    double s = m;
+  double m[8], own = 0.0;
+  const int v0 = lo + 8 * lane;
 #pragma unroll
-    for (int off = 1; off < 32; off <<= 1) {
-      const double t = __shfl_up_sync(0xffffffffu, s, off);
-      if (lane >= off) s += t;
-    }
-    const unsigned pass = __ballot_sync(0xffffffffu, m > 0.0 && base + s > goal);
-    if (pass) return v0 + __ffs(pass) - 1;
-    const unsigned any = __ballot_sync(0xffffffffu, m > 0.0);
-    if (any) last = v0 + 31 - __clz(any);
-    base += __shfl_sync(0xffffffffu, s, 31);
+  for (int i = 0; i < 8; ++i) m[i] = v0 + i < hi ? r.mass(v0 + i) : 0.0;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) own += m[i];
+  double s = own;
+#pragma unroll
+  for (int off = 1; off < 32; off <<= 1) {
+    const double t = __shfl_up_sync(0xffffffffu, s, off);
+    if (lane >= off) s += t;
   }
-  return last;
+  const unsigned pass = __ballot_sync(0xffffffffu, own > 0.0 && base + s > goal);
+  const unsigned any = __ballot_sync(0xffffffffu, own > 0.0);
+  if (!any) return -1;
+  const int who = pass ? __ffs(pass) - 1 : 31 - __clz(any);
+  const double before = __shfl_up_sync(0xffffffffu, s, 1);
+  double run = base + (lane > 0 ? before : 0.0);
+  int v = -1;
+  bool found = false;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    run += m[i];
+    if (m[i] > 0.0 && !found) {
+      v = v0 + i;
+      found = run > goal;
+    }
+  }
+  return __shfl_sync(0xffffffffu, v, who);
 }
 
 struct Shared {
@@ -187,11 +231,11 @@ __global__ void __launch_bounds__(kWarps * 32) accept_kernel(AcceptArgs a) {
   __syncthreads();
   int f0 = min(hi, lo + sh.pick * chunk), f1 = min(hi, f0 + chunk);
   double base = sh.base;
-  while (f1 - f0 > kFine) {  // a long chunk: its 16 parts, then one of them
+  while (f1 - f0 > kFine) {  // a long chunk: a part a warp, then one of them
     const int part = ((f1 - f0 + kWarps - 1) / kWarps + 31) / 32 * 32;
     const int p0 = min(f1, f0 + warp * part), p1 = min(f1, p0 + part);
     const double s = warp_mass(r, p0, p1, lane);
-    __syncthreads();
+    __syncthreads();  // the last sums have been read
     if (lane == 0) sh.sum[warp] = s;
     __syncthreads();
     double run = base;
@@ -218,10 +262,10 @@ __global__ void __launch_bounds__(kWarps * 32) accept_kernel(AcceptArgs a) {
 }  // namespace
 
 cudaError_t launch_accept(const AcceptArgs &a, int num_sms, cudaStream_t stream) {
-  // Blocks a sequence: as many as fill the SMs once (two blocks fit an SM), up to the portable cluster of 8, and
-  // none with less than 4096 elements, below which the exchange costs more than the reading it spreads.
+  // Blocks a sequence: up to the portable cluster of 8 while there are fewer than eight blocks an SM in all (uneven
+  // rows then average out), none with less than 2048 elements, one round of loads of a block.
   int blocks = 1;
-  while (blocks < 8 && (long long)a.batch * blocks * 2 <= 2LL * num_sms && a.vocab / (blocks * 2) >= 4096) blocks *= 2;
+  while (blocks < 8 && (long long)a.batch * blocks <= 8LL * num_sms && a.vocab / (blocks * 2) >= 2048) blocks *= 2;
   cudaLaunchConfig_t cfg{};
   cfg.gridDim = dim3((unsigned)a.batch * blocks);
   cfg.blockDim = dim3(kWarps * 32);

@@ -93,6 +93,8 @@ def test_entries_without_mass(cuda_ok):
         a[:, :, 10:20] = np.nan
         a[:, :, 30:40] = np.inf
         a[:, :, 50:60] = -1.0
+    target[0, :, 60] = 3e38  # with the -3e38 below beyond fp32's range, but finite in 64 bits
+    draft[0, :, 60] = -3e38
     target[3:5] = 0.0
     target[5] = np.nan
     tokens[6:8, 0] = (-3, 700)
