@@ -20,7 +20,7 @@ BUILD = os.path.join(PKG, "_build")
 LIB = os.path.join(PKG, "lib", "librssm.so")
 INCLUDE = os.path.join(os.path.dirname(PKG), "include")
 SOURCES = ["api.cu", "mamba2.cu", "gdn.cu", "lowprec.cu", "conv.cu", "small.cu", "sched.cu", "scan.cu",
-           "scan_tc.cu", "shortconv.cu", "accept.cu"]
+           "scan_tc.cu", "scan_mma.cu", "shortconv.cu", "accept.cu"]
 ARCH = ["-gencode", "arch=compute_100a,code=sm_100a"]
 FLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC", "-I", INCLUDE]
 

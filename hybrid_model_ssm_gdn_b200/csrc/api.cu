@@ -460,7 +460,12 @@ static rssm_status run_scan(const rssm_config &c, const Prompts &p, const rssm_t
     if (work_bytes < scan_tc_workspace(a.H, a.P, prompt_pieces(p.total, p.nseq, a.piece_len), nullptr))
       return RSSM_ERR_ARENA_TOO_SMALL;
   }
-  const cudaError_t e = c.in_dtype == RSSM_BF16 && p.total > 0 ? launch_scan_tc(a, p, st) : launch_scan(a, p, esize(c), num_sms, st);
+  const char *mm = getenv("RSSM_MMA");
+  const bool shrt = mm && atoi(mm);
+  cudaError_t e;
+  if (c.in_dtype != RSSM_BF16) e = launch_scan(a, p, num_sms, st);
+  else if (p.total == 0 || (shrt && a.piece_len > p.total)) e = launch_scan_mma(a, p, st);
+  else e = launch_scan_tc(a, p, st);
   return e == cudaSuccess ? RSSM_OK : cuda_fail(e);
 }
 

@@ -115,10 +115,13 @@ struct ScanArgs {
   int *err;                         // error word, may be null
   long long wait_cycles;            // bound of the tensor-core kernel's waits
 };
-// tensor cores: bf16 inputs, total > 0
+// short prompts: bf16 inputs, prompts not cut
+cudaError_t launch_scan_mma(const ScanArgs &a, const Prompts &pr, cudaStream_t stream);
+// long prompts: bf16 inputs, total > 0
 cudaError_t launch_scan_tc(const ScanArgs &a, const Prompts &pr, cudaStream_t stream);
 size_t scan_tc_workspace(int H, int P, int pieces, size_t *seg_dt);
-cudaError_t launch_scan(const ScanArgs &a, const Prompts &pr, int esz, int num_sms, cudaStream_t stream);
+// fp32 inputs, prompts not cut
+cudaError_t launch_scan(const ScanArgs &a, const Prompts &pr, int num_sms, cudaStream_t stream);
 cudaError_t launch_prefill_meta(const Prompts &pr, const int4 *meta_in, int4 *meta_out, unsigned char *skip, int H,
                                 int *err, cudaStream_t stream);
 

@@ -158,8 +158,8 @@ cudaError_t launch_scan_t(const ScanArgs &a, const Prompts &pr, int num_sms, cud
 
 }  // namespace
 
-cudaError_t launch_scan(const ScanArgs &a, const Prompts &pr, int esz, int num_sms, cudaStream_t stream) {
-  return esz == 2 ? launch_scan_t<__nv_bfloat16>(a, pr, num_sms, stream) : launch_scan_t<float>(a, pr, num_sms, stream);
+cudaError_t launch_scan(const ScanArgs &a, const Prompts &pr, int num_sms, cudaStream_t stream) {
+  return launch_scan_t<float>(a, pr, num_sms, stream);
 }
 
 cudaError_t launch_prefill_meta(const Prompts &pr, const int4 *meta_in, int4 *meta_out, unsigned char *skip, int H,
