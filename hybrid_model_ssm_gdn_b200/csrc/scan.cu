@@ -1,10 +1,12 @@
-// scan.cu -- the Mamba-2 recurrence over whole prompts, on CUDA cores.
+// scan.cu -- the Mamba-2 recurrence over whole prompts on CUDA cores (fp32 inputs), and a context's bookkeeping after it.
 //
 //   S_t = exp(dt_t A_h) S_{t-1} + dt_t x_t B_t^T,   y_t = S_t C_t + D_h x_t
 //
-// A block carries R rows of one head's state along one prompt: four threads a row, each with 32 of its 128 columns in
-// registers as packed fp32 pairs, so a token costs a thread 48 packed multiply-adds and the columns' sum two shuffles.
-// Tokens are staged in shared memory 16 at a time.
+// Token by token in fp32: inputs of 24 bits would need six bf16 products for each one of the chunk form.  A warp carries
+// 8 rows of one head's state: 16 lanes take 8 columns each (two runs of 4, so that B and C come from shared memory
+// without bank conflicts) of 4 rows, 32 fp32 values a lane as packed pairs; a token costs 48 packed operations, five
+// 16-byte reads and four shuffles that sum the four rows' columns.  Tokens are staged 16 at a time, the next ones on
+// their way.  The chain of tokens sets the time of few prompts, so blocks are as small as it takes to use the SMs.
 #include "kernels.h"
 #include "packed.cuh"
 
@@ -14,90 +16,128 @@ namespace {
 
 constexpr int kTok = 16;   // tokens staged at a time
 
+// 16 bytes to shared memory, zeros where `live` is not set
+__device__ __forceinline__ void copy16(void *dst, const void *src, bool live) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(smem_u32(dst)), "l"(src), "r"(live ? 16 : 0) : "memory");
+}
+
 template <int R>
 struct Stage {
   float b[kTok][kCols], c[kTok][kCols];
   float x[kTok][R];
-  float dt[kTok], decay[kTok];
+  float2 dt[kTok];  // dt, exp(dt A)
 };
 
-template <typename TI, int R>
+// R rows of head blockIdx.y from row blockIdx.z * R on
+template <int R>
 __global__ void __launch_bounds__(4 * R) scan_kernel(ScanArgs a, Prompts pr) {
-  __shared__ __align__(16) Stage<R> st;
+  __shared__ __align__(16) Stage<R> st[2];
   __shared__ int found;
   Piece pc;
   const int h = blockIdx.y, row0 = blockIdx.z * R;
   if (!find_piece(pr, blockIdx.x, a.piece_len, pc, &found)) return;
   const int len = pc.end - pc.begin;
-  if (pc.first >= len && pc.index > 0) return;
-  const int tid = threadIdx.x, q = tid & 3, row = row0 + (tid >> 2);
-  const bool live = row < a.P;
+  if (len == 0 && pc.resume) return;
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, l16 = lane & 15;
+  const int mine = 8 * warp + 4 * (lane >> 4);  // this lane's four rows within the block
   const int g = h / (a.H / a.G);
   const float A = a.A[h], D = a.D[h];
+  const float *xg = static_cast<const float *>(a.x) + ((size_t)pc.begin * a.H + h) * a.P + row0;
+  const float *Bg = static_cast<const float *>(a.Bin) + ((size_t)pc.begin * a.G + g) * kCols;
+  const float *Cg = static_cast<const float *>(a.C) + ((size_t)pc.begin * a.G + g) * kCols;
+  const float *dg = static_cast<const float *>(a.dt) + (size_t)pc.begin * a.H + h;
 
-  // column 4 (q + 4 i) + j of the row sits in s[2 i + j / 2]
-  f2 s[16];
-  float *Sg = a.S + (((size_t)pc.slot * a.H + h) * a.P + row) * kCols;
-#pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    float4 v = f4zero();
-    if (pc.resume && live) v = *reinterpret_cast<const float4 *>(Sg + 4 * (q + 4 * i));
-    s[2 * i] = pack2(v.x, v.y);
-    s[2 * i + 1] = pack2(v.z, v.w);
-  }
-  const TI *xg = reinterpret_cast<const TI *>(a.x), *Bg = reinterpret_cast<const TI *>(a.Bin);
-  const TI *Cg = reinterpret_cast<const TI *>(a.C), *dg = reinterpret_cast<const TI *>(a.dt);
-
-  for (int t0 = 0; t0 < len; t0 += kTok) {
-    const int m = min(kTok, len - t0);
-    __syncthreads();
-    for (int e = tid; e < m * (kCols / 4); e += 4 * R) {
+  float dt_next = 0.f;
+  auto fetch = [&](int t0, Stage<R> &s) {
+    for (int e = tid; e < kTok * (kCols / 4); e += 4 * R) {
       const int t = e / (kCols / 4), n = 4 * (e % (kCols / 4));
-      const size_t tok = (size_t)(pc.begin + t0 + t) * a.G + g;
-      *reinterpret_cast<float4 *>(&st.b[t][n]) = load4(Bg + tok * kCols + n);
-      *reinterpret_cast<float4 *>(&st.c[t][n]) = load4(Cg + tok * kCols + n);
+      const bool live = t0 + t < len;
+      const size_t at = live ? (size_t)(t0 + t) * a.G * kCols + n : 0;
+      copy16(&s.b[t][n], Bg + at, live);
+      copy16(&s.c[t][n], Cg + at, live);
     }
-    for (int e = tid; e < m * R; e += 4 * R) {
-      const int t = e / R, r = e % R;
-      st.x[t][r] = row0 + r < a.P ? to_f32(xg[((size_t)(pc.begin + t0 + t) * a.H + h) * a.P + row0 + r]) : 0.f;
+    for (int e = tid; e < kTok * (R / 4); e += 4 * R) {
+      const int t = e / (R / 4), r = 4 * (e % (R / 4));
+      const bool live = t0 + t < len && row0 + r < a.P;  // P is a multiple of 8
+      copy16(&s.x[t][r], xg + (live ? (size_t)(t0 + t) * a.H * a.P + r : 0), live);
     }
-    if (tid < m) {
-      const float dt = to_f32(dg[(size_t)(pc.begin + t0 + tid) * a.H + h]);
-      st.dt[tid] = dt;
-      st.decay[tid] = expf(dt * A);
+    asm volatile("cp.async.commit_group;" ::: "memory");
+    if (tid < kTok) dt_next = t0 + tid < len ? dg[(size_t)(t0 + tid) * a.H] : 0.f;
+  };
+  if (len > 0) fetch(0, st[0]);
+
+  // columns 4 l16 + 64 i + 2 j .. of row mine + r in s[r][2 i + j]
+  f2 s[4][4];
+  float *Sg = a.S + (((size_t)pc.slot * a.H + h) * a.P + row0 + mine) * kCols + 4 * l16;
+#pragma unroll
+  for (int r = 0; r < 4; ++r)
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      float4 v = f4zero();
+      if (pc.resume && row0 + mine + r < a.P) v = *reinterpret_cast<const float4 *>(Sg + r * kCols + 64 * i);
+      s[r][2 * i] = pack2(v.x, v.y);
+      s[r][2 * i + 1] = pack2(v.z, v.w);
     }
+  // after the sums below, this lane holds row `out` of the block
+  const int out = mine + 2 * ((lane >> 3) & 1) + ((lane >> 2) & 1);
+  const bool write = (lane & 3) == 0 && row0 + out < a.P;
+  float *yg = a.y + ((size_t)pc.begin * a.H + h) * a.P + row0 + out;
+
+  for (int t0 = 0, k = 0; t0 < len; t0 += kTok, k ^= 1) {
+    if (tid < kTok) st[k].dt[tid] = make_float2(dt_next, expf(dt_next * A));
+    asm volatile("cp.async.wait_group 0;" ::: "memory");
     __syncthreads();
-    for (int t = 0; t < m; ++t) {
-      const float x = st.x[t][tid >> 2], w = st.dt[t] * x, da = st.decay[t];
-      const f2 w2 = pack2(w, w), d2 = pack2(da, da);
-      f2 acc0 = pack2(0.f, 0.f), acc1 = acc0;
+    if (t0 + kTok < len) fetch(t0 + kTok, st[k ^ 1]);  // read last before the barrier above
+    const Stage<R> &m = st[k];
+    const int n = min(kTok, len - t0);
+#pragma unroll 4
+    for (int t = 0; t < n; ++t) {
+      const float2 d = m.dt[t];
+      const float4 x = *reinterpret_cast<const float4 *>(&m.x[t][mine]);
+      const float4 b0 = *reinterpret_cast<const float4 *>(&m.b[t][4 * l16]);
+      const float4 b1 = *reinterpret_cast<const float4 *>(&m.b[t][4 * l16 + 64]);
+      const float4 c0 = *reinterpret_cast<const float4 *>(&m.c[t][4 * l16]);
+      const float4 c1 = *reinterpret_cast<const float4 *>(&m.c[t][4 * l16 + 64]);
+      const f2 bb[4] = {pack2(b0.x, b0.y), pack2(b0.z, b0.w), pack2(b1.x, b1.y), pack2(b1.z, b1.w)};
+      const f2 cc[4] = {pack2(c0.x, c0.y), pack2(c0.z, c0.w), pack2(c1.x, c1.y), pack2(c1.z, c1.w)};
+      const float xs[4] = {x.x, x.y, x.z, x.w};
+      const f2 da = pack2(d.y, d.y);
+      float v[4];
 #pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        const float4 b = *reinterpret_cast<const float4 *>(&st.b[t][4 * (q + 4 * i)]);
-        const float4 c = *reinterpret_cast<const float4 *>(&st.c[t][4 * (q + 4 * i)]);
-        s[2 * i] = fma2(w2, pack2(b.x, b.y), mul2(d2, s[2 * i]));
-        s[2 * i + 1] = fma2(w2, pack2(b.z, b.w), mul2(d2, s[2 * i + 1]));
-        acc0 = fma2(s[2 * i], pack2(c.x, c.y), acc0);
-        acc1 = fma2(s[2 * i + 1], pack2(c.z, c.w), acc1);
+      for (int r = 0; r < 4; ++r) {
+        const float w = d.x * xs[r];
+        const f2 ww = pack2(w, w);
+        f2 acc = pack2(0.f, 0.f);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          s[r][i] = fma2(ww, bb[i], mul2(da, s[r][i]));
+          acc = fma2(s[r][i], cc[i], acc);
+        }
+        float lo, hi;
+        unpack2(acc, lo, hi);
+        v[r] = lo + hi;
       }
-      float y0, y1, y2, y3;
-      unpack2(acc0, y0, y1);
-      unpack2(acc1, y2, y3);
-      float y = (y0 + y1) + (y2 + y3);
-      y += __shfl_xor_sync(0xffffffffu, y, 1);
+      // the 16 lanes' sums: two rows are handed over, then one
+      const bool up = lane & 8;
+      const float a0 = (up ? v[2] : v[0]) + __shfl_xor_sync(0xffffffffu, up ? v[0] : v[2], 8);
+      const float a1 = (up ? v[3] : v[1]) + __shfl_xor_sync(0xffffffffu, up ? v[1] : v[3], 8);
+      const bool up2 = lane & 4;
+      float y = (up2 ? a1 : a0) + __shfl_xor_sync(0xffffffffu, up2 ? a0 : a1, 4);
       y += __shfl_xor_sync(0xffffffffu, y, 2);
-      if (q == 0 && live) a.y[((size_t)(pc.begin + t0 + t) * a.H + h) * a.P + row] = fmaf(D, x, y);
+      y += __shfl_xor_sync(0xffffffffu, y, 1);
+      if (write) yg[(size_t)(t0 + t) * a.H * a.P] = fmaf(D, m.x[t][out], y);
     }
   }
-  if (live && (len > 0 || !pc.resume)) {
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      float4 v;
-      unpack2(s[2 * i], v.x, v.y);
-      unpack2(s[2 * i + 1], v.z, v.w);
-      *reinterpret_cast<float4 *>(Sg + 4 * (q + 4 * i)) = v;
-    }
-  }
+  for (int r = 0; r < 4; ++r)
+    if (row0 + mine + r < a.P)
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        float4 v;
+        unpack2(s[r][2 * i], v.x, v.y);
+        unpack2(s[r][2 * i + 1], v.z, v.w);
+        *reinterpret_cast<float4 *>(Sg + r * kCols + 64 * i) = v;
+      }
 }
 
 // The bookkeeping of a context after a prefill: one thread a sequence looks for the prompt that names it.
@@ -144,22 +184,21 @@ __global__ void prefill_meta_kernel(Prompts pr, const int4 *meta_in, int4 *meta_
   meta_out[b] = o;
 }
 
-template <typename TI>
-cudaError_t launch_scan_t(const ScanArgs &a, const Prompts &pr, int num_sms, cudaStream_t stream) {
-  const int pieces = prompt_pieces(pr.total, pr.nseq, a.piece_len);
-  // 64 rows a block share one staging of B and C; 16 rows give four times the blocks when heads and prompts are few
-  if ((long long)pieces * a.H >= num_sms || a.P <= 16) {
-    scan_kernel<TI, 64><<<dim3(pieces, a.H, (a.P + 63) / 64), 256, 0, stream>>>(a, pr);
-  } else {
-    scan_kernel<TI, 16><<<dim3(pieces, a.H, (a.P + 15) / 16), 64, 0, stream>>>(a, pr);
-  }
+template <int R>
+cudaError_t launch_rows(const ScanArgs &a, const Prompts &pr, int pieces, cudaStream_t stream) {
+  scan_kernel<R><<<dim3(pieces, a.H, (a.P + R - 1) / R), 4 * R, 0, stream>>>(a, pr);
   return cudaGetLastError();
 }
 
 }  // namespace
 
 cudaError_t launch_scan(const ScanArgs &a, const Prompts &pr, int num_sms, cudaStream_t stream) {
-  return launch_scan_t<float>(a, pr, num_sms, stream);
+  const int pieces = prompt_pieces(pr.total, pr.nseq, a.piece_len);
+  // All 64 rows a block share one staging of B and C; 8 rows, one warp, spread few heads and prompts over the SMs.
+  const long long heads = (long long)pieces * a.H;
+  if (heads >= 2LL * num_sms) return launch_rows<64>(a, pr, pieces, stream);
+  if (heads * 2 >= num_sms) return launch_rows<16>(a, pr, pieces, stream);
+  return launch_rows<8>(a, pr, pieces, stream);
 }
 
 cudaError_t launch_prefill_meta(const Prompts &pr, const int4 *meta_in, int4 *meta_out, unsigned char *skip, int H,
