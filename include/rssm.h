@@ -196,7 +196,9 @@ rssm_status rssm_flush(rssm_ctx *ctx, const unsigned char *mask, rssm_stream str
  * inputs have the leading dimension [total] and no padding.  A prompt may be empty.  Rows of no prompt are neither
  * read into a result nor written.  Prompt i belongs to sequence slots[i] of the state (i itself without slots); other
  * sequences keep theirs.
- * If any offset or slot is out of range nothing is written at all; prompts that share a slot are left out. */
+ * If any offset or slot is out of range nothing is written at all; prompts that share a slot are left out.
+ * Kernels are chosen by total and nseq, so a prompt's results can differ in their last bits with the company it is in;
+ * the same call gives the same bits. */
 typedef struct {
   int total, nseq;              /* tokens in all, prompts; total >= 0, nseq >= 1 */
   const int *offsets;           /* device [nseq + 1], non-decreasing within 0..total */
