@@ -153,7 +153,12 @@ __global__ void __launch_bounds__(128, 4) scan_mma_kernel(ScanArgs a, Prompts pr
 #pragma unroll
       for (int r = 0; r < 2; ++r) {
         const float rise = exp2_ftz(lA * cj[r]);
-        y[0][2 * r] *= rise; y[0][2 * r + 1] *= rise; y[1][2 * r] *= rise; y[1][2 * r + 1] *= rise;
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {  // D x in fp32: on M's diagonal it would be cut like M
+          const uint32_t x = *reinterpret_cast<const uint32_t *>(m.x + (g + 8 * r) * kPitchX + 2 * (p0 + 8 * i + 2 * t));
+          y[i][2 * r] = fmaf(D, __uint_as_float(x << 16), y[i][2 * r] * rise);
+          y[i][2 * r + 1] = fmaf(D, __uint_as_float(x & 0xffff0000u), y[i][2 * r + 1] * rise);
+        }
 #pragma unroll
         for (int half = 0; half < 2; ++half) {
           float v[2];
@@ -161,7 +166,7 @@ __global__ void __launch_bounds__(128, 4) scan_mma_kernel(ScanArgs a, Prompts pr
           for (int e = 0; e < 2; ++e) {
             const int i = 2 * half + e, col = 2 * t + e + 8 * half, row = g + 8 * r;
             const float w = G[half][2 * r + e] * (exp2_ftz(lA * (cj[r] - ci[i])) * di[i]);
-            v[e] = col < row ? w : col == row ? w + D : 0.f;
+            v[e] = col <= row ? w : 0.f;
           }
           cut2(pack2(v[0], v[1]), hi[r + 2 * half], lo[r + 2 * half]);
         }

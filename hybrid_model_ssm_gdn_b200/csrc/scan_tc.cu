@@ -3,8 +3,8 @@
 // Chunks of Q = 128 tokens turn the recurrence into matrix products.  With c_j the sum of dt over the chunk's tokens up
 // to j (included), per head:
 //   G   = C B^T                                          tokens x tokens, one for all heads of a group
-//   M   = [j >= i] G_ji exp(A (c_j - c_i)) dt_i + D [j = i]
-//   Y   = M X + diag(exp(A c)) C S^T                      tokens x P
+//   M   = [j >= i] G_ji exp(A (c_j - c_i)) dt_i
+//   Y   = M X + diag(exp(A c)) C S^T + D X                tokens x P
 //   S  <- exp(A c_Q) S + (diag(exp(A (c_Q - c)) dt) X)^T B   P x 128
 // A block carries two heads of one group (2 x 64 rows of state fill the 128 lanes of tensor memory) along one piece of a
 // prompt, chunk after chunk, so the state never leaves the chip.
@@ -298,7 +298,6 @@ __global__ void __launch_bounds__(kTcThreads, 1)
       constexpr int step = kTile >> 4;
       for (int c = 0; c < chunks; ++c) {
         const int s = c & 1;
-        const bool carried = c > 0 || init != nullptr;
         wait(sh.full_B[s], c >> 1);
         wait(sh.full_C, c);
         tm_fence_after();
@@ -317,8 +316,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
           for (int p = 0; p < 2; ++p)
 #pragma unroll
             for (int k = 0; k < 8; ++k)
-              mma_ts(tm + kColY + 64 * h, tm + kColM + 64 * p + 8 * k, dX + h * step + 128 * k, shape_y,
-                     carried || p > 0 || k > 0);
+              mma_ts(tm + kColY + 64 * h, tm + kColM + 64 * p + 8 * k, dX + h * step + 128 * k, shape_y, true);
           mma_commit(h ? &sh.y2_done : &sh.y20_done);
         }
       }
@@ -461,7 +459,6 @@ __global__ void __launch_bounds__(kTcThreads, 1)
               }
             } else {
               // the block on the diagonal: its columns' tokens are this warp's rows
-              const float D = h ? D1 : D0;
 #pragma unroll
               for (int k = 0; k < 16; k += 4) {
                 const float4 ci = *reinterpret_cast<const float4 *>(&sh.cl[h][32 * i + 16 * g + k]);
@@ -472,7 +469,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                 for (int j = 0; j < 4; ++j) {
                   const int col = 16 * g + k + j;
                   const float v = __uint_as_float(G[k + j]) * (exp2_approx(lA * (cl - cs[j])) * ds[j]);
-                  m[j] = col < lane ? v : col == lane ? v + D : 0.f;
+                  m[j] = col <= lane ? v : 0.f;
                 }
                 cut2(pack2(m[0], m[1]), hi[k / 2], lo[k / 2]);
                 cut2(pack2(m[2], m[3]), hi[k / 2 + 1], lo[k / 2 + 1]);
@@ -482,24 +479,37 @@ __global__ void __launch_bounds__(kTcThreads, 1)
             tm_st8(tm + lanes + kColM + 64 + 16 * i + 8 * g, lo);
           }
           if (h == 0) {
-            // diag(exp(A c)) C S^T in place, before M X is added; this warp's half of the columns is head g
+            // diag(exp(A c)) C S^T + D X in place, before M X is added; this warp's half of the columns is head g.
+            // D X stays fp32: on M's diagonal, D would be cut like M and lose 2^-17 of what is often most of y.
             float sum = sh.cl[g][row];
 #pragma unroll
             for (int i = 0; i < 3; ++i) sum += i < q ? sh.tot[b][g][i] : 0.f;
             const float rise = exp2_approx((g ? lA1 : lA0) * sum);
-            const f2 rise2 = pack2(rise, rise);
+            const f2 rise2 = pack2(rise, rise), D2 = g ? pack2(D1, D1) : pack2(D0, D0);
+            wait(sh.full_X, c);
             wait(sh.y1_done, c);
             tm_fence_after();
-            if (c > 0 || init != nullptr) {
 #pragma unroll 1
-              for (int part = 0; part < 2; ++part) {
-                uint32_t v[32];
+            for (int part = 0; part < 2; ++part) {
+              uint32_t v[32] = {};
+              if (c > 0 || init != nullptr) {
                 tm_ld32(tm + lanes + kColY + 64 * g + 32 * part, v);
                 tm_wait_ld();
-#pragma unroll
-                for (int i = 0; i < 32; i += 2) scale2(v[i], v[i + 1], rise2);
-                tm_st32(tm + lanes + kColY + 64 * g + 32 * part, v);
               }
+#pragma unroll
+              for (int i = 0; i < 4; ++i) {
+                const uint4 x = *reinterpret_cast<const uint4 *>(sh.X[g] + row * 128 + ((4 * part + i) ^ (row & 7)) * 16);
+                const uint32_t xs[4] = {x.x, x.y, x.z, x.w};
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                  uint32_t &lo = v[8 * i + 2 * j], &hi = v[8 * i + 2 * j + 1];
+                  float y0, y1;
+                  unpack2(fma2(pack2(xs[j] << 16, xs[j] & 0xffff0000u), D2, mul2(pack2(lo, hi), rise2)), y0, y1);
+                  lo = __float_as_uint(y0);
+                  hi = __float_as_uint(y1);
+                }
+              }
+              tm_st32(tm + lanes + kColY + 64 * g + 32 * part, v);
             }
           }
           tm_wait_st();
