@@ -448,13 +448,14 @@ static int scan_piece_len(const rssm_config &c, int total, int nseq, int num_sms
 }
 
 static rssm_status run_scan(const rssm_config &c, const Prompts &p, const rssm_tokens *tok, float *S, float *y,
-                            void *work, size_t work_bytes, int *err, long long wait_cycles, int num_sms, cudaStream_t st) {
+                            void *work, size_t work_bytes, int *err, long long wait_cycles, int withhold, int num_sms,
+                            cudaStream_t st) {
   if (c.nheads > 65535) return RSSM_ERR_SHAPE;  // one grid row a head
   ScanArgs a{};
   a.H = c.nheads; a.P = c.headdim; a.G = c.ngroups;
   a.piece_len = scan_piece_len(c, p.total, p.nseq, num_sms);
   a.x = tok->x; a.Bin = tok->B; a.C = tok->C; a.dt = tok->dt; a.A = c.A; a.D = c.D; a.S = S; a.y = y;
-  a.work = work; a.err = err; a.wait_cycles = wait_cycles;
+  a.work = work; a.err = err; a.wait_cycles = wait_cycles; a.withhold = withhold;
   if (a.piece_len <= p.total) {
     if (!work || ((uintptr_t)work & 255u)) return RSSM_ERR_ARG;
     if (work_bytes < scan_tc_workspace(a.H, a.P, prompt_pieces(p.total, p.nseq, a.piece_len), nullptr))
@@ -499,8 +500,8 @@ rssm_status rssm_mamba2_scan(const rssm_config *cfg, const rssm_prompts *pr, con
   int sms = 0;
   s = sm_count(&sms);
   if (s != RSSM_OK) return s;
-  return run_scan(*cfg, device_prompts(pr, cfg->batch, nullptr), tok, S, y, work, work_bytes, nullptr, kWaitCycles, sms,
-                  reinterpret_cast<cudaStream_t>(stream));
+  return run_scan(*cfg, device_prompts(pr, cfg->batch, nullptr), tok, S, y, work, work_bytes, nullptr, kWaitCycles, -1,
+                  sms, reinterpret_cast<cudaStream_t>(stream));
 }
 
 rssm_status rssm_mamba2_prefill(rssm_ctx *x, const rssm_prompts *pr, const rssm_tokens *tok, float *y, void *work,
@@ -513,7 +514,8 @@ rssm_status rssm_mamba2_prefill(rssm_ctx *x, const rssm_prompts *pr, const rssm_
   cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
   const Prompts p = device_prompts(pr, x->cfg.batch, meta_cur(x));
   s = run_scan(x->cfg, p, tok, reinterpret_cast<float *>(x->arena + x->lay.hp), y, work, work_bytes, err_word(x),
-               x->wait_cycles, x->num_sms, st);
+               x->wait_cycles, x->withhold, x->num_sms, st);
+  x->withhold = -1;  // the test hook fires on one launch only
   if (s != RSSM_OK) return s;
   unsigned char *skip = x->cfg.skip_tau > 0.f ? x->arena + x->lay.skip : nullptr;
   const cudaError_t e = launch_prefill_meta(p, meta_cur(x), meta_next(x), skip, x->cfg.nheads, err_word(x), st);

@@ -114,6 +114,7 @@ struct ScanArgs {
   void *work;                       // piece states, where prompts are cut (piece_len <= total)
   int *err;                         // error word, may be null
   long long wait_cycles;            // bound of the tensor-core kernel's waits
+  int withhold;                     // test hook: no block loads X of this chunk (-1: off)
 };
 // short prompts: bf16 inputs, prompts not cut
 cudaError_t launch_scan_mma(const ScanArgs &a, const Prompts &pr, cudaStream_t stream);

@@ -18,8 +18,8 @@
 //
 // Tensor memory (512 columns): S 128 (row = head and p, column = n), Y 128 (row = token, column = head and p), G 128, and
 // M as hi | lo pairs 128, for one head after the other; M is the left operand straight from tensor memory.  Shared
-// memory: C, X, two stages of B, and one 64 KB buffer that holds the pieces of S until C S^T is done and then the pieces
-// of the weighted X; 192 KB in all, so one block an SM.
+// memory: C, three buffers for B and X, a stage for Y, and one 64 KB buffer that holds the pieces of S until C S^T is done and then the pieces
+// of the weighted X; all of an SM's, so one block each.
 //
 // Decays never divide and never exceed what they stand for: a token's weight is a product of exp of sums of dt over
 // tokens between, by blocks of 32: within the row's block exp(A (c_j - c_i)), else exp(A (c_j - end)) exp(A (end - c_i))
@@ -50,22 +50,28 @@ constexpr int kByLength = 64;
 // 227 KB to the last few bytes, and tiles start on 1024-byte boundaries: there is no static shared memory in this
 // file's kernels, so the block's dynamic part starts aligned (checked).
 struct TcShared {
-  unsigned char C[2][kTile];        // K-major, halves of n
-  unsigned char X[2][kTile];        // token rows, per head
-  unsigned char B[2][2][kTile];     // stages, halves of n
+  unsigned char in[4][2][kTile];    // 0: C (halves of n); the others B (halves of n) and X (token rows, per head)
   unsigned char U[4][kTile];        // S pieces: hi, lo x halves of n; weighted X pieces: hi, lo x heads
   unsigned char Y[8][4096];         // Y on its way out: 32 tokens by 32 columns a warp
   float cl[2][Q];                   // sum of dt within the token's block of 32, included  (head, token)
   float e[2][Q];                    // exp(A (end of block - c_i)) dt_i
   __nv_bfloat16 dt[2][Q];
   float tot[2][2][4];               // sums of the blocks of 32 (chunk parity, head, block)
-  uint64_t full_C, full_X, full_B[2], tab_full, tab_free, tot_full;
-  uint64_t g_done, y1_done, y20_done, y2_done, y_free, s_done[2], sp_ready[2], m_ready[2], xs_ready[2], drained[2];
+  uint64_t full_C, full_X[2], full_B[2], tab_full, tab_free, tot_full;
+  uint64_t g_done, y1_done, y20_done, y2_done[2], y_free, s_done[2], sp_ready[2], m_ready[2], xs_ready[2], drained[2];
   uint32_t tmem;
   int abort, found;
 };
 constexpr int kTcSmem = (int)sizeof(TcShared);
 static_assert(kTcSmem <= 227 * 1024, "shared memory of a block");
+
+// The buffers of a chunk's B and X: B(0), X(0), B(1), X(1), ... take three in turn, so that X of a chunk follows B of the
+// chunk before, free when that chunk's state is done, and B follows X of two chunks before.  Without outputs there is no C:
+// its buffer is a fourth, and both have two of their own.
+template <bool kState>
+__device__ __forceinline__ int buffer_B(int c) { return kState ? 1 + (c & 1) : 1 + 2 * c % 3; }
+template <bool kState>
+__device__ __forceinline__ int buffer_X(int c) { return kState ? 3 * (c & 1) : 1 + (2 * c + 1) % 3; }
 
 struct TcArgs {
   int H, P, G, pairs;       // pairs of heads in a group
@@ -79,6 +85,7 @@ struct TcArgs {
   float *seg_dt;            // their sums of dt [pieces][H]
   int *err;                 // may be null
   long long wait_cycles;
+  int withhold;             // test hook: no block loads X of this chunk (-1: off)
 };
 
 __device__ __forceinline__ void scale2(uint32_t &a, uint32_t &b, f2 by) {
@@ -99,6 +106,19 @@ struct Waiter {
     if (!mbar_wait_or_abort(&bar, phase & 1, &sh->abort, ws)) {
       *(volatile int *)&sh->abort = 1;
       if (err) record_error(err, seq, RSSM_DEV_TIMEOUT);
+    }
+  }
+  // by a whole warp, whose lanes stay together
+  __device__ __forceinline__ void warp(uint64_t &bar, int phase) const {
+    if (__all_sync(0xffffffffu, mbar_try_wait(&bar, phase & 1, ws.hint_ns))) return;
+    const long long t0 = clock64();
+    while (!__all_sync(0xffffffffu, mbar_try_wait(&bar, phase & 1, ws.hint_ns))) {
+      const bool late = clock64() - t0 > ws.limit;
+      if (late) {
+        *(volatile int *)&sh->abort = 1;
+        if (err) record_error(err, seq, RSSM_DEV_TIMEOUT);
+      }
+      if (__any_sync(0xffffffffu, late || *(volatile int *)&sh->abort)) return;
     }
   }
 };
@@ -170,8 +190,8 @@ __global__ void __launch_bounds__(kTcThreads, 1)
   const int t0 = pc.begin + pc.first;
 
   if (tid == 0) {
-    uint64_t *one[] = {&sh.full_C, &sh.full_X, &sh.full_B[0], &sh.full_B[1], &sh.tab_full, &sh.tot_full, &sh.g_done, &sh.y1_done,
-                       &sh.y20_done, &sh.y2_done, &sh.s_done[0], &sh.s_done[1], &sh.drained[0],
+    uint64_t *one[] = {&sh.full_C, &sh.full_X[0], &sh.full_X[1], &sh.full_B[0], &sh.full_B[1], &sh.tab_full, &sh.tot_full, &sh.g_done, &sh.y1_done,
+                       &sh.y20_done, &sh.y2_done[0], &sh.y2_done[1], &sh.s_done[0], &sh.s_done[1], &sh.drained[0],
                        &sh.drained[1]};
     for (uint64_t *b : one) mbar_init(b, 1);
     uint64_t *team[] = {&sh.y_free, &sh.sp_ready[0], &sh.sp_ready[1], &sh.m_ready[0],
@@ -191,136 +211,124 @@ __global__ void __launch_bounds__(kTcThreads, 1)
   if (warp == kWarpLoad) {
     if (lane == 0) {
       for (int c = 0; c < chunks; ++c) {
-        const int t = t0 + c * Q;
-        if (c > 1) wait(sh.s_done[c & 1], (c - 2) >> 1);
-        mbar_arrive_expect_tx(&sh.full_B[c & 1], 2 * kTile);
-        tma_load_2d(sh.B[c & 1][0], &map_B, group * kCols, t, &sh.full_B[c & 1]);
-        tma_load_2d(sh.B[c & 1][1], &map_B, group * kCols + 64, t, &sh.full_B[c & 1]);
+        const int t = t0 + c * Q, s = c & 1;
+        unsigned char *b = sh.in[buffer_B<kState>(c)][0], *x = sh.in[buffer_X<kState>(c)][0];
+        if (c > 1) {  // with outputs, that chunk's state was waited for with the last X
+          if (kState) wait(sh.s_done[s], (c - 2) >> 1);
+          else wait(sh.y2_done[s], (c - 2) >> 1);
+        }
+        mbar_arrive_expect_tx(&sh.full_B[s], 2 * kTile);
+        tma_load_2d(b, &map_B, group * kCols, t, &sh.full_B[s]);
+        tma_load_2d(b + kTile, &map_B, group * kCols + 64, t, &sh.full_B[s]);
         if (!kState) {
           if (c > 0) {
             wait(sh.y1_done, c - 1);
             wait(sh.g_done, c - 1);
           }
           mbar_arrive_expect_tx(&sh.full_C, 2 * kTile);
-          tma_load_2d(sh.C[0], &map_C, group * kCols, t, &sh.full_C);
-          tma_load_2d(sh.C[1], &map_C, group * kCols + 64, t, &sh.full_C);
+          tma_load_2d(sh.in[0][0], &map_C, group * kCols, t, &sh.full_C);
+          tma_load_2d(sh.in[0][1], &map_C, group * kCols + 64, t, &sh.full_C);
         }
-        if (kState) {  // C's buffer is the second one for X; the wait above has freed either
-          uint64_t &full = c & 1 ? sh.full_C : sh.full_X;
-          unsigned char *x = c & 1 ? sh.C[0] : sh.X[0];
-          mbar_arrive_expect_tx(&full, 2 * kTile);
-          tma_load_3d(x, &map_x, 0, h0, t, &full);
-          tma_load_3d(x + kTile, &map_x, 0, h1, t, &full);
-          continue;
-        }
-        if (c > 0) {
-          wait(sh.xs_ready[1], c - 1);
-          wait(sh.y2_done, c - 1);
-        }
-        mbar_arrive_expect_tx(&sh.full_X, 2 * kTile);
-        tma_load_3d(sh.X[0], &map_x, 0, h0, t, &sh.full_X);
-        tma_load_3d(sh.X[1], &map_x, 0, h1, t, &sh.full_X);
-        if (c + 1 < chunks) {  // X has one buffer: have the next chunk's in L2
-          tma_prefetch_3d(&map_x, 0, h0, t + Q);
-          tma_prefetch_3d(&map_x, 0, h1, t + Q);
-        }
+        if (!kState && c > 0) wait(sh.s_done[1 - s], (c - 1) >> 1);
+        mbar_arrive_expect_tx(&sh.full_X[s], 2 * kTile);
+        if (c == a.withhold) continue;  // test hook: this chunk's X never comes
+        tma_load_3d(x, &map_x, 0, h0, t, &sh.full_X[s]);
+        tma_load_3d(x + kTile, &map_x, 0, h1, t, &sh.full_X[s]);
       }
       if (*(volatile int *)&sh.abort) {  // otherwise every load has been consumed when the block ends
-        if (kState) {
-          mbar_wait(chunks & 1 ? &sh.full_X : &sh.full_C, ((chunks - 1) >> 1) & 1, wait.ws);
-          if (chunks > 1) mbar_wait(chunks & 1 ? &sh.full_C : &sh.full_X, ((chunks - 2) >> 1) & 1, wait.ws);
-        } else {
-          mbar_wait(&sh.full_C, (chunks - 1) & 1, wait.ws);
-          mbar_wait(&sh.full_X, (chunks - 1) & 1, wait.ws);
+        if (!kState) mbar_wait(&sh.full_C, (chunks - 1) & 1, wait.ws);
+        for (int c = chunks > 1 ? chunks - 2 : 0; c < chunks; ++c) {
+          mbar_wait(&sh.full_X[c & 1], (c >> 1) & 1, wait.ws);
+          mbar_wait(&sh.full_B[c & 1], (c >> 1) & 1, wait.ws);
         }
-        mbar_wait(&sh.full_B[(chunks - 1) & 1], ((chunks - 1) >> 1) & 1, wait.ws);
-        if (chunks > 1) mbar_wait(&sh.full_B[chunks & 1], ((chunks - 2) >> 1) & 1, wait.ws);
       }
     }
     __syncwarp();
-  } else if (warp == kWarpState) {
-    if (lane == 0) {
+  } else if (warp == kWarpState || warp == kWarpToken) {
+    // The products: the whole warp goes through the steps, on values the compiler knows to be the same in every lane.
+    const uint32_t leader = lane == 0, td = __shfl_sync(0xffffffffu, tm, 0);
+    const int n = __shfl_sync(0xffffffffu, chunks, 0), rest = __shfl_sync(0xffffffffu, ntok, 0) - (n - 1) * Q;
+    const uint32_t started = __shfl_sync(0xffffffffu, init != nullptr, 0), ends = __shfl_sync(0xffffffffu, final != nullptr, 0);
+    const uint32_t dC = tile_desc(sh.in[0][0], 16);
+    constexpr int step = kTile >> 4;
+    if (warp == kWarpState) {
       constexpr uint32_t shape_y = mma_shape(128, 128, false, false), shape_s = mma_shape(128, 128, true, true);
-      const uint32_t dC = tile_desc(sh.C[0], 16), dSp = tile_desc(sh.U[0], 16);        // K-major
-      const uint32_t dXs = tile_desc(sh.U[0], kTile), dB = tile_desc(sh.B[0][0], kTile);  // MN-major, two tiles
-      constexpr int step = kTile >> 4;
-      for (int c = 0; c < chunks; ++c) {
+      const uint32_t dSp = tile_desc(sh.U[0], 16);                                        // K-major
+      const uint32_t dXs = tile_desc(sh.U[0], kTile), dB = tile_desc(sh.in[0][0], kTile);  // MN-major, two tiles
+      for (int c = 0; c < n; ++c) {
         const int s = c & 1;
-        const bool carried = c > 0 || init != nullptr;
+        const uint32_t carried = c > 0 || started;
         if (!kState) {
-          wait(sh.full_C, c);
-          if (c > 0) wait(sh.y_free, c - 1);
-#pragma unroll 1
+          wait.warp(sh.full_C, c);
+          if (c > 0) wait.warp(sh.y_free, c - 1);
+#pragma unroll
           for (int part = 0; part < 2; ++part) {  // columns n of S as their pieces arrive: 32 of each half
-            wait(sh.sp_ready[part], c);
+            wait.warp(sh.sp_ready[part], c);
             tm_fence_after();
             if (carried) {
-#pragma unroll 1
+#pragma unroll
               for (int p = 0; p < 2; ++p)
 #pragma unroll
                 for (int k = 0; k < 4; ++k) {
                   const int at = (k >> 1) * step + 2 * (k & 1) + 4 * part;
-                  mma_ss(tm + kColY, dC + at, dSp + 2 * p * step + at, shape_y, part > 0 || p > 0 || k > 0);
+                  mma_ss(td + kColY, dC + at, dSp + 2 * p * step + at, shape_y, part > 0 || p > 0 || k > 0, leader);
                 }
             }
           }
-          mma_commit(&sh.y1_done);
+          mma_commit(&sh.y1_done, leader);
         } else {
-          wait(sh.sp_ready[0], c);
-          wait(sh.sp_ready[1], c);
+          wait.warp(sh.sp_ready[0], c);
+          wait.warp(sh.sp_ready[1], c);
         }
-        wait(sh.full_B[s], c >> 1);
-#pragma unroll 1
+        wait.warp(sh.full_B[s], c >> 1);
+#pragma unroll
         for (int part = 0; part < 2; ++part) {  // tokens as their weighted X arrives
-          wait(sh.xs_ready[part], c);
+          wait.warp(sh.xs_ready[part], c);
           tm_fence_after();
-          if (c + 1 < chunks || final) {
-#pragma unroll 1
+          if (c + 1 < n || ends) {
+#pragma unroll
             for (int p = 0; p < 2; ++p)
 #pragma unroll
               for (int k = 0; k < 4; ++k) {  // 16 token rows are 2048 bytes
                 const int at = 128 * (4 * part + k);
-                mma_ss(tm + kColS, dXs + 2 * p * step + at, dB + 2 * s * step + at, shape_s,
-                       carried || part > 0 || p > 0 || k > 0);
+                mma_ss(td + kColS, dXs + 2 * p * step + at, dB + 2 * buffer_B<kState>(c) * step + at, shape_s,
+                       part > 0 || p > 0 || k > 0 ? 1u : carried, leader);
               }
           }
         }
-        mma_commit(&sh.s_done[s]);
+        mma_commit(&sh.s_done[s], leader);
       }
-      mma_commit(&sh.drained[0]);
+      mma_commit(&sh.drained[0], leader);
       mbar_wait(&sh.drained[0], 0, wait.ws);
-    }
-    __syncwarp();
-  } else if (warp == kWarpToken) {
-    if (!kState && lane == 0) {
+    } else if (!kState) {
       constexpr uint32_t shape_g = mma_shape(128, 128, false, false), shape_y = mma_shape(128, 64, false, true);
-      const uint32_t dC = tile_desc(sh.C[0], 16), dB = tile_desc(sh.B[0][0], 16), dX = tile_desc(sh.X[0], 16);
-      constexpr int step = kTile >> 4;
-      for (int c = 0; c < chunks; ++c) {
-        const int s = c & 1;
-        wait(sh.full_B[s], c >> 1);
-        wait(sh.full_C, c);
+      const uint32_t dB = tile_desc(sh.in[0][0], 16);
+      for (int c = 0; c < n; ++c) {
+        wait.warp(sh.full_B[c & 1], c >> 1);
+        wait.warp(sh.full_C, c);
         tm_fence_after();
+        const uint32_t b = dB + 2 * buffer_B<kState>(c) * step, x = dB + 2 * buffer_X<kState>(c) * step;
 #pragma unroll
-        for (int k = 0; k < 8; ++k)
-          mma_ss(tm + kColG, dC + (k >> 2) * step + 2 * (k & 3), dB + (2 * s + (k >> 2)) * step + 2 * (k & 3), shape_g,
-                 k > 0);
-        mma_commit(&sh.g_done);
-        wait(sh.full_X, c);
-        if (ntok - c * Q < Q) wait(sh.xs_ready[0], c);  // the rows behind the prompt's end have been cleared
-#pragma unroll 1
+        for (int k = 0; k < 8; ++k) {
+          const int at = (k >> 2) * step + 2 * (k & 3);
+          mma_ss(td + kColG, dC + at, b + at, shape_g, k > 0, leader);
+        }
+        mma_commit(&sh.g_done, leader);
+        wait.warp(sh.full_X[c & 1], c >> 1);
+        if (c + 1 == n && rest < Q) wait.warp(sh.xs_ready[0], c);  // the rows behind the prompt's end have been cleared
+#pragma unroll
         for (int h = 0; h < 2; ++h) {
-          wait(sh.m_ready[h], c);
+          wait.warp(sh.m_ready[h], c);
           tm_fence_after();
-#pragma unroll 1
+#pragma unroll
           for (int p = 0; p < 2; ++p)
 #pragma unroll
             for (int k = 0; k < 8; ++k)
-              mma_ts(tm + kColY + 64 * h, tm + kColM + 64 * p + 8 * k, dX + h * step + 128 * k, shape_y, true);
-          mma_commit(h ? &sh.y2_done : &sh.y20_done);
+              mma_ts(td + kColY + 64 * h, td + kColM + 64 * p + 8 * k, x + h * step + 128 * k, shape_y, 1, leader);
+          mma_commit(h ? &sh.y2_done[c & 1] : &sh.y20_done, leader);
         }
       }
-      mma_commit(&sh.drained[1]);
+      mma_commit(&sh.drained[1], leader);
       mbar_wait(&sh.drained[1], 0, wait.ws);
     }
     __syncwarp();
@@ -486,7 +494,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
             for (int i = 0; i < 3; ++i) sum += i < q ? sh.tot[b][g][i] : 0.f;
             const float rise = exp2_approx((g ? lA1 : lA0) * sum);
             const f2 rise2 = pack2(rise, rise), D2 = g ? pack2(D1, D1) : pack2(D0, D0);
-            wait(sh.full_X, c);
+            wait(sh.full_X[b], c >> 1);
             wait(sh.y1_done, c);
             tm_fence_after();
 #pragma unroll 1
@@ -498,7 +506,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
               }
 #pragma unroll
               for (int i = 0; i < 4; ++i) {
-                const uint4 x = *reinterpret_cast<const uint4 *>(sh.X[g] + row * 128 + ((4 * part + i) ^ (row & 7)) * 16);
+                const uint4 x = *reinterpret_cast<const uint4 *>(sh.in[buffer_X<kState>(c)][g] + row * 128 + ((4 * part + i) ^ (row & 7)) * 16);
                 const uint32_t xs[4] = {x.x, x.y, x.z, x.w};
 #pragma unroll
                 for (int j = 0; j < 4; ++j) {
@@ -518,7 +526,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
           if (lane == 0) mbar_arrive(&sh.m_ready[h]);
         }
         if (lane == 0) mbar_arrive(&sh.tab_free);
-        wait(sh.y2_done, c);
+        wait(sh.y2_done[b], c >> 1);
         tm_fence_after();
         uint32_t Y[2][32];
         tm_ld32(tm + lanes + kColY + 64 * g, Y[0]);
@@ -590,13 +598,13 @@ __global__ void __launch_bounds__(kTcThreads, 1)
     for (int c = 0; c < chunks; ++c) {
       const int b = c & 1, valid = min(Q, ntok - c * Q);
       wait(sh.tab_full, c);
-      wait(kState && b ? sh.full_C : sh.full_X, kState ? c >> 1 : c);
-      unsigned char *const X = (kState && b ? sh.C[0] : sh.X[0]) + g * kTile;
+      wait(sh.full_X[b], c >> 1);
+      unsigned char *const X = sh.in[buffer_X<kState>(c)][g];
       if (valid < Q) {  // rows of the chunk that belong to other prompts must not reach a sum, whatever they hold
         wait(sh.full_B[b], c >> 1);
         for (int i = t128 + valid * 8; i < Q * 8; i += 128) {
           *reinterpret_cast<uint4 *>(X + 16 * i) = make_uint4(0, 0, 0, 0);
-          *reinterpret_cast<uint4 *>(sh.B[b][g] + 16 * i) = make_uint4(0, 0, 0, 0);
+          *reinterpret_cast<uint4 *>(sh.in[buffer_B<kState>(c)][g] + 16 * i) = make_uint4(0, 0, 0, 0);
         }
       }
       if (!kState) wait(sh.y1_done, c);  // the pieces of S have been used
@@ -740,7 +748,7 @@ cudaError_t launch_scan_tc(const ScanArgs &s, const Prompts &pr, cudaStream_t st
   a.pairs = (s.H / s.G + 1) / 2;
   a.piece_len = s.piece_len;
   a.A = s.A; a.D = s.D; a.dt = static_cast<const __nv_bfloat16 *>(s.dt); a.S = s.S; a.y = s.y;
-  a.err = s.err; a.wait_cycles = s.wait_cycles;
+  a.err = s.err; a.wait_cycles = s.wait_cycles; a.withhold = s.withhold;
   const int pieces = prompt_pieces(pr.total, pr.nseq, s.piece_len);
   const bool cut_up = s.piece_len <= pr.total;
   if (cut_up) {

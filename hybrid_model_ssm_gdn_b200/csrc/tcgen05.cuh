@@ -22,10 +22,17 @@ __device__ __forceinline__ void tm_fence_after() { asm volatile("tcgen05.fence::
 __device__ __forceinline__ void tm_wait_ld() { asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory"); }
 __device__ __forceinline__ void tm_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
 
-// arrive on `bar` once every tcgen05 operation this thread has issued so far is complete
-__device__ __forceinline__ void mma_commit(uint64_t *bar) {
-  asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(smem_u32(bar))
-               : "memory");
+// The issuing functions below are called by a whole warp; `leader` is set in the one lane that issues.  Operands of these
+// instructions live in uniform registers: code that only one lane runs moves each of them there for every instruction,
+// which took three times as long as the tensor core (190 cycles a product of 128 x 64 x 16).
+
+// arrive on `bar` once every tcgen05 operation the leader has issued so far is complete
+__device__ __forceinline__ void mma_commit(uint64_t *bar, uint32_t leader) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\tsetp.ne.u32 p, %1, 0;\n\t"
+      "@p tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n\t}" ::"r"(smem_u32(bar)),
+      "r"(leader)
+      : "memory");
 }
 
 // lanes of the warp's quarter (row = lane), N consecutive 32-bit columns from taddr
@@ -76,22 +83,24 @@ __host__ __device__ constexpr uint32_t mma_shape(int M, int N, bool a_mn_major, 
   return (1u << 4) | (1u << 7) | (1u << 10) | ((a_mn_major ? 1u : 0u) << 15) | ((b_mn_major ? 1u : 0u) << 16) |
          ((uint32_t)(N >> 3) << 17) | ((uint32_t)(M >> 4) << 24);
 }
-// d[M x N] (+)= a b over K = 16; one thread issues
-__device__ __forceinline__ void mma_ss(uint32_t d, uint32_t a, uint32_t b, uint32_t shape, bool accumulate) {
+// d[M x N] (+)= a b over K = 16
+__device__ __forceinline__ void mma_ss(uint32_t d, uint32_t a, uint32_t b, uint32_t shape, uint32_t accumulate,
+                                       uint32_t leader) {
   asm volatile(
-      "{\n\t.reg .pred p;\n\t.reg .b64 da, db;\n\tsetp.ne.u32 p, %4, 0;\n\t"
+      "{\n\t.reg .pred p, q;\n\t.reg .b64 da, db;\n\tsetp.ne.u32 p, %4, 0;\n\tsetp.ne.u32 q, %6, 0;\n\t"
       "mov.b64 da, {%1, %5};\n\tmov.b64 db, {%2, %5};\n\t"
-      "tcgen05.mma.cta_group::1.kind::f16 [%0], da, db, %3, p;\n\t}" ::"r"(d),
-      "r"(a), "r"(b), "r"(shape), "r"((uint32_t)accumulate), "r"(kTileDescHigh)
+      "@q tcgen05.mma.cta_group::1.kind::f16 [%0], da, db, %3, p;\n\t}" ::"r"(d),
+      "r"(a), "r"(b), "r"(shape), "r"(accumulate), "r"(kTileDescHigh), "r"(leader)
       : "memory");
 }
 // the same with a in tensor memory: lane = row, 8 columns of bf16 pairs
-__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint32_t b, uint32_t shape, bool accumulate) {
+__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint32_t b, uint32_t shape, uint32_t accumulate,
+                                       uint32_t leader) {
   asm volatile(
-      "{\n\t.reg .pred p;\n\t.reg .b64 db;\n\tsetp.ne.u32 p, %4, 0;\n\t"
+      "{\n\t.reg .pred p, q;\n\t.reg .b64 db;\n\tsetp.ne.u32 p, %4, 0;\n\tsetp.ne.u32 q, %6, 0;\n\t"
       "mov.b64 db, {%2, %5};\n\t"
-      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], db, %3, p;\n\t}" ::"r"(d),
-      "r"(a), "r"(b), "r"(shape), "r"((uint32_t)accumulate), "r"(kTileDescHigh)
+      "@q tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], db, %3, p;\n\t}" ::"r"(d),
+      "r"(a), "r"(b), "r"(shape), "r"(accumulate), "r"(kTileDescHigh), "r"(leader)
       : "memory");
 }
 
@@ -115,6 +124,16 @@ __device__ __forceinline__ void tma_load_3d(void *dst, const void *map, int x, i
 __device__ __forceinline__ void tma_prefetch_3d(const void *map, int x, int y, int z) {
   asm volatile("cp.async.bulk.prefetch.tensor.3d.L2.global.tile [%0, {%1, %2, %3}];" ::"l"(map), "r"(x), "r"(y), "r"(z)
                : "memory");
+}
+
+// move registers between the warps of a block: every warp of a group of four executes it
+template <int N>
+__device__ __forceinline__ void more_registers() {
+  asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N));
+}
+template <int N>
+__device__ __forceinline__ void fewer_registers() {
+  asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N));
 }
 
 // tiled TMA store, tracked by the issuing thread's bulk async-group; coordinates are not negative

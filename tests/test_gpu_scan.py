@@ -270,3 +270,24 @@ def test_workspace_of_the_caller(cuda_ok):
         mamba2_scan(*args, y=y, workspace=work[:1024])
     with pytest.raises(RuntimeError, match="RSSM_ERR_ARG"):
         mamba2_scan(*args, y=y, workspace=work[16:])
+
+
+def test_a_load_that_never_comes_times_out_and_the_context_recovers(cuda_ok, monkeypatch):
+    """Every wait of the 128-token kernel is bounded: with one chunk's load withheld (and the bound shortened to about a
+    millisecond) the launch ends, the context reports it, and after a reload it serves prompts again."""
+    d = make(21, torch.bfloat16, 400, 4, 64, 2, 2)
+    g = on_gpu(d, torch.bfloat16)
+    tok = (g["x"], g["B"], g["C"], g["dt"])
+    monkeypatch.setenv("RSSM_WAIT_CYCLES", "2000000")
+    monkeypatch.setenv("RSSM_WITHHOLD_TILE", "1")
+    layer = context(d, torch.bfloat16, 2)
+    monkeypatch.delenv("RSSM_WITHHOLD_TILE")
+    monkeypatch.delenv("RSSM_WAIT_CYCLES")
+    layer.prefill(*tok, idx([0, 150, 400]))
+    code, seq = layer.get_error()
+    assert code == abi.DEV_TIMEOUT and 0 <= seq < 2
+    layer.load_checkpoint(torch.from_numpy(d["S"]).cuda())
+    y = torch.full((400, 4, 64), 7.0, device="cuda")
+    layer.prefill(*tok, idx([0, 150, 400]), y=y)
+    compare(d, [0, 150, 400], None, None, layer.export(ring=False)["S"].cpu().numpy(), y.cpu().numpy())
+    assert layer.get_error() == (0, -1)
