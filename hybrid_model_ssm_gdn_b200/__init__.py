@@ -160,6 +160,9 @@ class ReplaySSM:
         """Run packed prompts (rssm_mamba2_prefill): x [total][H][P], B, C [total][G][128], dt [total][H];
         offsets int32 [n+1]; slots int32 [n] (sequence of each prompt), resume uint8 [n] -> y fp32 [total][H][P]."""
         H, P, G = self.nheads, self.rows, self.ngroups
+        if self.arena.get_device() != torch._C._cuda_getDevice():
+            raise ValueError(f"the context is on {self.arena.device}, but the current device is "
+                             f"cuda:{torch.cuda.current_device()}")
         total, pr, tok, y = _scan_args(x, B, C_, dt, offsets, slots, resume, y, H, P, G, self.in_dtype)
         work = _scan_work(self.lib, self.cfg, total, pr.nseq, workspace)
         abi.check(self.lib.rssm_mamba2_prefill(self.handle, C.byref(pr), C.byref(tok), _addr(y), _addr(work),
@@ -238,7 +241,7 @@ def _arr(t, dtype, name, shape, optional=False):
         return None
     if t.shape != shape:
         raise ValueError(f"{name}: expected shape {tuple(shape)}, got {tuple(t.shape)}")
-    if t.dtype is not dtype or not t.is_cuda or not t.is_contiguous():
+    if t.dtype is not dtype or not t.is_contiguous() or t.get_device() < 0:
         raise ValueError(f"{name}: expected a contiguous CUDA tensor of {dtype}, got {t.dtype} on {t.device}")
     if t.get_device() != torch._C._cuda_getDevice():
         raise ValueError(f"{name}: on {t.device}, but the current device is cuda:{torch.cuda.current_device()}")
@@ -281,7 +284,7 @@ def _scan_args(x, B, C_, dt, offsets, slots, resume, y, H, P, G, dtype):
     if y is None:
         y = torch.empty(total, H, P, dtype=torch.float32, device=x.device)
     _arr(y, torch.float32, "y", (total, H, P))
-    tok = abi.Tokens(x=x.data_ptr(), B=B.data_ptr(), C=C_.data_ptr(), dt=dt.data_ptr())
+    tok = abi.Tokens(x.data_ptr(), B.data_ptr(), C_.data_ptr(), dt.data_ptr())
     return total, pr, tok, y
 
 
@@ -292,9 +295,10 @@ def _scan_work(lib, cfg, total, nseq, workspace):
     if n.value == 0:
         return None
     if workspace is not None:
-        if not workspace.is_cuda or workspace.dtype != torch.uint8 or not workspace.is_contiguous() or \
-                workspace.numel() < n.value:
-            raise ValueError(f"workspace: expected a contiguous CUDA tensor of uint8 with at least {n.value} elements")
+        if workspace.get_device() != torch._C._cuda_getDevice() or workspace.dtype != torch.uint8 or \
+                not workspace.is_contiguous() or workspace.numel() < n.value:
+            raise ValueError(f"workspace: expected a contiguous tensor of uint8 on the current CUDA device with at least "
+                             f"{n.value} elements")
         return workspace
     return torch.empty(n.value, dtype=torch.uint8, device="cuda")
 
@@ -312,8 +316,8 @@ def mamba2_scan(S, x, B, C_, dt, A, D, offsets, slots=None, resume=None, y=None,
     _arr(A, torch.float32, "A", (H,))
     _arr(D, torch.float32, "D", (H,))
     total, pr, tok, y = _scan_args(x, B, C_, dt, offsets, slots, resume, y, H, P, B.shape[1], dtype)
-    cfg = abi.Config(kind=abi.MAMBA2, batch=S.shape[0], nheads=H, headdim=P, dstate=128, ngroups=B.shape[1], window=1,
-                     in_dtype=_DT[dtype], A=A.data_ptr(), D=D.data_ptr())
+    cfg = abi.Config(abi.MAMBA2, S.shape[0], H, P, 128, B.shape[1], 1, 0, _DT[dtype], abi.HP_F32, abi.READ_SAME, 0, 1.0,
+                     A.data_ptr(), D.data_ptr(), 0.0)
     lib = abi.load()
     work = _scan_work(lib, cfg, total, pr.nseq, workspace)
     abi.check(lib.rssm_mamba2_scan(C.byref(cfg), C.byref(pr), C.byref(tok), _addr(S), _addr(y), _addr(work),
@@ -357,7 +361,7 @@ def _shortconv(hist, cur, x, weight, bias, splits, activation, out, lead):
         raise ValueError(f"splits: expected up to three positive sizes that sum to {ch}, got {splits}")
     if activation is not None and activation != "silu":
         raise ValueError(f"activation: expected None or 'silu', got {activation!r}")
-    if x.shape != (*lead, ch) or not x.is_cuda or x.get_device() != hist.get_device():
+    if x.shape != (*lead, ch) or x.get_device() != hist.get_device():
         raise ValueError(f"x: expected shape {(*lead, ch)} on the current CUDA device, got {tuple(x.shape)} on {x.device}")
     stride = _row_stride(x, lead, ch)
     if out is None:
@@ -416,13 +420,13 @@ def shortconv_commit(hist, cur, accepted, width):
 
 def _rows(t, name, batch, rows, vocab):
     """The row stride of [batch][rows][vocab] probabilities whose rows lie evenly apart."""
-    if t.shape != (batch, rows, vocab) or t.dtype is not torch.float32 or not t.is_cuda or \
+    if t.shape != (batch, rows, vocab) or t.dtype is not torch.float32 or t.get_device() < 0 or \
             t.get_device() != torch._C._cuda_getDevice():
         raise ValueError(f"{name}: expected fp32 of shape {(batch, rows, vocab)} on the current CUDA device, got {t.dtype} "
                          f"of {tuple(t.shape)} on {t.device}")
-    if t.numel() == 0:
+    if t.is_contiguous():
         return vocab
-    ld = t.stride(1) if rows > 1 else (t.stride(0) if batch > 1 else vocab)
+    ld = t.stride(1) if rows > 1 else t.stride(0)
     if t.stride(2) != 1 and vocab > 1 or ld < vocab or (rows > 1 and batch > 1 and t.stride(0) != rows * ld):
         raise ValueError(f"{name}: expected contiguous rows that lie evenly apart, got strides {t.stride()}")
     return ld
@@ -440,12 +444,12 @@ def accept_drafts(target, tokens, u, draft=None, count=None):
     _arr(tokens, torch.int32, "tokens", (batch, T))
     _arr(u, torch.float32, "u", (batch, T + 1))
     _arr(count, torch.int32, "count", (batch,), optional=True)
-    got = torch.empty(3, batch, dtype=torch.int32, device=target.device)
-    accepted, committed, nxt = got[0], got[1], got[2]
+    got = torch.empty((3, batch), dtype=torch.int32, device=target.device)
+    at = got.data_ptr()
     abi.check(abi.load().rssm_accept_drafts(batch, T, vocab, _addr(target), ld_t, _addr(draft), ld_d, _addr(tokens),
-                                            _addr(count), _addr(u), _addr(accepted), _addr(committed), _addr(nxt),
-                                            _raw_stream()), "rssm_accept_drafts")
-    return accepted, committed, nxt
+                                            _addr(count), _addr(u), at, at + 4 * batch, at + 8 * batch, _raw_stream()),
+              "rssm_accept_drafts")
+    return got.unbind(0)
 
 
 # ---------------------------------------------------------------------- comparison kernels

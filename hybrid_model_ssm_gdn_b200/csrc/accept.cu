@@ -13,6 +13,9 @@
 //
 // A cluster of blocks shares a sequence (when there are few, so that one row is read by several SMs); the blocks'
 // totals are exchanged through distributed shared memory.
+//
+// Measured: 256 sequences, vocabulary 131072, with draft rows, 64 us (226 MB, 35 us at the copy bandwidth; DRAM 45 % busy:
+// the draw's dependent steps are what is left); one sequence of 32000 15 us with its launch.
 #include <cooperative_groups.h>
 
 #include "kernels.h"

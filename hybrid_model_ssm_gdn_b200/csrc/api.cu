@@ -416,11 +416,14 @@ static rssm_status scan_validate(const rssm_config *cfg) {
   return c.kind == RSSM_MAMBA2 ? RSSM_OK : RSSM_ERR_UNSUPPORTED;
 }
 
+// (the kernels' token positions, rounded up to tiles, stay below 2^31)
+static bool prompts_size(int total, int nseq, int batch) {
+  return total >= 0 && total <= (1 << 30) && nseq >= 1 && nseq <= batch && (long long)total + nseq <= 0x7fffffffLL;
+}
+
 static rssm_status prompts_validate(const rssm_prompts *pr, int batch) {
   if (!pr || !pr->offsets) return RSSM_ERR_ARG;
-  if (pr->total < 0 || pr->nseq < 1 || pr->nseq > batch) return RSSM_ERR_SHAPE;
-  if ((long long)pr->total + pr->nseq > 0x7fffffffLL) return RSSM_ERR_SHAPE;
-  return RSSM_OK;
+  return prompts_size(pr->total, pr->nseq, batch) ? RSSM_OK : RSSM_ERR_SHAPE;
 }
 
 static Prompts device_prompts(const rssm_prompts *pr, int nslots, const int4 *meta) {
@@ -482,7 +485,7 @@ rssm_status rssm_mamba2_scan_workspace(const rssm_config *cfg, int total, int ns
   rssm_status s = scan_validate(cfg);
   if (s != RSSM_OK) return s;
   if (!bytes) return RSSM_ERR_ARG;
-  if (total < 0 || nseq < 1 || nseq > cfg->batch) return RSSM_ERR_SHAPE;
+  if (!prompts_size(total, nseq, cfg->batch)) return RSSM_ERR_SHAPE;
   int sms = 0;
   s = sm_count(&sms);
   if (s != RSSM_OK) return s;
@@ -545,14 +548,32 @@ static rssm_status shortconv_validate(const rssm_shortconv_config *c, int tokens
   return RSSM_OK;
 }
 
+static int shortconv_esize(const rssm_shortconv_config *c) { return c->in_dtype == RSSM_BF16 ? 2 : 4; }
+
+// whether [out, out + bytes) meets one of `rows` rows of `row` bytes that start `stride` bytes apart from `in`: tokens are
+// loaded ahead of the outputs before them, and a prompt's tiles read rows that are another block's
+static bool overlaps(const void *out, unsigned long long bytes, const void *in, long long rows, unsigned long long row,
+                     unsigned long long stride) {
+  const unsigned long long o = (uintptr_t)out, i = (uintptr_t)in;
+  if (o + bytes <= i) return false;
+  if (o < i) return true;
+  const unsigned long long r = (o - i) / stride;  // the last row that starts at or before `out`
+  if (r >= (unsigned long long)rows) return false;
+  return o < i + r * stride + row || (r + 1 < (unsigned long long)rows && o + bytes > i + (r + 1) * stride);
+}
+
 static rssm_status shortconv_args(const rssm_shortconv_config *c, void *hist, const int *cur, const void *in,
-                                  long long in_stride, void *const out[3], bool rows, ShortConvArgs &a) {
+                                  long long in_stride, void *const out[3], long long rows, ShortConvArgs &a) {
   if (!hist || !aligned16(hist) || !cur || !out) return RSSM_ERR_ARG;
-  if (rows) {
+  if (rows > 0) {
     if (!in || !aligned16(in)) return RSSM_ERR_ARG;
     for (int s = 0; s < 3; ++s)
       if (c->split[s] > 0 && (!out[s] || !aligned16(out[s]))) return RSSM_ERR_ARG;
     if (in_stride < c->channels || in_stride % 8 != 0) return RSSM_ERR_SHAPE;
+    const unsigned long long esz = shortconv_esize(c);
+    for (int s = 0; s < 3; ++s)
+      if (c->split[s] > 0 && overlaps(out[s], rows * c->split[s] * esz, in, rows, c->channels * esz, in_stride * esz))
+        return RSSM_ERR_ARG;
   }
   a.batch = c->batch; a.channels = c->channels; a.width = c->width; a.ring = c->ring; a.silu = c->silu != 0;
   a.weight = c->weight; a.bias = c->bias; a.hist = hist; a.cur = cur; a.in = in; a.in_stride = in_stride;
@@ -563,15 +584,13 @@ static rssm_status shortconv_args(const rssm_shortconv_config *c, void *hist, co
   return RSSM_OK;
 }
 
-static int shortconv_esize(const rssm_shortconv_config *c) { return c->in_dtype == RSSM_BF16 ? 2 : 4; }
-
 rssm_status rssm_shortconv_prefill(const rssm_shortconv_config *cfg, const rssm_prompts *pr, void *hist, const int *cur,
                                    const void *in, long long in_stride, void *const out[3], rssm_stream stream) {
   rssm_status s = shortconv_validate(cfg, 0);
   if (s == RSSM_OK) s = prompts_validate(pr, cfg->batch);
   if (s != RSSM_OK) return s;
   ShortConvArgs a{};
-  s = shortconv_args(cfg, hist, cur, in, in_stride, out, pr->total > 0, a);
+  s = shortconv_args(cfg, hist, cur, in, in_stride, out, pr->total, a);
   if (s != RSSM_OK) return s;
   int sms = 0;
   s = sm_count(&sms);
@@ -586,7 +605,7 @@ rssm_status rssm_shortconv_step(const rssm_shortconv_config *cfg, void *hist, in
   rssm_status s = shortconv_validate(cfg, 1);
   if (s != RSSM_OK) return s;
   ShortConvArgs a{};
-  s = shortconv_args(cfg, hist, cur, in, in_stride, out, true, a);
+  s = shortconv_args(cfg, hist, cur, in, in_stride, out, cfg->batch, a);
   if (s != RSSM_OK) return s;
   a.cur_out = cur;
   int sms = 0;
@@ -603,7 +622,7 @@ rssm_status rssm_shortconv_verify(const rssm_shortconv_config *cfg, int T, void 
   rssm_status s = shortconv_validate(cfg, T);
   if (s != RSSM_OK) return s;
   ShortConvArgs a{};
-  s = shortconv_args(cfg, hist, cur, in, in_stride, out, true, a);
+  s = shortconv_args(cfg, hist, cur, in, in_stride, out, (long long)cfg->batch * T, a);
   if (s != RSSM_OK) return s;
   int sms = 0;
   s = sm_count(&sms);

@@ -36,32 +36,46 @@ __device__ __forceinline__ bool prompt_bad(const Prompts &p, int i) {
   return o0 < 0 || o1 < o0 || o1 > p.total || s < 0 || s >= p.nslots;
 }
 
+// what the owner of a piece leaves for its block, in shared memory
+struct PieceWord {
+  int seq, begin, end, slot, resume;
+};
+
 // Collective over the block; false: nothing to do for this piece (bad prompts, refused slot, number without owner).
-// found: a word of shared memory.
-__device__ __forceinline__ bool find_piece(const Prompts &p, int number, int len, Piece &out, int *found) {
-  if (threadIdx.x == 0) *found = -1;
+// A block can do nothing before it knows its piece, so the loads are one round trip: a thread reads all of its prompt at
+// once, before the first barrier, and the owner hands it on.
+__device__ __forceinline__ bool find_piece(const Prompts &p, int number, int len, Piece &out, PieceWord *word) {
+  int o0 = 0, o1 = 0, s0 = 0, r0 = 0;
+  auto load = [&](int i, int &s, int &r) {
+    o0 = p.off[i];
+    o1 = p.off[i + 1];
+    s = p.slots ? p.slots[i] : i;
+    r = p.resume ? p.resume[i] : 0;
+  };
+  if ((int)threadIdx.x < p.nseq) load(threadIdx.x, s0, r0);
+  if (threadIdx.x == 0) word->seq = -1;
   __syncthreads();
   bool bad = false;
+  int s = s0, r = r0;
   for (int i = threadIdx.x; i < p.nseq; i += blockDim.x) {
-    const int o0 = p.off[i], o1 = p.off[i + 1];
-    const int s = p.slots ? p.slots[i] : i;
+    if (i >= (int)blockDim.x) load(i, s, r);
     bad |= o0 < 0 || o1 < o0 || o1 > p.total || s < 0 || s >= p.nslots;
-    if (!bad && o0 / len + i <= number && number <= o1 / len + i) *found = i;
+    if (!bad && o0 / len + i <= number && number <= o1 / len + i) *word = PieceWord{i, o0, o1, s, r};
   }
   bad = __syncthreads_or(bad);
-  const int i = *found;
-  if (bad || i < 0) return false;
-  out.seq = i;
-  out.begin = p.off[i];
-  out.end = p.off[i + 1];
-  out.slot = p.slots ? p.slots[i] : i;
-  out.index = number - (out.begin / len + i);
+  if (bad || word->seq < 0) return false;
+  out.seq = word->seq;
+  out.begin = word->begin;
+  out.end = word->end;
+  out.slot = word->slot;
+  out.index = number - (out.begin / len + out.seq);
   out.first = out.index * len;
-  out.resume = p.resume && p.resume[i];
+  out.resume = word->resume != 0;
   if (out.resume && p.meta && (p.meta[out.slot].x != 0 || p.meta[out.slot].z != 0)) return false;
   if (p.slots) {  // a slot named twice
     bool twice = false;
-    for (int j = threadIdx.x; j < p.nseq; j += blockDim.x) twice |= j != i && p.slots[j] == out.slot;
+    for (int j = threadIdx.x; j < p.nseq; j += blockDim.x)
+      twice |= j != out.seq && (j < (int)blockDim.x ? s0 : p.slots[j]) == out.slot;
     if (__syncthreads_or(twice)) return false;
   }
   return true;

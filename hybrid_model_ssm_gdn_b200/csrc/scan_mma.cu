@@ -8,7 +8,7 @@
 // A prompt of a few tokens is a read and a write of its state (64 KB a head) around little work.  Here four blocks share
 // an SM, so one block's state is on its way while the others compute; a block of the 128-token kernel has an SM to
 // itself and pays its start, its loads and its whole chunk of products one after the other: 48 resumed prompts of 31
-// tokens on average take MMA us here and 342 us there.  Per token this kernel costs more (every 16 tokens the state is
+// tokens on average (128 heads; 483 MB) take 157 us here and 342 us there.  Per token this kernel costs more (every 16 tokens the state is
 // cut anew, and mma.sync runs at a quarter of tcgen05's rate), so longer prompts go there.
 #include "kernels.h"
 #include "packed.cuh"
@@ -38,7 +38,7 @@ __device__ __forceinline__ void copy16(void *dst, const void *src, bool live) {
 
 __global__ void __launch_bounds__(128, 4) scan_mma_kernel(ScanArgs a, Prompts pr) {
   __shared__ MmaStage st[2];
-  __shared__ int found;
+  __shared__ PieceWord found;
   Piece pc;
   if (!find_piece(pr, blockIdx.x, a.piece_len, pc, &found)) return;
   const int h = blockIdx.y, len = pc.end - pc.begin;

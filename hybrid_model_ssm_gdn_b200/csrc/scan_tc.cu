@@ -12,14 +12,19 @@
 // Precision: C, B and X are bf16 and enter exactly; sums are fp32.  The three fp32 operands M, S and the weighted X are
 // cut into two bf16 pieces (hi = RN(v), lo = RN(v - hi): what is lost is below 2^-17 of v) and multiplied twice, which
 // keeps the library's fp32 outputs and checkpoints at the accuracy its other kernels have; one bf16 piece would leave
-// them at 2^-9.  That doubles three of the four products: 14.7 M multiply-adds for a chunk of two heads, 3600 cycles of
-// the tensor core, against the 2.3 us that its bytes take at the measured bandwidth (x, y and the group's share of B
-// and C): both limits lie close together, and tcgen05 is needed for either (mma.sync measured a quarter of its rate).
+// them at 2^-9.  That doubles three of the four products: 14.7 M multiply-adds for a chunk of two heads, 4600 cycles of
+// the tensor core (M X has 64 columns a head, and an instruction of 64 takes as long as one of 128), against the 2.3 us that
+// its bytes take at the measured bandwidth (x, y and the group's share of B and C): both limits lie close together, and
+// tcgen05 is needed for either (mma.sync measured a quarter of its rate).
+//
+// Measured: 16384 tokens in 8 prompts of 128 heads, P 64, 8 groups, 0.40 ms (910 MB, 0.14 ms at the copy bandwidth), some
+// 12000 cycles a chunk of two heads; one prompt of 8191 tokens 0.29 ms.  What bounds a chunk is the loop below with its
+// conversions, which run on half-rate ALU instructions, not the tensor core and not memory.
 //
 // Tensor memory (512 columns): S 128 (row = head and p, column = n), Y 128 (row = token, column = head and p), G 128, and
 // M as hi | lo pairs 128, for one head after the other; M is the left operand straight from tensor memory.  Shared
-// memory: C, three buffers for B and X, a stage for Y, and one 64 KB buffer that holds the pieces of S until C S^T is done and then the pieces
-// of the weighted X; all of an SM's, so one block each.
+// memory: C, three buffers for B and X, a stage for Y, and one 64 KB buffer that holds the pieces of S until C S^T is done
+// and then the pieces of the weighted X; all of an SM's, so one block each.
 //
 // Decays never divide and never exceed what they stand for: a token's weight is a product of exp of sums of dt over
 // tokens between, by blocks of 32: within the row's block exp(A (c_j - c_i)), else exp(A (c_j - end)) exp(A (end - c_i))
@@ -29,7 +34,8 @@
 // products along the state (C S^T, S), one for those along the tokens (G, M X), one for the decay tables.  The loop that
 // bounds a chunk is  cut S -> C S^T -> weigh X -> S product -> cut S; all else runs beside it.
 // Every wait is bounded; after one runs out the others stop waiting and the block goes through its remaining steps, so
-// all barriers and the release of tensor memory are still reached.
+// all barriers and the release of tensor memory are still reached, and then writes NaN over its outputs and its state:
+// a context reports it, a call on the caller's own states has nothing else to show it.
 #include <cuda.h>
 
 #include "kernels.h"
@@ -60,7 +66,8 @@ struct TcShared {
   uint64_t full_C, full_X[2], full_B[2], tab_full, tab_free, tot_full;
   uint64_t g_done, y1_done, y20_done, y2_done[2], y_free, s_done[2], sp_ready[2], m_ready[2], xs_ready[2], drained[2];
   uint32_t tmem;
-  int abort, found;
+  int abort;
+  PieceWord found;
 };
 constexpr int kTcSmem = (int)sizeof(TcShared);
 static_assert(kTcSmem <= 227 * 1024, "shared memory of a block");
@@ -154,10 +161,10 @@ __global__ void __launch_bounds__(kTcThreads, 1)
       const int mine = lens[threadIdx.x];
       int rank = 0;
       for (int j = 0; j < pr.nseq; ++j) rank += lens[j] > mine || (lens[j] == mine && j < (int)threadIdx.x);
-      if (rank == number) sh.found = threadIdx.x;
+      if (rank == number) sh.found.seq = threadIdx.x;
     }
     __syncthreads();
-    number = sh.found;
+    number = sh.found.seq;
     __syncthreads();
   }
   Piece pc;
@@ -679,12 +686,24 @@ __global__ void __launch_bounds__(kTcThreads, 1)
     tm_fence_after();
     tm_free(tm, 512);
   }
+  if (*(volatile int *)&sh.abort) {  // a wait gave up: nothing that looks like a result stays
+    if (!kState && lane == 0) bulk_wait_all();  // this warp's own stores of Y
+    __syncthreads();
+    const float nan = __int_as_float(0x7fffffff);
+    for (int h = h0; h <= h1; ++h) {
+      if (final)
+        for (int i = tid; i < (int)head_elems; i += kTcThreads) final[h * head_elems + i] = nan;
+      if (!kState)
+        for (int i = warp; i < ntok; i += kTcThreads / 32)
+          for (int p = lane; p < a.P; p += 32) a.y[((size_t)(t0 + i) * a.H + h) * a.P + p] = nan;
+    }
+  }
 }
 
 // States at the starts of the pieces of prompts that are cut: seg[s] <- state before piece s, from the pieces' own end
 // states and decays, one thread four elements.  Small against the pieces' tokens, and its loads mostly hit L2.
 __global__ void __launch_bounds__(256) join_kernel(TcArgs a, Prompts pr) {
-  __shared__ int found;
+  __shared__ PieceWord found;
   Piece pc;
   if (!find_piece(pr, pr.off[blockIdx.x] / a.piece_len + (int)blockIdx.x, a.piece_len, pc, &found)) return;
   const int len = pc.end - pc.begin, h = blockIdx.y;

@@ -176,7 +176,7 @@ __device__ __forceinline__ void walk(const Filter<TI, K, V> &f, float (&win)[K -
 template <typename TI, int K>
 __global__ void __launch_bounds__(kPromptThreads) prompt_kernel(ShortConvArgs a, Prompts pr, int tile) {
   constexpr int V = kPromptV;
-  __shared__ int found;
+  __shared__ PieceWord found;
   Piece pc;
   if (!find_piece(pr, blockIdx.x, tile, pc, &found)) return;
   const int c = (blockIdx.y * kPromptThreads + threadIdx.x) * V;

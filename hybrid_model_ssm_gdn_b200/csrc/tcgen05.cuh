@@ -120,22 +120,6 @@ __device__ __forceinline__ void tma_load_3d(void *dst, const void *map, int x, i
       : "memory");
 }
 
-// bring a box into L2 ahead of its load
-__device__ __forceinline__ void tma_prefetch_3d(const void *map, int x, int y, int z) {
-  asm volatile("cp.async.bulk.prefetch.tensor.3d.L2.global.tile [%0, {%1, %2, %3}];" ::"l"(map), "r"(x), "r"(y), "r"(z)
-               : "memory");
-}
-
-// move registers between the warps of a block: every warp of a group of four executes it
-template <int N>
-__device__ __forceinline__ void more_registers() {
-  asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N));
-}
-template <int N>
-__device__ __forceinline__ void fewer_registers() {
-  asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N));
-}
-
 // tiled TMA store, tracked by the issuing thread's bulk async-group; coordinates are not negative
 __device__ __forceinline__ void tma_store_3d(const void *map, const void *src, int x, int y, int z) {
   asm volatile("cp.async.bulk.tensor.3d.global.shared::cta.tile.bulk_group [%0, {%1, %2, %3}], [%4];" ::"l"(map), "r"(x),

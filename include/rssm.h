@@ -197,10 +197,11 @@ rssm_status rssm_flush(rssm_ctx *ctx, const unsigned char *mask, rssm_stream str
  * read into a result nor written.  Prompt i belongs to sequence slots[i] of the state (i itself without slots); other
  * sequences keep theirs.
  * If any offset or slot is out of range nothing is written at all; prompts that share a slot are left out.
+ * Outputs overlap no input.
  * Kernels are chosen by total and nseq, so a prompt's results can differ in their last bits with the company it is in;
  * the same call gives the same bits. */
 typedef struct {
-  int total, nseq;              /* tokens in all, prompts; total >= 0, nseq >= 1 */
+  int total, nseq;              /* tokens in all, prompts; 0 <= total <= 2^30, nseq >= 1 */
   const int *offsets;           /* device [nseq + 1], non-decreasing within 0..total */
   const int *slots;             /* device [nseq] or NULL */
   const unsigned char *resume;  /* device [nseq] or NULL: nonzero = continue from the sequence's state, else from zero */
@@ -214,7 +215,8 @@ rssm_status rssm_mamba2_scan_workspace(const rssm_config *cfg, int total, int ns
  * number of sequences of S).  tok: x [total][H][P], B, C [total][G][N], dt [total][H] in cfg.in_dtype;
  *   S device fp32 [batch][H][P][N], the prompts' sequences rewritten;  y device fp32 [total][H][P];
  *   work device, 256-byte aligned, >= rssm_mamba2_scan_workspace bytes (NULL if that is 0), free again when the
- *   call's work on the stream is done. */
+ *   call's work on the stream is done.
+ * Heads whose asynchronous copies did not arrive within the bound of the waits have NaN in y and S. */
 rssm_status rssm_mamba2_scan(const rssm_config *cfg, const rssm_prompts *pr, const rssm_tokens *tok, float *S, float *y,
                              void *work, size_t work_bytes, rssm_stream stream);
 
@@ -231,7 +233,7 @@ rssm_status rssm_mamba2_prefill(rssm_ctx *ctx, const rssm_prompts *pr, const rss
  * summed in fp32 and rounded once to the input type.  Its state follows the scheme of the replay buffer: a ring of
  * the last raw inputs, hist [batch][ring][channels] in the input type, with a cursor cur [batch] (the slot of the next
  * token, 0..ring-1; any other value is taken modulo ring).  A draft is a tentative row and commit moves the cursor.
- * Row r of `in` starts at in + r * in_stride elements.  Outputs are up to three contiguous tensors out[s]
+ * Row r of `in` starts at in + r * in_stride elements; outputs that overlap its rows are refused.  Outputs are up to three contiguous tensors out[s]
  * [rows][split[s]], the channels cut in order, so that a step or verify call can take them as they are. */
 typedef struct {
   int batch;         /* sequences of hist, >= 1 */

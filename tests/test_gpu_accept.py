@@ -116,3 +116,17 @@ def test_long_rows_few_sequences(cuda_ok):
                                   torch.from_numpy(u).cuda())
         for b in (0, batch - 1):
             assert int(nxt[b]) == oracle_accept(t[b:b + 1], np.zeros((1, 0), int), u[b:b + 1])[1][0]
+
+
+def test_rows_past_32_bits(cuda_ok):
+    """Rows that lie so far apart that the last ones start past 2^31 elements."""
+    V, apart = 1000, 2 ** 30 + 8
+    r, target, tokens, u, draft = case(9, 2, 1, V)
+    wide = torch.empty(3 * apart + V, device="cuda").as_strided((2, 2, V), (2 * apart, apart, 1))
+    wide.copy_(torch.from_numpy(target))
+    for q in (draft, None):
+        got = accept_drafts(wide, torch.from_numpy(tokens).int().cuda(), torch.from_numpy(u).cuda(),
+                            draft=None if q is None else torch.from_numpy(q).cuda())
+        want = oracle_accept(target, tokens, u, q, None)
+        np.testing.assert_array_equal(got[0].cpu().numpy(), want[0])
+        np.testing.assert_array_equal(got[2].cpu().numpy(), want[1])

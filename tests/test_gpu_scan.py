@@ -291,3 +291,41 @@ def test_a_load_that_never_comes_times_out_and_the_context_recovers(cuda_ok, mon
     layer.prefill(*tok, idx([0, 150, 400]), y=y)
     compare(d, [0, 150, 400], None, None, layer.export(ring=False)["S"].cpu().numpy(), y.cpu().numpy())
     assert layer.get_error() == (0, -1)
+
+
+@pytest.mark.parametrize("H,lens", [(4, (150, 250)), (2, (1900,))])
+def test_a_scan_that_timed_out_leaves_nan(cuda_ok, monkeypatch, H, lens):
+    """With one chunk's load withheld from every block, whole prompts and pieces: all outputs and states are NaN."""
+    offsets = np.concatenate([[0], np.cumsum(lens)]).tolist()
+    total = offsets[-1]
+    d = make(22, torch.bfloat16, total, H, 64, 1, len(lens), decay=0.05)
+    g = on_gpu(d, torch.bfloat16)
+    monkeypatch.setenv("RSSM_WAIT_CYCLES", "2000000")
+    monkeypatch.setenv("RSSM_WITHHOLD_TILE", "1")
+    layer = context(d, torch.bfloat16, len(lens))
+    y = torch.full((total, H, 64), 7.0, device="cuda")
+    layer.prefill(g["x"], g["B"], g["C"], g["dt"], idx(offsets), y=y)
+    assert layer.get_error()[0] == abi.DEV_TIMEOUT
+    assert torch.isnan(y).all()
+    assert torch.isnan(layer.export(ring=False)["S"]).all()
+
+
+@pytest.mark.parametrize("dtype,H,total,nseq", [(torch.bfloat16, 8, 2 ** 23 + 1000, 1), (torch.float32, 8, 2 ** 23 + 1000, 1),
+                                                (torch.bfloat16, 128, 2 ** 19 + 1000, 6700)])
+def test_rows_past_32_bits(cuda_ok, dtype, H, total, nseq):
+    """The last rows of inputs with more than 2^32 elements, in the last sequence of many, in each of the kernels."""
+    n, P = 150 if nseq == 1 else 40, 64
+    d = make(23, dtype, n, H, P, 1, 1)
+    g = on_gpu(d, dtype)
+    big = {k: torch.empty(total, *g[k].shape[1:], dtype=dtype, device="cuda") for k in ("x", "B", "C", "dt")}
+    for k, t in big.items():
+        t[-n:] = g[k]
+    y = torch.empty(total, H, P, device="cuda")
+    y[:-n].view(torch.int32)[-1000:] = 7
+    S = torch.empty(nseq, H, P, 128, device="cuda")
+    S[-1] = g["S"][0]
+    offsets = [total - n] * nseq + [total]
+    mamba2_scan(S, big["x"], big["B"], big["C"], big["dt"], g["A"], g["D"], idx(offsets), resume=idx([1] * nseq, torch.uint8),
+                y=y)
+    assert (y[:-n].view(torch.int32)[-1000:] == 7).all()
+    compare(d, [0, n], None, [1], S[-1:].cpu().numpy(), y[-n:].cpu().numpy())

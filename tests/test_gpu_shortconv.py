@@ -135,3 +135,33 @@ def test_infinities_stay_in_their_window(cuda_ok):
     c.w.fill_(0.25)
     out, = shortconv_prefill(c.hist, c.cur, c.dev(x), c.w, None, idx([0, 20]), **c.kw)
     assert torch.isnan(out[5:9]).all() and torch.isfinite(out[:5]).all() and torch.isfinite(out[9:]).all()
+
+
+def test_rows_past_32_bits(cuda_ok):
+    """The last rows of inputs with more than 2^32 elements."""
+    c = Case(3, BF, (1024,), 4, 3, 2)
+    n, total = 300, 2 ** 22 + 1000
+    x = c.dev(c.rows(n))
+    wide = torch.empty(total, 1024, dtype=BF, device="cuda")
+    wide[-n:] = x
+    out = (torch.empty(total, 1024, dtype=BF, device="cuda"),)
+    shortconv_prefill(c.hist, c.cur, wide, c.w, c.b, idx([total - n, total]), idx([2]), out=out, **c.kw)
+    xn = x.float().cpu().numpy()
+    c.check((out[0][-n:],), c.orc.prefill(xn, [0, n], [2]), c.mag.prefill(np.abs(xn), [0, n], [2]))
+    c.check_state()
+
+
+def test_outputs_between_the_rows_of_their_input(cuda_ok):
+    """Rows that lie apart leave room for outputs; those that meet a row are refused."""
+    c = Case(4, BF, (64,), 4, 2, 2)
+    wide = torch.zeros(2, 512, dtype=BF, device="cuda")
+    x, out = wide[:, :64], wide[0, 64:192].view(2, 64)
+    x.copy_(c.dev(c.rows(2)))
+    xn = x.float().cpu().numpy()
+    shortconv_step(c.hist, c.cur, x, c.w, c.b, out=(out,), **c.kw)
+    c.check((out,), c.orc.step(xn), c.mag.step(np.abs(xn)))
+    c.check_state()
+    for bad in (wide[0, 56:184], wide.view(-1)[448:576]):
+        with pytest.raises(RuntimeError, match="RSSM_ERR_ARG"):
+            shortconv_step(c.hist, c.cur, x, c.w, c.b, out=(bad.view(2, 64),), **c.kw)
+    c.check_state()

@@ -91,6 +91,25 @@ def test_shortconv_refusals(lib):
     assert lib.rssm_shortconv_commit(C.byref(conv(ring=2)), p16, p16, None) == SHAPE
 
 
+def test_size_and_overlap_refusals(lib):
+    """More tokens than positions rounded up to tiles can count; convolution outputs that meet their inputs."""
+    n = C.c_size_t()
+    for total in (2 ** 30 + 1, 2 ** 31 - 1):
+        assert lib.rssm_mamba2_scan_workspace(C.byref(cfg()), total, 1, C.byref(n)) == SHAPE
+    base, row, stride = 1 << 20, 64 * 2, 96 * 2  # four rows of 64 bf16, 96 elements apart
+    outs = lambda *p: (C.c_void_p * 3)(*p)  # noqa: E731
+    far = 1 << 24
+    for out in (outs(base, far, far), outs(far, base + 3 * stride, far), outs(far, far, base + 3 * stride + row - 16),
+                outs(base - 16, far, far), outs(base + row, far, far)):
+        assert lib.rssm_shortconv_step(C.byref(conv()), C.c_void_p(far), C.c_void_p(16), C.c_void_p(base), 96,
+                                       C.byref(out), None) == ARG
+    pr = abi.Prompts(4, 2, 16)
+    assert lib.rssm_shortconv_prefill(C.byref(conv()), C.byref(pr), C.c_void_p(far), C.c_void_p(16), C.c_void_p(base), 96,
+                                      C.byref(outs(base, far, far)), None) == ARG
+    assert lib.rssm_shortconv_verify(C.byref(conv(ring=8)), 4, C.c_void_p(far), C.c_void_p(16), C.c_void_p(base), 96,
+                                     C.byref(outs(far, base + 15 * stride, far)), None) == ARG
+
+
 def test_accept_refusals(lib):
     p = C.c_void_p(16)
 
