@@ -4,9 +4,13 @@
 //
 // A few multiply-adds per value against one read and one write of it: the bound is memory.  A thread owns V
 // consecutive channels, keeps their K taps and the last K-1 inputs in registers as fp32 and walks along the tokens, so
-// every input is loaded once (plus K-1 rows where a prompt is cut into tiles), a group of tokens ahead of its use.  SiLU
-// is one exponential and one reciprocal of the special-function unit, which alone would take three quarters of the
+// every input is loaded once (plus K-1 rows where a prompt is cut into tiles).  Its next rows are on their way to shared
+// memory: as many bytes in flight as the bandwidth times the latency ask for do not fit the registers beside the taps.
+// SiLU is one exponential and one reciprocal of the special-function unit, which alone would take three quarters of the
 // memory's time; the exact division and expf took twice that.
+//
+// Measured (bf16, 10240 channels, K 4): 16384 tokens in 8 prompts 132 us, 5.1 TB/s (four tokens ahead in registers 145 us);
+// 8 drafts of 512 sequences with their commit 57 us, 4.9 TB/s (two tokens ahead in registers 81 us).
 #include <cooperative_groups.h>
 
 #include "kernels.h"
@@ -18,11 +22,8 @@ namespace rssm {
 namespace {
 
 constexpr int kPromptThreads = 128, kTokenThreads = 256;
-// Channels a thread and tokens loaded together: 16 bytes of bf16 and four tokens ahead for prompts (143 us for 16384 tokens
-// of 10240 channels, 4 channels: 150 us); decoding has registers for two ahead (8 drafts of 512 sequences 80 us; 4
-// channels with twice the threads: 92 us).
-constexpr int kPromptV = 8, kPromptGroup = 4;
-constexpr int kTokenV = 8, kTokenGroup = 2, kTokenBlocks = 2;
+// Channels a thread: 16 bytes of bf16 (half as many with rows ahead in registers: prompts 150 us for 143, drafts 92 for 80).
+constexpr int kPromptV = 8, kTokenV = 8, kTokenBlocks = 2;
 
 // V values as they lie in memory
 template <typename TI, int V>
@@ -142,49 +143,61 @@ __device__ __forceinline__ TI *split_out(const ShortConvArgs &a, int c, int &row
   return reinterpret_cast<TI *>(p) + (c < c1 ? c : c < c2 ? c - c1 : c - c2);
 }
 
-// n tokens from `in` through the filter, loaded a group ahead; `keep(raw)` sees every input in turn
-template <typename TI, int K, int V, int kGroup, typename Keep>
-__device__ __forceinline__ void walk(const Filter<TI, K, V> &f, float (&win)[K - 1][V], const TI *in, size_t in_stride,
-                                     TI *out, int row, int n, Keep keep) {
-  Raw<TI, V> now[kGroup], next[kGroup];
+// A thread's own rows on their way, in shared memory: kAheadBytes of them, the oldest taken while a new one is asked for.
+// Only the thread itself writes and reads its slots, so there is nothing to wait for but its own copies.
+constexpr int kAheadBytes = 128;
+template <typename TI, int V, int kThreads>
+struct Ahead {
+  static constexpr int kWords = V * (int)sizeof(TI) / 16, kRows = kAheadBytes / (16 * kWords);
+  uint4 (*slots)[kThreads];  // [kRows * kWords]
+  int put, get;
+  __device__ __forceinline__ void ask(const TI *p, bool live) {
+    if (live) {
 #pragma unroll
-  for (int i = 0; i < kGroup; ++i)
-    if (i < n) now[i].load(in + i * in_stride);
-  for (int t = 0; t < n; t += kGroup) {
-#pragma unroll
-    for (int i = 0; i < kGroup; ++i)
-      if (t + kGroup + i < n) next[i].load(in + (t + kGroup + i) * in_stride);
-#pragma unroll
-    for (int i = 0; i < kGroup; ++i) {
-      if (t + i < n) {
-        float x[V], o[V];
-        now[i].widen(x);
-        f.apply(win, x, o);
-        push<K, V>(win, x);
-        Raw<TI, V> r;
-        r.round(o);
-        r.store(out + (size_t)(t + i) * row);
-        keep(now[i]);
-      }
-      now[i] = next[i];
+      for (int i = 0; i < kWords; ++i)
+        asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(smem_u32(&slots[put * kWords + i][threadIdx.x])),
+                     "l"(p + 16 / sizeof(TI) * i)
+                     : "memory");
     }
+    asm volatile("cp.async.commit_group;" ::: "memory");
+    put = (put + 1) % kRows;
   }
-}
+  __device__ __forceinline__ void take(Raw<TI, V> &r) {  // after kRows rows were asked for beyond the last one taken
+    asm volatile("cp.async.wait_group %0;" ::"n"(kRows - 1) : "memory");
+#pragma unroll
+    for (int i = 0; i < kWords; ++i) {
+      uint4 v;
+      asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
+                   : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+                   : "r"(smem_u32(&slots[get * kWords + i][threadIdx.x]))
+                   : "memory");
+      r.u[4 * i] = v.x; r.u[4 * i + 1] = v.y; r.u[4 * i + 2] = v.z; r.u[4 * i + 3] = v.w;
+    }
+    get = (get + 1) % kRows;
+  }
+};
 
 // Prompts.  blockIdx.x: tile of a prompt; blockIdx.y: block of channels.  The block of a prompt's first tile alone
 // reads and rewrites the sequence's history, each thread its own channels, so the rewrite is safe in place.
 template <typename TI, int K>
 __global__ void __launch_bounds__(kPromptThreads) prompt_kernel(ShortConvArgs a, Prompts pr, int tile) {
   constexpr int V = kPromptV;
+  using Rows = Ahead<TI, V, kPromptThreads>;
+  __shared__ uint4 slots[kAheadBytes / 16][kPromptThreads];
   __shared__ PieceWord found;
   Piece pc;
   if (!find_piece(pr, blockIdx.x, tile, pc, &found)) return;
   const int c = (blockIdx.y * kPromptThreads + threadIdx.x) * V;
   const int len = pc.end - pc.begin;
   if (c >= a.channels || (pc.first >= len && pc.index > 0)) return;
+  const TI *in = reinterpret_cast<const TI *>(a.in) + (size_t)pc.begin * a.in_stride + c;
+  const int n = min(tile, len - pc.first);
+  Rows rows{slots, 0, 0};
+  const TI *next = in + (size_t)pc.first * a.in_stride;
+#pragma unroll
+  for (int i = 0; i < Rows::kRows; ++i, next += a.in_stride) rows.ask(next, i < n);
   Filter<TI, K, V> f;
   f.load(a, c);
-  const TI *in = reinterpret_cast<const TI *>(a.in) + (size_t)pc.begin * a.in_stride + c;
   float win[K - 1][V];
   if (pc.index == 0) {
     TI *hist = reinterpret_cast<TI *>(a.hist) + (size_t)pc.slot * a.ring * a.channels + c;
@@ -223,16 +236,27 @@ __global__ void __launch_bounds__(kPromptThreads) prompt_kernel(ShortConvArgs a,
   int row;
   TI *out = split_out<TI>(a, c, row);
   out += (size_t)(pc.begin + pc.first) * row;
-  walk<TI, K, V, kPromptGroup>(f, win, in + (size_t)pc.first * a.in_stride, a.in_stride, out, row,
-                               min(tile, len - pc.first), [](const Raw<TI, V> &) {});
+  for (int t = 0; t < n; ++t) {
+    Raw<TI, V> r;
+    rows.take(r);
+    rows.ask(next, t + Rows::kRows < n);
+    next += a.in_stride;
+    float x[V], o[V];
+    r.widen(x);
+    f.apply(win, x, o);
+    push<K, V>(win, x);
+    r.round(o);
+    r.store(out);
+    out += row;
+  }
 }
 
-// T tokens a sequence on top of its history.  A thread keeps the taps of its channels and takes the sequences of its
-// cluster one after the other, with one token (kOne) the next sequence's rows on their way.  The blocks of a cluster
-// share out the channels, so that the cursors can advance in place once all of them have read them (`advance`: one token
-// that stands; otherwise the rows stay tentative).
-template <typename TI, int K, bool kOne>
-__global__ void __launch_bounds__(kTokenThreads, kTokenBlocks) token_kernel(ShortConvArgs a, int T, int advance) {
+// One token a sequence on top of its history.  A thread keeps the taps of its channels and takes the sequences of its
+// cluster one after the other, the next sequence's rows on their way.  The blocks of a cluster share out the channels, so
+// that the cursors can advance in place once all of them have read them (`advance`: the token stands; otherwise it is a
+// tentative row).
+template <typename TI, int K>
+__global__ void __launch_bounds__(kTokenThreads, kTokenBlocks) token_kernel(ShortConvArgs a, int advance) {
   constexpr int V = kTokenV;
   cg::cluster_group cluster = cg::this_cluster();
   const int blocks = cluster.num_blocks(), rank = cluster.block_rank();
@@ -243,55 +267,34 @@ __global__ void __launch_bounds__(kTokenThreads, kTokenBlocks) token_kernel(Shor
     const TI *in0 = reinterpret_cast<const TI *>(a.in) + c;
     int row;
     TI *out0 = split_out<TI>(a, c, row);
-    if (kOne) {
-      Raw<TI, V> now[K], next[K];  // K-1 rows of history, then the token
-      auto load = [&](int b, int cur, Raw<TI, V>(&r)[K]) {
+    Raw<TI, V> now[K], next[K];  // K-1 rows of history, then the token
+    auto load = [&](int b, int cur, Raw<TI, V>(&r)[K]) {
 #pragma unroll
-        for (int k = 0; k < K - 1; ++k)
-          r[k].load(hist0 + ((size_t)b * a.ring + wrap(cur - (K - 1) + k, a.ring)) * row_hist);
-        r[K - 1].load(in0 + (size_t)b * a.in_stride);
-      };
-      int cur = wrap(a.cur[first], a.ring);
-      load(first, cur, now);
-      Filter<TI, K, V> f;
-      f.load(a, c);
-      int cur_next = first + stride < a.batch ? wrap(a.cur[first + stride], a.ring) : 0;
-      for (int b = first; b < a.batch; b += stride) {
-        const int after = b + 2 * stride < a.batch ? a.cur[b + 2 * stride] : 0;
-        if (b + stride < a.batch) load(b + stride, cur_next, next);
-        float win[K - 1][V], x[V], o[V];
+      for (int k = 0; k < K - 1; ++k)
+        r[k].load(hist0 + ((size_t)b * a.ring + wrap(cur - (K - 1) + k, a.ring)) * row_hist);
+      r[K - 1].load(in0 + (size_t)b * a.in_stride);
+    };
+    int cur = wrap(a.cur[first], a.ring);
+    load(first, cur, now);
+    Filter<TI, K, V> f;
+    f.load(a, c);
+    int cur_next = first + stride < a.batch ? wrap(a.cur[first + stride], a.ring) : 0;
+    for (int b = first; b < a.batch; b += stride) {
+      const int after = b + 2 * stride < a.batch ? a.cur[b + 2 * stride] : 0;
+      if (b + stride < a.batch) load(b + stride, cur_next, next);
+      float win[K - 1][V], x[V], o[V];
 #pragma unroll
-        for (int k = 0; k < K - 1; ++k) now[k].widen(win[k]);
-        now[K - 1].widen(x);
-        f.apply(win, x, o);
-        now[K - 1].store(hist0 + ((size_t)b * a.ring + cur) * row_hist);
-        Raw<TI, V> r;
-        r.round(o);
-        r.store(out0 + (size_t)b * row);
-        cur = cur_next;
-        cur_next = wrap(after, a.ring);
+      for (int k = 0; k < K - 1; ++k) now[k].widen(win[k]);
+      now[K - 1].widen(x);
+      f.apply(win, x, o);
+      now[K - 1].store(hist0 + ((size_t)b * a.ring + cur) * row_hist);
+      Raw<TI, V> r;
+      r.round(o);
+      r.store(out0 + (size_t)b * row);
+      cur = cur_next;
+      cur_next = wrap(after, a.ring);
 #pragma unroll
-        for (int k = 0; k < K; ++k) now[k] = next[k];
-      }
-    } else {
-      Filter<TI, K, V> f;
-      f.load(a, c);
-      for (int b = first; b < a.batch; b += stride) {
-        int slot = wrap(a.cur[b], a.ring);
-        TI *hist = hist0 + (size_t)b * a.ring * row_hist;
-        float win[K - 1][V];
-#pragma unroll
-        for (int k = 0; k < K - 1; ++k) {
-          Raw<TI, V> r;
-          r.load(hist + (size_t)wrap(slot - (K - 1) + k, a.ring) * row_hist);
-          r.widen(win[k]);
-        }
-        walk<TI, K, V, kTokenGroup>(f, win, in0 + (size_t)b * T * a.in_stride, a.in_stride, out0 + (size_t)b * T * row,
-                                    row, T, [&](const Raw<TI, V> &r) {
-                                      r.store(hist + (size_t)slot * row_hist);
-                                      slot = slot + 1 == a.ring ? 0 : slot + 1;
-                                    });
-      }
+      for (int k = 0; k < K; ++k) now[k] = next[k];
     }
   }
   if (advance) {
@@ -301,6 +304,71 @@ __global__ void __launch_bounds__(kTokenThreads, kTokenBlocks) token_kernel(Shor
         const int cur = wrap(a.cur[b], a.ring);
         a.cur_out[b] = cur + 1 == a.ring ? 0 : cur + 1;
       }
+  }
+}
+
+// T drafts a sequence on top of its history: tentative rows, the cursors stay.  blockIdx.x: which sequences, blockIdx.y:
+// block of channels.  A thread sees one stream of rows, K-1 of history and T of input for each of its sequences in turn, and
+// asks for them several ahead, across sequences.
+template <typename TI, int K>
+__global__ void __launch_bounds__(kTokenThreads, kTokenBlocks) draft_kernel(ShortConvArgs a, int T) {
+  constexpr int V = kTokenV;
+  using Rows = Ahead<TI, V, kTokenThreads>;
+  __shared__ uint4 slots[kAheadBytes / 16][kTokenThreads];
+  const int c = (blockIdx.y * kTokenThreads + threadIdx.x) * V, stride = gridDim.x;
+  if (c >= a.channels) return;
+  TI *hist0 = reinterpret_cast<TI *>(a.hist) + c;
+  const TI *in0 = reinterpret_cast<const TI *>(a.in) + c;
+  auto cursor = [&](int b) { return b < a.batch ? wrap(a.cur[b], a.ring) : 0; };
+  int row;
+  TI *out0 = split_out<TI>(a, c, row);
+
+  Rows rows{slots, 0, 0};
+  int ab = blockIdx.x, at = 1 - K;  // the row to ask for: history below 0, else a draft
+  int acur = cursor(ab), acur_next = cursor(ab + stride);
+  auto ask = [&] {
+    const TI *p = at < 0 ? hist0 + ((size_t)ab * a.ring + wrap(acur + at, a.ring)) * a.channels
+                         : in0 + ((size_t)ab * T + at) * a.in_stride;
+    rows.ask(p, ab < a.batch);
+    if (++at == T) {
+      at = 1 - K;
+      ab += stride;
+      acur = acur_next;
+      acur_next = cursor(ab + stride);
+    }
+  };
+#pragma unroll
+  for (int i = 0; i < Rows::kRows; ++i) ask();
+  Filter<TI, K, V> f;
+  f.load(a, c);
+  int slot_next = cursor(blockIdx.x);
+  for (int b = blockIdx.x; b < a.batch; b += stride) {
+    int slot = slot_next;
+    slot_next = cursor(b + stride);
+    TI *hist = hist0 + (size_t)b * a.ring * a.channels;
+    TI *out = out0 + (size_t)b * T * row;
+    float win[K - 1][V];
+#pragma unroll
+    for (int k = 0; k < K - 1; ++k) {
+      Raw<TI, V> r;
+      rows.take(r);
+      ask();
+      r.widen(win[k]);
+    }
+    for (int t = 0; t < T; ++t) {
+      Raw<TI, V> r;
+      rows.take(r);
+      ask();
+      r.store(hist + (size_t)slot * a.channels);
+      slot = slot + 1 == a.ring ? 0 : slot + 1;
+      float x[V], o[V];
+      r.widen(x);
+      f.apply(win, x, o);
+      push<K, V>(win, x);
+      r.round(o);
+      r.store(out);
+      out += row;
+    }
   }
 }
 
@@ -328,6 +396,12 @@ cudaError_t launch_prompt(const ShortConvArgs &a, const Prompts &pr, int num_sms
 template <typename TI, int K>
 cudaError_t launch_tokens(const ShortConvArgs &a, int T, int advance, int num_sms, cudaStream_t stream) {
   const int vectors = a.channels / kTokenV;
+  if (T > 1) {  // as many blocks as fit the SMs at once: the taps are read once a block
+    const int columns = (vectors + kTokenThreads - 1) / kTokenThreads;
+    const int groups = max(1, min(a.batch, kTokenBlocks * num_sms / columns));
+    draft_kernel<TI, K><<<dim3(groups, columns), kTokenThreads, 0, stream>>>(a, T);
+    return cudaGetLastError();
+  }
   int threads = (vectors + 31) / 32 * 32;
   threads = threads > kTokenThreads ? kTokenThreads : threads;
   int blocks = (vectors + threads - 1) / threads;
@@ -346,8 +420,7 @@ cudaError_t launch_tokens(const ShortConvArgs &a, int T, int advance, int num_sm
   attr[0].val.clusterDim.z = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  return T == 1 ? cudaLaunchKernelEx(&cfg, token_kernel<TI, K, true>, a, T, advance)
-                : cudaLaunchKernelEx(&cfg, token_kernel<TI, K, false>, a, T, advance);
+  return cudaLaunchKernelEx(&cfg, token_kernel<TI, K>, a, advance);
 }
 
 template <typename TI>
