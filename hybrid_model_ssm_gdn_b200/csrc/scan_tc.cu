@@ -66,7 +66,7 @@ struct TcShared {
   uint64_t full_C, full_X[2], full_B[2], tab_full, tab_free, tot_full;
   uint64_t g_done, y1_done, y20_done, y2_done[2], y_free, s_done[2], sp_ready[2], m_ready[2], xs_ready[2], drained[2];
   uint32_t tmem;
-  int abort;
+  int abort, number;
   PieceWord found;
 };
 constexpr int kTcSmem = (int)sizeof(TcShared);
@@ -206,6 +206,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
     for (uint64_t *b : team) mbar_init(b, 8);
     mbar_init(&sh.tab_free, kState ? 8 : 16);
     sh.abort = 0;
+    sh.number = number;
     fence_barrier_init();
   }
   if (warp == kWarpLoad) tm_alloc(&sh.tmem, 512);
@@ -686,16 +687,26 @@ __global__ void __launch_bounds__(kTcThreads, 1)
     tm_fence_after();
     tm_free(tm, 512);
   }
-  if (*(volatile int *)&sh.abort) {  // a wait gave up: nothing that looks like a result stays
-    if (!kState && lane == 0) bulk_wait_all();  // this warp's own stores of Y
+  // A wait gave up: nothing that looks like a result stays.  What to overwrite is worked out anew, from shared memory: kept
+  // in registers all along it made the whole kernel 3 % slower.
+  if (*(volatile int *)&sh.abort) {
+    if (!kState && threadIdx.x % 32 == 0) bulk_wait_all();  // this warp's own stores of Y
     __syncthreads();
+    const volatile PieceWord &w = sh.found;
+    const int per = a.G * a.pairs, r = a.H / a.G, u = blockIdx.x % per;
+    const int ha = u / a.pairs * r + 2 * (u % a.pairs), hb = min(ha + 2, (u / a.pairs + 1) * r);
+    const int first = (*(volatile int *)&sh.number - (w.begin / a.piece_len + w.seq)) * a.piece_len;
+    const int len = w.end - w.begin, n = min(a.piece_len, len - first);
+    float *S = nullptr;
+    if (kState) S = a.seg + (size_t)sh.number * a.H * a.P * kCols;
+    else if (first + n >= len) S = a.S + (size_t)w.slot * a.H * a.P * kCols;
     const float nan = __int_as_float(0x7fffffff);
-    for (int h = h0; h <= h1; ++h) {
-      if (final)
-        for (int i = tid; i < (int)head_elems; i += kTcThreads) final[h * head_elems + i] = nan;
+    for (int h = ha; h < hb; ++h) {
+      if (S)
+        for (int i = threadIdx.x; i < a.P * kCols; i += kTcThreads) S[(size_t)h * a.P * kCols + i] = nan;
       if (!kState)
-        for (int i = warp; i < ntok; i += kTcThreads / 32)
-          for (int p = lane; p < a.P; p += 32) a.y[((size_t)(t0 + i) * a.H + h) * a.P + p] = nan;
+        for (int i = threadIdx.x / 32; i < n; i += kTcThreads / 32)
+          for (int p = threadIdx.x % 32; p < a.P; p += 32) a.y[((size_t)(w.begin + first + i) * a.H + h) * a.P + p] = nan;
     }
   }
 }
