@@ -160,13 +160,13 @@ class ReplaySSM:
         """Run packed prompts (rssm_mamba2_prefill): x [total][H][P], B, C [total][G][128], dt [total][H];
         offsets int32 [n+1]; slots int32 [n] (sequence of each prompt), resume uint8 [n] -> y fp32 [total][H][P]."""
         H, P, G = self.nheads, self.rows, self.ngroups
-        if self.arena.get_device() != torch._C._cuda_getDevice():
-            raise ValueError(f"the context is on {self.arena.device}, but the current device is "
-                             f"cuda:{torch.cuda.current_device()}")
-        total, pr, tok, y = _scan_args(x, B, C_, dt, offsets, slots, resume, y, H, P, G, self.in_dtype)
-        work = _scan_work(self.lib, self.cfg, total, pr.nseq, workspace)
+        device = _device(x, "x")
+        if self.arena.get_device() != device:
+            raise ValueError(f"the context is on {self.arena.device}, but the current device is cuda:{device}")
+        total, pr, tok, y = _scan_args(x, B, C_, dt, offsets, slots, resume, y, H, P, G, self.in_dtype, device)
+        work = _scan_work(self.lib, self.cfg, total, pr.nseq, workspace, device)
         abi.check(self.lib.rssm_mamba2_prefill(self.handle, C.byref(pr), C.byref(tok), _addr(y), _addr(work),
-                                               0 if work is None else work.numel(), _raw_stream()), "rssm_mamba2_prefill")
+                                               0 if work is None else work.numel(), _stream_of(device)), "rssm_mamba2_prefill")
         return y
 
     def flush(self, mask=None):
@@ -235,37 +235,40 @@ class ReplaySSM:
 
 # ---------------------------------------------------------------------- prompts and drafts
 
-def _arr(t, dtype, name, shape, optional=False):
-    """``t`` after checking that it is a contiguous tensor of ``dtype`` and exactly ``shape`` on the current device."""
-    if t is None and optional:
+def _arr(t, dtype, name, shape, device):
+    """The address of ``t`` (None: null) after checking that it is a contiguous tensor of ``dtype`` and exactly ``shape`` on
+    the current device, number ``device``."""
+    if t is None:
         return None
+    if t.dtype is dtype and t.shape == shape and t.get_device() == device and t.is_contiguous():
+        return t.data_ptr()
     if t.shape != shape:
         raise ValueError(f"{name}: expected shape {tuple(shape)}, got {tuple(t.shape)}")
-    if t.dtype is not dtype or not t.is_contiguous() or t.get_device() < 0:
+    if t.dtype is not dtype or not t.is_contiguous() or not t.is_cuda:
         raise ValueError(f"{name}: expected a contiguous CUDA tensor of {dtype}, got {t.dtype} on {t.device}")
-    if t.get_device() != torch._C._cuda_getDevice():
-        raise ValueError(f"{name}: on {t.device}, but the current device is cuda:{torch.cuda.current_device()}")
-    return t
+    raise ValueError(f"{name}: on {t.device}, but the current device is cuda:{device}")
 
 
-def _raw_stream():
-    """The current stream's handle, without building a stream object (these calls are short)."""
-    return torch._C._cuda_getCurrentRawStream(torch._C._cuda_getDevice())
+def _device(t, name):
+    """The current device's number; ``t`` has to be on a GPU (on which, ``_arr`` and its like check)."""
+    if t.get_device() < 0:
+        raise ValueError(f"{name}: expected a contiguous CUDA tensor, got {t.dtype} on {t.device}")
+    return torch._C._cuda_getDevice()
+
+
+_stream_of = torch._C._cuda_getCurrentRawStream  # a device's current stream, without building an object
 
 
 def _addr(t):
     return None if t is None else t.data_ptr()
 
 
-def _prompts(total, offsets, slots, resume):
+def _prompts(total, offsets, slots, resume, device):
     n = offsets.numel() - 1
     if n < 1:
         raise ValueError(f"offsets: needs at least 2 elements, got {n + 1}")
-    _arr(offsets, torch.int32, "offsets", (n + 1,))
-    _arr(slots, torch.int32, "slots", (n,), optional=True)
-    _arr(resume, torch.uint8, "resume", (n,), optional=True)
-    return abi.Prompts(total, n, offsets.data_ptr(), None if slots is None else slots.data_ptr(),
-                       None if resume is None else resume.data_ptr())
+    return abi.Prompts(total, n, _arr(offsets, torch.int32, "offsets", (n + 1,), device),
+                       _arr(slots, torch.int32, "slots", (n,), device), _arr(resume, torch.uint8, "resume", (n,), device))
 
 
 def _in_dtype(t, name):
@@ -274,28 +277,26 @@ def _in_dtype(t, name):
     return t.dtype
 
 
-def _scan_args(x, B, C_, dt, offsets, slots, resume, y, H, P, G, dtype):
+def _scan_args(x, B, C_, dt, offsets, slots, resume, y, H, P, G, dtype, device):
     total = x.shape[0]
-    _arr(x, dtype, "x", (total, H, P))
-    _arr(B, dtype, "B", (total, G, 128))
-    _arr(C_, dtype, "C", (total, G, 128))
-    _arr(dt, dtype, "dt", (total, H))
-    pr = _prompts(total, offsets, slots, resume)
+    tok = abi.Tokens(_arr(x, dtype, "x", (total, H, P), device), _arr(B, dtype, "B", (total, G, 128), device),
+                     _arr(C_, dtype, "C", (total, G, 128), device), _arr(dt, dtype, "dt", (total, H), device))
+    pr = _prompts(total, offsets, slots, resume, device)
     if y is None:
-        y = torch.empty(total, H, P, dtype=torch.float32, device=x.device)
-    _arr(y, torch.float32, "y", (total, H, P))
-    tok = abi.Tokens(x.data_ptr(), B.data_ptr(), C_.data_ptr(), dt.data_ptr())
+        y = x.new_empty((total, H, P), dtype=torch.float32)
+    else:
+        _arr(y, torch.float32, "y", (total, H, P), device)
     return total, pr, tok, y
 
 
-def _scan_work(lib, cfg, total, nseq, workspace):
+def _scan_work(lib, cfg, total, nseq, workspace, device):
     """The scratch tensor of a scan: the caller's, or a new one from the caching allocator (None if none is needed)."""
     n = C.c_size_t()
     abi.check(lib.rssm_mamba2_scan_workspace(C.byref(cfg), total, nseq, C.byref(n)), "rssm_mamba2_scan_workspace")
     if n.value == 0:
         return None
     if workspace is not None:
-        if workspace.get_device() != torch._C._cuda_getDevice() or workspace.dtype != torch.uint8 or \
+        if workspace.get_device() != device or workspace.dtype != torch.uint8 or \
                 not workspace.is_contiguous() or workspace.numel() < n.value:
             raise ValueError(f"workspace: expected a contiguous tensor of uint8 on the current CUDA device with at least "
                              f"{n.value} elements")
@@ -312,16 +313,15 @@ def mamba2_scan(S, x, B, C_, dt, A, D, offsets, slots=None, resume=None, y=None,
         raise ValueError("x, B and S: expected 3, 3 and 4 dimensions")
     total, H, P = x.shape
     dtype = _in_dtype(x, "x")
-    _arr(S, torch.float32, "S", (S.shape[0], H, P, 128))
-    _arr(A, torch.float32, "A", (H,))
-    _arr(D, torch.float32, "D", (H,))
-    total, pr, tok, y = _scan_args(x, B, C_, dt, offsets, slots, resume, y, H, P, B.shape[1], dtype)
+    device = _device(S, "S")
+    at = _arr(S, torch.float32, "S", (S.shape[0], H, P, 128), device)
     cfg = abi.Config(abi.MAMBA2, S.shape[0], H, P, 128, B.shape[1], 1, 0, _DT[dtype], abi.HP_F32, abi.READ_SAME, 0, 1.0,
-                     A.data_ptr(), D.data_ptr(), 0.0)
+                     _arr(A, torch.float32, "A", (H,), device), _arr(D, torch.float32, "D", (H,), device), 0.0)
+    total, pr, tok, y = _scan_args(x, B, C_, dt, offsets, slots, resume, y, H, P, B.shape[1], dtype, device)
     lib = abi.load()
-    work = _scan_work(lib, cfg, total, pr.nseq, workspace)
-    abi.check(lib.rssm_mamba2_scan(C.byref(cfg), C.byref(pr), C.byref(tok), _addr(S), _addr(y), _addr(work),
-                                   0 if work is None else work.numel(), _raw_stream()), "rssm_mamba2_scan")
+    work = _scan_work(lib, cfg, total, pr.nseq, workspace, device)
+    abi.check(lib.rssm_mamba2_scan(C.byref(cfg), C.byref(pr), C.byref(tok), at, y.data_ptr(), _addr(work),
+                                   0 if work is None else work.numel(), _stream_of(device)), "rssm_mamba2_scan")
     return y
 
 
@@ -345,54 +345,53 @@ def _row_stride(x, lead, ch):
 
 
 def _shortconv(hist, cur, x, weight, bias, splits, activation, out, lead):
-    """Config, outputs and row stride of a short-convolution call; ``lead``: the leading dimensions of x."""
+    """Arguments of a short-convolution call (config, addresses of hist, cur and x, row stride, the outputs and their
+    addresses, device); ``lead``: the leading dimensions of x."""
     if hist.dim() != 3 or weight.dim() != 2:
         raise ValueError("hist and weight: expected 3 and 2 dimensions")
     dtype = _in_dtype(x, "x")
     batch, ring, ch = hist.shape
     width = weight.shape[1]
-    _arr(hist, dtype, "hist", (batch, ring, ch))
-    _arr(cur, torch.int32, "cur", (batch,))
-    _arr(weight, dtype, "weight", (ch, width))
-    _arr(bias, dtype, "bias", (ch,), optional=True)
+    device = _device(hist, "hist")
+    hist_at = _arr(hist, dtype, "hist", (batch, ring, ch), device)
+    cur_at = _arr(cur, torch.int32, "cur", (batch,), device)
     splits = (ch,) if splits is None else tuple(splits)
-    n = len(splits)
-    if n > 3 or sum(splits) != ch or min(splits) < 1:
+    if len(splits) > 3 or sum(splits) != ch or min(splits) < 1:
         raise ValueError(f"splits: expected up to three positive sizes that sum to {ch}, got {splits}")
     if activation is not None and activation != "silu":
         raise ValueError(f"activation: expected None or 'silu', got {activation!r}")
-    if x.shape != (*lead, ch) or x.get_device() != hist.get_device():
+    if x.shape != (*lead, ch) or x.get_device() != device:
         raise ValueError(f"x: expected shape {(*lead, ch)} on the current CUDA device, got {tuple(x.shape)} on {x.device}")
     stride = _row_stride(x, lead, ch)
     if out is None:
-        device = x.device
-        out = tuple([torch.empty((*lead, c), dtype=dtype, device=device) for c in splits])
+        out = tuple([x.new_empty((*lead, c)) for c in splits])
+        ptrs = _P3(*[o.data_ptr() for o in out])
     else:
-        if len(out) != n:
-            raise ValueError(f"out: expected {n} tensors, got {len(out)}")
-        for o, c in zip(out, splits):
-            _arr(o, dtype, "out", (*lead, c))
+        if len(out) != len(splits):
+            raise ValueError(f"out: expected {len(splits)} tensors, got {len(out)}")
+        ptrs = _P3(*[_arr(o, dtype, "out", (*lead, c), device) for o, c in zip(out, splits)])
     cfg = abi.ShortConvConfig(batch, ch, width, ring, _DT[dtype], activation is not None, _I3(*splits),
-                              weight.data_ptr(), None if bias is None else bias.data_ptr())
-    return cfg, _P3(*[o.data_ptr() for o in out]), out, stride
+                              _arr(weight, dtype, "weight", (ch, width), device), _arr(bias, dtype, "bias", (ch,), device))
+    return C.byref(cfg), hist_at, cur_at, x.data_ptr(), stride, out, C.byref(ptrs), device
 
 
 def shortconv_prefill(hist, cur, x, weight, bias, offsets, slots=None, resume=None, splits=None, activation="silu",
                       out=None):
     """Short causal convolution over packed prompts (rssm_shortconv_prefill): x [total][channels]; hist
     [batch][ring][channels] and cur int32 [batch] are the sequences' histories -> one tensor [total][n] a split."""
-    cfg, ptrs, out, stride = _shortconv(hist, cur, x, weight, bias, splits, activation, out, (x.shape[0],))
-    pr = _prompts(x.shape[0], offsets, slots, resume)
-    abi.check(abi.load().rssm_shortconv_prefill(C.byref(cfg), C.byref(pr), _addr(hist), _addr(cur), _addr(x), stride,
-                                                C.byref(ptrs), _raw_stream()), "rssm_shortconv_prefill")
+    cfg, h, c, at, stride, out, ptrs, device = _shortconv(hist, cur, x, weight, bias, splits, activation, out,
+                                                          (x.shape[0],))
+    pr = _prompts(x.shape[0], offsets, slots, resume, device)
+    abi.check(abi.load().rssm_shortconv_prefill(cfg, C.byref(pr), h, c, at, stride, ptrs, _stream_of(device)),
+              "rssm_shortconv_prefill")
     return out
 
 
 def shortconv_step(hist, cur, x, weight, bias=None, splits=None, activation="silu", out=None):
     """One token a sequence: x [batch][channels] -> one tensor [batch][n] a split; cur advances."""
-    cfg, ptrs, out, stride = _shortconv(hist, cur, x, weight, bias, splits, activation, out, (hist.shape[0],))
-    abi.check(abi.load().rssm_shortconv_step(C.byref(cfg), _addr(hist), _addr(cur), _addr(x), stride, C.byref(ptrs),
-                                             _raw_stream()), "rssm_shortconv_step")
+    cfg, h, c, at, stride, out, ptrs, device = _shortconv(hist, cur, x, weight, bias, splits, activation, out,
+                                                          (hist.shape[0],))
+    abi.check(abi.load().rssm_shortconv_step(cfg, h, c, at, stride, ptrs, _stream_of(device)), "rssm_shortconv_step")
     return out
 
 
@@ -402,26 +401,26 @@ def shortconv_verify(hist, cur, x, weight, bias=None, splits=None, activation="s
     if x.dim() != 3:
         raise ValueError(f"x: expected 3 dimensions, got {x.dim()}")
     T = x.shape[1]
-    cfg, ptrs, out, stride = _shortconv(hist, cur, x, weight, bias, splits, activation, out, (hist.shape[0], T))
-    abi.check(abi.load().rssm_shortconv_verify(C.byref(cfg), T, _addr(hist), _addr(cur), _addr(x), stride, C.byref(ptrs),
-                                               _raw_stream()), "rssm_shortconv_verify")
+    cfg, h, c, at, stride, out, ptrs, device = _shortconv(hist, cur, x, weight, bias, splits, activation, out,
+                                                          (hist.shape[0], T))
+    abi.check(abi.load().rssm_shortconv_verify(cfg, T, h, c, at, stride, ptrs, _stream_of(device)),
+              "rssm_shortconv_verify")
     return out
 
 
 def shortconv_commit(hist, cur, accepted, width):
     """Advance the cursors by the accepted prefixes, int32 [batch]; ``width`` is the filter's."""
     batch, ring = hist.shape[:2]
-    _arr(cur, torch.int32, "cur", (batch,))
-    _arr(accepted, torch.int32, "accepted", (batch,))
+    device = _device(cur, "cur")
     cfg = abi.ShortConvConfig(batch=batch, width=width, ring=ring)
-    abi.check(abi.load().rssm_shortconv_commit(C.byref(cfg), _addr(cur), _addr(accepted), _raw_stream()),
-              "rssm_shortconv_commit")
+    abi.check(abi.load().rssm_shortconv_commit(C.byref(cfg), _arr(cur, torch.int32, "cur", (batch,), device),
+                                               _arr(accepted, torch.int32, "accepted", (batch,), device),
+                                               _stream_of(device)), "rssm_shortconv_commit")
 
 
-def _rows(t, name, batch, rows, vocab):
+def _rows(t, name, batch, rows, vocab, device):
     """The row stride of [batch][rows][vocab] probabilities whose rows lie evenly apart."""
-    if t.shape != (batch, rows, vocab) or t.dtype is not torch.float32 or t.get_device() < 0 or \
-            t.get_device() != torch._C._cuda_getDevice():
+    if t.shape != (batch, rows, vocab) or t.dtype is not torch.float32 or t.get_device() != device:
         raise ValueError(f"{name}: expected fp32 of shape {(batch, rows, vocab)} on the current CUDA device, got {t.dtype} "
                          f"of {tuple(t.shape)} on {t.device}")
     if t.is_contiguous():
@@ -439,16 +438,16 @@ def accept_drafts(target, tokens, u, draft=None, count=None):
     if target.dim() != 3:
         raise ValueError(f"target: expected 3 dimensions, got {target.dim()}")
     batch, T, vocab = target.shape[0], target.shape[1] - 1, target.shape[2]
-    ld_t = _rows(target, "target", batch, T + 1, vocab)
-    ld_d = 0 if draft is None else _rows(draft, "draft", batch, T, vocab)
-    _arr(tokens, torch.int32, "tokens", (batch, T))
-    _arr(u, torch.float32, "u", (batch, T + 1))
-    _arr(count, torch.int32, "count", (batch,), optional=True)
-    got = torch.empty((3, batch), dtype=torch.int32, device=target.device)
+    device = _device(target, "target")
+    ld_t = _rows(target, "target", batch, T + 1, vocab, device)
+    ld_d = 0 if draft is None else _rows(draft, "draft", batch, T, vocab, device)
+    got = target.new_empty((3, batch), dtype=torch.int32)
     at = got.data_ptr()
-    abi.check(abi.load().rssm_accept_drafts(batch, T, vocab, _addr(target), ld_t, _addr(draft), ld_d, _addr(tokens),
-                                            _addr(count), _addr(u), at, at + 4 * batch, at + 8 * batch, _raw_stream()),
-              "rssm_accept_drafts")
+    abi.check(abi.load().rssm_accept_drafts(batch, T, vocab, target.data_ptr(), ld_t, _addr(draft), ld_d,
+                                            _arr(tokens, torch.int32, "tokens", (batch, T), device),
+                                            _arr(count, torch.int32, "count", (batch,), device),
+                                            _arr(u, torch.float32, "u", (batch, T + 1), device),
+                                            at, at + 4 * batch, at + 8 * batch, _stream_of(device)), "rssm_accept_drafts")
     return got.unbind(0)
 
 
