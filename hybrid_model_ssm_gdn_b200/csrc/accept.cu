@@ -9,13 +9,14 @@
 // fp64: fp32 sums of a vocabulary's values would move the border by more than many tokens' mass.  Conversions to fp64
 // run at an eighth of the fp32 rate, so the long pass makes one an element instead of two: the fp32 difference goes to the
 // fp64 sum, and its rounding error, which fp32 arithmetic gives exactly, to an fp32 sum of its own (errors are below 2^-24
-// of their values and lose 2^-24 of that in turn).
+// of their values and lose 2^-24 of that in turn).  Infinities are not looked for: they show in the sum.
 //
 // A cluster of blocks shares a sequence (when there are few, so that one row is read by several SMs); the blocks'
 // totals are exchanged through distributed shared memory.
 //
-// Measured: 256 sequences, vocabulary 131072, with draft rows, 64 us (226 MB, 35 us at the copy bandwidth; DRAM 45 % busy:
-// the draw's dependent steps are what is left); one sequence of 32000 15 us with its launch.
+// Measured: 256 sequences, vocabulary 131072, with draft rows, 54 us (226 MB, 35 us at the copy bandwidth), 64 us
+// with five blocks an SM instead of eight and lines left in L1.  What is left besides the stream are a
+// sequence's dependent steps: drafts, their probabilities, sums, totals, search.
 #include <cooperative_groups.h>
 
 #include "kernels.h"
@@ -28,6 +29,7 @@ namespace {
 
 constexpr int kWarps = 8;
 constexpr int kUnroll = 8;
+constexpr int kBlocksSm = 8;  // 32 registers a thread: more loads in flight count for more than longer rounds
 constexpr int kFine = 256;  // longest run that one warp searches by itself: 8 consecutive elements a lane
 
 struct Row {
@@ -41,6 +43,14 @@ struct Row {
   }
 };
 
+// A load that keeps its place in the source, so that all of a round are on their way before the first is used, and leaves
+// no line in L1, which the stream would only fill (256 rows of 131072: 64 us with the L2 cold; with lines in L1 72 us).
+__device__ __forceinline__ float load_now(const float *p) {
+  float v;
+  asm volatile("ld.global.L1::no_allocate.f32 %0, [%1];" : "=f"(v) : "l"(p));
+  return v;
+}
+
 __device__ __forceinline__ double warp_sum_f64(double v) {
 #pragma unroll
   for (int off = 16; off >= 1; off >>= 1) v += __shfl_xor_sync(0xffffffffu, v, off);
@@ -50,19 +60,16 @@ __device__ __forceinline__ double warp_sum_f64(double v) {
 // sum of the masses of [lo, hi), the whole warp
 template <bool kDraft>
 __device__ __forceinline__ double warp_mass(const Row &r, int lo, int hi, int lane) {
-  const float inf = __int_as_float(0x7f800000);
   double s = 0.0;
   float lost = 0.f;
   auto add = [&](float p, float q, int v) {
     if (kDraft) {
-      const bool some = p > q && p < inf && q > -inf;
-      p = some ? p : 0.f;
-      q = some ? q : 0.f;
       const float d = p - q, back = d - p;
-      s += (double)d;
-      lost += (p - (d - back)) - (q + back);  // p - q = d + this
+      const float err = (p - (d - back)) - (q + back);  // p - q = d + err, unless d overflows: then err is no number
+      s += (double)(d > 0.f ? d : 0.f);
+      lost += d > 0.f ? err : 0.f;
     } else {
-      s += (double)(p > 0.f && p < inf && v != r.hot ? p : 0.f);
+      s += (double)(p > 0.f && v != r.hot ? p : 0.f);
     }
   };
   int v = lo + lane;
@@ -70,15 +77,15 @@ __device__ __forceinline__ double warp_mass(const Row &r, int lo, int hi, int la
     float p[kUnroll], q[kUnroll];
 #pragma unroll
     for (int i = 0; i < kUnroll; ++i) {
-      p[i] = r.p[v + 32 * i];
-      q[i] = kDraft ? r.q[v + 32 * i] : 0.f;
+      p[i] = load_now(r.p + v + 32 * i);
+      q[i] = kDraft ? load_now(r.q + v + 32 * i) : 0.f;
     }
 #pragma unroll
     for (int i = 0; i < kUnroll; ++i) add(p[i], q[i], v + 32 * i);
   }
   for (; v < hi; v += 32) add(r.p[v], kDraft ? r.q[v] : 0.f, v);
   s = warp_sum_f64(s + (double)lost);
-  if (kDraft && !(s < (double)inf)) {  // a difference beyond fp32's range: once more in fp64
+  if (!(s < __longlong_as_double(0x7ff0000000000000LL))) {  // an infinity, or a difference beyond fp32's range: once more
     s = 0.0;
     for (v = lo + lane; v < hi; v += 32) s += r.mass(v);
     s = warp_sum_f64(s);
@@ -127,11 +134,9 @@ struct Shared {
   double sum[kWarps];   // masses of the warps' chunks
   double total;         // of the block's slice
   int n, count;
-  int pick;
-  double base;
 };
 
-__global__ void __launch_bounds__(kWarps * 32) accept_kernel(AcceptArgs a) {
+__global__ void __launch_bounds__(kWarps * 32, kBlocksSm) accept_kernel(AcceptArgs a) {
   __shared__ Shared sh;
   cg::cluster_group cluster = cg::this_cluster();
   const int rank = cluster.block_rank(), blocks = cluster.num_blocks();
@@ -140,14 +145,16 @@ __global__ void __launch_bounds__(kWarps * 32) accept_kernel(AcceptArgs a) {
   const int T = a.T;
 
   if (warp == 0) {  // every block of the cluster tests the drafts for itself
+    // a draft past the sequence's own number is read all the same, so that its number and its token come together
     const int count = a.count ? max(0, min(T, a.count[b])) : T;
     bool stands = false;
-    if (lane < count) {
+    if (lane < T) {
       const int d = a.tokens[(size_t)b * T + lane];
-      if (d >= 0 && d < a.vocab) {
+      const double u = a.u[(size_t)b * (T + 1) + lane];
+      if (lane < count && d >= 0 && d < a.vocab) {
         const double p = a.target[((size_t)b * (T + 1) + lane) * a.ld_target + d];
         const double q = a.draft ? (double)a.draft[((size_t)b * T + lane) * a.ld_draft + d] : 1.0;
-        stands = (double)a.u[(size_t)b * (T + 1) + lane] * q < p;  // 24 x 24 bits: exact
+        stands = u * q < p;  // 24 x 24 bits: exact
       }
     }
     const unsigned fell = ~__ballot_sync(0xffffffffu, stands);
@@ -186,20 +193,18 @@ __global__ void __launch_bounds__(kWarps * 32) accept_kernel(AcceptArgs a) {
     }
     cluster.sync();
     total = before = 0.0;
-    double mass = 0.0;
     int owner = -1;
-    double goal = 0.0;
-    for (int i = 0; i < blocks; ++i) total += *cluster.map_shared_rank(&sh.total, i);
-    goal = u * total;
+    const double slices = lane < blocks ? *cluster.map_shared_rank(&sh.total, lane) : 0.0;
+    for (int i = 0; i < blocks; ++i) total += __shfl_sync(0xffffffffu, slices, i);
+    const double goal = u * total;
     double run = 0.0;
     for (int i = 0; i < blocks; ++i) {  // the first slice whose end passes the goal, else the last with mass
-      const double t = *cluster.map_shared_rank(&sh.total, i);
+      const double t = __shfl_sync(0xffffffffu, slices, i);
       if (t > 0.0) {
         owner = i;
         before = run;
-        mass = run + t;
         run += t;
-        if (mass > goal) break;
+        if (run > goal) break;
       }
     }
     mine = owner == rank;
@@ -216,24 +221,17 @@ __global__ void __launch_bounds__(kWarps * 32) accept_kernel(AcceptArgs a) {
   }
   if (!mine) return;
   const double goal = u * total;
-  if (threadIdx.x == 0) {  // the chunk in the slice, by the same rule
-    double run = before;
-    int pick = 0;
-    double base = before;
-    for (int i = 0; i < kWarps; ++i) {
-      if (sh.sum[i] > 0.0) {
-        pick = i;
-        base = run;
-        run += sh.sum[i];
-        if (run > goal) break;
-      }
+  int pick = 0;  // the chunk in the slice, by the same rule
+  double base = before, run = before;
+  for (int i = 0; i < kWarps; ++i) {
+    if (sh.sum[i] > 0.0) {
+      pick = i;
+      base = run;
+      run += sh.sum[i];
+      if (run > goal) break;
     }
-    sh.pick = pick;
-    sh.base = base;
   }
-  __syncthreads();
-  int f0 = min(hi, lo + sh.pick * chunk), f1 = min(hi, f0 + chunk);
-  double base = sh.base;
+  int f0 = min(hi, lo + pick * chunk), f1 = min(hi, f0 + chunk);
   while (f1 - f0 > kFine) {  // a long chunk: a part a warp, then one of them
     const int part = ((f1 - f0 + kWarps - 1) / kWarps + 31) / 32 * 32;
     const int p0 = min(f1, f0 + warp * part), p1 = min(f1, p0 + part);
@@ -241,9 +239,9 @@ __global__ void __launch_bounds__(kWarps * 32) accept_kernel(AcceptArgs a) {
     __syncthreads();  // the last sums have been read
     if (lane == 0) sh.sum[warp] = s;
     __syncthreads();
-    double run = base;
-    int pick = 0;
     double at = base;
+    run = base;
+    pick = 0;
     for (int i = 0; i < kWarps; ++i) {
       if (sh.sum[i] > 0.0) {
         pick = i;
@@ -265,10 +263,10 @@ __global__ void __launch_bounds__(kWarps * 32) accept_kernel(AcceptArgs a) {
 }  // namespace
 
 cudaError_t launch_accept(const AcceptArgs &a, int num_sms, cudaStream_t stream) {
-  // Blocks a sequence: up to the portable cluster of 8 while there are fewer than eight blocks an SM in all (uneven
-  // rows then average out), none with less than 2048 elements, one round of loads of a block.
+  // Blocks a sequence: up to the portable cluster of 8 as long as all of them fit the SMs at once (eight an SM; 1024 rows
+  // of 8000: 25 us, and 29 us with twice the blocks), none with less than 2048 elements, one round of loads of a block.
   int blocks = 1;
-  while (blocks < 8 && (long long)a.batch * blocks <= 8LL * num_sms && a.vocab / (blocks * 2) >= 2048) blocks *= 2;
+  while (blocks < 8 && (long long)a.batch * blocks * 2 <= (long long)kBlocksSm * num_sms && a.vocab / (blocks * 2) >= 2048) blocks *= 2;
   cudaLaunchConfig_t cfg{};
   cfg.gridDim = dim3((unsigned)a.batch * blocks);
   cfg.blockDim = dim3(kWarps * 32);
