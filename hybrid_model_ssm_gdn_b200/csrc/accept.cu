@@ -19,7 +19,7 @@
 // sequence's dependent steps: drafts, their probabilities, sums, totals, search.
 #include <cooperative_groups.h>
 
-#include "kernels.h"
+#include "prompt_kernels.h"
 
 namespace cg = cooperative_groups;
 

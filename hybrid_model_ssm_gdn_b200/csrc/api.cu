@@ -7,7 +7,7 @@
 #include <stdlib.h>
 #include <string.h>
 
-#include "kernels.h"
+#include "prompt_kernels.h"
 #include "sched.h"
 
 using namespace rssm;

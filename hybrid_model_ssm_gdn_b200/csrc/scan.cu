@@ -8,7 +8,7 @@
 // 16-byte reads and four shuffles that sum the four rows' columns.  Tokens are staged 16 at a time, the next ones on
 // their way.  The chain of tokens sets the time of few prompts, so blocks are as small as it takes to use the SMs.
 // Measured: two prompts of 301 tokens in all, 8 heads, 44 us, 0.2 us a token of the longer one.
-#include "kernels.h"
+#include "prompt_kernels.h"
 #include "packed.cuh"
 
 namespace rssm {

@@ -10,7 +10,7 @@
 // itself and pays its start, its loads and its whole chunk of products one after the other: 48 resumed prompts of 31
 // tokens on average (128 heads; 483 MB) take 157 us here and 342 us there.  Per token this kernel costs more (every 16 tokens the state is
 // cut anew, and mma.sync runs at a quarter of tcgen05's rate), so longer prompts go there.
-#include "kernels.h"
+#include "prompt_kernels.h"
 #include "packed.cuh"
 
 namespace rssm {

@@ -38,7 +38,7 @@
 // a context reports it, a call on the caller's own states has nothing else to show it.
 #include <cuda.h>
 
-#include "kernels.h"
+#include "prompt_kernels.h"
 #include "packed.cuh"
 #include "tcgen05.cuh"
 
