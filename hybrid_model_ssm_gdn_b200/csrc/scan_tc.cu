@@ -218,6 +218,10 @@ __global__ void __launch_bounds__(kTcThreads, 1)
 
   if (warp == kWarpLoad) {
     if (lane == 0) {
+      // Once any wait of the block has given up nothing more is asked for: a buffer may not be free then, nor the barrier's
+      // last phase over, so that another arrival on it would count for the wrong one.
+      auto stopped = [&] { return *(volatile int *)&sh.abort != 0; };
+      int asked_B = 0, asked_C = 0, asked_X = 0;  // chunks whose loads are on their way or done
       for (int c = 0; c < chunks; ++c) {
         const int t = t0 + c * Q, s = c & 1;
         unsigned char *b = sh.in[buffer_B<kState>(c)][0], *x = sh.in[buffer_X<kState>(c)][0];
@@ -225,31 +229,34 @@ __global__ void __launch_bounds__(kTcThreads, 1)
           if (kState) wait(sh.s_done[s], (c - 2) >> 1);
           else wait(sh.y2_done[s], (c - 2) >> 1);
         }
+        if (stopped()) break;
         mbar_arrive_expect_tx(&sh.full_B[s], 2 * kTile);
         tma_load_2d(b, &map_B, group * kCols, t, &sh.full_B[s]);
         tma_load_2d(b + kTile, &map_B, group * kCols + 64, t, &sh.full_B[s]);
+        asked_B = c + 1;
         if (!kState) {
           if (c > 0) {
             wait(sh.y1_done, c - 1);
             wait(sh.g_done, c - 1);
           }
+          if (stopped()) break;
           mbar_arrive_expect_tx(&sh.full_C, 2 * kTile);
           tma_load_2d(sh.in[0][0], &map_C, group * kCols, t, &sh.full_C);
           tma_load_2d(sh.in[0][1], &map_C, group * kCols + 64, t, &sh.full_C);
+          asked_C = c + 1;
         }
         if (!kState && c > 0) wait(sh.s_done[1 - s], (c - 1) >> 1);
+        if (stopped() || c == a.withhold) break;  // test hook: this chunk's X never comes
         mbar_arrive_expect_tx(&sh.full_X[s], 2 * kTile);
-        if (c == a.withhold) continue;  // test hook: this chunk's X never comes
         tma_load_3d(x, &map_x, 0, h0, t, &sh.full_X[s]);
         tma_load_3d(x + kTile, &map_x, 0, h1, t, &sh.full_X[s]);
+        asked_X = c + 1;
       }
-      if (*(volatile int *)&sh.abort) {  // otherwise every load has been consumed when the block ends
-        if (!kState) mbar_wait(&sh.full_C, (chunks - 1) & 1, wait.ws);
-        for (int c = chunks > 1 ? chunks - 2 : 0; c < chunks; ++c) {
-          mbar_wait(&sh.full_X[c & 1], (c >> 1) & 1, wait.ws);
-          mbar_wait(&sh.full_B[c & 1], (c >> 1) & 1, wait.ws);
-        }
-      }
+      // No copy outlives the block: each barrier's last phase that was asked for (the ones before it are over, or their
+      // waiters would have stopped the loop).  Without an abort the other warps wait for the same.
+      if (asked_C) mbar_wait(&sh.full_C, (asked_C - 1) & 1, wait.ws);
+      for (int c = max(0, asked_B - 2); c < asked_B; ++c) mbar_wait(&sh.full_B[c & 1], (c >> 1) & 1, wait.ws);
+      for (int c = max(0, asked_X - 2); c < asked_X; ++c) mbar_wait(&sh.full_X[c & 1], (c >> 1) & 1, wait.ws);
     }
     __syncwarp();
   } else if (warp == kWarpState || warp == kWarpToken) {

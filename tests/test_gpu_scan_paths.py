@@ -1,0 +1,53 @@
+"""Paths of the prompt scan that depend on lengths, sizes and waits, against the float64 oracle (needs a B200)."""
+
+import ctypes as C
+
+import numpy as np
+import pytest
+import torch
+
+from hybrid_model_ssm_gdn_b200 import abi, make_config
+from test_gpu_scan import compare, context, idx, make, on_gpu
+
+pytestmark = pytest.mark.gpu
+
+BF = torch.bfloat16
+
+
+def packed(lens):
+    return np.concatenate([[0], np.cumsum(lens)]).tolist()
+
+
+def workspace(H, P, G, total, nseq):
+    """Bytes of scratch for prompts of this size: more than 0 where they are cut into pieces."""
+    cfg = make_config("mamba2", nseq, H, P, 128, G, 1, 0, BF, A=torch.empty(H), D=torch.empty(H))
+    n = C.c_size_t()
+    assert abi.load().rssm_mamba2_scan_workspace(C.byref(cfg), total, nseq, C.byref(n)) == 0
+    return n.value
+
+
+@pytest.mark.parametrize("withheld", [1, 3])
+@pytest.mark.parametrize("H,P,G,lens,cut", [(4, 64, 1, (790, 610), False), (64, 8, 1, (3900,), True)])
+def test_a_load_missing_from_long_prompts_ends_and_recovers(cuda_ok, monkeypatch, H, P, G, lens, cut, withheld):
+    """One chunk's load withheld with several behind it: the block asks for no more, ends within the bound of its waits
+    and leaves NaN, and the launches after it give the oracle's values."""
+    offsets = packed(lens)
+    total = offsets[-1]
+    assert (workspace(H, P, G, total, len(lens)) > 0) == cut
+    d = make(31, BF, total, H, P, G, len(lens), decay=0.05)
+    g = on_gpu(d, BF)
+    tok = (g["x"], g["B"], g["C"], g["dt"])
+    monkeypatch.setenv("RSSM_WAIT_CYCLES", "2000000")
+    monkeypatch.setenv("RSSM_WITHHOLD_TILE", str(withheld))
+    layer = context(d, BF, len(lens))
+    monkeypatch.delenv("RSSM_WITHHOLD_TILE")
+    monkeypatch.delenv("RSSM_WAIT_CYCLES")
+    y = torch.full((total, H, P), 7.0, device="cuda")
+    layer.prefill(*tok, idx(offsets), y=y)
+    assert layer.get_error()[0] == abi.DEV_TIMEOUT
+    assert torch.isnan(y).all() and torch.isnan(layer.export(ring=False)["S"]).all()
+    layer.load_checkpoint(g["S"])
+    y.fill_(7.0)
+    layer.prefill(*tok, idx(offsets), y=y)
+    assert layer.get_error() == (0, -1)
+    compare(d, offsets, None, None, layer.export(ring=False)["S"].cpu().numpy(), y.cpu().numpy())
