@@ -107,12 +107,12 @@ constexpr float kLog2e = 1.4426950408889634f;
 struct Waiter {
   TcShared *sh;
   int *err;
-  int seq;
+  int slot;
   WaitSpec ws;
   __device__ __forceinline__ void operator()(uint64_t &bar, int phase) const {
     if (!mbar_wait_or_abort(&bar, phase & 1, &sh->abort, ws)) {
       *(volatile int *)&sh->abort = 1;
-      if (err) record_error(err, seq, RSSM_DEV_TIMEOUT);
+      if (err) record_error(err, slot, RSSM_DEV_TIMEOUT);
     }
   }
   // by a whole warp, whose lanes stay together
@@ -123,7 +123,7 @@ struct Waiter {
       const bool late = clock64() - t0 > ws.limit;
       if (late) {
         *(volatile int *)&sh->abort = 1;
-        if (err) record_error(err, seq, RSSM_DEV_TIMEOUT);
+        if (err) record_error(err, slot, RSSM_DEV_TIMEOUT);
       }
       if (__any_sync(0xffffffffu, late || *(volatile int *)&sh->abort)) return;
     }
@@ -214,7 +214,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
   __syncthreads();
   tm_fence_after();
   const uint32_t tm = sh.tmem;
-  const Waiter wait{&sh, a.err, pc.seq, {a.wait_cycles, 0}};
+  const Waiter wait{&sh, a.err, pc.slot, {a.wait_cycles, 0}};  // errors name the sequence, not the prompt's place
 
   if (warp == kWarpLoad) {
     if (lane == 0) {

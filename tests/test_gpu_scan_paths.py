@@ -51,3 +51,16 @@ def test_a_load_missing_from_long_prompts_ends_and_recovers(cuda_ok, monkeypatch
     layer.prefill(*tok, idx(offsets), y=y)
     assert layer.get_error() == (0, -1)
     compare(d, offsets, None, None, layer.export(ring=False)["S"].cpu().numpy(), y.cpu().numpy())
+
+
+def test_a_timeout_names_the_sequence(cuda_ok, monkeypatch):
+    """With slots, the index reported is the slot of a prompt that gave up, as for every other code."""
+    d = make(32, BF, 400, 4, 64, 2, 6)
+    g = on_gpu(d, BF)
+    monkeypatch.setenv("RSSM_WAIT_CYCLES", "2000000")
+    monkeypatch.setenv("RSSM_WITHHOLD_TILE", "1")
+    layer = context(d, BF, 6)
+    layer.prefill(g["x"], g["B"], g["C"], g["dt"], idx([0, 150, 400]), idx([5, 3]))
+    assert layer.get_error() == (abi.DEV_TIMEOUT, 3)  # both gave up: the lowest
+    S = layer.export(ring=False)["S"]
+    assert torch.isnan(S[[3, 5]]).all() and torch.equal(S[[0, 1, 2, 4]], g["S"][[0, 1, 2, 4]])
