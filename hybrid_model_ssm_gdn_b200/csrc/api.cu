@@ -524,9 +524,9 @@ rssm_status rssm_mamba2_prefill(rssm_ctx *x, const rssm_prompts *pr, const rssm_
   const cudaError_t e = launch_prefill_meta(p, meta_cur(x), meta_next(x), skip, x->cfg.nheads, err_word(x), st);
   if (e != cudaSuccess) return cuda_fail(e);
   x->parity ^= 1;
-  // all counts stay known as 0 where they were, or where every sequence starts again
-  if (!(x->pos == 0 || (!pr->slots && pr->nseq == x->cfg.batch))) x->pos = -1;
-  else x->pos = 0;
+  // Counts that were all 0 stay so.  Otherwise they are unknown, even where every sequence is named: the device may refuse
+  // prompts (a bad offset refuses all of them), whose sequences keep what they have buffered.
+  if (x->pos != 0) x->pos = -1;
   return RSSM_OK;
 }
 

@@ -64,3 +64,25 @@ def test_a_timeout_names_the_sequence(cuda_ok, monkeypatch):
     assert layer.get_error() == (abi.DEV_TIMEOUT, 3)  # both gave up: the lowest
     S = layer.export(ring=False)["S"]
     assert torch.isnan(S[[3, 5]]).all() and torch.equal(S[[0, 1, 2, 4]], g["S"][[0, 1, 2, 4]])
+
+
+def test_refused_prompts_leave_the_counts_known(cuda_ok):
+    """A prefill that the device refuses (prompts that resume on buffered records; a bad offset) changes nothing, so the
+    steps after it, the fold among them, give the bits of a context that never saw the call."""
+    batch, H, P, G = 3, 4, 64, 2
+    d = make(33, BF, 12 * batch, H, P, G, batch)
+    g = on_gpu(d, BF)
+    tok = (g["x"], g["B"], g["C"], g["dt"])
+    plain, refused, bad = (context(d, BF, batch) for _ in range(3))
+    for t in range(12):  # a window of 8: one fold
+        if t == 5:
+            refused.prefill(*tok, idx([0, 9, 10, 36]), resume=idx([1, 1, 1], torch.uint8))
+            assert refused.get_error() == (abi.DEV_BUFFERED, 0)
+            bad.prefill(*tok, idx([0, 9, 10, 37]))
+            assert bad.get_error() == (abi.DEV_PROMPT, 2)
+        now = tuple(v[t * batch:(t + 1) * batch].contiguous() for v in tok)
+        ys = [layer.mamba2_step(*now) for layer in (plain, refused, bad)]
+        assert torch.equal(ys[0], ys[1]) and torch.equal(ys[0], ys[2]), t
+    a, b, c = (layer.export(ring=False) for layer in (plain, refused, bad))
+    for e in (b, c):
+        assert torch.equal(a["S"], e["S"]) and torch.equal(a["meta"], e["meta"])
