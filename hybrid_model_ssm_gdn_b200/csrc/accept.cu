@@ -154,7 +154,7 @@ __global__ void __launch_bounds__(kWarps * 32, kBlocksSm) accept_kernel(AcceptAr
       if (lane < count && d >= 0 && d < a.vocab) {
         const double p = a.target[((size_t)b * (T + 1) + lane) * a.ld_target + d];
         const double q = a.draft ? (double)a.draft[((size_t)b * T + lane) * a.ld_draft + d] : 1.0;
-        stands = u * q < p;  // 24 x 24 bits: exact
+        stands = p > 0.0 && p < __longlong_as_double(0x7ff0000000000000LL) && u * q < p;  // 24 x 24 bits: exact
       }
     }
     const unsigned fell = ~__ballot_sync(0xffffffffu, stands);

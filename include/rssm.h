@@ -270,7 +270,7 @@ rssm_status rssm_shortconv_commit(const rssm_shortconv_config *cfg, int *cur, co
  * whose inclusive sum exceeds u_T times the sum over all v (the last v with mass if none does).  Without q (drafts
  * that were looked up, not sampled) q_j is 1 at d_j and 0 elsewhere.  Masses and their sums are 64-bit, and the product
  * above is exact.  Entries that are not positive finite numbers carry no mass; if max(p_n - q_n, 0) has none, p_n is
- * used, and if that has none next is -1.  A draft outside 0..vocab-1 never stands.
+ * used, and if that has none next is -1.  A draft outside 0..vocab-1, or to which the target gives no mass, never stands.
  *   target device fp32, row (b, j), j = 0..T, at target + (b (T+1) + j) ld_target;  draft likewise with T rows a
  *   sequence, or NULL;  tokens device int32 [batch][T];  count device int32 [batch] (drafts of sequence b, clamped to
  *   0..T) or NULL = T;  u device fp32 [batch][T+1] in [0, 1): u_0 .. u_{T-1} for the drafts, u_T for the draw;

@@ -110,7 +110,7 @@ def accept_drafts(target, tokens, u, draft=None, count=None):
             if not 0 <= d < V:
                 break
             q = 1.0 if draft is None else f64(draft[b, n, d])
-            if not f64(u[b, n]) * q < f64(target[b, n, d]):
+            if not _mass(target[b, n, d]) > 0 or not f64(u[b, n]) * q < f64(target[b, n, d]):
                 break
             n += 1
         p = _mass(target[b, n])

@@ -130,3 +130,19 @@ def test_rows_past_32_bits(cuda_ok):
         want = oracle_accept(target, tokens, u, q, None)
         np.testing.assert_array_equal(got[0].cpu().numpy(), want[0])
         np.testing.assert_array_equal(got[2].cpu().numpy(), want[1])
+
+
+@pytest.mark.parametrize("probs", [True, False])
+def test_drafts_that_the_target_gives_no_mass_fall(cuda_ok, probs):
+    """An entry that is not a positive finite number carries no mass, so a draft of it never stands, whatever the draft's
+    own probability: target inf, NaN, 0 and negative against q = -1, 0, 0.25 and u = 0 and 0.5."""
+    V = 64
+    cases = [(p, q, u) for p in (np.inf, np.nan, 0.0, -0.5) for q in (-1.0, 0.0, 0.25) for u in (0.0, 0.5)]
+    n = len(cases)
+    target = np.full((n, 2, V), 1.0 / V, np.float32)
+    draft = np.full((n, 1, V), 1.0 / (2 * V), np.float32)
+    tokens, us = np.full((n, 1), 7), np.full((n, 2), 0.25)
+    for i, (p, q, u) in enumerate(cases):
+        target[i, 0, 7], draft[i, 0, 7], us[i, 0] = p, q, u
+    acc = check(target, tokens, us, draft if probs else None)
+    assert (acc == 0).all()

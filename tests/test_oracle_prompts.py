@@ -141,3 +141,12 @@ def test_accept_draw_by_enumeration():
                 if want is None and run > uu * m.sum() * (1 + 1e-15) and m[v] > 0:
                     want = v
             assert nxt[0] == want
+
+
+def test_accept_needs_mass_at_the_draft():
+    """A draft whose target entry is not a positive finite number falls, whatever its own probability."""
+    for p in (np.inf, np.nan, 0.0, -1.0):
+        target, draft = np.full((1, 2, 4), 0.25), np.full((1, 1, 4), 0.25)
+        target[0, 0, 2], draft[0, 0, 2] = p, -0.5
+        for u in (0.0, 0.5):
+            assert accept_drafts(target, np.array([[2]]), np.array([[u, 0.5]]), draft)[0][0] == 0
