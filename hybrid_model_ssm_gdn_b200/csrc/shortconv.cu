@@ -101,12 +101,26 @@ struct Filter {
     r.widen(b);
     silu = a.silu;
   }
-  // v / (1 + exp(-v)), to about 2^-21 of it; where exp overflows the quotient is -0
+  // v / (1 + exp(-v)).  For bf16 outputs with the rounding of v log2(e), which costs |v| 2^-24 of the exponential, far below
+  // their own rounding of 2^-9; where exp(-v) passes 2^126 (v < -87.3) the quotient, below 2^-119, is -0 (a form that
+  // kept those, too, cost prompts 20 % more time).  For fp32 outputs to within 2^-20 of the value down to its last bits: the
+  // rounding is given back to first order, and for v < 0 the quotient is v h h / (1 + h h) with h = exp(v / 2), which stays
+  // in the normal range as long as the result has bits.
   __device__ __forceinline__ float act(float v) const {
+    constexpr float kL = 1.4426950408889634f, kRest = (float)(1.4426950408889634 - (double)kL), kLn2 = 0.69314718f;
     float e, r;
-    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e) : "f"(v * -1.4426950408889634f));
-    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(1.f + e));
-    return silu ? v * r : v;
+    if constexpr (sizeof(TI) == 2) {
+      asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e) : "f"(v * -kL));
+      asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(1.f + e));
+      return silu ? v * r : v;
+    } else {
+      const float a = fminf(fabsf(v), 1e6f), t = a * (-0.5f * kL);
+      asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e) : "f"(t));
+      const float h = fmaf(e * kLn2, fmaf(a, -0.5f * kRest, fmaf(a, -0.5f * kL, -t)), e);
+      asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(fmaf(h, h, 1.f)));
+      const float q = v * r;
+      return silu ? v < 0.f ? q * h * h : q : v;
+    }
   }
   __device__ __forceinline__ void apply(const float (&win)[K - 1][V], const float (&x)[V], float (&o)[V]) const {
 #pragma unroll

@@ -232,7 +232,8 @@ rssm_status rssm_mamba2_prefill(rssm_ctx *ctx, const rssm_prompts *pr, const rss
 /* ---------------------------------------------------------------- short convolution
  * The causal depthwise filter in front of a layer's inputs (x, B, C of Mamba-2; q, k, v of GDN):
  *   out[t][c] = act(bias[c] + sum_{k < K} weight[c][k] in[t - (K-1) + k][c]),
- * summed in fp32 and rounded once to the input type.  Its state follows the scheme of the replay buffer: a ring of
+ * summed in fp32 and rounded once to the input type (SiLU in fp32 is within 2^-20 of its value; with bf16 results whose
+ * magnitude is below 2^-119 may be 0).  Its state follows the scheme of the replay buffer: a ring of
  * the last raw inputs, hist [batch][ring][channels] in the input type, with a cursor cur [batch] (the slot of the next
  * token, 0..ring-1; any other value is taken modulo ring).  A draft is a tentative row and commit moves the cursor.
  * Row r of `in` starts at in + r * in_stride elements; outputs that overlap its rows are refused.  Outputs are up to three contiguous tensors out[s]

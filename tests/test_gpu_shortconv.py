@@ -165,3 +165,22 @@ def test_outputs_between_the_rows_of_their_input(cuda_ok):
         with pytest.raises(RuntimeError, match="RSSM_ERR_ARG"):
             shortconv_step(c.hist, c.cur, x, c.w, c.b, out=(bad.view(2, 64),), **c.kw)
     c.check_state()
+
+
+@pytest.mark.parametrize("dtype", [BF, F32])
+def test_silu_over_its_whole_range(cuda_ok, dtype):
+    """act alone (taps 0, 0, 0, 1): to 2^-20 of its value, the rounding to the type apart.  fp32 down to where the result
+    leaves the normal numbers (half a step of 2^-149 there, and one before the last product).  bf16 results below 2^-119
+    may be 0: exp(-v) is beyond 2^126 only for v < -87.33, where |v| exp(v) <= 87.4 * 2^-126."""
+    v = np.linspace(-96, 96, 20 * 8 * 64).astype(np.float32).reshape(-1, 8)
+    c = Case(6, dtype, (8,), 4, 1, bias=False)
+    v = c.f(v)
+    c.w.copy_(torch.tensor([0.0, 0.0, 0.0, 1.0]))
+    c.hist.zero_()
+    out, = shortconv_prefill(c.hist, c.cur, c.dev(v), c.w, None, idx([0, len(v)]), **c.kw)
+    v = v.astype(np.float64)
+    ref = np.where(v < 0, v * np.exp(-np.abs(v)), v) / (1 + np.exp(-np.abs(v)))
+    err = np.abs(out.double().cpu().numpy() - ref)
+    bound = (2.0 ** -20 + (torch.finfo(BF).eps / 2 if dtype == BF else 0)) * np.abs(ref)
+    bound += 2.0 ** -119 if dtype == BF else 2.0 ** -148
+    assert (err / bound).max() <= 1.0
