@@ -218,18 +218,17 @@ __global__ void __launch_bounds__(kTcThreads, 1)
 
   if (warp == kWarpLoad) {
     if (lane == 0) {
-      // Once any wait of the block has given up nothing more is asked for: a buffer may not be free then, nor the barrier's
-      // last phase over, so that another arrival on it would count for the wrong one.
+      // After a wait of the block has given up nothing more is asked for than the chunk's own loads.  A barrier is armed again
+      // only with its last phase over, and the products of the chunk that it was for show that as long as nobody gave up:
+      // s_done of chunk c - 2 for B and X, y1_done of chunk c - 1 for C.
       auto stopped = [&] { return *(volatile int *)&sh.abort != 0; };
       int asked_B = 0, asked_C = 0, asked_X = 0;  // chunks whose loads are on their way or done
       for (int c = 0; c < chunks; ++c) {
         const int t = t0 + c * Q, s = c & 1;
         unsigned char *b = sh.in[buffer_B<kState>(c)][0], *x = sh.in[buffer_X<kState>(c)][0];
-        if (c > 1) {  // with outputs, that chunk's state was waited for with the last X
-          if (kState) wait(sh.s_done[s], (c - 2) >> 1);
-          else wait(sh.y2_done[s], (c - 2) >> 1);
-        }
+        if (kState && c > 1) wait(sh.s_done[s], (c - 2) >> 1);  // with outputs, it was waited for with the last X
         if (stopped()) break;
+        if (!kState && c > 1) wait(sh.y2_done[s], (c - 2) >> 1);
         mbar_arrive_expect_tx(&sh.full_B[s], 2 * kTile);
         tma_load_2d(b, &map_B, group * kCols, t, &sh.full_B[s]);
         tma_load_2d(b + kTile, &map_B, group * kCols + 64, t, &sh.full_B[s]);
@@ -238,22 +237,21 @@ __global__ void __launch_bounds__(kTcThreads, 1)
           if (c > 0) {
             wait(sh.y1_done, c - 1);
             wait(sh.g_done, c - 1);
+            if (stopped()) break;
           }
-          if (stopped()) break;
           mbar_arrive_expect_tx(&sh.full_C, 2 * kTile);
           tma_load_2d(sh.in[0][0], &map_C, group * kCols, t, &sh.full_C);
           tma_load_2d(sh.in[0][1], &map_C, group * kCols + 64, t, &sh.full_C);
           asked_C = c + 1;
         }
         if (!kState && c > 0) wait(sh.s_done[1 - s], (c - 1) >> 1);
-        if (stopped() || c == a.withhold) break;  // test hook: this chunk's X never comes
+        if (c == a.withhold) break;  // test hook: this chunk's X never comes
         mbar_arrive_expect_tx(&sh.full_X[s], 2 * kTile);
         tma_load_3d(x, &map_x, 0, h0, t, &sh.full_X[s]);
         tma_load_3d(x + kTile, &map_x, 0, h1, t, &sh.full_X[s]);
         asked_X = c + 1;
       }
-      // No copy outlives the block: each barrier's last phase that was asked for (the ones before it are over, or their
-      // waiters would have stopped the loop).  Without an abort the other warps wait for the same.
+      // No copy outlives the block: the last phase of each barrier that was asked for.
       if (asked_C) mbar_wait(&sh.full_C, (asked_C - 1) & 1, wait.ws);
       for (int c = max(0, asked_B - 2); c < asked_B; ++c) mbar_wait(&sh.full_B[c & 1], (c >> 1) & 1, wait.ws);
       for (int c = max(0, asked_X - 2); c < asked_X; ++c) mbar_wait(&sh.full_X[c & 1], (c >> 1) & 1, wait.ws);
