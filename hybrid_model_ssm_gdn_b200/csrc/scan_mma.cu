@@ -36,6 +36,47 @@ __device__ __forceinline__ void copy16(void *dst, const void *src, bool live) {
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(smem_u32(dst)), "l"(src), "r"(live ? 16 : 0) : "memory");
 }
 
+// whether one of 8 bf16 values is an infinity or no number: times 0 those give no number, all others 0
+__device__ __forceinline__ bool not_finite(uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
+  const __nv_bfloat162 zero = __floats2bfloat162_rn(0.f, 0.f);
+  __nv_bfloat162 s = zero;
+  for (const uint32_t v : {a, b, c, d}) s = __hfma2(*reinterpret_cast<const __nv_bfloat162 *>(&v), zero, s);
+  return *reinterpret_cast<const uint32_t *>(&s) & 0x7fff7fffu;
+}
+
+// Fragments of X, 16 tokens by 16 values, with values that are not finite as 0, and of Y with NaN from the first of them on.
+struct Cleared {
+  float y[8];
+  uint32_t x[4];
+};
+__device__ __noinline__ Cleared clear_not_finite(float y0, float y1, float y2, float y3, float y4, float y5, float y6, float y7,
+                                                 uint32_t x0, uint32_t x1, uint32_t x2, uint32_t x3) {
+  Cleared f{{y0, y1, y2, y3, y4, y5, y6, y7}, {x0, x1, x2, x3}};
+  const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    int from = kTok;  // first such token of column 8 i + g
+#pragma unroll
+    for (int k = 3; k >= 0; --k) {
+      uint32_t &w = f.x[2 * i + (k >> 1)];
+      const uint32_t mask = k & 1 ? 0x7f800000u : 0x7f80u;
+      if ((w & mask) == mask) {
+        from = 2 * t + (k & 1) + 8 * (k >> 1);
+        w &= k & 1 ? 0xffffu : 0xffff0000u;
+      }
+    }
+    from = min(from, __shfl_xor_sync(0xffffffffu, from, 1));
+    from = min(from, __shfl_xor_sync(0xffffffffu, from, 2));
+#pragma unroll
+    for (int e = 0; e < 2; ++e) {
+      const int col = __shfl_sync(0xffffffffu, from, 4 * (2 * t + e));
+      if (g >= col) f.y[4 * i + e] = __int_as_float(0x7fffffff);
+      if (g + 8 >= col) f.y[4 * i + 2 + e] = __int_as_float(0x7fffffff);
+    }
+  }
+  return f;
+}
+
 __global__ void __launch_bounds__(128, 4) scan_mma_kernel(ScanArgs a, Prompts pr) {
   __shared__ MmaStage st[2];
   __shared__ PieceWord found;
@@ -172,7 +213,17 @@ __global__ void __launch_bounds__(128, 4) scan_mma_kernel(ScanArgs a, Prompts pr
         }
       }
       uint32_t x0, x1, x2, x3;  // tokens 0-7, 8-15 of rows p0.., of rows p0 + 8..
-      ldmatrix_x4_trans(m.x + ((q & 1) * 8 + r8) * kPitchX + 2 * p0 + (q >> 1) * 16, x0, x1, x2, x3);
+      const unsigned char *xt = m.x + ((q & 1) * 8 + r8) * kPitchX + 2 * p0 + (q >> 1) * 16;
+      ldmatrix_x4_trans(xt, x0, x1, x2, x3);
+      // M's zeros above the diagonal would carry values that are not finite to earlier tokens: they enter as 0, and the
+      // outputs from the first of them on become NaN here
+      const bool odd = __any_sync(0xffffffffu, not_finite(x0, x1, x2, x3));
+      if (odd) {
+        const Cleared f = clear_not_finite(y[0][0], y[0][1], y[0][2], y[0][3], y[1][0], y[1][1], y[1][2], y[1][3], x0, x1, x2, x3);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) y[i >> 2][i & 3] = f.y[i];
+        x0 = f.x[0]; x1 = f.x[1]; x2 = f.x[2]; x3 = f.x[3];
+      }
       mma_16816(y[0], hi[0], hi[1], hi[2], hi[3], x0, x1);
       mma_16816(y[0], lo[0], lo[1], lo[2], lo[3], x0, x1);
       mma_16816(y[1], hi[0], hi[1], hi[2], hi[3], x2, x3);
@@ -187,6 +238,7 @@ __global__ void __launch_bounds__(128, 4) scan_mma_kernel(ScanArgs a, Prompts pr
         }
       }
       // S <- decay S + (weighted X)^T B
+      if (odd) ldmatrix_x4_trans(xt, x0, x1, x2, x3);
       uint32_t xh[4], xl[4];
       const uint32_t xs[4] = {x0, x2, x1, x3};  // as a left operand: rows g, g + 8 of tokens 0-7, then of 8-15
 #pragma unroll

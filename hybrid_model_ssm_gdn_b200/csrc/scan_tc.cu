@@ -67,6 +67,7 @@ struct TcShared {
   uint64_t g_done, y1_done, y20_done, y2_done[2], y_free, s_done[2], sp_ready[2], m_ready[2], xs_ready[2], drained[2];
   uint32_t tmem;
   int abort, number;
+  int not_finite;                   // X held values that are not finite (see overwrite)
   PieceWord found;
 };
 constexpr int kTcSmem = (int)sizeof(TcShared);
@@ -85,6 +86,7 @@ struct TcArgs {
   int piece_len;
   int by_length;            // hand out the prompts by length (at most kByLength of them, not cut)
   const float *A, *D;
+  const __nv_bfloat16 *x;   // [total][H][P]
   const __nv_bfloat16 *dt;  // [total][H]
   float *S;                 // [nslots][H][P][128]
   float *y;                 // [total][H][P]
@@ -138,12 +140,62 @@ __device__ __forceinline__ void warp_arrive(uint64_t &bar, int lane) {
   if (lane == 0) mbar_arrive(&bar);
 }
 
+// the values of a row of X, 64 bf16, that are not finite become 0
+__device__ __noinline__ void clear_not_finite(unsigned char *row) {
+  for (int i = 0; i < 64; ++i) {
+    unsigned short *v = reinterpret_cast<unsigned short *>(row) + i;
+    if ((*v & 0x7f80) == 0x7f80) *v = 0;
+  }
+  fence_async_smem();
+}
+
+// A wait gave up: nothing that looks like a result stays.  Or x holds values that are not finite: M X saw zeros in their
+// place, so that its own zeros above the diagonal do not carry them to earlier tokens, and from the first of them on
+// the row's outputs and its state become NaN here.  What to overwrite is worked out anew, from shared memory and x: kept
+// in registers all along it made the whole kernel 3 % slower, and within the kernel's own code 1.5 %.
+template <bool kState>
+__device__ __noinline__ void overwrite(const TcArgs &a, TcShared &sh) {
+  const bool gave_up = *(volatile int *)&sh.abort;
+  if (!kState && threadIdx.x % 32 == 0) bulk_wait_all();  // this warp's own stores of Y
+  __syncthreads();
+  const volatile PieceWord &w = sh.found;
+  const int per = a.G * a.pairs, r = a.H / a.G, u = blockIdx.x % per;
+  const int ha = u / a.pairs * r + 2 * (u % a.pairs), hb = min(ha + 2, (u / a.pairs + 1) * r);
+  const int first = (*(volatile int *)&sh.number - (w.begin / a.piece_len + w.seq)) * a.piece_len;
+  const int len = w.end - w.begin, n = min(a.piece_len, len - first);
+  float *S = nullptr;
+  if (kState) S = a.seg + (size_t)sh.number * a.H * a.P * kCols;
+  else if (first + n >= len) S = a.S + (size_t)w.slot * a.H * a.P * kCols;
+  const float nan = __int_as_float(0x7fffffff);
+  int *from = reinterpret_cast<int *>(sh.cl);  // per value of a row, the first token of the piece to overwrite
+  for (int h = ha; h < hb; ++h) {
+    for (int p = threadIdx.x; p < a.P; p += kTcThreads) from[p] = gave_up ? 0 : n;
+    __syncthreads();
+    if (!gave_up) {
+      for (int i = threadIdx.x / 32; i < n; i += kTcThreads / 32)
+        for (int p = threadIdx.x % 32; p < a.P; p += 32) {
+          const float v = __bfloat162float(a.x[((size_t)(w.begin + first + i) * a.H + h) * a.P + p]);
+          if (!(fabsf(v) < __int_as_float(0x7f800000))) atomicMin(&from[p], i);
+        }
+      __syncthreads();
+    }
+    if (S)
+      for (int i = threadIdx.x; i < a.P * kCols; i += kTcThreads)
+        if (from[i / kCols] < n) S[(size_t)h * a.P * kCols + i] = nan;
+    if (!kState)
+      for (int i = threadIdx.x / 32; i < n; i += kTcThreads / 32)
+        for (int p = threadIdx.x % 32; p < a.P; p += 32)
+          if (i >= from[p]) a.y[((size_t)(w.begin + first + i) * a.H + h) * a.P + p] = nan;
+    __syncthreads();
+  }
+}
+
 // kState: only the state at the piece's end, from zero (first pass of prompts that are cut into pieces)
 template <bool kState>
 __global__ void __launch_bounds__(kTcThreads, 1)
     scan_tc_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_constant__ CUtensorMap map_B,
-                   const __grid_constant__ CUtensorMap map_C, const __grid_constant__ CUtensorMap map_y, TcArgs a,
-                   Prompts pr) {
+                   const __grid_constant__ CUtensorMap map_C, const __grid_constant__ CUtensorMap map_y,
+                   const __grid_constant__ TcArgs a, Prompts pr) {
   extern __shared__ __align__(1024) unsigned char raw[];
   TcShared &sh = *reinterpret_cast<TcShared *>(raw);
   if (smem_u32(raw) & 1023u) {
@@ -205,7 +257,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                         &sh.m_ready[1], &sh.xs_ready[0], &sh.xs_ready[1]};
     for (uint64_t *b : team) mbar_init(b, 8);
     mbar_init(&sh.tab_free, kState ? 8 : 16);
-    sh.abort = 0;
+    sh.abort = sh.not_finite = 0;
     sh.number = number;
     fence_barrier_init();
   }
@@ -510,6 +562,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
             wait(sh.full_X[b], c >> 1);
             wait(sh.y1_done, c);
             tm_fence_after();
+            uint32_t seen = 0;  // stays 0 (or -0) while the row's values are finite: the others times 0 give NaN
 #pragma unroll 1
             for (int part = 0; part < 2; ++part) {
               uint32_t v[32] = {};
@@ -525,12 +578,17 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                 for (int j = 0; j < 4; ++j) {
                   uint32_t &lo = v[8 * i + 2 * j], &hi = v[8 * i + 2 * j + 1];
                   float y0, y1;
+                  asm("fma.rn.bf16x2 %0, %1, %2, %0;" : "+r"(seen) : "r"(xs[j]), "r"(0));
                   unpack2(fma2(pack2(xs[j] << 16, xs[j] & 0xffff0000u), D2, mul2(pack2(lo, hi), rise2)), y0, y1);
                   lo = __float_as_uint(y0);
                   hi = __float_as_uint(y1);
                 }
               }
               tm_st32(tm + lanes + kColY + 64 * g + 32 * part, v);
+            }
+            if ((seen & 0x7fff7fffu) && row < ntok - c * Q) {
+              clear_not_finite(sh.in[buffer_X<kState>(c)][g] + row * 128);
+              *(volatile int *)&sh.not_finite = 1;
             }
           }
           tm_wait_st();
@@ -692,28 +750,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
     tm_fence_after();
     tm_free(tm, 512);
   }
-  // A wait gave up: nothing that looks like a result stays.  What to overwrite is worked out anew, from shared memory: kept
-  // in registers all along it made the whole kernel 3 % slower.
-  if (*(volatile int *)&sh.abort) {
-    if (!kState && threadIdx.x % 32 == 0) bulk_wait_all();  // this warp's own stores of Y
-    __syncthreads();
-    const volatile PieceWord &w = sh.found;
-    const int per = a.G * a.pairs, r = a.H / a.G, u = blockIdx.x % per;
-    const int ha = u / a.pairs * r + 2 * (u % a.pairs), hb = min(ha + 2, (u / a.pairs + 1) * r);
-    const int first = (*(volatile int *)&sh.number - (w.begin / a.piece_len + w.seq)) * a.piece_len;
-    const int len = w.end - w.begin, n = min(a.piece_len, len - first);
-    float *S = nullptr;
-    if (kState) S = a.seg + (size_t)sh.number * a.H * a.P * kCols;
-    else if (first + n >= len) S = a.S + (size_t)w.slot * a.H * a.P * kCols;
-    const float nan = __int_as_float(0x7fffffff);
-    for (int h = ha; h < hb; ++h) {
-      if (S)
-        for (int i = threadIdx.x; i < a.P * kCols; i += kTcThreads) S[(size_t)h * a.P * kCols + i] = nan;
-      if (!kState)
-        for (int i = threadIdx.x / 32; i < n; i += kTcThreads / 32)
-          for (int p = threadIdx.x % 32; p < a.P; p += 32) a.y[((size_t)(w.begin + first + i) * a.H + h) * a.P + p] = nan;
-    }
-  }
+  if (*(volatile int *)&sh.abort || *(volatile int *)&sh.not_finite) overwrite<kState>(a, sh);
 }
 
 // States at the starts of the pieces of prompts that are cut: seg[s] <- state before piece s, from the pieces' own end
@@ -783,6 +820,7 @@ cudaError_t launch_scan_tc(const ScanArgs &s, const Prompts &pr, cudaStream_t st
   a.pairs = (s.H / s.G + 1) / 2;
   a.piece_len = s.piece_len;
   a.A = s.A; a.D = s.D; a.dt = static_cast<const __nv_bfloat16 *>(s.dt); a.S = s.S; a.y = s.y;
+  a.x = static_cast<const __nv_bfloat16 *>(s.x);
   a.err = s.err; a.wait_cycles = s.wait_cycles; a.withhold = s.withhold;
   const int pieces = prompt_pieces(pr.total, pr.nseq, s.piece_len);
   const bool cut_up = s.piece_len <= pr.total;

@@ -216,8 +216,8 @@ rssm_status rssm_mamba2_scan_workspace(const rssm_config *cfg, int total, int ns
  *   S device fp32 [batch][H][P][N], the prompts' sequences rewritten;  y device fp32 [total][H][P];
  *   work device, 256-byte aligned, >= rssm_mamba2_scan_workspace bytes (NULL if that is 0), free again when the
  *   call's work on the stream is done.
- * With bf16 inputs a value of x that is not finite can make outputs of up to 127 tokens before it in its prompt NaN (chunks
- * of tokens are multiplied by weights of which those are 0); other prompts are not touched.
+ * From a value of x that is not finite on, its row's outputs in that prompt are not finite, nor its row of the state; no
+ * other output is touched.
  * Heads whose asynchronous copies did not arrive within the bound of the waits have NaN in y and S. */
 rssm_status rssm_mamba2_scan(const rssm_config *cfg, const rssm_prompts *pr, const rssm_tokens *tok, float *S, float *y,
                              void *work, size_t work_bytes, rssm_stream stream);

@@ -6,7 +6,7 @@ import numpy as np
 import pytest
 import torch
 
-from hybrid_model_ssm_gdn_b200 import abi, make_config
+from hybrid_model_ssm_gdn_b200 import abi, make_config, mamba2_scan
 from test_gpu_scan import compare, context, idx, make, on_gpu
 
 pytestmark = pytest.mark.gpu
@@ -86,3 +86,67 @@ def test_refused_prompts_leave_the_counts_known(cuda_ok):
     a, b, c = (layer.export(ring=False) for layer in (plain, refused, bad))
     for e in (b, c):
         assert torch.equal(a["S"], e["S"]) and torch.equal(a["meta"], e["meta"])
+
+
+@pytest.mark.parametrize("value", [np.inf, -np.inf, np.nan])
+@pytest.mark.parametrize("H,P,G,lens,cut", [(4, 64, 2, (40, 1, 23), False), (3, 24, 1, (33, 16), False),
+                                            (4, 64, 2, (300, 1, 260), False), (3, 40, 1, (128, 400), False),
+                                            (2, 64, 1, (1900,), True), (64, 8, 1, (3900,), True)])
+def test_values_that_are_not_finite_reach_no_earlier_token(cuda_ok, H, P, G, lens, cut, value):
+    """From a value of x that is not finite on, its head's row p has no finite outputs and no finite state; everything
+    else, the same row before it above all, keeps its bits."""
+    offsets = packed(lens)
+    total, n = offsets[-1], len(lens)
+    assert (workspace(H, P, G, total, n) > 0) == cut
+    d = make(34, BF, total, H, P, G, n, decay=0.2)
+    g = on_gpu(d, BF)
+    r = np.random.default_rng(35)
+    at = {(total - 1, 0, 1), (offsets[1] - 1, H - 1, P - 1), (0, 0, 0)}
+    at |= {(int(r.integers(total)), int(r.integers(H)), int(r.integers(P))) for _ in range(6)}
+    hit_y = torch.zeros(total, H, P, dtype=torch.bool, device="cuda")
+    hit_S = torch.zeros(n, H, P, dtype=torch.bool, device="cuda")
+    x = g["x"].clone()
+    for t, h, p in at:
+        i = int(np.searchsorted(offsets, t, side="right")) - 1
+        x[t, h, p] = value
+        hit_y[t:offsets[i + 1], h, p] = True
+        hit_S[i, h, p] = True
+    got = []
+    for xs in (g["x"], x):
+        S = g["S"].clone()
+        y = mamba2_scan(S, xs, g["B"], g["C"], g["dt"], g["A"], g["D"], idx(offsets), resume=idx([1] * n, torch.uint8))
+        got.append((S, y))
+    (S0, y0), (S1, y1) = got
+    assert torch.isfinite(y0).all() and torch.isfinite(S0).all()
+    assert torch.equal(y0[~hit_y], y1[~hit_y]) and torch.equal(S0[~hit_S], S1[~hit_S])
+    assert not torch.isfinite(y1[hit_y]).any() and not torch.isfinite(S1[hit_S]).any()
+
+
+@pytest.mark.parametrize("key", ["B", "C", "dt"])
+@pytest.mark.parametrize("lens", [(40, 1, 23), (300, 1, 260)])
+def test_other_inputs_that_are_not_finite_reach_no_earlier_token(cuda_ok, lens, key):
+    """NaN and infinities in B, C or dt: tokens before theirs and other prompts keep their bits, with C all others do."""
+    offsets = packed(lens)
+    total, n = offsets[-1], len(lens)
+    d = make(38, BF, total, 4, 64, 2, n)
+    g = on_gpu(d, BF)
+    for value in (np.nan, np.inf):
+        for t in (offsets[1] - 10, offsets[1], total - 1, offsets[2] + 17):
+            bad = {k: v.clone() for k, v in g.items()}
+            bad[key][t, 0, ...] = value  # the first group's heads, or the first head
+            got = []
+            for e in (g, bad):
+                S = e["S"].clone()
+                y = mamba2_scan(S, e["x"], e["B"], e["C"], e["dt"], e["A"], e["D"], idx(offsets),
+                                resume=idx([1] * n, torch.uint8))
+                got.append((S, y))
+            (S0, y0), (S1, y1) = got
+            i = int(np.searchsorted(offsets, t, side="right")) - 1
+            heads = 1 if key == "dt" else 2
+            hit = torch.zeros_like(y0, dtype=torch.bool)
+            hit[t:(t + 1 if key == "C" else offsets[i + 1]), :heads] = True
+            assert torch.equal(y0[~hit], y1[~hit])
+            assert not torch.isfinite(y1[t, :heads]).any()
+            others = [s for s in range(n) if s != i]
+            assert torch.equal(S0[others], S1[others])
+            assert torch.equal(S0, S1) if key == "C" else not torch.isfinite(S1[i, :heads]).any()
