@@ -158,7 +158,8 @@ class ReplaySSM:
 
     def prefill(self, x, B, C_, dt, offsets, slots=None, resume=None, y=None, workspace=None):
         """Run packed prompts (rssm_mamba2_prefill): x [total][H][P], B, C [total][G][128], dt [total][H];
-        offsets int32 [n+1]; slots int32 [n] (sequence of each prompt), resume uint8 [n] -> y fp32 [total][H][P]."""
+        offsets int32 [n+1]; slots int32 [n] (sequence of each prompt), resume uint8 [n] -> y fp32 [total][H][P], with NaN
+        for refused prompts where the call makes it."""
         H, P, G = self.nheads, self.rows, self.ngroups
         device = _device(x, "x")
         if self.arena.get_device() != device:
@@ -263,12 +264,13 @@ def _addr(t):
     return None if t is None else t.data_ptr()
 
 
-def _prompts(total, offsets, slots, resume, device):
+def _prompts(total, offsets, slots, resume, device, fresh):
     n = offsets.numel() - 1
     if n < 1:
         raise ValueError(f"offsets: needs at least 2 elements, got {n + 1}")
     return abi.Prompts(total, n, _arr(offsets, torch.int32, "offsets", (n + 1,), device),
-                       _arr(slots, torch.int32, "slots", (n,), device), _arr(resume, torch.uint8, "resume", (n,), device))
+                       _arr(slots, torch.int32, "slots", (n,), device), _arr(resume, torch.uint8, "resume", (n,), device),
+                       fresh)
 
 
 def _in_dtype(t, name):
@@ -281,7 +283,7 @@ def _scan_args(x, B, C_, dt, offsets, slots, resume, y, H, P, G, dtype, device):
     total = x.shape[0]
     tok = abi.Tokens(_arr(x, dtype, "x", (total, H, P), device), _arr(B, dtype, "B", (total, G, 128), device),
                      _arr(C_, dtype, "C", (total, G, 128), device), _arr(dt, dtype, "dt", (total, H), device))
-    pr = _prompts(total, offsets, slots, resume, device)
+    pr = _prompts(total, offsets, slots, resume, device, y is None)
     if y is None:
         y = x.new_empty((total, H, P), dtype=torch.float32)
     else:
@@ -308,7 +310,8 @@ def mamba2_scan(S, x, B, C_, dt, A, D, offsets, slots=None, resume=None, y=None,
     """Mamba-2 over packed prompts on the caller's states (rssm_mamba2_scan): S fp32 [batch][H][P][128], the prompts'
     sequences rewritten in place; x [total][H][P], B, C [total][G][128], dt [total][H] (bf16 or fp32), A, D fp32 [H];
     prompt i is rows offsets[i] .. offsets[i+1]-1 and belongs to S[slots[i]] (S[i] without slots), from which it
-    continues where resume[i] is set -> y fp32 [total][H][P]."""
+    continues where resume[i] is set -> y fp32 [total][H][P].  Without ``y``, rows of refused prompts (an offset or slot out
+    of range: all rows; a slot named twice) are NaN in the new one; with it they stay as they were."""
     if x.dim() != 3 or B.dim() != 3 or S.dim() != 4:
         raise ValueError("x, B and S: expected 3, 3 and 4 dimensions")
     total, H, P = x.shape
@@ -378,10 +381,12 @@ def _shortconv(hist, cur, x, weight, bias, splits, activation, out, lead):
 def shortconv_prefill(hist, cur, x, weight, bias, offsets, slots=None, resume=None, splits=None, activation="silu",
                       out=None):
     """Short causal convolution over packed prompts (rssm_shortconv_prefill): x [total][channels]; hist
-    [batch][ring][channels] and cur int32 [batch] are the sequences' histories -> one tensor [total][n] a split."""
+    [batch][ring][channels] and cur int32 [batch] are the sequences' histories -> one tensor [total][n] a split.
+    Without ``out``, rows of refused prompts are NaN."""
+    fresh = out is None
     cfg, h, c, at, stride, out, ptrs, device = _shortconv(hist, cur, x, weight, bias, splits, activation, out,
                                                           (x.shape[0],))
-    pr = _prompts(x.shape[0], offsets, slots, resume, device)
+    pr = _prompts(x.shape[0], offsets, slots, resume, device, fresh)
     abi.check(abi.load().rssm_shortconv_prefill(cfg, C.byref(pr), h, c, at, stride, ptrs, _stream_of(device)),
               "rssm_shortconv_prefill")
     return out

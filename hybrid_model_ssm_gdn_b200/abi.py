@@ -37,7 +37,7 @@ class Tokens(C.Structure):
 
 class Prompts(C.Structure):
     _fields_ = [("total", C.c_int), ("nseq", C.c_int), ("offsets", C.c_void_p), ("slots", C.c_void_p),
-                ("resume", C.c_void_p)]
+                ("resume", C.c_void_p), ("refused_nan", C.c_int)]
 
 
 class ShortConvConfig(C.Structure):

@@ -430,6 +430,7 @@ static Prompts device_prompts(const rssm_prompts *pr, int nslots, const int4 *me
   Prompts p{};
   p.total = pr->total; p.nseq = pr->nseq; p.nslots = nslots;
   p.off = pr->offsets; p.slots = pr->slots; p.resume = pr->resume; p.meta = meta;
+  p.refused_nan = pr->refused_nan;
   return p;
 }
 
@@ -470,6 +471,7 @@ static rssm_status run_scan(const rssm_config &c, const Prompts &p, const rssm_t
   if (c.in_dtype != RSSM_BF16) e = launch_scan(a, p, num_sms, st);
   else if (a.piece_len > p.total && p.total <= 80LL * p.nseq) e = launch_scan_mma(a, p, st);
   else e = launch_scan_tc(a, p, st);
+  if (e == cudaSuccess && p.refused_nan && p.total > 0) e = launch_refuse(p, y, c.nheads * c.headdim, num_sms, st);
   return e == cudaSuccess ? RSSM_OK : cuda_fail(e);
 }
 

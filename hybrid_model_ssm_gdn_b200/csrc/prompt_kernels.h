@@ -27,6 +27,8 @@ cudaError_t launch_scan_tc(const ScanArgs &a, const Prompts &pr, cudaStream_t st
 size_t scan_tc_workspace(int H, int P, int pieces, size_t *seg_dt);
 // fp32 inputs, prompts not cut
 cudaError_t launch_scan(const ScanArgs &a, const Prompts &pr, int num_sms, cudaStream_t stream);
+// NaN in the output rows of refused prompts
+cudaError_t launch_refuse(const Prompts &pr, float *y, int row, int num_sms, cudaStream_t stream);
 cudaError_t launch_prefill_meta(const Prompts &pr, const int4 *meta_in, int4 *meta_out, unsigned char *skip, int H,
                                 int *err, cudaStream_t stream);
 

@@ -18,6 +18,7 @@ struct Prompts {
   const int *slots;             // may be null
   const unsigned char *resume;  // may be null
   const int4 *meta;             // bookkeeping of a context (a resumed sequence needs an empty buffer), or null
+  int refused_nan;              // whether output rows of refused prompts become NaN
 };
 
 struct Piece {
@@ -41,10 +42,14 @@ struct PieceWord {
   int seq, begin, end, slot, resume;
 };
 
-// Collective over the block; false: nothing to do for this piece (bad prompts, refused slot, number without owner).
+// what find_piece found: a number without owner, a piece to work on, one of a refused prompt (slot named twice, buffered
+// records), or an offset or slot out of range somewhere in the call
+enum PieceStatus { kPieceNone, kPieceRun, kPieceRefused, kPieceBad };
+
+// Collective over the block.
 // A block can do nothing before it knows its piece, so the loads are one round trip: a thread reads all of its prompt at
 // once, before the first barrier, and the owner hands it on.
-__device__ __forceinline__ bool find_piece(const Prompts &p, int number, int len, Piece &out, PieceWord *word) {
+__device__ __forceinline__ PieceStatus find_piece(const Prompts &p, int number, int len, Piece &out, PieceWord *word) {
   int o0 = 0, o1 = 0, s0 = 0, r0 = 0;
   auto load = [&](int i, int &s, int &r) {
     o0 = p.off[i];
@@ -63,7 +68,8 @@ __device__ __forceinline__ bool find_piece(const Prompts &p, int number, int len
     if (!bad && o0 / len + i <= number && number <= o1 / len + i) *word = PieceWord{i, o0, o1, s, r};
   }
   bad = __syncthreads_or(bad);
-  if (bad || word->seq < 0) return false;
+  if (bad) return kPieceBad;
+  if (word->seq < 0) return kPieceNone;
   out.seq = word->seq;
   out.begin = word->begin;
   out.end = word->end;
@@ -71,14 +77,33 @@ __device__ __forceinline__ bool find_piece(const Prompts &p, int number, int len
   out.index = number - (out.begin / len + out.seq);
   out.first = out.index * len;
   out.resume = word->resume != 0;
-  if (out.resume && p.meta && (p.meta[out.slot].x != 0 || p.meta[out.slot].z != 0)) return false;
+  if (out.resume && p.meta && (p.meta[out.slot].x != 0 || p.meta[out.slot].z != 0)) return kPieceRefused;
   if (p.slots) {  // a slot named twice
     bool twice = false;
     for (int j = threadIdx.x; j < p.nseq; j += blockDim.x)
       twice |= j != out.seq && (j < (int)blockDim.x ? s0 : p.slots[j]) == out.slot;
-    if (__syncthreads_or(twice)) return false;
+    if (__syncthreads_or(twice)) return kPieceRefused;
   }
-  return true;
+  return kPieceRun;
+}
+
+// lets refuse_kernel start once all blocks have come here
+__device__ __forceinline__ void allow_next() { asm volatile("griddepcontrol.launch_dependents;"); }
+
+template <typename T>
+__device__ __forceinline__ void fill_nan(T *p, size_t elems, size_t part, size_t parts) {
+  for (size_t i = part * blockDim.x + threadIdx.x; i < elems; i += parts * blockDim.x) p[i] = (T)__int_as_float(0x7fffffff);
+}
+
+// A block that found a piece of `len` tokens refused, or a bad offset or slot anywhere: its share of the rows of y
+// [total][row] that become NaN.  `part` of `parts` blocks have the same piece.
+template <typename T>
+__device__ __forceinline__ void refuse(const Prompts &p, PieceStatus found, const Piece &pc, int len, T *y, size_t row,
+                                       int part, int parts) {
+  if (found == kPieceBad)
+    fill_nan(y, p.total * row, blockIdx.y * gridDim.x + blockIdx.x, gridDim.x * gridDim.y);
+  else if (found == kPieceRefused && pc.first < pc.end - pc.begin)
+    fill_nan(y + (size_t)(pc.begin + pc.first) * row, min(len, pc.end - pc.begin - pc.first) * row, part, parts);
 }
 
 }  // namespace rssm

@@ -81,7 +81,8 @@ __global__ void __launch_bounds__(128, 4) scan_mma_kernel(ScanArgs a, Prompts pr
   __shared__ MmaStage st[2];
   __shared__ PieceWord found;
   Piece pc;
-  if (!find_piece(pr, blockIdx.x, a.piece_len, pc, &found)) return;
+  allow_next();
+  if (find_piece(pr, blockIdx.x, a.piece_len, pc, &found) != kPieceRun) return;
   const int h = blockIdx.y, len = pc.end - pc.begin;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, t = lane & 3;
   const int group = h / (a.H / a.G), p0 = 16 * warp;

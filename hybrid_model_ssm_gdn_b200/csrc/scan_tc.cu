@@ -202,6 +202,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
     if (threadIdx.x == 0 && a.err) record_error(a.err, 0, RSSM_DEV_TIMEOUT);
     return;
   }
+  if (!kState) allow_next();
   const int units = a.G * a.pairs;
   int number = blockIdx.x / units;
   const int unit = blockIdx.x % units;
@@ -220,7 +221,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
     __syncthreads();
   }
   Piece pc;
-  if (!find_piece(pr, number, a.piece_len, pc, &sh.found)) return;
+  if (find_piece(pr, number, a.piece_len, pc, &sh.found) != kPieceRun) return;
   const int r = a.H / a.G, group = unit / a.pairs;
   const int h0 = group * r + 2 * (unit % a.pairs);
   const bool two = h0 + 1 < (group + 1) * r;  // without a second head the first is computed twice and stored once
@@ -758,7 +759,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
 __global__ void __launch_bounds__(256) join_kernel(TcArgs a, Prompts pr) {
   __shared__ PieceWord found;
   Piece pc;
-  if (!find_piece(pr, pr.off[blockIdx.x] / a.piece_len + (int)blockIdx.x, a.piece_len, pc, &found)) return;
+  if (find_piece(pr, pr.off[blockIdx.x] / a.piece_len + (int)blockIdx.x, a.piece_len, pc, &found) != kPieceRun) return;
   const int len = pc.end - pc.begin, h = blockIdx.y;
   if (len <= a.piece_len) return;
   const int elem = 4 * (blockIdx.z * 256 + threadIdx.x);

@@ -200,7 +200,13 @@ __global__ void __launch_bounds__(kPromptThreads) prompt_kernel(ShortConvArgs a,
   __shared__ uint4 slots[kAheadBytes / 16][kPromptThreads];
   __shared__ PieceWord found;
   Piece pc;
-  if (!find_piece(pr, blockIdx.x, tile, pc, &found)) return;
+  const PieceStatus status = find_piece(pr, blockIdx.x, tile, pc, &found);
+  if (status != kPieceRun) {
+    if (pr.refused_nan)
+      for (int s = 0; s < 3; ++s)
+        refuse(pr, status, pc, tile, reinterpret_cast<TI *>(a.out[s]), a.split[s], blockIdx.y, gridDim.y);
+    return;
+  }
   const int c = (blockIdx.y * kPromptThreads + threadIdx.x) * V;
   const int len = pc.end - pc.begin;
   if (c >= a.channels || (pc.first >= len && pc.index > 0)) return;

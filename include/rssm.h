@@ -196,7 +196,9 @@ rssm_status rssm_flush(rssm_ctx *ctx, const unsigned char *mask, rssm_stream str
  * inputs have the leading dimension [total] and no padding.  A prompt may be empty.  Rows of no prompt are neither
  * read into a result nor written.  Prompt i belongs to sequence slots[i] of the state (i itself without slots); other
  * sequences keep theirs.
- * If any offset or slot is out of range nothing is written at all; prompts that share a slot are left out.
+ * If any offset or slot is out of range nothing is written at all; prompts that share a slot are left out.  With
+ * refused_nan the output rows that such prompts would have had, all rows in the first case, become NaN instead of
+ * staying as they were; states, histories and checkpoints stay in any case.
  * Outputs overlap no input.
  * Kernels are chosen by total and nseq, so a prompt's results can differ in their last bits with the company it is in;
  * the same call gives the same bits. */
@@ -205,6 +207,7 @@ typedef struct {
   const int *offsets;           /* device [nseq + 1], non-decreasing within 0..total */
   const int *slots;             /* device [nseq] or NULL */
   const unsigned char *resume;  /* device [nseq] or NULL: nonzero = continue from the sequence's state, else from zero */
+  int refused_nan;              /* nonzero: outputs of refused prompts are set to NaN */
 } rssm_prompts;
 
 /* Bytes of device scratch that rssm_mamba2_scan and rssm_mamba2_prefill want for prompts of this size (0 is

@@ -150,3 +150,46 @@ def test_other_inputs_that_are_not_finite_reach_no_earlier_token(cuda_ok, lens, 
             others = [s for s in range(n) if s != i]
             assert torch.equal(S0[others], S1[others])
             assert torch.equal(S0, S1) if key == "C" else not torch.isfinite(S1[i, :heads]).any()
+
+
+def stale(*shape, dtype=torch.float32):
+    """Leave memory that looks like results where the next tensor of this size will lie."""
+    torch.full(shape, 5.0, dtype=dtype, device="cuda")
+
+
+@pytest.mark.parametrize("dtype", [BF, torch.float32])
+@pytest.mark.parametrize("H,total", [(2, 90), (3, 260), (2, 2100)])
+def test_refused_prompts_in_new_outputs_are_nan(cuda_ok, dtype, H, total):
+    """Where the call makes the outputs, rows of prompts that it refuses are NaN: all of them for a bad offset or slot,
+    those of the prompts themselves for a slot named twice.  Each kernel, prompts cut into pieces among them."""
+    P, a, b = 40, total // 3, total // 2
+    d = make(36, dtype, total, H, P, 1, 4, decay=0.1)
+    g = on_gpu(d, dtype)
+    args = (g["x"], g["B"], g["C"], g["dt"], g["A"], g["D"])
+    for offsets, slots in (([0, b, a, total], None), ([0, total + 1], None), ([-1, total], None), ([0, total], [4]),
+                           ([0, a, total], [0, -1])):
+        stale(total, H, P)
+        y = mamba2_scan(g["S"], *args, idx(offsets), idx(slots))
+        assert torch.isnan(y).all(), (offsets, slots)
+        assert np.array_equal(g["S"].cpu().numpy(), d["S"])
+    stale(total, H, P)
+    y = mamba2_scan(g["S"], *args, idx([0, a, b, total]), idx([2, 1, 2]))
+    assert torch.isnan(y[:a]).all() and torch.isfinite(y[a:b]).all() and torch.isnan(y[b:]).all()
+    S = g["S"].cpu().numpy()
+    assert all(np.array_equal(S[i], d["S"][i]) for i in (0, 2, 3))
+
+
+def test_refused_prompts_of_a_context_are_nan(cuda_ok):
+    """Prompts that resume on buffered records, and a slot named twice, in outputs that the call makes."""
+    d = make(37, BF, 300, 4, 64, 2, 4)
+    g = on_gpu(d, BF)
+    tok = (g["x"], g["B"], g["C"], g["dt"])
+    layer = context(d, BF, 4)
+    layer.mamba2_step(*(v[:4].contiguous() for v in tok))
+    stale(300, 4, 64)
+    y = layer.prefill(*tok, idx([0, 100, 120, 300]), idx([3, 0, 1]), idx([1, 0, 1], torch.uint8))
+    assert layer.get_error() == (abi.DEV_BUFFERED, 1)
+    assert torch.isnan(y[:100]).all() and torch.isfinite(y[100:120]).all() and torch.isnan(y[120:]).all()
+    stale(300, 4, 64)
+    y = layer.prefill(*tok, idx([0, 100, 120, 300]), idx([2, 0, 2]))
+    assert torch.isnan(y[:100]).all() and torch.isfinite(y[100:120]).all() and torch.isnan(y[120:]).all()

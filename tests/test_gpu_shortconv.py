@@ -184,3 +184,23 @@ def test_silu_over_its_whole_range(cuda_ok, dtype):
     bound = (2.0 ** -20 + (torch.finfo(BF).eps / 2 if dtype == BF else 0)) * np.abs(ref)
     bound += 2.0 ** -119 if dtype == BF else 2.0 ** -148
     assert (err / bound).max() <= 1.0
+
+
+@pytest.mark.parametrize("dtype", [BF, F32])
+def test_refused_prompts_in_new_outputs_are_nan(cuda_ok, dtype):
+    """Where the call makes the outputs: all rows for a bad offset or slot, the prompts' own for a slot named twice."""
+    c = Case(5, dtype, (64, 1032), 4, 4)
+    x = c.dev(c.rows(300))
+    for offsets, slots in (([0, 150, 100, 300], None), ([0, 301], None), ([-1, 300], None), ([0, 300], [4])):
+        torch.full((300, 1032), 5.0, dtype=dtype, device="cuda")
+        out = shortconv_prefill(c.hist, c.cur, x, c.w, c.b, idx(offsets), idx(slots), **c.kw)
+        assert all(torch.isnan(o).all() for o in out), (offsets, slots)
+        c.check_state()
+    torch.full((300, 1032), 5.0, dtype=dtype, device="cuda")
+    out = shortconv_prefill(c.hist, c.cur, x, c.w, c.b, idx([0, 100, 130, 300]), idx([3, 1, 3]), **c.kw)
+    for o in out:
+        assert torch.isnan(o[:100]).all() and torch.isnan(o[130:]).all()
+    xn = x.float().cpu().numpy()
+    ref, mag = c.orc.prefill(xn, [100, 130], [1]), c.mag.prefill(np.abs(xn), [100, 130], [1])
+    c.check([o[100:130] for o in out], ref[100:130], mag[100:130])
+    c.check_state()
