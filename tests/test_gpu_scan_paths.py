@@ -7,7 +7,7 @@ import pytest
 import torch
 
 from hybrid_model_ssm_gdn_b200 import abi, make_config, mamba2_scan
-from test_gpu_scan import compare, context, idx, make, on_gpu
+from test_gpu_scan import SHAPES, compare, context, idx, make, on_gpu
 
 pytestmark = pytest.mark.gpu
 
@@ -193,3 +193,157 @@ def test_refused_prompts_of_a_context_are_nan(cuda_ok):
     stale(300, 4, 64)
     y = layer.prefill(*tok, idx([0, 100, 120, 300]), idx([2, 0, 2]))
     assert torch.isnan(y[:100]).all() and torch.isfinite(y[100:120]).all() and torch.isnan(y[120:]).all()
+
+
+def check_prompts(d, dtype, lens, slots, resume):
+    offsets = packed(lens)
+    g = on_gpu(d, dtype)
+    y = torch.full(d["x"].shape, 7.0, device="cuda")
+    mamba2_scan(g["S"], g["x"], g["B"], g["C"], g["dt"], g["A"], g["D"], idx(offsets), idx(slots), idx(resume, torch.uint8),
+                y=y)
+    compare(d, offsets, slots, resume, g["S"].cpu().numpy(), y.cpu().numpy())
+
+
+@pytest.mark.parametrize("H,P,G", SHAPES)
+def test_mixed_lengths_above_the_short_kernel(cuda_ok, H, P, G):
+    """Empty (from zero and resumed), single-token, tile-sized and long prompts that average more than 80 tokens, so that
+    chunks of 128 take them: odd heads, several groups, every height of X."""
+    lens = [1, 0, 130, 127, 300, 128, 0, 257, 3]
+    assert sum(lens) > 80 * len(lens) and workspace(H, P, G, sum(lens), len(lens)) == 0
+    d = make(H * 1000 + P, BF, sum(lens), H, P, G, 12)
+    check_prompts(d, BF, lens, [4, 9, 0, 7, 2, 10, 1, 5, 11], [0, 0, 1, 0, 1, 1, 1, 0, 1])
+
+
+@pytest.mark.parametrize("H,P,G,lens", [(3, 40, 1, (700, 0, 1400, 390, 800, 5)), (2, 8, 1, (130, 900))])
+def test_uneven_long_prompts_handed_out_by_length(cuda_ok, H, P, G, lens):
+    """Whole prompts of 512 tokens or more on average go to the blocks longest first."""
+    n = len(lens)
+    assert sum(lens) >= 512 * n and workspace(H, P, G, sum(lens), n) == 0
+    d = make(41, BF, sum(lens), H, P, G, n + 2, decay=0.1)
+    r = np.random.default_rng(42)
+    check_prompts(d, BF, lens, r.permutation(n + 2)[:n].tolist(), [i % 3 != 1 for i in range(n)])
+
+
+@pytest.mark.parametrize("n", [64, 65])
+def test_the_number_of_prompts_handed_out_by_length(cuda_ok, n):
+    """As many prompts as are sorted, and one more: each repeats one of two, so that two runs of the oracle cover them."""
+    lens = [300 + 500 * (i % 2) for i in range(n)]
+    d = make(43, BF, 800, 1, 8, 1, 1, decay=0.1)
+    g = on_gpu(d, BF)
+    x, B, C, dt = (torch.cat([g[k][:m] for m in lens]) for k in ("x", "B", "C", "dt"))
+    assert workspace(1, 8, 1, sum(lens), n) == 0
+    S = torch.zeros(n, 1, 8, 128, device="cuda")
+    y = mamba2_scan(S, x, B, C, dt, g["A"], g["D"], idx(packed(lens)))
+    off = packed(lens)
+    for i in range(2):
+        compare({**d, **{k: d[k][:lens[i]] for k in ("x", "B", "C", "dt")}}, [0, lens[i]], None, None,
+                S[i:i + 1].cpu().numpy(), y[off[i]:off[i + 1]].cpu().numpy())
+    for i in range(2, n):
+        assert torch.equal(y[off[i]:off[i + 1]], y[off[i % 2]:off[i % 2 + 1]]) and torch.equal(S[i], S[i % 2])
+
+
+@pytest.mark.parametrize("dtype,each,n", [(BF, 85, 700), (BF, 40, 300), (torch.float32, 20, 300)])
+def test_more_prompts_than_threads_of_a_block(cuda_ok, dtype, each, n):
+    """Every block looks through more prompts than it has threads; all prompts are the same, to slots in reverse."""
+    d = make(44, dtype, each, 2, 16, 1, 1)
+    g = on_gpu(d, dtype)
+    x, B, C, dt = (g[k].repeat(n, *[1] * (g[k].dim() - 1)) for k in ("x", "B", "C", "dt"))
+    S = g["S"].repeat(n + 1, 1, 1, 1)
+    y = mamba2_scan(S, x, B, C, dt, g["A"], g["D"], idx(packed([each] * n)), idx(list(range(n, 0, -1))),
+                    idx([1] * n, torch.uint8)).view(n, each, 2, 16)
+    compare(d, [0, each], None, [1], S[1:2].cpu().numpy(), y[0].cpu().numpy())
+    assert (y == y[:1]).all() and (S[1:] == S[1:2]).all() and torch.equal(S[0], g["S"][0])
+
+
+@pytest.mark.parametrize("dtype", [BF, torch.float32])
+@pytest.mark.parametrize("lens", [[700] + [1] * 20, [1] * 9 + [400]])
+def test_one_long_prompt_among_single_tokens(cuda_ok, dtype, lens):
+    d = make(45, dtype, sum(lens), 4, 64, 2, len(lens), decay=0.2)
+    check_prompts(d, dtype, lens, None, [i % 2 for i in range(len(lens))])
+
+
+def test_prefill_captured(cuda_ok):
+    """Two calls of a context's prefill (an even number keeps its bookkeeping in place) in a graph, replayed on new
+    prompts while another sequence goes on decoding between the replays."""
+    batch, H, P, G = 3, 4, 64, 2
+    d = make(46, BF, 300, H, P, G, batch)
+    g = on_gpu(d, BF)
+    layer, eager = context(d, BF, batch), context(d, BF, batch)
+    tok = tuple(g[k].clone() for k in ("x", "B", "C", "dt"))
+    first, second = (idx([0, 90]), idx([1])), (idx([90, 300]), idx([1]), idx([1], torch.uint8))
+    y = torch.empty(300, H, P, device="cuda")
+
+    def prompt(layer, tok, y):
+        layer.prefill(*tok, *first, y=y)
+        layer.prefill(*tok, *second, y=y)
+
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph, stream=side):
+        prompt(layer, tok, y)
+    for seed in (47, 48, 49):
+        new = on_gpu(make(seed, BF, 300, H, P, G, batch), BF)
+        for t, k in zip(tok, ("x", "B", "C", "dt")):
+            t.copy_(new[k])
+        graph.replay()
+        y2 = torch.empty_like(y)
+        prompt(eager, tok, y2)
+        assert torch.equal(y, y2)
+        for _ in range(2):
+            now = tuple(t[:batch].contiguous() for t in tok)
+            assert torch.equal(layer.mamba2_step(*now), eager.mamba2_step(*now))
+    a, b = layer.export(ring=False), eager.export(ring=False)
+    assert torch.equal(a["S"], b["S"]) and torch.equal(a["meta"], b["meta"])
+    assert layer.get_error() == (0, -1)
+    del graph
+
+
+def test_cut_prompts_on_two_streams(cuda_ok):
+    """Prompts that are cut into pieces, at once on two streams, each call with scratch of its own."""
+    H, P, G, total = 8, 64, 1, 3000
+    assert workspace(H, P, G, total, 1) > 0
+    gs = [on_gpu(make(50 + i, BF, total, H, P, G, 1, decay=0.1), BF) for i in range(2)]
+
+    def run(g):
+        S = g["S"].clone()
+        return S, mamba2_scan(S, g["x"], g["B"], g["C"], g["dt"], g["A"], g["D"], idx([0, total]),
+                              resume=idx([1], torch.uint8))
+
+    want = [run(g) for g in gs]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    for _ in range(5):
+        got = []
+        for g, st in zip(gs, streams):
+            st.wait_stream(torch.cuda.current_stream())
+            with torch.cuda.stream(st):
+                got.append(run(g))
+        torch.cuda.synchronize()
+        for (S, y), (S0, y0) in zip(got, want):
+            assert torch.equal(S, S0) and torch.equal(y, y0)
+
+
+@pytest.mark.parametrize("dtype,each", [(BF, 40), (BF, 150), (torch.float32, 40)])
+def test_captured_with_outputs_of_its_own(cuda_ok, dtype, each):
+    """A captured call that makes its outputs, replayed on good offsets, bad ones and good ones again."""
+    total = 3 * each
+    d = make(52, dtype, total, 4, 64, 2, 3)
+    g = on_gpu(d, dtype)
+    offsets = idx([0, each, 2 * each, total])
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph, stream=side):
+        y = mamba2_scan(g["S"], g["x"], g["B"], g["C"], g["dt"], g["A"], g["D"], offsets)
+        after = y + 1
+    for off in ([0, each, 2 * each, total], [0, each, 2 * each, total + 1], [0, 1, 2 * each + 5, total]):
+        offsets.copy_(idx(off))
+        graph.replay()
+        torch.cuda.synchronize()
+        if off[-1] > total:
+            assert torch.isnan(y).all() and torch.isnan(after).all()
+        else:
+            compare(d, off, None, None, g["S"].cpu().numpy(), y.cpu().numpy())
+            assert torch.equal(after, y + 1)
+    del graph

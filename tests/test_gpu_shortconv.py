@@ -204,3 +204,16 @@ def test_refused_prompts_in_new_outputs_are_nan(cuda_ok, dtype):
     ref, mag = c.orc.prefill(xn, [100, 130], [1]), c.mag.prefill(np.abs(xn), [100, 130], [1])
     c.check([o[100:130] for o in out], ref[100:130], mag[100:130])
     c.check_state()
+
+
+@pytest.mark.parametrize("dtype", [BF, F32])
+def test_more_prompts_than_threads_of_a_block(cuda_ok, dtype):
+    r = np.random.default_rng(7)
+    lens = r.integers(0, 6, 300)
+    offsets, slots = np.concatenate([[0], np.cumsum(lens)]).tolist(), r.permutation(310)[:300].tolist()
+    resume = r.integers(0, 2, 300).tolist()
+    c = Case(8, dtype, (64, 32), 4, 310)
+    x = c.rows(offsets[-1])
+    out = shortconv_prefill(c.hist, c.cur, c.dev(x), c.w, c.b, idx(offsets), idx(slots), idx(resume, torch.uint8), **c.kw)
+    c.check(out, c.orc.prefill(x, offsets, slots, resume), c.mag.prefill(np.abs(x), offsets, slots, resume))
+    c.check_state()
