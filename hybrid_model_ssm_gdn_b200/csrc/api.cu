@@ -439,6 +439,7 @@ static Prompts device_prompts(const rssm_prompts *pr, int nslots, const int4 *me
 // into pieces a prompt costs a first pass over all but its last one for their end states (some 0.45 of the full pass a
 // chunk) and a start per piece (about two chunks), so it pays where one prompt's chain is what takes the time: one prompt
 // of 8191 tokens and 64 pairs on 148 SMs takes 0.38 ms whole, 0.28 ms in two pieces of 4096 and 0.34 ms in eight of 1024.
+// Every prompt counts as a long one, whatever its length: with 64 pairs a second prompt of one token ends the cutting.
 static int scan_piece_len(const rssm_config &c, int total, int nseq, int num_sms) {
   const int whole = total + 1;
   if (c.in_dtype != RSSM_BF16) return whole;
@@ -465,8 +466,10 @@ static rssm_status run_scan(const rssm_config &c, const Prompts &p, const rssm_t
     if (work_bytes < scan_tc_workspace(a.H, a.P, prompt_pieces(p.total, p.nseq, a.piece_len), nullptr))
       return RSSM_ERR_ARENA_TOO_SMALL;
   }
-  // Prompts of up to 80 tokens on average go to the kernel with chunks of 16: the two meet between 64 and 110 (64
-  // prompts of 32 tokens, 128 heads: 139 and 329 us; 48 of 96: 246 and 266; 32 of 128: 213 and 185).
+  // Prompts of up to 80 tokens on average go to the kernel with chunks of 16: for prompts alike in length the two meet
+  // between 64 and 110 (64 prompts of 32 tokens, 128 heads: 139 and 329 us; 48 of 96: 246 and 266; 32 of 128: 213 and
+  // 185).  The host does not know the lengths, so one long prompt among many short ones goes there, too, and is walked
+  // there from end to end in chunks of 16.
   cudaError_t e;
   if (c.in_dtype != RSSM_BF16) e = launch_scan(a, p, num_sms, st);
   else if (a.piece_len > p.total && p.total <= 80LL * p.nseq) e = launch_scan_mma(a, p, st);

@@ -8,8 +8,9 @@
 // A prompt of a few tokens is a read and a write of its state (64 KB a head) around little work.  Here four blocks share
 // an SM, so one block's state is on its way while the others compute; a block of the 128-token kernel has an SM to
 // itself and pays its start, its loads and its whole chunk of products one after the other: 48 resumed prompts of 31
-// tokens on average (128 heads; 483 MB) take 157 us here and 342 us there.  Per token this kernel costs more (every 16 tokens the state is
-// cut anew, and mma.sync runs at a quarter of tcgen05's rate), so longer prompts go there.
+// tokens on average (128 heads; 483 MB) take 160 us here and 342 us there.  Per token this kernel costs more (every 16
+// tokens the state is cut anew, and mma.sync runs at a quarter of tcgen05's rate), so longer prompts go there.  What
+// bounds it: the LSU data path (59 % busy) and a block's latency; DRAM 33 %, tensor pipe 25 %.
 #include "prompt_kernels.h"
 #include "packed.cuh"
 

@@ -10,16 +10,19 @@
 // prompt, chunk after chunk, so the state never leaves the chip.
 //
 // Precision: C, B and X are bf16 and enter exactly; sums are fp32.  The three fp32 operands M, S and the weighted X are
-// cut into two bf16 pieces (hi = RN(v), lo = RN(v - hi): what is lost is below 2^-17 of v) and multiplied twice, which
-// keeps the library's fp32 outputs and checkpoints at the accuracy its other kernels have; one bf16 piece would leave
-// them at 2^-9.  That doubles three of the four products: 14.7 M multiply-adds for a chunk of two heads, 4600 cycles of
-// the tensor core (M X has 64 columns a head, and an instruction of 64 takes as long as one of 128), against the 2.3 us that
-// its bytes take at the measured bandwidth (x, y and the group's share of B and C): both limits lie close together, and
-// tcgen05 is needed for either (mma.sync measured a quarter of its rate).
+// cut into two bf16 pieces (hi = RN(v), lo = RN(v - hi): what is lost is below 2^-17 of v) and multiplied twice.  Outputs
+// and states are 3e-7 to 6e-7 off in all, where fp32 arithmetic throughout is 4e-8 to 7e-8 off: coarser than the decode
+// kernels' folds, whose three pieces are exact, for which shared memory has no room here; one piece would leave 2^-9.
+// Differences of sums of dt within a block of 32 tokens carry the rounding of those sums.  Two pieces double three of the
+// four products: 14.7 M multiply-adds for a chunk of two heads, 3500 cycles of the tensor core as measured, against the
+// 2.3 us that its bytes take at the measured bandwidth (x, y and the group's share of B and C): both limits lie close
+// together, and tcgen05 is needed for either (mma.sync measured a quarter of its rate).
 //
-// Measured: 16384 tokens in 8 prompts of 128 heads, P 64, 8 groups, 0.40 ms (910 MB, 0.14 ms at the copy bandwidth), some
-// 12000 cycles a chunk of two heads; one prompt of 8191 tokens 0.29 ms.  What bounds a chunk is the loop below with its
-// conversions, which run on half-rate ALU instructions, not the tensor core and not memory.
+// Measured: 16384 tokens in 8 prompts of 128 heads, P 64, 8 groups, 0.41 ms (910 MB, 0.14 ms at the copy bandwidth), some
+// 13000 cycles a chunk of two heads; one prompt of 8191 tokens 0.29 ms.  What bounds a chunk is the loop below with its
+// conversions, not the tensor core (27 % busy) and not memory (25 %).  Two of the waits in it come from buffers that are
+// shared, not from the recurrence: the weighted X waits until C S^T has used the pieces of S, and M of the second head
+// until M X of the first is done.
 //
 // Tensor memory (512 columns): S 128 (row = head and p, column = n), Y 128 (row = token, column = head and p), G 128, and
 // M as hi | lo pairs 128, for one head after the other; M is the left operand straight from tensor memory.  Shared

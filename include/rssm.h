@@ -37,7 +37,10 @@
  *     code; read it with rssm_get_error.
  *   - Calls on one context must be ordered on one stream (or ordered by the
  *     caller with events); the library flips an internal parity bit on every
- *     call that changes the bookkeeping.
+ *     call that changes the bookkeeping (step, verify, commit, flush, prefill).
+ *     A captured graph has the parity of its capture, so one that is replayed
+ *     more than once, or followed by other calls, holds an even number of such
+ *     calls of each context.
  *   - Token inputs are row-major with the leading dimensions named, and must
  *     start on 16-byte boundaries; rows of length P, N, d_k or d_v in the
  *     input dtype must be multiples of 16 bytes.
@@ -239,8 +242,9 @@ rssm_status rssm_mamba2_prefill(rssm_ctx *ctx, const rssm_prompts *pr, const rss
  * magnitude is below 2^-119 may be 0).  Its state follows the scheme of the replay buffer: a ring of
  * the last raw inputs, hist [batch][ring][channels] in the input type, with a cursor cur [batch] (the slot of the next
  * token, 0..ring-1; any other value is taken modulo ring).  A draft is a tentative row and commit moves the cursor.
- * Row r of `in` starts at in + r * in_stride elements; outputs that overlap its rows are refused.  Outputs are up to three contiguous tensors out[s]
- * [rows][split[s]], the channels cut in order, so that a step or verify call can take them as they are. */
+ * Row r of `in` starts at in + r * in_stride elements; outputs that overlap its rows are refused.  Outputs are up to three
+ * contiguous tensors out[s] [rows][split[s]], the channels cut in order, so that a step or verify call can take them as
+ * they are. */
 typedef struct {
   int batch;         /* sequences of hist, >= 1 */
   int channels;      /* multiple of 8 */
