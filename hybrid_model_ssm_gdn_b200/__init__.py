@@ -311,7 +311,8 @@ def mamba2_scan(S, x, B, C_, dt, A, D, offsets, slots=None, resume=None, y=None,
     sequences rewritten in place; x [total][H][P], B, C [total][G][128], dt [total][H] (bf16 or fp32), A, D fp32 [H];
     prompt i is rows offsets[i] .. offsets[i+1]-1 and belongs to S[slots[i]] (S[i] without slots), from which it
     continues where resume[i] is set -> y fp32 [total][H][P].  Without ``y``, rows of refused prompts (an offset or slot out
-    of range: all rows; a slot named twice) are NaN in the new one; with it they stay as they were."""
+    of range: all rows; a slot named twice) are NaN in the new one; with it they stay as they were.  Rows of no prompt are
+    not written in either."""
     if x.dim() != 3 or B.dim() != 3 or S.dim() != 4:
         raise ValueError("x, B and S: expected 3, 3 and 4 dimensions")
     total, H, P = x.shape
