@@ -9,8 +9,9 @@ device memory (the context's arena, outputs) and the current CUDA stream.
     layer.load_checkpoint(S0)            # fp32 [Bt][H][P][N]
     y = layer.mamba2_step(x, B, C, dt)   # fp32 [Bt][H][P]
 
-Prompts and drafts around it: ``ReplaySSM.prefill`` / ``mamba2_scan``, ``shortconv_prefill`` / ``_step`` / ``_verify`` /
-``_commit`` and ``accept_drafts``.
+Prompts and drafts around it: ``ReplaySSM.prefill`` / ``mamba2_scan``, ``ReplaySSM.gdn_prefill`` / ``gdn_scan``,
+``shortconv_prefill`` / ``_step`` / ``_verify`` / ``_commit`` and ``accept_drafts``.  Between a layer's projections:
+``gdn_inputs``, ``add_rmsnorm`` and ``gated_rmsnorm``.
 """
 
 from __future__ import annotations
@@ -24,7 +25,7 @@ from .abi import RSSMError
 
 __all__ = ["ReplaySSM", "RSSMError", "conv_mamba2_step", "conv_gdn_step", "snap_verify", "snap_commit", "sched_probe",
            "make_config", "abi", "mamba2_scan", "shortconv_prefill", "shortconv_step", "shortconv_verify",
-           "shortconv_commit", "accept_drafts"]
+           "shortconv_commit", "accept_drafts", "gdn_scan", "gdn_inputs", "add_rmsnorm", "gated_rmsnorm"]
 
 _DT = {torch.float32: abi.F32, torch.bfloat16: abi.BF16}
 _HP = {"f32": abi.HP_F32, "f16sr": abi.HP_F16_SR, "f8sr": abi.HP_F8_SR}
@@ -170,6 +171,20 @@ class ReplaySSM:
                                                0 if work is None else work.numel(), _stream_of(device)), "rssm_mamba2_prefill")
         return y
 
+    def gdn_prefill(self, q, k, v, alpha, beta, offsets, slots=None, resume=None, y=None, workspace=None):
+        """Run packed prompts (rssm_gdn_prefill): q, k [total][heads or a divisor of them][128], v [total][H][d_v], alpha,
+        beta fp32 [total][H]; offsets int32 [n+1]; slots int32 [n], resume uint8 [n] -> y fp32 [total][H][d_v], with NaN for
+        refused prompts where the call makes it."""
+        device = _device(v, "v")
+        if self.arena.get_device() != device:
+            raise ValueError(f"the context is on {self.arena.device}, but the current device is cuda:{device}")
+        total, pr, tok, y, Hk = _gdn_args(q, k, v, alpha, beta, offsets, slots, resume, y, self.nheads, self.rows,
+                                          self.in_dtype, device)
+        work = _scan_work(self.lib, self.cfg, total, pr.nseq, workspace, device, "rssm_gdn_scan_workspace")
+        abi.check(self.lib.rssm_gdn_prefill(self.handle, Hk, C.byref(pr), C.byref(tok), _addr(y), _addr(work),
+                                            0 if work is None else work.numel(), _stream_of(device)), "rssm_gdn_prefill")
+        return y
+
     def flush(self, mask=None):
         m = _dev(mask, torch.uint8, "mask", self.batch)
         abi.check(self.lib.rssm_flush(self.handle, _ptr(m), _stream()), "rssm_flush")
@@ -291,10 +306,10 @@ def _scan_args(x, B, C_, dt, offsets, slots, resume, y, H, P, G, dtype, device):
     return total, pr, tok, y
 
 
-def _scan_work(lib, cfg, total, nseq, workspace, device):
+def _scan_work(lib, cfg, total, nseq, workspace, device, size="rssm_mamba2_scan_workspace"):
     """The scratch tensor of a scan: the caller's, or a new one from the caching allocator (None if none is needed)."""
     n = C.c_size_t()
-    abi.check(lib.rssm_mamba2_scan_workspace(C.byref(cfg), total, nseq, C.byref(n)), "rssm_mamba2_scan_workspace")
+    abi.check(getattr(lib, size)(C.byref(cfg), total, nseq, C.byref(n)), size)
     if n.value == 0:
         return None
     if workspace is not None:
@@ -326,6 +341,43 @@ def mamba2_scan(S, x, B, C_, dt, A, D, offsets, slots=None, resume=None, y=None,
     work = _scan_work(lib, cfg, total, pr.nseq, workspace, device)
     abi.check(lib.rssm_mamba2_scan(C.byref(cfg), C.byref(pr), C.byref(tok), at, y.data_ptr(), _addr(work),
                                    0 if work is None else work.numel(), _stream_of(device)), "rssm_mamba2_scan")
+    return y
+
+
+def _gdn_args(q, k, v, alpha, beta, offsets, slots, resume, y, H, R, dtype, device):
+    total, Hk = v.shape[0], q.shape[1] if q.dim() == 3 else 0
+    if Hk < 1 or H % Hk:
+        raise ValueError(f"q: expected [total][heads that divide {H}][128], got {tuple(q.shape)}")
+    tok = abi.Tokens(None, None, None, None, _arr(q, dtype, "q", (total, Hk, 128), device),
+                     _arr(k, dtype, "k", (total, Hk, 128), device), _arr(v, dtype, "v", (total, H, R), device),
+                     _arr(alpha, torch.float32, "alpha", (total, H), device),
+                     _arr(beta, torch.float32, "beta", (total, H), device))
+    pr = _prompts(total, offsets, slots, resume, device, y is None)
+    if y is None:
+        y = v.new_empty((total, H, R), dtype=torch.float32)
+    else:
+        _arr(y, torch.float32, "y", (total, H, R), device)
+    return total, pr, tok, y, Hk
+
+
+def gdn_scan(S, q, k, v, alpha, beta, offsets, slots=None, resume=None, q_scale=1.0, y=None, workspace=None):
+    """The gated delta rule over packed prompts on the caller's states (rssm_gdn_scan): S fp32 [batch][H][d_v][128], the
+    prompts' sequences rewritten in place; q, k [total][heads or a divisor of them][128], v [total][H][d_v] (bf16 or fp32),
+    alpha, beta fp32 [total][H]; offsets, slots, resume, refused prompts and rows of no prompt as for ``mamba2_scan``
+    -> y fp32 [total][H][d_v]."""
+    if v.dim() != 3 or S.dim() != 4:
+        raise ValueError("v and S: expected 3 and 4 dimensions")
+    H, R = v.shape[1:]
+    dtype = _in_dtype(v, "v")
+    device = _device(S, "S")
+    at = _arr(S, torch.float32, "S", (S.shape[0], H, R, 128), device)
+    cfg = abi.Config(abi.GDN, S.shape[0], H, R, 128, 1, 1, 0, _DT[dtype], abi.HP_F32, abi.READ_SAME, 0, q_scale, None, None,
+                     0.0)
+    total, pr, tok, y, Hk = _gdn_args(q, k, v, alpha, beta, offsets, slots, resume, y, H, R, dtype, device)
+    lib = abi.load()
+    work = _scan_work(lib, cfg, total, pr.nseq, workspace, device, "rssm_gdn_scan_workspace")
+    abi.check(lib.rssm_gdn_scan(C.byref(cfg), Hk, C.byref(pr), C.byref(tok), at, y.data_ptr(), _addr(work),
+                                0 if work is None else work.numel(), _stream_of(device)), "rssm_gdn_scan")
     return y
 
 
@@ -455,6 +507,135 @@ def accept_drafts(target, tokens, u, draft=None, count=None):
                                             _arr(u, torch.float32, "u", (batch, T + 1), device),
                                             at, at + 4 * batch, at + 8 * batch, _stream_of(device)), "rssm_accept_drafts")
     return got.unbind(0)
+
+
+# ---------------------------------------------------------------------- between a layer's projections
+
+def _apart(t, name, lead, width, inner, dtype, device):
+    """The row stride of t [*lead][*inner], rows of ``width`` contiguous elements that lie evenly apart."""
+    if t.shape != (*lead, *inner) or t.dtype is not dtype or t.get_device() != device:
+        raise ValueError(f"{name}: expected {dtype} of shape {(*lead, *inner)} on the current CUDA device, got {t.dtype} of "
+                         f"{tuple(t.shape)} on {t.device}")
+    if t.is_contiguous():
+        return width
+    at, step = width, 1
+    for n, s in zip(reversed(t.shape[len(lead):]), reversed(t.stride()[len(lead):])):
+        if n > 1 and s != step:
+            raise ValueError(f"{name}: expected contiguous rows, got strides {t.stride()}")
+        step *= n
+    step = None
+    for n, s in zip(reversed(t.shape[:len(lead)]), reversed(t.stride()[:len(lead)])):
+        if n == 1:
+            continue
+        if step is None:
+            at = step = s
+        elif s != step:
+            raise ValueError(f"{name}: the rows must lie evenly apart, got strides {t.stride()}")
+        step *= n
+    if at < width:
+        raise ValueError(f"{name}: the rows overlap, strides {t.stride()}")
+    return at
+
+
+def _count(shape):
+    n = 1
+    for s in shape:
+        n *= s
+    return n
+
+
+def gdn_inputs(q, k, a, b, A_log, dt_bias, eps=1e-6, expand=False, out=None):
+    """Inputs of the gated delta rule from a layer's projections and convolution (rssm_gdn_inputs): q, k [...][Hk][128] and
+    a, b [...][H] (bf16 or fp32; rows may lie apart), A_log, dt_bias fp32 [H], H a multiple of Hk -> (q, k, alpha, beta):
+    q and k with length 1, [...][Hk][128], or with ``expand`` [...][H][128] as the decode calls take them; alpha =
+    exp(-exp(A_log) softplus(a + dt_bias)), beta = sigmoid(b), fp32 [...][H]."""
+    if q.dim() < 2 or a.dim() < 1:
+        raise ValueError("q and a: expected at least 2 dimensions and 1")
+    dtype = _in_dtype(q, "q")
+    device = _device(q, "q")
+    lead, Hk, H = q.shape[:-2], q.shape[-2], a.shape[-1]
+    if Hk < 1 or H < 1 or H % Hk:
+        raise ValueError(f"q: expected [...][heads that divide {H}][128], got {tuple(q.shape)}")
+    heads, rows = H if expand else Hk, _count(lead)
+    strides = [_apart(t, n, lead, _count(inner), inner, dtype, device)
+               for t, n, inner in ((q, "q", (Hk, 128)), (k, "k", (Hk, 128)), (a, "a", (H,)), (b, "b", (H,)))]
+    if out is None:
+        out = (q.new_empty((*lead, heads, 128)), q.new_empty((*lead, heads, 128)),
+               q.new_empty((*lead, H), dtype=torch.float32), q.new_empty((*lead, H), dtype=torch.float32))
+    else:
+        for t, n, s, d in zip(out, ("q", "k", "alpha", "beta"), ((heads, 128), (heads, 128), (H,), (H,)),
+                              (dtype, dtype, torch.float32, torch.float32), strict=True):
+            _arr(t, d, "out " + n, (*lead, *s), device)
+    cfg = abi.GdnInputsConfig(rows, H, Hk, heads, _DT[dtype], eps, q.data_ptr(), k.data_ptr(), a.data_ptr(), b.data_ptr(),
+                              *strides, _arr(A_log, torch.float32, "A_log", (H,), device),
+                              _arr(dt_bias, torch.float32, "dt_bias", (H,), device))
+    abi.check(abi.load().rssm_gdn_inputs(C.byref(cfg), *[t.data_ptr() for t in out], _stream_of(device)), "rssm_gdn_inputs")
+    return out
+
+
+_SCALES = {None: abi.SCALE_NONE, "row": abi.SCALE_ROW, "block": abi.SCALE_BLOCK}
+
+
+def _norm(x, weight, columns, group, eps, offset, out_dtype, scale, out, gate_dtype, norm_first, device):
+    """(config, address of the weight, output, scales, and what the call returns) of a norm over the last dimension."""
+    if scale not in _SCALES:
+        raise ValueError(f"scale: expected None, 'row' or 'block', got {scale!r}")
+    if group < 1 or columns % group:
+        raise ValueError(f"group: expected a divisor of {columns}, got {group}")
+    wcols = columns if weight.numel() == columns else group
+    lead = x.shape[:-1]
+    if scale is None:
+        if out_dtype not in _DT:
+            raise ValueError(f"out_dtype: expected torch.float32 or torch.bfloat16, got {out_dtype}")
+        kind, want, scales = _DT[out_dtype], out_dtype, None
+    else:
+        kind, want = abi.F32, torch.float8_e4m3fn
+        scales = lead if scale == "row" else (*lead, (columns + 127) // 128)
+    if out is None:
+        y = x.new_empty(x.shape, dtype=want)
+        got = y if scale is None else (y, x.new_empty(scales, dtype=torch.float32))
+    else:
+        got = out
+        _arr(out if scale is None else out[0], want, "out", x.shape, device)
+        if scale is not None:
+            _arr(out[1], torch.float32, "scales", scales, device)
+    y, s = (got, None) if scale is None else got
+    cfg = abi.NormConfig(_count(lead), columns, group, wcols, _DT[_in_dtype(x, "x")], gate_dtype,
+                         _DT[_in_dtype(weight, "weight")], kind, _SCALES[scale], norm_first, eps, offset)
+    return cfg, _arr(weight, weight.dtype, "weight", (wcols,), device), y.data_ptr(), _addr(s), got
+
+
+def add_rmsnorm(x, weight, residual=None, eps=1e-6, offset=0.0, out_dtype=None, scale=None, out=None):
+    """Root-mean-square norm over the last dimension with the residual's addition (rssm_add_rmsnorm): h = x + residual goes
+    back to ``residual`` in place; x, residual [...][n] (bf16 or fp32; rows may lie apart), weight [n] -> h / rms(h) (offset +
+    weight) in ``out_dtype`` (x's), or with ``scale`` "row" or "block" (of 128 columns) the pair (float8_e4m3fn, scales fp32
+    [...] or [...][ceil(n/128)])."""
+    n, dtype = x.shape[-1], _in_dtype(x, "x")
+    device = _device(x, "x")
+    lead = x.shape[:-1]
+    stride = _apart(x, "x", lead, n, (n,), dtype, device)
+    r_stride = 0 if residual is None else _apart(residual, "residual", lead, n, (n,), dtype, device)
+    cfg, w, y, s, got = _norm(x, weight, n, n, eps, offset, out_dtype or dtype, scale, out, 0, 0, device)
+    abi.check(abi.load().rssm_add_rmsnorm(C.byref(cfg), x.data_ptr(), stride, _addr(residual), r_stride, w, y, s,
+                                          _stream_of(device)), "rssm_add_rmsnorm")
+    return got
+
+
+def gated_rmsnorm(y, gate, weight, group=None, eps=1e-6, offset=0.0, norm_first=True, out_dtype=None, scale=None, out=None):
+    """The gated norm behind a layer (rssm_gated_rmsnorm): y [...][n], gate [...][n] (bf16 or fp32 each; rows may lie apart),
+    weight [n], or [group] for all groups -> with s = silu(gate), the norm of each ``group`` columns (all) of y times s, or
+    without ``norm_first`` of y s; in ``out_dtype`` (gate's) or in 8 bits as for ``add_rmsnorm``."""
+    n = y.shape[-1]
+    device = _device(y, "y")
+    lead = y.shape[:-1]
+    gate_dtype = _in_dtype(gate, "gate")
+    stride = _apart(y, "y", lead, n, (n,), _in_dtype(y, "y"), device)
+    g_stride = _apart(gate, "gate", lead, n, (n,), gate_dtype, device)
+    cfg, w, o, s, got = _norm(y, weight, n, group or n, eps, offset, out_dtype or gate_dtype, scale, out, _DT[gate_dtype],
+                              norm_first, device)
+    abi.check(abi.load().rssm_gated_rmsnorm(C.byref(cfg), y.data_ptr(), stride, gate.data_ptr(), g_stride, w, o, s,
+                                            _stream_of(device)), "rssm_gated_rmsnorm")
+    return got
 
 
 # ---------------------------------------------------------------------- comparison kernels

@@ -17,6 +17,7 @@ MAMBA2, GDN = 0, 1
 F32, BF16 = 0, 1
 HP_F32, HP_F16_SR, HP_F8_SR = 0, 1, 2
 READ_SAME, READ_NVFP4, READ_SHARED_NVFP4, READ_NVFP4D = 0, 1, 2, 3
+SCALE_NONE, SCALE_ROW, SCALE_BLOCK = 0, 1, 2
 STATUS = {0: "RSSM_OK", 1: "RSSM_ERR_ARG", 2: "RSSM_ERR_SHAPE", 3: "RSSM_ERR_UNSUPPORTED",
           4: "RSSM_ERR_ARENA_TOO_SMALL", 5: "RSSM_ERR_CUDA", 6: "RSSM_ERR_DEVICE"}
 DEV_OK, DEV_PENDING, DEV_NO_VERIFY, DEV_ACCEPTED, DEV_TIMEOUT, DEV_PROMPT, DEV_BUFFERED = 0, 1, 2, 3, 4, 5, 6
@@ -44,6 +45,19 @@ class ShortConvConfig(C.Structure):
     _fields_ = [("batch", C.c_int), ("channels", C.c_int), ("width", C.c_int), ("ring", C.c_int),
                 ("in_dtype", C.c_int), ("silu", C.c_int), ("split", C.c_int * 3), ("weight", C.c_void_p),
                 ("bias", C.c_void_p)]
+
+
+class GdnInputsConfig(C.Structure):
+    _fields_ = [("rows", C.c_int), ("nheads", C.c_int), ("qk_heads", C.c_int), ("out_heads", C.c_int),
+                ("in_dtype", C.c_int), ("eps", C.c_float), ("q", C.c_void_p), ("k", C.c_void_p), ("a", C.c_void_p),
+                ("b", C.c_void_p), ("q_stride", C.c_longlong), ("k_stride", C.c_longlong), ("a_stride", C.c_longlong),
+                ("b_stride", C.c_longlong), ("A_log", C.c_void_p), ("bias", C.c_void_p)]
+
+
+class NormConfig(C.Structure):
+    _fields_ = [("rows", C.c_int), ("columns", C.c_int), ("group", C.c_int), ("weight_columns", C.c_int),
+                ("x_dtype", C.c_int), ("gate_dtype", C.c_int), ("weight_dtype", C.c_int), ("out_dtype", C.c_int),
+                ("scale", C.c_int), ("norm_first", C.c_int), ("eps", C.c_float), ("offset", C.c_float)]
 
 
 class RSSMError(RuntimeError):
@@ -76,6 +90,12 @@ _SIGS = {
     "rssm_mamba2_scan_workspace": [C.POINTER(Config), C.c_int, C.c_int, C.POINTER(C.c_size_t)],
     "rssm_mamba2_scan": [C.POINTER(Config), C.POINTER(Prompts), C.POINTER(Tokens), _P, _P, _P, C.c_size_t, _P],
     "rssm_mamba2_prefill": [_P, C.POINTER(Prompts), C.POINTER(Tokens), _P, _P, C.c_size_t, _P],
+    "rssm_gdn_scan_workspace": [C.POINTER(Config), C.c_int, C.c_int, C.POINTER(C.c_size_t)],
+    "rssm_gdn_scan": [C.POINTER(Config), C.c_int, C.POINTER(Prompts), C.POINTER(Tokens), _P, _P, _P, C.c_size_t, _P],
+    "rssm_gdn_prefill": [_P, C.c_int, C.POINTER(Prompts), C.POINTER(Tokens), _P, _P, C.c_size_t, _P],
+    "rssm_gdn_inputs": [C.POINTER(GdnInputsConfig), _P, _P, _P, _P, _P],
+    "rssm_add_rmsnorm": [C.POINTER(NormConfig), _P, C.c_longlong, _P, C.c_longlong, _P, _P, _P, _P],
+    "rssm_gated_rmsnorm": [C.POINTER(NormConfig), _P, C.c_longlong, _P, C.c_longlong, _P, _P, _P, _P],
     "rssm_shortconv_prefill": [C.POINTER(ShortConvConfig), C.POINTER(Prompts), _P, _P, _P, C.c_longlong,
                                C.POINTER(_P * 3), _P],
     "rssm_shortconv_step": [C.POINTER(ShortConvConfig), _P, _P, _P, C.c_longlong, C.POINTER(_P * 3), _P],

@@ -7,6 +7,7 @@
 #include <stdlib.h>
 #include <string.h>
 
+#include "layer_kernels.h"
 #include "prompt_kernels.h"
 #include "sched.h"
 
@@ -533,6 +534,188 @@ rssm_status rssm_mamba2_prefill(rssm_ctx *x, const rssm_prompts *pr, const rssm_
   // prompts (a bad offset refuses all of them), whose sequences keep what they have buffered.
   if (x->pos != 0) x->pos = -1;
   return RSSM_OK;
+}
+
+// the shape rules of a GDN state; with the formats (of a context) or without
+static rssm_status gdn_scan_validate(const rssm_config *cfg, int qk_heads, bool formats) {
+  if (!cfg) return RSSM_ERR_ARG;
+  rssm_config c = *cfg;
+  if (!formats) {
+    c.hp = RSSM_HP_F32;
+    c.read = RSSM_READ_SAME;
+    c.skip_tau = 0.f;
+    c.window = 1;
+    c.max_draft = 0;
+  }
+  rssm_status s = validate(&c);
+  if (s != RSSM_OK) return s;
+  if (c.kind != RSSM_GDN) return RSSM_ERR_UNSUPPORTED;
+  if (c.nheads > 65535 || qk_heads < 1 || c.nheads % qk_heads != 0) return RSSM_ERR_SHAPE;  // one grid row a head
+  return RSSM_OK;
+}
+
+// whether a context's checkpoint is not simply the fp32 state
+static bool gdn_converted(const rssm_config &c) { return c.hp != RSSM_HP_F32 || c.read != RSSM_READ_SAME; }
+
+static size_t gdn_state_bytes(const rssm_config &c, int nseq) {
+  return align_up((size_t)nseq * c.nheads * c.headdim * kCols * 4, 256);
+}
+
+static rssm_status run_gdn_scan(const rssm_config &c, int qk_heads, const Prompts &p, const rssm_tokens *tok, float *S,
+                                bool by_prompt, float *y, int *err, long long wait_cycles, int withhold, int num_sms,
+                                cudaStream_t st) {
+  GdnScanArgs a{};
+  a.H = c.nheads; a.Hk = qk_heads; a.R = c.headdim; a.by_prompt = by_prompt; a.q_scale = c.q_scale;
+  a.q = tok->q; a.k = tok->k; a.v = tok->v; a.alpha = tok->alpha; a.beta = tok->beta; a.S = S; a.y = y;
+  a.err = err; a.wait_cycles = wait_cycles; a.withhold = withhold;
+  cudaError_t e = launch_gdn_scan(a, p, esize(c), num_sms, st);
+  if (e == cudaSuccess && p.refused_nan && p.total > 0) e = launch_refuse(p, y, c.nheads * c.headdim, num_sms, st);
+  return e == cudaSuccess ? RSSM_OK : cuda_fail(e);
+}
+
+static bool gdn_scan_pointers(const rssm_prompts *pr, const rssm_tokens *tok, const float *y) {
+  if (!tok) return false;
+  if (pr->total == 0) return true;
+  return tok->q && tok->k && tok->v && tok->alpha && tok->beta && y && aligned16(tok->q) && aligned16(tok->k) &&
+         aligned16(tok->v) && aligned16(y);
+}
+
+rssm_status rssm_gdn_scan_workspace(const rssm_config *cfg, int total, int nseq, size_t *bytes) {
+  rssm_status s = gdn_scan_validate(cfg, 1, true);
+  if (s != RSSM_OK) return s;
+  if (!bytes) return RSSM_ERR_ARG;
+  if (!prompts_size(total, nseq, cfg->batch)) return RSSM_ERR_SHAPE;
+  *bytes = gdn_converted(*cfg) ? gdn_state_bytes(*cfg, nseq) : 0;
+  return RSSM_OK;
+}
+
+rssm_status rssm_gdn_scan(const rssm_config *cfg, int qk_heads, const rssm_prompts *pr, const rssm_tokens *tok, float *S,
+                          float *y, void *work, size_t work_bytes, rssm_stream stream) {
+  rssm_status s = gdn_scan_validate(cfg, qk_heads, false);
+  if (s == RSSM_OK) s = prompts_validate(pr, cfg->batch);
+  if (s != RSSM_OK) return s;
+  if (!S || !aligned16(S) || !gdn_scan_pointers(pr, tok, y)) return RSSM_ERR_ARG;
+  int sms = 0;
+  s = sm_count(&sms);
+  if (s != RSSM_OK) return s;
+  return run_gdn_scan(*cfg, qk_heads, device_prompts(pr, cfg->batch, nullptr), tok, S, false, y, nullptr, kWaitCycles, -1,
+                      sms, reinterpret_cast<cudaStream_t>(stream));
+}
+
+rssm_status rssm_gdn_prefill(rssm_ctx *x, int qk_heads, const rssm_prompts *pr, const rssm_tokens *tok, float *y,
+                             void *work, size_t work_bytes, rssm_stream stream) {
+  if (!x) return RSSM_ERR_ARG;
+  if (x->cfg.kind != RSSM_GDN || !x->loaded) return RSSM_ERR_UNSUPPORTED;
+  const rssm_config &c = x->cfg;
+  rssm_status s = gdn_scan_validate(&c, qk_heads, true);
+  if (s == RSSM_OK) s = prompts_validate(pr, c.batch);
+  if (s != RSSM_OK) return s;
+  if (!gdn_scan_pointers(pr, tok, y)) return RSSM_ERR_ARG;
+  const bool converted = gdn_converted(c);
+  if (converted) {
+    if (!work || ((uintptr_t)work & 255u)) return RSSM_ERR_ARG;
+    if (work_bytes < gdn_state_bytes(c, pr->nseq)) return RSSM_ERR_ARENA_TOO_SMALL;
+  }
+  cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+  const Prompts p = device_prompts(pr, c.batch, meta_cur(x));
+  PromptStateArgs ps{};
+  ps.H = c.nheads; ps.rows = c.headdim; ps.hp_mode = c.hp; ps.read_mode = c.read; ps.states = static_cast<float *>(work);
+  ps.hp = x->arena + x->lay.hp; ps.hs = reinterpret_cast<float *>(x->arena + x->lay.hs);
+  ps.rq = x->arena + x->lay.rq; ps.rs = x->arena + x->lay.rs; ps.rg = reinterpret_cast<float *>(x->arena + x->lay.rg);
+  ps.rc = x->arena + x->lay.rc; ps.seed = c.seed;
+  cudaError_t e = cudaSuccess;
+  if (converted && pr->resume) e = launch_prompt_states(ps, p, false, st);
+  if (e != cudaSuccess) return cuda_fail(e);
+  s = run_gdn_scan(c, qk_heads, p, tok, converted ? ps.states : reinterpret_cast<float *>(x->arena + x->lay.hp), converted,
+                   y, err_word(x), x->wait_cycles, x->withhold, x->num_sms, st);
+  x->withhold = -1;  // the test hook fires on one launch only
+  if (s != RSSM_OK) return s;
+  if (converted) e = launch_prompt_states(ps, p, true, st);
+  unsigned char *skip = c.skip_tau > 0.f ? x->arena + x->lay.skip : nullptr;
+  if (e == cudaSuccess) e = launch_prefill_meta(p, meta_cur(x), meta_next(x), skip, c.nheads, err_word(x), st);
+  if (e != cudaSuccess) return cuda_fail(e);
+  x->parity ^= 1;
+  if (x->pos != 0) x->pos = -1;  // as in rssm_mamba2_prefill
+  return RSSM_OK;
+}
+
+// ------------------------------------------------------------------ between a layer's projections
+
+static bool dtype_ok(int d) { return d == RSSM_F32 || d == RSSM_BF16; }
+
+rssm_status rssm_gdn_inputs(const rssm_gdn_inputs_config *c, void *q_out, void *k_out, float *alpha, float *beta,
+                            rssm_stream stream) {
+  if (!c || !dtype_ok(c->in_dtype) || !(c->eps >= 0.f)) return RSSM_ERR_ARG;
+  if (c->rows < 0 || c->rows > (1 << 30) || c->nheads < 1 || c->nheads > 65535 || c->qk_heads < 1 ||
+      c->nheads % c->qk_heads != 0 || (c->out_heads != c->qk_heads && c->out_heads != c->nheads))
+    return RSSM_ERR_SHAPE;
+  // blocks of the launch: a block takes 16 vectors or 256 gates
+  if (((long long)c->rows * c->qk_heads >> 3) + ((long long)c->rows * c->nheads >> 8) > 0x7ffffff0LL) return RSSM_ERR_SHAPE;
+  if (c->rows == 0) return RSSM_OK;
+  const long long vec = (long long)c->qk_heads * kCols;
+  if (c->q_stride < vec || c->k_stride < vec || c->q_stride % 8 != 0 || c->k_stride % 8 != 0 || c->a_stride < c->nheads ||
+      c->b_stride < c->nheads)
+    return RSSM_ERR_SHAPE;
+  if (!c->q || !c->k || !c->a || !c->b || !c->A_log || !c->bias || !q_out || !k_out || !alpha || !beta ||
+      !aligned16(c->q) || !aligned16(c->k) || !aligned16(q_out) || !aligned16(k_out))
+    return RSSM_ERR_ARG;
+  GdnInputsArgs a{};
+  a.rows = c->rows; a.H = c->nheads; a.Hk = c->qk_heads; a.out_heads = c->out_heads; a.eps = c->eps;
+  a.q = c->q; a.k = c->k; a.a = c->a; a.b = c->b;
+  a.stride_q = c->q_stride; a.stride_k = c->k_stride; a.stride_a = c->a_stride; a.stride_b = c->b_stride;
+  a.A_log = c->A_log; a.bias = c->bias; a.q_out = q_out; a.k_out = k_out; a.alpha = alpha; a.beta = beta;
+  int sms = 0;
+  const rssm_status s = sm_count(&sms);
+  if (s != RSSM_OK) return s;
+  const cudaError_t e = launch_gdn_inputs(a, c->in_dtype == RSSM_BF16 ? 2 : 4, sms, reinterpret_cast<cudaStream_t>(stream));
+  return e == cudaSuccess ? RSSM_OK : cuda_fail(e);
+}
+
+static rssm_status norm_args(const rssm_norm_config *c, bool gated, const void *x, long long x_stride, const void *weight,
+                             void *out, float *scales, NormArgs &a) {
+  if (!c || !dtype_ok(c->x_dtype) || !dtype_ok(c->weight_dtype) || (gated && !dtype_ok(c->gate_dtype))) return RSSM_ERR_ARG;
+  if (c->scale != RSSM_SCALE_NONE && c->scale != RSSM_SCALE_ROW && c->scale != RSSM_SCALE_BLOCK) return RSSM_ERR_ARG;
+  if (c->scale == RSSM_SCALE_NONE && !dtype_ok(c->out_dtype)) return RSSM_ERR_ARG;
+  if (!(c->eps >= 0.f)) return RSSM_ERR_ARG;
+  if (c->rows < 0 || c->columns < 8 || c->columns > 32768 || c->columns % 8 != 0 || c->group < 8 || c->group % 8 != 0 ||
+      c->columns % c->group != 0 || (c->weight_columns != c->columns && c->weight_columns != c->group))
+    return RSSM_ERR_SHAPE;
+  if (!gated && (c->group != c->columns || c->weight_columns != c->columns)) return RSSM_ERR_SHAPE;
+  if (c->rows > 0) {
+    if (x_stride < c->columns || x_stride % 8 != 0) return RSSM_ERR_SHAPE;
+    if (!x || !weight || !out || !aligned16(x) || !aligned16(weight) || !aligned16(out) ||
+        (c->scale != RSSM_SCALE_NONE && !scales))
+      return RSSM_ERR_ARG;
+  }
+  a.rows = c->rows; a.columns = c->columns; a.group = c->group; a.weight_columns = c->weight_columns;
+  a.x_dtype = c->x_dtype; a.gate_dtype = c->gate_dtype; a.weight_dtype = c->weight_dtype; a.out_dtype = c->out_dtype;
+  a.scale = c->scale; a.norm_first = c->norm_first != 0; a.eps = c->eps; a.offset = c->offset;
+  a.x = x; a.stride_x = x_stride; a.weight = weight; a.out = out; a.scales = scales;
+  return RSSM_OK;
+}
+
+rssm_status rssm_add_rmsnorm(const rssm_norm_config *cfg, const void *x, long long x_stride, void *residual,
+                             long long residual_stride, const void *weight, void *out, float *scales, rssm_stream stream) {
+  NormArgs a{};
+  const rssm_status s = norm_args(cfg, false, x, x_stride, weight, out, scales, a);
+  if (s != RSSM_OK || a.rows == 0) return s;
+  if (residual && (residual_stride < a.columns || residual_stride % 8 != 0)) return RSSM_ERR_SHAPE;
+  if (residual && !aligned16(residual)) return RSSM_ERR_ARG;
+  a.residual = residual; a.stride_residual = residual_stride;
+  const cudaError_t e = launch_norm(a, false, reinterpret_cast<cudaStream_t>(stream));
+  return e == cudaSuccess ? RSSM_OK : cuda_fail(e);
+}
+
+rssm_status rssm_gated_rmsnorm(const rssm_norm_config *cfg, const void *x, long long x_stride, const void *gate,
+                               long long gate_stride, const void *weight, void *out, float *scales, rssm_stream stream) {
+  NormArgs a{};
+  const rssm_status s = norm_args(cfg, true, x, x_stride, weight, out, scales, a);
+  if (s != RSSM_OK || a.rows == 0) return s;
+  if (gate_stride < a.columns || gate_stride % 8 != 0) return RSSM_ERR_SHAPE;
+  if (!gate || !aligned16(gate)) return RSSM_ERR_ARG;
+  a.gate = gate; a.stride_gate = gate_stride;
+  const cudaError_t e = launch_norm(a, true, reinterpret_cast<cudaStream_t>(stream));
+  return e == cudaSuccess ? RSSM_OK : cuda_fail(e);
 }
 
 // ------------------------------------------------------------------ short convolution

@@ -2,25 +2,25 @@
 // stored formats (fp32, fp16 or FP8 E4M3 with stochastic rounding at epoch 0, plus the
 // NVFP4 read copy) and widen the stored checkpoint back to fp32 for export.  The rounding rules are
 // those of lowprec.cuh.  One block of 64 threads per 64-row tile of a head's state;
-// thread r owns row r (128 columns).
-#include "kernels.h"
+// thread r owns row r (128 columns).  The same for the states of packed prompts.
+#include "prompt_kernels.h"
 #include "lowprec.cuh"
 
 namespace rssm {
 
 namespace {
 
-__global__ void store_state_kernel(const float *S, void *hp, float *hs, int hp_mode, unsigned char *rq,
-                                   unsigned char *rs, float *rg, unsigned char *rc, int read_mode, int rows_per_head,
-                                   unsigned long long seed) {
+// Tile t of a head's fp32 state `head` [rows_per_head][128] into the stored formats of unit (sequence, head).
+__device__ __forceinline__ void store_tile(const float *head, size_t unit, int t, uint32_t epoch, void *hp, float *hs,
+                                           int hp_mode, unsigned char *rq, unsigned char *rs, float *rg,
+                                           unsigned char *rc, int read_mode, int rows_per_head,
+                                           unsigned long long seed) {
   const int nrb = (rows_per_head + kFp4Rows - 1) / kFp4Rows;
-  const size_t unit = blockIdx.x / nrb;
-  const int t = blockIdx.x % nrb;
   const int rows = min(kFp4Rows, rows_per_head - kFp4Rows * t);
   const int row = threadIdx.x;
   const bool live = row < rows;
   const int rowg = kFp4Rows * t + row;
-  const float *src = S + (unit * rows_per_head + rowg) * kCols;
+  const float *src = head + (size_t)rowg * kCols;
   __shared__ float red[64];
   float am = 0.f;
   if (live)
@@ -38,7 +38,7 @@ __global__ void store_state_kernel(const float *S, void *hp, float *hs, int hp_m
       unsigned char *dst = reinterpret_cast<unsigned char *>(hp) + (unit * rows_per_head + rowg) * kCols;
       for (int c = 0; c < kCols; c += 4) {
         const uint32_t elem = (uint32_t)(rowg * kCols + c);
-        const uint4 rw = philox4x32_10(make_uint4((uint32_t)unit, 0u, elem >> 2, 0u), (uint32_t)seed,
+        const uint4 rw = philox4x32_10(make_uint4((uint32_t)unit, epoch, elem >> 2, 0u), (uint32_t)seed,
                                        (uint32_t)(seed >> 32));
         dst[c] = (unsigned char)fp8_sr_code(__fdiv_rn(src[c], s8), rw.x);
         dst[c + 1] = (unsigned char)fp8_sr_code(__fdiv_rn(src[c + 1], s8), rw.y);
@@ -52,7 +52,7 @@ __global__ void store_state_kernel(const float *S, void *hp, float *hs, int hp_m
       __half *dst = reinterpret_cast<__half *>(hp) + (unit * rows_per_head + rowg) * kCols;
       for (int c = 0; c < kCols; c += 4) {
         const uint32_t elem = (uint32_t)(rowg * kCols + c);
-        const uint4 rw = philox4x32_10(make_uint4((uint32_t)unit, 0u, elem >> 2, 0u), (uint32_t)seed,
+        const uint4 rw = philox4x32_10(make_uint4((uint32_t)unit, epoch, elem >> 2, 0u), (uint32_t)seed,
                                        (uint32_t)(seed >> 32));
         dst[c] = fp16_sr(src[c], rw.x);
         dst[c + 1] = fp16_sr(src[c + 1], rw.y);
@@ -112,17 +112,25 @@ __global__ void store_state_kernel(const float *S, void *hp, float *hs, int hp_m
   }
 }
 
-__global__ void widen_state_kernel(const void *hp, const float *hs, int hp_mode, const unsigned char *rq,
-                                   const unsigned char *rs, const float *rg, int read_mode, float *out,
-                                   int rows_per_head) {
+__global__ void store_state_kernel(const float *S, void *hp, float *hs, int hp_mode, unsigned char *rq,
+                                   unsigned char *rs, float *rg, unsigned char *rc, int read_mode, int rows_per_head,
+                                   unsigned long long seed) {
   const int nrb = (rows_per_head + kFp4Rows - 1) / kFp4Rows;
   const size_t unit = blockIdx.x / nrb;
-  const int t = blockIdx.x % nrb;
+  store_tile(S + unit * rows_per_head * kCols, unit, blockIdx.x % nrb, 0u, hp, hs, hp_mode, rq, rs, rg, rc, read_mode,
+             rows_per_head, seed);
+}
+
+// The stored state of tile t of unit (sequence, head), widened into `head` [rows_per_head][128].
+__device__ __forceinline__ void widen_tile(float *head, size_t unit, int t, const void *hp, const float *hs, int hp_mode,
+                                           const unsigned char *rq, const unsigned char *rs, const float *rg,
+                                           int read_mode, int rows_per_head) {
+  const int nrb = (rows_per_head + kFp4Rows - 1) / kFp4Rows;
   const int rows = min(kFp4Rows, rows_per_head - kFp4Rows * t);
   const int row = threadIdx.x;
   if (row >= rows) return;
   const size_t r = unit * rows_per_head + kFp4Rows * t + row;
-  float *dst = out + r * kCols;
+  float *dst = head + (size_t)(kFp4Rows * t + row) * kCols;
   if (read_mode == RSSM_READ_SHARED_NVFP4) {
     const float g = rg[unit * nrb + t];
     for (int blk = 0; blk < kCols / 16; ++blk) {
@@ -145,6 +153,35 @@ __global__ void widen_state_kernel(const void *hp, const float *hs, int hp_mode,
   }
 }
 
+__global__ void widen_state_kernel(const void *hp, const float *hs, int hp_mode, const unsigned char *rq,
+                                   const unsigned char *rs, const float *rg, int read_mode, float *out,
+                                   int rows_per_head) {
+  const int nrb = (rows_per_head + kFp4Rows - 1) / kFp4Rows;
+  const size_t unit = blockIdx.x / nrb;
+  widen_tile(out + unit * rows_per_head * kCols, unit, blockIdx.x % nrb, hp, hs, hp_mode, rq, rs, rg, read_mode,
+             rows_per_head);
+}
+
+// The states of packed prompts, fp32 [nseq][H][rows][128] by prompt: from the stored formats of their sequences, where a
+// prompt resumes, or into them, with the sequence's next epoch.  One block a (prompt, head, tile).
+template <bool kStore>
+__global__ void __launch_bounds__(kFp4Rows) prompt_state_kernel(PromptStateArgs a, Prompts pr) {
+  __shared__ PieceWord found;
+  Piece pc;
+  const int nrb = (a.rows + kFp4Rows - 1) / kFp4Rows;
+  const int t = blockIdx.x % nrb, h = blockIdx.x / nrb % a.H, prompt = blockIdx.x / nrb / a.H;
+  if (find_piece(pr, prompt, pr.total + 1, pc, &found) != kPieceRun) return;
+  float *head = a.states + ((size_t)prompt * a.H + h) * a.rows * kCols;
+  const size_t unit = (size_t)pc.slot * a.H + h;
+  if (kStore) {
+    if (pc.resume && pc.end == pc.begin) return;  // an empty prompt leaves its sequence as it is
+    store_tile(head, unit, t, (uint32_t)pr.meta[pc.slot].y + 1u, a.hp, a.hs, a.hp_mode, a.rq, a.rs, a.rg, a.rc,
+               a.read_mode, a.rows, a.seed);
+  } else if (pc.resume) {
+    widen_tile(head, unit, t, a.hp, a.hs, a.hp_mode, a.rq, a.rs, a.rg, a.read_mode, a.rows);
+  }
+}
+
 }  // namespace
 
 cudaError_t launch_store_state(const float *S, void *hp, float *hs, int hp_mode, unsigned char *rq, unsigned char *rs,
@@ -162,6 +199,13 @@ cudaError_t launch_widen_state(const void *hp, const float *hs, int hp_mode, con
   const int nrb = (rows + kFp4Rows - 1) / kFp4Rows;
   widen_state_kernel<<<(unsigned)((size_t)units * nrb), kFp4Rows, 0, stream>>>(hp, hs, hp_mode, rq, rs, rg, read_mode,
                                                                                  out, rows);
+  return cudaGetLastError();
+}
+
+cudaError_t launch_prompt_states(const PromptStateArgs &a, const Prompts &pr, bool store, cudaStream_t stream) {
+  const size_t blocks = (size_t)pr.nseq * a.H * ((a.rows + kFp4Rows - 1) / kFp4Rows);
+  if (store) prompt_state_kernel<true><<<(unsigned)blocks, kFp4Rows, 0, stream>>>(a, pr);
+  else prompt_state_kernel<false><<<(unsigned)blocks, kFp4Rows, 0, stream>>>(a, pr);
   return cudaGetLastError();
 }
 

@@ -32,6 +32,34 @@ cudaError_t launch_refuse(const Prompts &pr, float *y, int row, int num_sms, cud
 cudaError_t launch_prefill_meta(const Prompts &pr, const int4 *meta_in, int4 *meta_out, unsigned char *skip, int H,
                                 int *err, cudaStream_t stream);
 
+// Gated delta rule over packed prompts
+struct GdnScanArgs {
+  int H, Hk, R;                     // heads of v; of q and k (Hk divides H); rows of a head's state (d_v)
+  int by_prompt;                    // S is indexed by prompt instead of by slot
+  float q_scale;
+  const void *q, *k, *v;            // [total][Hk][128] x2, [total][H][R]
+  const float *alpha, *beta;        // [total][H]
+  float *S;                         // [nslots or nseq][H][R][128]
+  float *y;                         // [total][H][R]
+  int *err;                         // error word, may be null
+  long long wait_cycles;            // bound of the tensor-core kernel's waits
+  int withhold;                     // test hook: no block loads k of this chunk (-1: off)
+};
+// token by token: fp32 inputs, prompts of a few tokens
+cudaError_t launch_gdn_scan(const GdnScanArgs &a, const Prompts &pr, int esz, int num_sms, cudaStream_t stream);
+// states of packed prompts [nseq][H][rows][128] from and to a GDN context's stored formats
+struct PromptStateArgs {
+  int H, rows, hp_mode, read_mode;
+  float *states;
+  void *hp;
+  float *hs;
+  unsigned char *rq, *rs;
+  float *rg;
+  unsigned char *rc;
+  unsigned long long seed;
+};
+cudaError_t launch_prompt_states(const PromptStateArgs &a, const Prompts &pr, bool store, cudaStream_t stream);
+
 // short causal convolution
 struct ShortConvArgs {
   int batch, channels, width, ring, silu;

@@ -194,8 +194,7 @@ rssm_status rssm_commit(rssm_ctx *ctx, const int *accepted, rssm_stream stream);
 rssm_status rssm_flush(rssm_ctx *ctx, const unsigned char *mask, rssm_stream stream);
 
 /* ---------------------------------------------------------------- prompts
- * The pages start from a checkpoint and leave open what makes one; these calls do, from the published Mamba-2
- * recurrence.  Prompts come packed: prompt i holds tokens offsets[i] .. offsets[i+1]-1 of `total`, so the token
+ * The pages start from a checkpoint and leave open what makes one; these calls do, from the published recurrences.  Prompts come packed: prompt i holds tokens offsets[i] .. offsets[i+1]-1 of `total`, so the token
  * inputs have the leading dimension [total] and no padding.  A prompt may be empty.  Rows of no prompt are neither
  * read into a result nor written.  Prompt i belongs to sequence slots[i] of the state (i itself without slots); other
  * sequences keep theirs.
@@ -235,6 +234,26 @@ rssm_status rssm_mamba2_scan(const rssm_config *cfg, const rssm_prompts *pr, con
 rssm_status rssm_mamba2_prefill(rssm_ctx *ctx, const rssm_prompts *pr, const rssm_tokens *tok, float *y, void *work,
                                 size_t work_bytes, rssm_stream stream);
 
+/* Bytes of device scratch that rssm_gdn_scan (cfg with RSSM_HP_F32 and RSSM_READ_SAME) and rssm_gdn_prefill (the context's
+ * cfg) want for prompts of this size; 0 is possible.  Depends on the arguments alone. */
+rssm_status rssm_gdn_scan_workspace(const rssm_config *cfg, int total, int nseq, size_t *bytes);
+
+/* The gated delta rule over whole prompts, on a state that the caller keeps.  Of cfg: kind, batch (sequences of S), nheads
+ * H, headdim d_v, dstate, in_dtype, q_scale.  tok: q, k [total][qk_heads][128], v [total][H][d_v] in cfg.in_dtype, alpha,
+ * beta fp32 [total][H];  qk_heads divides H, and value head h takes query and key head h / (H / qk_heads).
+ *   S device fp32 [batch][H][d_v][128], the prompts' sequences rewritten;  y device fp32 [total][H][d_v];
+ *   work as for rssm_mamba2_scan.
+ * From a value of v that is not finite on, its row's outputs in that prompt are not finite, nor its row of the state; from a
+ * value of k, alpha or beta on, all of that head's; a value of q touches its own token's outputs alone.
+ * alpha is any finite number; decays are products of it, so values beyond 1 can overflow as they do token by token. */
+rssm_status rssm_gdn_scan(const rssm_config *cfg, int qk_heads, const rssm_prompts *pr, const rssm_tokens *tok, float *S,
+                          float *y, void *work, size_t work_bytes, rssm_stream stream);
+
+/* The same on a context, as rssm_mamba2_prefill: the states become the sequences' checkpoints in the context's formats
+ * (stochastic rounding takes the words of the sequence's new epoch), with their read copies. */
+rssm_status rssm_gdn_prefill(rssm_ctx *ctx, int qk_heads, const rssm_prompts *pr, const rssm_tokens *tok, float *y,
+                             void *work, size_t work_bytes, rssm_stream stream);
+
 /* ---------------------------------------------------------------- short convolution
  * The causal depthwise filter in front of a layer's inputs (x, B, C of Mamba-2; q, k, v of GDN):
  *   out[t][c] = act(bias[c] + sum_{k < K} weight[c][k] in[t - (K-1) + k][c]),
@@ -269,6 +288,55 @@ rssm_status rssm_shortconv_verify(const rssm_shortconv_config *cfg, int T, void 
                                   long long in_stride, void *const out[3], rssm_stream stream);
 /* cur[b] moves by accepted[b] (device int32 [batch]; clamped to 0..ring-(K-1)).  Uses cfg's batch, width and ring. */
 rssm_status rssm_shortconv_commit(const rssm_shortconv_config *cfg, int *cur, const int *accepted, rssm_stream stream);
+
+/* ---------------------------------------------------------------- between a layer's projections
+ * What the decode and prompt calls leave to a layer around them, on any number of token rows (a decode step's sequences,
+ * a packed prompt's tokens).  The published layers' formulas; sums are fp32, each result is rounded once.
+ * Strides count elements from one row to the next: rows may be slices of a wider projection; those of vectors start on
+ * 16-byte boundaries.  Outputs are contiguous and overlap no input.  rows = 0 does nothing. */
+
+/* Inputs of the gated delta rule, per row and head:
+ *   q_out = q / sqrt(sum q^2 + eps), k_out likewise (in_dtype, [rows][out_heads][128]; out_heads = qk_heads, or nheads:
+ *   each head repeated nheads / qk_heads times, as rssm_gdn_step and rssm_verify take them);
+ *   alpha = exp(-exp(A_log) softplus(a + bias)), beta = 1 / (1 + exp(-b))   (fp32 [rows][nheads]). */
+typedef struct {
+  int rows, nheads, qk_heads, out_heads;
+  int in_dtype;                      /* rssm_dtype of q, k, a, b, q_out, k_out */
+  float eps;                         /* >= 0 */
+  const void *q, *k;                 /* device, rows of [qk_heads][128] */
+  const void *a, *b;                 /* device, rows of [nheads] */
+  long long q_stride, k_stride, a_stride, b_stride;
+  const float *A_log, *bias;         /* device [nheads] */
+} rssm_gdn_inputs_config;
+rssm_status rssm_gdn_inputs(const rssm_gdn_inputs_config *cfg, void *q_out, void *k_out, float *alpha, float *beta,
+                            rssm_stream stream);
+
+/* Root-mean-square norms: out = h / sqrt(mean h^2 + eps) (offset + weight), the mean over each group of columns.
+ * With a scale the output is E4M3 (saturating, to nearest) of out / scale, scale = max |out| / 448 over the row or each
+ * block of 128 columns of it (fp32 [rows] or [rows][ceil(columns / 128)]; at least 2^-126; NaN where out has one). */
+typedef enum { RSSM_SCALE_NONE = 0, RSSM_SCALE_ROW = 1, RSSM_SCALE_BLOCK = 2 } rssm_scale;
+typedef struct {
+  int rows;
+  int columns;        /* multiple of 8, 8..32768 */
+  int group;          /* columns of a group: multiple of 8 that divides columns */
+  int weight_columns; /* columns, or group: one weight for all groups */
+  int x_dtype;        /* rssm_dtype of x and residual */
+  int gate_dtype;     /* of gate */
+  int weight_dtype;
+  int out_dtype;      /* rssm_dtype without a scale */
+  int scale;          /* rssm_scale */
+  int norm_first;     /* gated: 1 = norm, then gate; 0 = gate, then norm */
+  float eps, offset;
+} rssm_norm_config;
+
+/* In front of a layer: h = x + residual (fp32), which goes back to residual, rounded once (the norm takes h before that).
+ * residual may be NULL: h = x.  Takes cfg.group = cfg.weight_columns = columns. */
+rssm_status rssm_add_rmsnorm(const rssm_norm_config *cfg, const void *x, long long x_stride, void *residual,
+                             long long residual_stride, const void *weight, void *out, float *scales, rssm_stream stream);
+
+/* Behind a layer: with s = gate / (1 + exp(-gate)), the norm of x times s (norm_first), or the norm of (x s). */
+rssm_status rssm_gated_rmsnorm(const rssm_norm_config *cfg, const void *x, long long x_stride, const void *gate,
+                               long long gate_stride, const void *weight, void *out, float *scales, rssm_stream stream);
 
 /* ---------------------------------------------------------------- draft verification
  * Which drafts of a speculative round stand ([HMD] Interpretation 3rd paragraph leaves the test itself open; this is

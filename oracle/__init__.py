@@ -35,6 +35,7 @@ Modules:
   commit, flush) and the separate-precision modes.
 * ``prompts`` -- packed prompts through the recurrence, the short convolution
   with its history ring, and the verification of drafted tokens.
+* ``layer`` -- inputs of the gated delta rule, norms and their 8-bit outputs.
 
 Pins: every function is checked by tests marked ``not gpu`` against closed
 forms, invariants stated by the pages, brute force on tiny shapes, library

@@ -1,6 +1,6 @@
 """Prompts, the short convolution and draft verification in float64 (oracle; test infrastructure only).
 
-* ``mamba2_scan`` -- the Mamba-2 recurrence of ``recurrence.mamba2_step`` token by token over packed prompts.
+* ``mamba2_scan``, ``gdn_scan`` -- the recurrences of ``recurrence`` token by token over packed prompts.
 * ``shortconv`` -- the causal depthwise filter over one sequence of rows, with its history as leading rows.
 * ``ShortConvRing`` -- the history ring and its cursor: prompts, steps, tentative rows and their commit.
 * ``accept_drafts`` -- the rejection rule of speculative sampling (Leviathan, Kalman & Matias, "Fast inference from
@@ -11,7 +11,7 @@ from __future__ import annotations
 
 import numpy as np
 
-from .recurrence import mamba2_step
+from .recurrence import gdn_step, mamba2_step
 
 f64 = np.float64
 
@@ -132,3 +132,19 @@ def accept_drafts(target, tokens, u, draft=None, count=None):
         over = np.nonzero((cdf > f64(u[b, T]) * cdf[-1]) & (m > 0))[0]
         nxt[b] = over[0] if len(over) else np.nonzero(m)[0][-1]
     return acc, nxt
+
+
+def gdn_scan(S, q, k, v, alpha, beta, offsets, slots=None, resume=None, q_scale=1.0):
+    """S [batch][H][dv][dk]; q, k [total][Hk][dk]; v [total][H][dv]; alpha, beta [total][H]: (new S, y [total][H][dv]).
+
+    Value head h takes query and key head h // (H / Hk).  Rows of no prompt are NaN in y."""
+    S = np.array(S, f64)
+    heads = np.arange(v.shape[1]) // (v.shape[1] // q.shape[1])
+    y = np.full(v.shape, np.nan)
+    for i in range(len(offsets) - 1):
+        slot = i if slots is None else int(slots[i])
+        s = S[slot] if resume is not None and resume[i] else np.zeros_like(S[slot])
+        for t in range(int(offsets[i]), int(offsets[i + 1])):
+            s, y[t] = gdn_step(s, q[t][heads], k[t][heads], v[t], alpha[t], beta[t], q_scale)
+        S[slot] = s
+    return S, y

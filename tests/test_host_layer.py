@@ -1,0 +1,126 @@
+"""Argument checks of the gated-delta-rule prompts and of the calls between a layer's projections, before any device work
+(no GPU)."""
+
+import ctypes as C
+
+import pytest
+import torch
+
+from hybrid_model_ssm_gdn_b200 import abi, add_rmsnorm, gated_rmsnorm, gdn_inputs, gdn_scan
+from hybrid_model_ssm_gdn_b200.build import build
+
+ARG, SHAPE, UNSUPPORTED = 1, 2, 3
+
+
+@pytest.fixture(scope="module")
+def lib():
+    build()
+    return abi.load()
+
+
+def cfg(**kw):
+    base = dict(kind=abi.GDN, batch=4, nheads=4, headdim=128, dstate=128, ngroups=1, window=1, in_dtype=abi.BF16,
+                q_scale=1.0)
+    base.update(kw)
+    return abi.Config(**base)
+
+
+def test_gdn_scan_refusals(lib):
+    tok, p16 = abi.Tokens(q=16, k=16, v=16, alpha=16, beta=16), C.c_void_p(16)
+    ok = dict(total=8, nseq=2, offsets=16)
+
+    def scan(c=None, hk=4, pr=None, tok=tok, S=p16, y=p16):
+        pr = abi.Prompts(**{**ok, **(pr or {})})
+        return lib.rssm_gdn_scan(C.byref(c or cfg()), hk, C.byref(pr), None if tok is None else C.byref(tok), S, y, None, 0,
+                                 None)
+
+    assert lib.rssm_gdn_scan(None, 4, None, None, None, None, None, 0, None) == ARG
+    assert lib.rssm_gdn_scan(C.byref(cfg()), 4, None, C.byref(tok), p16, p16, None, 0, None) == ARG
+    assert scan(c=cfg(kind=abi.MAMBA2, headdim=64, A=16, D=16)) == UNSUPPORTED
+    for bad in (dict(dstate=64), dict(headdim=136), dict(headdim=20), dict(ngroups=2), dict(batch=0), dict(nheads=65536)):
+        assert scan(c=cfg(**bad), hk=1) == SHAPE, bad
+    for hk in (0, -1, 3, 8):
+        assert scan(hk=hk) == SHAPE
+    assert scan(pr=dict(offsets=None)) == ARG
+    for bad in (dict(nseq=0), dict(nseq=5), dict(total=-1), dict(total=2 ** 30 + 1)):
+        assert scan(pr=bad) == SHAPE, bad
+    assert scan(tok=None) == ARG
+    for name in ("q", "k", "v", "alpha", "beta"):
+        assert scan(tok=abi.Tokens(**{**dict(q=16, k=16, v=16, alpha=16, beta=16), name: None})) == ARG
+    for name in ("q", "k", "v"):
+        assert scan(tok=abi.Tokens(**{**dict(q=16, k=16, v=16, alpha=16, beta=16), name: 24})) == ARG
+    assert scan(S=C.c_void_p(8)) == ARG
+    assert scan(y=None) == ARG
+    n = C.c_size_t()
+    assert lib.rssm_gdn_scan_workspace(C.byref(cfg()), 8, 5, C.byref(n)) == SHAPE
+    assert lib.rssm_gdn_scan_workspace(C.byref(cfg()), 8, 2, None) == ARG
+    assert lib.rssm_gdn_scan_workspace(C.byref(cfg(kind=abi.MAMBA2, headdim=64, A=16, D=16)), 8, 2, C.byref(n)) == UNSUPPORTED
+    assert lib.rssm_gdn_prefill(None, 4, None, None, None, None, 0, None) == ARG
+
+
+def test_gdn_inputs_refusals(lib):
+    p = C.c_void_p(16)
+    base = dict(rows=3, nheads=4, qk_heads=2, out_heads=2, in_dtype=abi.BF16, eps=1e-6, q=16, k=16, a=2, b=2, q_stride=256,
+                k_stride=256, a_stride=4, b_stride=4, A_log=4, bias=4)
+
+    def call(q_out=p, alpha=p, **kw):
+        return lib.rssm_gdn_inputs(C.byref(abi.GdnInputsConfig(**{**base, **kw})), q_out, p, alpha, p, None)
+
+    assert lib.rssm_gdn_inputs(None, p, p, p, p, None) == ARG
+    for bad in (dict(in_dtype=2), dict(eps=-1.0), dict(eps=float("nan")), dict(q=None), dict(k=None), dict(a=None),
+                dict(b=None), dict(A_log=None), dict(bias=None), dict(q=24), dict(k=8), dict(q_out=None),
+                dict(q_out=C.c_void_p(8)), dict(alpha=None)):
+        assert call(**bad) == ARG, bad
+    for bad in (dict(rows=-1), dict(nheads=0), dict(qk_heads=0), dict(qk_heads=3), dict(out_heads=3), dict(out_heads=1),
+                dict(q_stride=248), dict(k_stride=260), dict(a_stride=3), dict(b_stride=0),
+                dict(rows=1 << 30, qk_heads=64, out_heads=64, nheads=64)):
+        assert call(**bad) == SHAPE, bad
+    assert call(rows=0, q=None, q_out=None) == 0
+
+
+def test_norm_refusals(lib):
+    p = C.c_void_p(16)
+    base = dict(rows=3, columns=64, group=64, weight_columns=64, x_dtype=1, gate_dtype=1, weight_dtype=1, out_dtype=1,
+                scale=0, norm_first=1, eps=1e-6, offset=0.0)
+
+    def add(x=p, xs=64, r=p, rs=64, w=p, out=p, s=None, **kw):
+        return lib.rssm_add_rmsnorm(C.byref(abi.NormConfig(**{**base, **kw})), x, xs, r, rs, w, out, s, None)
+
+    def gate(x=p, xs=64, z=p, zs=64, w=p, out=p, s=None, **kw):
+        return lib.rssm_gated_rmsnorm(C.byref(abi.NormConfig(**{**base, **kw})), x, xs, z, zs, w, out, s, None)
+
+    assert lib.rssm_add_rmsnorm(None, p, 64, p, 64, p, p, None, None) == ARG
+    assert lib.rssm_gated_rmsnorm(None, p, 64, p, 64, p, p, None, None) == ARG
+    for f in (add, gate):
+        for bad in (dict(x_dtype=2), dict(weight_dtype=-1), dict(out_dtype=2), dict(scale=3), dict(eps=-1e-9), dict(x=None),
+                    dict(w=None), dict(out=None), dict(x=C.c_void_p(8)), dict(w=C.c_void_p(4)), dict(out=C.c_void_p(24)),
+                    dict(scale=1), dict(scale=2)):
+            assert f(**bad) == ARG, bad
+        for bad in (dict(rows=-1), dict(columns=60, group=60, weight_columns=60), dict(columns=0), dict(columns=32776),
+                    dict(group=24), dict(group=4), dict(group=0), dict(weight_columns=32), dict(xs=56), dict(xs=68)):
+            assert f(**bad) == SHAPE, bad
+        assert f(rows=0, x=None, out=None) == 0
+    assert add(group=32) == SHAPE
+    assert add(rs=60) == SHAPE and add(r=C.c_void_p(8)) == ARG
+    assert gate(gate_dtype=2) == ARG and gate(z=None) == ARG and gate(z=C.c_void_p(8)) == ARG and gate(zs=63) == SHAPE
+
+
+def test_binding_checks_shapes_and_devices():
+    """Shapes and types are refused with ValueError, and tensors off the GPU before a pointer is taken from them."""
+    t = torch.zeros
+    args = dict(S=t(2, 4, 64, 128), q=t(9, 2, 128), k=t(9, 2, 128), v=t(9, 4, 64), alpha=t(9, 4), beta=t(9, 4),
+                offsets=t(3, dtype=torch.int32))
+    for bad in (dict(), dict(S=t(2, 4, 64)), dict(v=t(9, 64)), dict(v=t(9, 4, 64).half())):
+        with pytest.raises(ValueError):
+            gdn_scan(**{**args, **bad})
+    q, a, w = t(3, 2, 128), t(3, 4), t(4)
+    with pytest.raises(ValueError, match="contiguous CUDA tensor"):
+        gdn_inputs(q, q, a, a, w, w)
+    with pytest.raises(ValueError, match="dimensions"):
+        gdn_inputs(w, w, a, a, w, w)
+    with pytest.raises(ValueError, match="float32 or torch.bfloat16"):
+        add_rmsnorm(t(3, 64).half(), t(64))
+    with pytest.raises(ValueError, match="contiguous CUDA tensor"):
+        add_rmsnorm(t(3, 64), t(64))
+    with pytest.raises(ValueError, match="contiguous CUDA tensor"):
+        gated_rmsnorm(t(3, 64), t(3, 64), t(64))
