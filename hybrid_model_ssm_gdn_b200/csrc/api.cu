@@ -568,7 +568,8 @@ static rssm_status run_gdn_scan(const rssm_config &c, int qk_heads, const Prompt
   a.H = c.nheads; a.Hk = qk_heads; a.R = c.headdim; a.by_prompt = by_prompt; a.q_scale = c.q_scale;
   a.q = tok->q; a.k = tok->k; a.v = tok->v; a.alpha = tok->alpha; a.beta = tok->beta; a.S = S; a.y = y;
   a.err = err; a.wait_cycles = wait_cycles; a.withhold = withhold;
-  cudaError_t e = launch_gdn_scan(a, p, esize(c), num_sms, st);
+  const bool chunks = c.in_dtype == RSSM_BF16 && p.total >= 16LL * p.nseq;
+  cudaError_t e = chunks ? launch_gdn_tc(a, p, st) : launch_gdn_scan(a, p, esize(c), num_sms, st);
   if (e == cudaSuccess && p.refused_nan && p.total > 0) e = launch_refuse(p, y, c.nheads * c.headdim, num_sms, st);
   return e == cudaSuccess ? RSSM_OK : cuda_fail(e);
 }

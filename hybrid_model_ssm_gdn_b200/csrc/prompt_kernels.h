@@ -33,6 +33,7 @@ cudaError_t launch_prefill_meta(const Prompts &pr, const int4 *meta_in, int4 *me
                                 int *err, cudaStream_t stream);
 
 // Gated delta rule over packed prompts
+constexpr int kGdnChunk = 64;        // tokens of a chunk on the tensor cores
 struct GdnScanArgs {
   int H, Hk, R;                     // heads of v; of q and k (Hk divides H); rows of a head's state (d_v)
   int by_prompt;                    // S is indexed by prompt instead of by slot
@@ -47,6 +48,8 @@ struct GdnScanArgs {
 };
 // token by token: fp32 inputs, prompts of a few tokens
 cudaError_t launch_gdn_scan(const GdnScanArgs &a, const Prompts &pr, int esz, int num_sms, cudaStream_t stream);
+// chunks on the tensor cores: bf16 inputs, total > 0
+cudaError_t launch_gdn_tc(const GdnScanArgs &a, const Prompts &pr, cudaStream_t stream);
 // states of packed prompts [nseq][H][rows][128] from and to a GDN context's stored formats
 struct PromptStateArgs {
   int H, rows, hp_mode, read_mode;

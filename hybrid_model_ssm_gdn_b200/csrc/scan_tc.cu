@@ -39,11 +39,10 @@
 // Every wait is bounded; after one runs out the others stop waiting and the block goes through its remaining steps, so
 // all barriers and the release of tensor memory are still reached, and then writes NaN over its outputs and its state:
 // a context reports it, a call on the caller's own states has nothing else to show it.
-#include <cuda.h>
-
 #include "prompt_kernels.h"
 #include "packed.cuh"
 #include "tcgen05.cuh"
+#include "tensor_map.h"
 
 namespace rssm {
 
@@ -785,31 +784,6 @@ __global__ void __launch_bounds__(256) join_kernel(TcArgs a, Prompts pr) {
   }
 }
 
-using EncodeTiled = CUresult (*)(CUtensorMap *, CUtensorMapDataType, cuuint32_t, void *, const cuuint64_t *,
-                                 const cuuint64_t *, const cuuint32_t *, const cuuint32_t *, CUtensorMapInterleave,
-                                 CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
-
-// cuTensorMapEncodeTiled from the driver that is loaded (the library links the runtime alone)
-cudaError_t encoder(EncodeTiled *fn) {
-  void *p = nullptr;
-  cudaDriverEntryPointQueryResult found;
-  const cudaError_t e = cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &p, 12000, cudaEnableDefault, &found);
-  if (e != cudaSuccess) return e;
-  if (found != cudaDriverEntryPointSuccess || !p) return cudaErrorNotSupported;
-  *fn = reinterpret_cast<EncodeTiled>(p);
-  return cudaSuccess;
-}
-
-// rows of 128 bytes with the 128-byte swizzle; what lies outside the tensor reads as zero and is not written
-cudaError_t make_map(EncodeTiled fn, CUtensorMap *map, CUtensorMapDataType type, const void *p, int dims,
-                     const cuuint64_t *size, const cuuint64_t *stride, const cuuint32_t *box) {
-  const cuuint32_t one[3] = {1, 1, 1};
-  const CUresult r = fn(map, type, dims, const_cast<void *>(p), size, stride, box, one,
-                        CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_128B,
-                        CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
-  return r == CUDA_SUCCESS ? cudaSuccess : cudaErrorInvalidValue;
-}
-
 }  // namespace
 
 size_t scan_tc_workspace(int H, int P, int pieces, size_t *seg_dt) {
@@ -837,7 +811,7 @@ cudaError_t launch_scan_tc(const ScanArgs &s, const Prompts &pr, cudaStream_t st
   // finding the order costs each block some 500 cycles, worth it where a prompt has a few chunks
   a.by_length = !cut_up && pr.nseq > 1 && pr.nseq <= kByLength && pr.total / pr.nseq >= 4 * Q;
   EncodeTiled fn;
-  cudaError_t e = encoder(&fn);
+  cudaError_t e = map_encoder(&fn);
   if (e != cudaSuccess) return e;
   CUtensorMap mx, mB, mC, my;
   const CUtensorMapDataType bf16 = CU_TENSOR_MAP_DATA_TYPE_BFLOAT16;
