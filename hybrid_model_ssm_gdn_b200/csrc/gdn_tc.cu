@@ -19,30 +19,37 @@ namespace {
 constexpr int Q = kGdnChunk;
 constexpr int kHalf = Q * 128;  // bytes of a tile: 64 rows of 64 bf16
 constexpr int kStages = 3;      // of q and k: one chunk in the chain of the state, one in front of it, one on its way
-constexpr uint32_t kColR = 0, kColU = 64, kColY = 128, kColG = 192, kColD = 256, kColS = 384;
+// Tensor memory.  K S^T, U and the increment of S are cut where they lie: a warp's 16 (32) columns of results become 24 (48)
+// of pieces in a range of its own, so results stand in the middle of the two ranges that they share.
+constexpr uint32_t kColR = 0, kColU = 96, kColS = 192, kColY = 384, kColG = 448;
 constexpr int kChain = 16;                                    // warps: lanes' quarter w % 4, columns' quarter w / 4
-constexpr int kWarpPrep = 16, kWarpLoad = 20, kWarpState = 21, kWarpGram = 22;
-constexpr int kGdnThreads = 23 * 32;
+constexpr int kWarpPrep = 16, kWarpLoad = 20, kWarpState = 21, kWarpGram = 22, kWarpLoadV = 23;
+constexpr int kGdnThreads = 24 * 32;
 constexpr int kByLength = 64;
+constexpr float kMild = 1.f / 65536.f;
 
+// Factors of a chunk's tokens, see the two forms above.
 struct __align__(16) Table {
-  float rise[Q], fall[Q], beta[Q];  // g_j, g_Q / g_j
-  float carry;                      // g_Q
-  int tokens;                       // of the chunk, or up to the first whose k, alpha or beta is not finite
+  float v[Q], k[Q];   // R = v V + k K S^T
+  float q[Q], u[Q];   // Y = q Q S^T + u M U
+  float fall[Q];      // g_Q / g_j
+  float carry;        // g_Q
+  int tokens;         // of the chunk, or up to the first whose k, alpha or beta is not finite
+  int mild;           // the form without decays within the chunk
 };
 
 struct GdnShared {
-  unsigned char in[kStages][4][kHalf];  // k, q of columns 0..63, k, q of columns 64..127
-  unsigned char V[2][2][kHalf];
-  unsigned char T[2][2][kHalf], M[2][2][kHalf];  // hi, lo; row = token j
-  unsigned char A[2][kHalf];
-  float diag[4][16][20];
+  unsigned char in[kStages][4][kHalf];  // k, q of columns 0..63, k, q of columns 64..127; then Y on its way out
+  __nv_bfloat16 V[Q][kCols];
+  unsigned char T[2][2][kHalf], M[2][3][kHalf];  // pieces; row = token j
+  unsigned char A[2][kHalf / 2];  // blocks of A below the diagonal, see a_row
+  float diag[4][16 * 20 + 16];  // blocks of A on the diagonal, [column][row]
   Table tab[2];
   float alpha[Q], prefix[Q], tot[4];
   int first[128];  // per row of the state, the first token of the prompt whose v is not finite
-  uint64_t full_kq[kStages], free_kq[kStages], full_v[2], free_v[2], full_t[2], free_t[2];
-  uint64_t ks_done, qs_done, u_done, d_done, y_done, g_done, g_free, drained[2];
-  uint64_t s_ready, r_ready, u_ready, y_free;
+  uint64_t full_kq[kStages], free_kq[kStages], full_v, free_v, full_t[2], free_t[2];
+  uint64_t ks_done[2], qs_done, u_done[2], d_done[2], y_done, g_done, g_free, drained[2];
+  uint64_t s_ready[2], r_ready[2], u_ready[2], y_taken, y_free;
   uint32_t tmem;
   int abort, not_finite, bad;
   PieceWord found;
@@ -125,7 +132,7 @@ __device__ __forceinline__ void mma(float (&d)[4], const uint32_t (&a)[4], uint3
 }
 
 // X^T (+)= Z^T B^T for blocks of 16 x 16, Z at (zr, zc) of T and B at (br, bc) of A, in two pieces each; x[n]: columns 8 n ..
-__device__ __forceinline__ void block_x(unsigned char (*T)[kHalf], int zr, int zc, unsigned char (*A)[kHalf], int br, int bc,
+__device__ __forceinline__ void block_x(unsigned char (*T)[kHalf], int zr, int zc, unsigned char (*A)[kHalf / 2], int br, int bc,
                                         int lane, float (&x)[2][4]) {
   uint32_t zh[4], zl[4], bh[4], bl[4];
   load_left_t(T[0], zr, zc, lane, zh);
@@ -171,6 +178,7 @@ __device__ __forceinline__ void store_block(unsigned char (*T)[kHalf], int row, 
 
 // A wait gave up: nothing that looks like a result stays.
 __device__ __noinline__ void overwrite(const GdnTcArgs &a, GdnShared &sh, int h, float *S) {
+  if (threadIdx.x % 32 == 0) bulk_wait_all();  // this warp's own stores of Y
   __syncthreads();
   const volatile PieceWord &w = sh.found;
   const float nan = __int_as_float(0x7fffffff);
@@ -179,9 +187,166 @@ __device__ __noinline__ void overwrite(const GdnTcArgs &a, GdnShared &sh, int h,
     for (int r = threadIdx.x % 32; r < a.R; r += 32) a.y[((size_t)t * a.H + h) * a.R + r] = nan;
 }
 
+// Rows of A (threads 0..63 of the preparing warps) and M (the others) of a chunk, from the Gram matrix in tensor memory.
+struct PrepRow {
+  int j, bj, jj;     // token, its block of 16 and place there
+  bool of_k;
+  int upper;         // rows of tokens 32..63
+  uint32_t gram;     // this warp's lanes of the Gram matrix
+  float by;          // beta, or 1
+  float f[4];        // product of alpha from the end of an earlier block to this token
+};
+
+// Where A is held, in tiles of 32 rows: the block of 32 x 32 below the diagonal at columns 0..31, and the two of 16 x 16
+// within the diagonal blocks of 32 at columns 32..47.
+__device__ __forceinline__ void store_a(GdnShared &sh, const PrepRow &r, int blk, const f2 (&v)[8]) {
+  const int row = blk < 2 * r.upper ? r.j - 32 : 16 * r.upper + r.jj, col = blk < 2 * r.upper ? 16 * blk : 32;
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    uint4 p0, p1;
+    cut2(v[4 * i], p0.x, p1.x);
+    cut2(v[4 * i + 1], p0.y, p1.y);
+    cut2(v[4 * i + 2], p0.z, p1.z);
+    cut2(v[4 * i + 3], p0.w, p1.w);
+    if (blk < r.bj) {
+      *reinterpret_cast<uint4 *>(at_tile(sh.A[0], row, col + 8 * i)) = p0;
+      *reinterpret_cast<uint4 *>(at_tile(sh.A[1], row, col + 8 * i)) = p1;
+    }
+  }
+}
+__device__ __forceinline__ void store_m(unsigned char (*M)[kHalf], const PrepRow &r, int blk, const f2 (&v)[8]) {
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    uint4 p0, p1, p2;
+    cut3(v[4 * i], p0.x, p1.x, p2.x);
+    cut3(v[4 * i + 1], p0.y, p1.y, p2.y);
+    cut3(v[4 * i + 2], p0.z, p1.z, p2.z);
+    cut3(v[4 * i + 3], p0.w, p1.w, p2.w);
+    if (blk <= r.bj) {
+      *reinterpret_cast<uint4 *>(at_tile(M[0], r.j, 16 * blk + 8 * i)) = p0;
+      *reinterpret_cast<uint4 *>(at_tile(M[1], r.j, 16 * blk + 8 * i)) = p1;
+      *reinterpret_cast<uint4 *>(at_tile(M[2], r.j, 16 * blk + 8 * i)) = p2;
+    }
+  }
+}
+
+// Without decays: A = beta_j G, M = G up to the diagonal.  Returns a sum that is not 0 where a value of k or beta that
+// this row uses, or that lies in its block, is not finite.  What rows before it take is finite: they take nothing behind
+// them, and M is selected up to the diagonal.
+__device__ __forceinline__ f2 prep_mild(GdnShared &sh, const PrepRow &r, unsigned char (*M)[kHalf]) {
+  f2 seen = pack2(0.f, 0.f);
+  const f2 zero = seen, by = pack2(r.by, r.by);
+#pragma unroll
+  for (int blk = 0; blk < 4; ++blk) {
+    if (blk > 2 * r.upper + 1) break;  // (above the diagonal of both blocks that this warp's rows lie in)
+    uint32_t G[16];
+    f2 v[8];
+    tm_ld16(r.gram + 16 * blk, G);
+    tm_wait_ld();
+    if (r.of_k) {
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        v[i] = mul2(by, pack2(G[2 * i], G[2 * i + 1]));
+        seen = fma2(v[i], zero, seen);
+      }
+      if (blk == r.bj) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          float e0, e1;
+          unpack2(v[i], e0, e1);
+          sh.diag[r.bj][40 * i + r.jj] = e0;
+          sh.diag[r.bj][40 * i + 20 + r.jj] = e1;
+        }
+      }
+      if (blk <= 2 * r.upper) store_a(sh, r, blk, v);
+    } else {
+      const int most = blk < r.bj ? 15 : r.jj;  // last column of this row (rows above the block are not stored)
+#pragma unroll
+      for (int i = 0; i < 8; ++i)
+        v[i] = blk < 2 * r.upper ? pack2(G[2 * i], G[2 * i + 1])
+                                 : pack2(2 * i <= most ? G[2 * i] : 0u, 2 * i + 1 <= most ? G[2 * i + 1] : 0u);
+      store_m(M, r, blk, v);
+    }
+  }
+  return seen;
+}
+
+// With decays: A = beta_j D G, M = D G; see prep_mild.
+__device__ __noinline__ f2 prep_strong(GdnShared &sh, PrepRow r, unsigned char (*M)[kHalf]) {
+  f2 seen = pack2(0.f, 0.f);
+  const f2 zero = seen;
+#pragma unroll 1
+  for (int blk = 0; blk < 2 * r.upper + 2; ++blk) {
+    uint32_t G[16];
+    f2 v[8];
+    tm_ld16(r.gram + 16 * blk, G);
+    const int own = blk == r.bj ? r.jj : -1;  // column of the diagonal in this block
+    const int most = blk < r.bj ? 15 : own;
+    const float f = blk == 0 ? r.f[0] : blk == 1 ? r.f[1] : blk == 2 ? r.f[2] : 0.f;
+    float d = r.by * f, e[16];
+    tm_wait_ld();
+#pragma unroll
+    for (int i = 12; i >= 0; i -= 4) {
+      const float4 a4 = *reinterpret_cast<const float4 *>(&sh.alpha[16 * blk + i]);
+      const float al[4] = {a4.x, a4.y, a4.z, a4.w};
+#pragma unroll
+      for (int k = 3; k >= 0; --k) {
+        if (i + k == own) d = r.by;
+        e[i + k] = r.of_k || i + k <= most ? d * __uint_as_float(G[i + k]) : 0.f;
+        d *= al[k];
+      }
+    }
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      v[i] = pack2(e[2 * i], e[2 * i + 1]);
+      seen = fma2(v[i], zero, seen);
+    }
+    if (r.of_k) {
+      if (blk == r.bj) {
+#pragma unroll
+        for (int i = 0; i < 16; ++i) sh.diag[r.bj][20 * i + r.jj] = e[i];
+      }
+      store_a(sh, r, blk, v);
+    } else {
+      store_m(M, r, blk, v);
+    }
+  }
+  return seen;
+}
+__device__ __forceinline__ bool not_zero(f2 v) {
+  float a, b;
+  unpack2(v, a, b);
+  return !(a + b == 0.f);
+}
+// Some value of the chunk is not finite.  From the first token on whose k, alpha or beta is not (k_j . k_j is not, if k_j is
+// not), the tokens change nothing; the state warps write NaN for them.  Rows before it have used none of them.  Returns that
+// token, or the number of tokens.
+__device__ __noinline__ int prep_careful(GdnShared &sh, PrepRow r, bool odd, int valid) {
+  uint32_t G[2][16];
+  tm_ld16(r.gram + 32 * r.upper, G[0]);
+  tm_ld16(r.gram + 32 * r.upper + 16, G[1]);
+  tm_wait_ld();
+  float own = r.by;
+#pragma unroll
+  for (int i = 0; i < 16; ++i)
+    if (i == r.jj) own = fmaf(__uint_as_float(r.bj & 1 ? G[1][i] : G[0][i]), 0.f, own);
+  if (threadIdx.x == 32 * kWarpPrep) sh.bad = valid;
+  prep_sync();
+  if (r.of_k && r.j < valid && (odd || !(own * 0.f == 0.f))) atomicMin(&sh.bad, r.j);
+  prep_sync();
+  const int bad = sh.bad;
+  if (r.of_k && r.j >= bad) {
+    for (int i = 0; i < 16; ++i) sh.diag[r.bj][20 * i + r.jj] = 0.f;
+    const f2 zero[8] = {};
+    for (int blk = 0; blk < r.bj; ++blk) store_a(sh, r, blk, zero);
+  }
+  return bad;
+}
+
 __global__ void __launch_bounds__(kGdnThreads, 1)
     gdn_tc_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant__ CUtensorMap map_k,
-                  const __grid_constant__ CUtensorMap map_v, const __grid_constant__ GdnTcArgs a, Prompts pr) {
+                  const __grid_constant__ CUtensorMap map_v, const __grid_constant__ CUtensorMap map_y,
+                  const __grid_constant__ GdnTcArgs a, Prompts pr) {
   extern __shared__ __align__(1024) unsigned char raw[];
   GdnShared &sh = *reinterpret_cast<GdnShared *>(raw);
   if (smem_u32(raw) & 1023u) {
@@ -216,14 +381,16 @@ __global__ void __launch_bounds__(kGdnThreads, 1)
     return;
   }
   if (tid == 0) {
-    uint64_t *one[] = {&sh.full_kq[0], &sh.full_kq[1], &sh.full_kq[2], &sh.free_kq[0], &sh.free_kq[1], &sh.free_kq[2],
-                       &sh.full_v[0], &sh.full_v[1], &sh.free_t[0], &sh.free_t[1], &sh.ks_done, &sh.qs_done, &sh.u_done,
-                       &sh.d_done, &sh.y_done, &sh.g_done, &sh.drained[0], &sh.drained[1]};
+    uint64_t *one[] = {&sh.full_kq[0], &sh.full_kq[1], &sh.full_kq[2], &sh.full_v, &sh.ks_done[0], &sh.ks_done[1], &sh.qs_done, &sh.u_done[0],
+                       &sh.u_done[1], &sh.d_done[0], &sh.d_done[1], &sh.y_done, &sh.g_done, &sh.drained[0], &sh.drained[1]};
     for (uint64_t *b : one) mbar_init(b, 1);
     uint64_t *prep[] = {&sh.full_t[0], &sh.full_t[1], &sh.g_free};
     for (uint64_t *b : prep) mbar_init(b, 4);
-    uint64_t *team[] = {&sh.free_v[0], &sh.free_v[1], &sh.s_ready, &sh.r_ready, &sh.u_ready, &sh.y_free};
+    uint64_t *half[] = {&sh.s_ready[0], &sh.s_ready[1], &sh.r_ready[0], &sh.r_ready[1], &sh.u_ready[0], &sh.u_ready[1]};
+    for (uint64_t *b : half) mbar_init(b, kChain / 2);
+    uint64_t *team[] = {&sh.free_kq[0], &sh.free_kq[1], &sh.free_kq[2], &sh.free_v, &sh.y_taken, &sh.y_free};
     for (uint64_t *b : team) mbar_init(b, kChain);
+    for (uint64_t &b : sh.free_t) mbar_init(&b, kChain + 1);
     sh.abort = sh.not_finite = 0;
     fence_barrier_init();
   }
@@ -237,122 +404,186 @@ __global__ void __launch_bounds__(kGdnThreads, 1)
 
   if (warp == kWarpLoad) {
     if (lane == 0) {
-      const int hk = h / (a.H / a.Hk), halves = a.R > 64 ? 2 : 1;
-      auto stopped = [&] { return *(volatile int *)&sh.abort != 0; };
-      int asked_kq = 0, asked_v = 0;  // chunks whose loads are on their way or done
+      const int hk = h / (a.H / a.Hk);
+      int asked = 0;  // chunks whose loads are on their way or done
       for (int c = 0; c < chunks; ++c) {
         const int s = c % kStages, t = t0 + c * Q;
         if (c >= kStages) wait(sh.free_kq[s], c / kStages - 1);
-        if (stopped() || c == a.withhold) break;
+        if (*(volatile int *)&sh.abort || c == a.withhold) break;
         mbar_arrive_expect_tx(&sh.full_kq[s], 4 * kHalf);
 #pragma unroll
         for (int half = 0; half < 2; ++half) {
           tma_load_2d(sh.in[s][2 * half], &map_k, hk * kCols + 64 * half, t, &sh.full_kq[s]);
           tma_load_2d(sh.in[s][2 * half + 1], &map_q, hk * kCols + 64 * half, t, &sh.full_kq[s]);
         }
-        asked_kq = c + 1;
-        if (c >= 2) wait(sh.free_v[c & 1], (c >> 1) - 1);
-        if (stopped()) break;
-        mbar_arrive_expect_tx(&sh.full_v[c & 1], halves * kHalf);
-        for (int half = 0; half < halves; ++half)
-          tma_load_3d(sh.V[c & 1][half], &map_v, 64 * half, h, t, &sh.full_v[c & 1]);
-        asked_v = c + 1;
+        asked = c + 1;
       }
       // No copy outlives the block: the last phase of each barrier that was asked for.
-      for (int c = max(0, asked_kq - kStages); c < asked_kq; ++c) mbar_wait(&sh.full_kq[c % kStages], (c / kStages) & 1, wait.ws);
-      for (int c = max(0, asked_v - 2); c < asked_v; ++c) mbar_wait(&sh.full_v[c & 1], (c >> 1) & 1, wait.ws);
+      for (int c = max(0, asked - kStages); c < asked; ++c) mbar_wait(&sh.full_kq[c % kStages], (c / kStages) & 1, wait.ws);
+    }
+    __syncwarp();
+  } else if (warp == kWarpLoadV) {
+    if (lane == 0) {
+      int asked = 0;
+      for (int c = 0; c < chunks; ++c) {
+        if (c > 0) wait(sh.free_v, c - 1);
+        if (*(volatile int *)&sh.abort) break;
+        mbar_arrive_expect_tx(&sh.full_v, 2 * kHalf);
+        tma_load_3d(sh.V, &map_v, 0, h, t0 + c * Q, &sh.full_v);
+        asked = c + 1;
+      }
+      if (asked) mbar_wait(&sh.full_v, (asked - 1) & 1, wait.ws);
     }
     __syncwarp();
   } else if (warp == kWarpState || warp == kWarpGram) {
-    // The products: the whole warp goes through the steps, on values the compiler knows to be the same in every lane.
-    const uint32_t leader = lane == 0, td = __shfl_sync(0xffffffffu, tm, 0);
+    // The products: the whole warp waits, one thread issues.
+    const uint32_t td = __shfl_sync(0xffffffffu, tm, 0);
     const int n = __shfl_sync(0xffffffffu, chunks, 0);
-    constexpr uint32_t shape = mma_shape(128, 64, false, false), shape_d = mma_shape(128, 128, false, true);
     constexpr uint32_t kStep = (2 * kHalf) >> 4, kStage = (4 * kHalf) >> 4;  // descriptor units between column halves, stages
     const uint32_t dk = tile_desc(sh.in[0][0], 16);
     int s = 0, turn = 0;  // c % kStages, c / kStages
     if (warp == kWarpGram) {
+      constexpr uint32_t shape = mma_shape(128, 64, false, false);
       for (int c = 0; c < n; ++c) {
         wait.warp(sh.full_kq[s], turn);
         if (c > 0) wait.warp(sh.g_free, c - 1);
         tm_fence_after();
-        const uint32_t k0 = dk + s * kStage;
+        const uint64_t k0 = wide_desc(dk + s * kStage);
+        if (elect_one()) {
 #pragma unroll
-        for (int k = 0; k < 8; ++k) {  // rows of k, then of q
-          const int at = (k >> 2) * kStep + 2 * (k & 3);
-          mma_ss(td + kColG, k0 + at, k0 + at, shape, k > 0, leader);
+          for (int k = 0; k < 8; ++k) {  // rows of k, then of q
+            const int at = (k >> 2) * kStep + 2 * (k & 3);
+            one_ss(td + kColG, k0 + at, k0 + at, shape, k > 0);
+          }
+          one_commit(&sh.g_done);
         }
-        mma_commit(&sh.g_done, leader);
+        __syncwarp();
         if (++s == kStages) s = 0, ++turn;
       }
-      mma_commit(&sh.drained[1], leader);
+      if (elect_one()) one_commit(&sh.drained[1]);
       mbar_wait(&sh.drained[1], 0, wait.ws);
     } else {
+      constexpr uint32_t half_q = mma_shape(128, 32, false, false), all_q = mma_shape(128, 64, false, false);
+      constexpr uint32_t half_d = mma_shape(128, 64, false, true);
+      constexpr uint32_t kRows = (32 * 128) >> 4;  // 32 token rows
       const uint32_t dkn = tile_desc(sh.in[0][0], 2 * kHalf);  // MN-major, two tiles
       const uint32_t dT = tile_desc(sh.T[0][0], 16), dM = tile_desc(sh.M[0][0], 16);
-      constexpr uint32_t kPiece = kHalf >> 4, kBuffer = (2 * kHalf) >> 4;
+      constexpr uint32_t kPiece = kHalf >> 4;
       for (int c = 0; c < n; ++c) {
         const int b = c & 1;
-        const uint32_t k0 = dk + s * kStage, q0 = k0 + (kHalf >> 4);
+        const uint64_t k0 = wide_desc(dk + s * kStage), q0 = k0 + (kHalf >> 4), kn = wide_desc(dkn + s * kStage);
+        const uint64_t T = wide_desc(dT + b * 2 * kPiece), M = wide_desc(dM + b * 3 * kPiece);
         wait.warp(sh.full_kq[s], turn);
-        wait.warp(sh.s_ready, c);
-        tm_fence_after();
 #pragma unroll
-        for (int k = 0; k < 8; ++k)
+        for (int part = 0; part < 2; ++part) {  // K S^T: halves of S as they come, the last ones by halves of the tokens
+          wait.warp(sh.s_ready[part], c);
+          tm_fence_after();
+          if (elect_one()) {
 #pragma unroll
-          for (int p = 0; p < 2; ++p)
-            mma_ts(td + kColR, td + kColS + 16 * k + 8 * p, k0 + (k >> 2) * kStep + 2 * (k & 3), shape, k > 0 || p > 0, leader);
-        mma_commit(&sh.ks_done, leader);
+            for (int half = 0; half < 2; ++half) {
+#pragma unroll
+              for (int k = 4 * part; k < 4 * part + 4; ++k)
+#pragma unroll
+                for (int p = 2; p >= 0; --p)
+                  one_ts(td + kColR + 48 * half + 8, td + kColS + 24 * k + 8 * p,
+                         k0 + (k >> 2) * kStep + 2 * (k & 3) + half * kRows, half_q, k > 0 || p < 2);
+              if (part == 1) one_commit(&sh.ks_done[half]);
+            }
+          }
+          __syncwarp();
+        }
         if (c > 0) wait.warp(sh.y_free, c - 1);
         tm_fence_after();
+        auto qs = [&](int part) {  // Q S^T over half of S
 #pragma unroll
-        for (int k = 0; k < 8; ++k)
+          for (int k = 4 * part; k < 4 * part + 4; ++k)
 #pragma unroll
-          for (int p = 0; p < 2; ++p)
-            mma_ts(td + kColY, td + kColS + 16 * k + 8 * p, q0 + (k >> 2) * kStep + 2 * (k & 3), shape, k > 0 || p > 0, leader);
-        mma_commit(&sh.qs_done, leader);
+            for (int p = 2; p >= 0; --p)
+              one_ts(td + kColY, td + kColS + 24 * k + 8 * p, q0 + (k >> 2) * kStep + 2 * (k & 3), all_q, k > 0 || p < 2);
+        };
+        if (elect_one()) qs(0);  // while R is formed
+        __syncwarp();
         wait.warp(sh.full_t[b], c >> 1);
-        wait.warp(sh.r_ready, c);
-        tm_fence_after();
+        const uint32_t kColE = sh.tab[b].mild ? kColU : kColR;  // U as it counts at the chunk's end
 #pragma unroll
-        for (int k = 0; k < 4; ++k) {  // pieces (hi, lo), (lo, hi), (hi, hi)
-          const uint32_t r = td + kColR + 16 * k, t = dT + b * kBuffer + 2 * k;
-          mma_ts(td + kColU, r, t + kPiece, shape, k > 0, leader);
-          mma_ts(td + kColU, r + 8, t, shape, 1, leader);
-          mma_ts(td + kColU, r, t, shape, 1, leader);
+        for (int half = 0; half < 2; ++half) {  // U of 32 tokens from R up to them
+          wait.warp(sh.r_ready[half], c);
+          tm_fence_after();
+          if (elect_one()) {
+#pragma unroll
+            for (int k = 0; k < 2 * half + 2; ++k) {  // pieces of R by pieces of T; the others are below 2^-24
+              const uint32_t r = td + kColR + 24 * k, u = td + kColU + 48 * half + 8;
+              const uint64_t t = T + half * kRows + 2 * k;
+              one_ts(u, r + 8, t + kPiece, half_q, k > 0);
+              one_ts(u, r + 16, t, half_q, true);
+              one_ts(u, r, t + kPiece, half_q, true);
+              one_ts(u, r + 8, t, half_q, true);
+              one_ts(u, r, t, half_q, true);
+            }
+            one_commit(&sh.u_done[half]);
+          }
+          __syncwarp();
         }
-        mma_commit(&sh.u_done, leader);
-        wait.warp(sh.u_ready, c);
-        tm_fence_after();
-#pragma unroll
-        for (int k = 0; k < 4; ++k)  // 16 token rows are 2048 bytes
-#pragma unroll
-          for (int p = 0; p < 2; ++p)
-            mma_ts(td + kColD, td + kColR + 16 * k + 8 * p, dkn + s * kStage + 128 * k, shape_d, k > 0 || p > 0, leader);
-        mma_commit(&sh.d_done, leader);
-        mma_commit(&sh.free_kq[s], leader);
-#pragma unroll
-        for (int k = 0; k < 4; ++k) {
-          const uint32_t u = td + kColU + 16 * k, m = dM + b * kBuffer + 2 * k;
-          mma_ts(td + kColY, u, m + kPiece, shape, k > 0, leader);
-          mma_ts(td + kColY, u + 8, m, shape, 1, leader);
-          mma_ts(td + kColY, u, m, shape, 1, leader);
+        if (elect_one()) {  // while U is cut
+          qs(1);
+          one_commit(&sh.qs_done);
         }
-        mma_commit(&sh.y_done, leader);
-        mma_commit(&sh.free_t[b], leader);
+        __syncwarp();
+        wait.warp(sh.u_ready[0], c);
+        wait.warp(sh.u_ready[1], c);
+        tm_fence_after();
+        if (elect_one()) {
+#pragma unroll
+          for (int part = 0; part < 2; ++part) {  // 64 columns of the state
+#pragma unroll
+            for (int k = 0; k < 4; ++k)  // 16 token rows are 2048 bytes
+#pragma unroll
+              for (int p = 2; p >= 0; --p)
+                one_ts(td + kColS + 96 * part + 16, td + kColE + 24 * k + 8 * p, kn + part * kStep + 128 * k, half_d,
+                       k > 0 || p < 2);
+            one_commit(&sh.d_done[part]);
+          }
+        }
+        __syncwarp();
+        wait.warp(sh.y_taken, c);
+        tm_fence_after();
+        if (elect_one()) {
+#pragma unroll
+          for (int half = 0; half < 2; ++half)
+#pragma unroll
+            for (int k = 0; k < 2 * half + 2; ++k) {
+              const uint32_t u = td + kColU + 24 * k, y = td + kColY + 32 * half;
+              const uint64_t m = M + half * kRows + 2 * k;
+              one_ts(y, u, m + 2 * kPiece, half_q, k > 0);
+              one_ts(y, u + 8, m + kPiece, half_q, true);
+              one_ts(y, u + 16, m, half_q, true);
+              one_ts(y, u, m + kPiece, half_q, true);
+              one_ts(y, u + 8, m, half_q, true);
+              one_ts(y, u, m, half_q, true);
+            }
+          one_commit(&sh.y_done);
+          one_commit(&sh.free_t[b]);
+        }
+        __syncwarp();
         if (++s == kStages) s = 0, ++turn;
       }
-      mma_commit(&sh.drained[0], leader);
+      if (elect_one()) one_commit(&sh.drained[0]);
       mbar_wait(&sh.drained[0], 0, wait.ws);
     }
     __syncwarp();
   } else if (warp >= kWarpPrep) {
     // A, T and M of a chunk, a chunk ahead of the state: lanes 0..63 of the Gram matrix are k_j . k_i, the others q_j . k_i
-    const int pw = warp - kWarpPrep, p = tid - 32 * kWarpPrep, j = p & 63, bj = j >> 4, jj = j & 15;
-    const bool of_k = p < 64;
-    const uint32_t lanes = (uint32_t)(32 * pw) << 16;
-    for (int i = p; i < 2 * 2 * 2 * kHalf / 16; i += 128)  // blocks above the diagonal stay zero
+    const int pw = warp - kWarpPrep, p = tid - 32 * kWarpPrep;
+    PrepRow r;
+    r.upper = pw & 1;
+    r.j = p & 63; r.bj = r.j >> 4; r.jj = r.j & 15;
+    r.of_k = p < 64;
+    r.gram = tm + ((uint32_t)(32 * pw) << 16) + kColG;
+    const int j = r.j, bj = r.bj, jj = r.jj;
+    const bool of_k = r.of_k;
+    for (int i = p; i < 2 * 2 * kHalf / 16; i += 128)  // blocks above the diagonal stay zero
       reinterpret_cast<uint4 *>(sh.T[0][0])[i] = make_uint4(0, 0, 0, 0);
+    for (int i = p; i < 2 * 3 * kHalf / 16; i += 128) reinterpret_cast<uint4 *>(sh.M[0][0])[i] = make_uint4(0, 0, 0, 0);
     const float *ag = a.alpha + (size_t)t0 * a.H + h, *bg = a.beta + (size_t)t0 * a.H + h;
     float alpha_next = 1.f, beta_next = 0.f;
     auto fetch = [&](int c) {
@@ -367,7 +598,8 @@ __global__ void __launch_bounds__(kGdnThreads, 1)
     fetch(0);
     for (int c = 0; c < chunks; ++c) {
       const int b = c & 1, valid = min(Q, ntok - c * Q);
-      const float al = alpha_next, be = beta_next;
+      const bool odd = !(fabsf(alpha_next) < __int_as_float(0x7f800000));
+      const float al = odd ? 1.f : alpha_next, be = beta_next;  // (the chunk ends before an odd one)
       if (c + 1 < chunks) fetch(c + 1);
       float up = al, down = al;  // products within the block of 16: up to this token, and behind it
       if (of_k) {
@@ -392,10 +624,29 @@ __global__ void __launch_bounds__(kGdnThreads, 1)
           *reinterpret_cast<uint4 *>(sh.in[c % kStages][2] + 16 * i) = make_uint4(0, 0, 0, 0);
         }
       }
-      prep_sync();
+      const bool strong = prep_sync_or(!(fabsf(down) >= kMild && fabsf(down) <= 1.f / kMild) ||
+                                 (jj == 15 && !(fabsf(up) >= kMild && fabsf(up) <= 1.f / kMild)));
       if (c > 1) wait(sh.free_t[b], (c >> 1) - 1);
       const float tot[4] = {sh.tot[0], sh.tot[1], sh.tot[2], sh.tot[3]};
       Table &tab = sh.tab[b];
+      r.by = of_k ? be : 1.f;
+      r.f[3] = 0.f;
+      {
+        float run = sh.prefix[j];
+#pragma unroll
+        for (int i = 2; i >= 0; --i) {
+          r.f[i] = i < bj ? run : 0.f;
+          if (i < bj) run *= tot[i];
+        }
+      }
+      int tokens = valid;
+      wait(sh.g_done, c);
+      tm_fence_after();
+      const f2 seen = strong ? prep_strong(sh, r, sh.M[b]) : prep_mild(sh, r, sh.M[b]);
+      if (prep_sync_or(of_k && (odd || not_zero(seen)))) {
+        tokens = prep_careful(sh, r, odd, valid);
+        prep_sync();
+      }
       if (of_k) {
         float rise = up, fall = down;
 #pragma unroll
@@ -403,101 +654,35 @@ __global__ void __launch_bounds__(kGdnThreads, 1)
           if (i < bj) rise *= tot[i];
           if (i > bj) fall *= tot[i];
         }
-        tab.rise[j] = rise;
+        const float carry = (tot[0] * tot[1]) * (tot[2] * tot[3]);
+        tab.v[j] = strong ? be : be * fall;
+        tab.k[j] = strong ? -be * rise : -be * carry;
+        tab.q[j] = a.q_scale * rise;
+        tab.u[j] = strong ? a.q_scale : a.q_scale / fall;
         tab.fall[j] = fall;
-        tab.beta[j] = be;
         if (j == 0) {
-          tab.carry = (tot[0] * tot[1]) * (tot[2] * tot[3]);
-          tab.tokens = valid;
-        }
-      }
-      float f[4];  // product of alpha from the end of a block to this token
-      f[3] = 0.f;
-      {
-        float run = sh.prefix[j];
-#pragma unroll
-        for (int i = 2; i >= 0; --i) {
-          f[i] = i < bj ? run : 0.f;
-          if (i < bj) run *= tot[i];
-        }
-      }
-      const float by = of_k ? be : 1.f;
-      float seen = fmaf(al, 0.f, be * 0.f);  // stays 0 while what goes into this row is finite
-      unsigned char(*const out)[kHalf] = of_k ? sh.A : sh.M[b];
-      wait(sh.g_done, c);
-      tm_fence_after();
-#pragma unroll
-      for (int blk = 0; blk < 4; ++blk) {
-        if (blk > 2 * (pw & 1) + 1) break;
-        uint32_t G[16];
-        tm_ld16(tm + lanes + kColG + 16 * blk, G);
-        const int own = blk == bj ? jj : -1;                  // column of the diagonal in this block
-        // columns of this row; a token behind the end has none (its beta is 0, but its k may hold anything)
-        const int most = of_k && j >= valid ? 0 : blk < bj ? 16 : own + (of_k ? 0 : 1);
-        float al16[16], v[16];
-#pragma unroll
-        for (int i = 0; i < 16; i += 4) *reinterpret_cast<float4 *>(al16 + i) = *reinterpret_cast<const float4 *>(&sh.alpha[16 * blk + i]);
-        float d = f[blk];
-        tm_wait_ld();
-#pragma unroll
-        for (int i = 15; i >= 0; --i) {
-          if (i == own) d = 1.f;
-          v[i] = i < most ? by * d * __uint_as_float(G[i]) : 0.f;
-          if (i == own) seen = fmaf(__uint_as_float(G[i]), 0.f, seen);
-          seen = fmaf(v[i], 0.f, seen);
-          d *= al16[i];
-        }
-        if (of_k && blk == bj) {
-#pragma unroll
-          for (int i = 0; i < 16; i += 4)
-            *reinterpret_cast<float4 *>(&sh.diag[bj][jj][i]) = make_float4(v[i], v[i + 1], v[i + 2], v[i + 3]);
-        }
-#pragma unroll
-        for (int i = 0; i < 2; ++i) {
-          uint4 hi, lo;
-          cut2(pack2(v[8 * i], v[8 * i + 1]), hi.x, lo.x);
-          cut2(pack2(v[8 * i + 2], v[8 * i + 3]), hi.y, lo.y);
-          cut2(pack2(v[8 * i + 4], v[8 * i + 5]), hi.z, lo.z);
-          cut2(pack2(v[8 * i + 6], v[8 * i + 7]), hi.w, lo.w);
-          *reinterpret_cast<uint4 *>(at_tile(out[0], j, 16 * blk + 8 * i)) = hi;
-          *reinterpret_cast<uint4 *>(at_tile(out[1], j, 16 * blk + 8 * i)) = lo;
+          tab.carry = carry;
+          tab.tokens = tokens;
+          tab.mild = !strong;
         }
       }
       warp_arrive(sh.g_free, lane);
-      if (prep_sync_or(of_k && j < valid && !(seen == 0.f))) {
-        // From the first token on whose k, alpha or beta is not finite, the chunk's tokens change nothing; the state warps
-        // write NaN for them.  Rows before it have used none of them.
-        if (p == 0) sh.bad = Q;
-        prep_sync();
-        if (of_k && j < valid && !(seen == 0.f)) atomicMin(&sh.bad, j);
-        prep_sync();
-        const int bad = sh.bad;
-        if (of_k && j >= bad) {
-          for (int i = 0; i < 16; ++i) sh.diag[bj][jj][i] = 0.f;
-          for (int i = 0; i < 8; ++i)
-            *reinterpret_cast<uint4 *>(at_tile(sh.A[0], j, 8 * i)) = *reinterpret_cast<uint4 *>(at_tile(sh.A[1], j, 8 * i)) =
-                make_uint4(0, 0, 0, 0);
-        }
-        if (p == 0) tab.tokens = bad;
-        prep_sync();
-      }
       unsigned char(*const T)[kHalf] = sh.T[b];
       {  // blocks on the diagonal by substitution, one a warp, lane = column
         const int col = lane & 15;
         float t[16];
-        t[0] = col == 0 ? 1.f : 0.f;
 #pragma unroll
-        for (int i = 1; i < 16; ++i) {
-          float s0 = col == i ? 1.f : 0.f, s1 = 0.f;
+        for (int i = 0; i < 16; ++i) t[i] = col == i ? 1.f : 0.f;
 #pragma unroll
-          for (int l = 0; l < i; l += 4) {
-            const float4 r = *reinterpret_cast<const float4 *>(&sh.diag[pw][i][l]);
-            s0 = fmaf(-r.x, t[l], s0);
-            if (l + 1 < i) s1 = fmaf(-r.y, t[l + 1], s1);
-            if (l + 2 < i) s0 = fmaf(-r.z, t[l + 2], s0);
-            if (l + 3 < i) s1 = fmaf(-r.w, t[l + 3], s1);
+        for (int i = 0; i < 15; ++i) {  // t_i is known: off it goes from the rows below
+#pragma unroll
+          for (int l = (i + 1) & ~3; l < 16; l += 4) {
+            const float4 v = *reinterpret_cast<const float4 *>(&sh.diag[pw][20 * i + l]);
+            if (l > i) t[l] = fmaf(-v.x, t[i], t[l]);
+            if (l + 1 > i) t[l + 1] = fmaf(-v.y, t[i], t[l + 1]);
+            if (l + 2 > i) t[l + 2] = fmaf(-v.z, t[i], t[l + 2]);
+            if (l + 3 > i) t[l + 3] = fmaf(-v.w, t[i], t[l + 3]);
           }
-          t[i] = s0 + s1;
         }
         const int lo = lane >> 4;  // lanes 0..15 write the first pieces, the others the second
 #pragma unroll
@@ -511,19 +696,23 @@ __global__ void __launch_bounds__(kGdnThreads, 1)
       if (!(pw & 1)) {  // T10 = -T11 A10 T00 in both blocks of 32
         const int r0 = 16 * pw;
         float x[2][4] = {}, t[2][4] = {};
-        block_x(T, r0, r0, sh.A, r0 + 16, r0, lane, x);
+        block_x(T, r0, r0, sh.A, r0 >> 1, 32, lane, x);
         block_t(T, r0 + 16, r0 + 16, lane, x, t);
         store_block(T, r0 + 16, r0, lane, t);
       }
       prep_sync();
       {  // the same of the whole: block (32 + 16 to, 16 from)
         const int to = pw >> 1, from = pw & 1;
-        float t[2][4] = {};
-        for (int l = 0; l <= to; ++l) {
-          float x[2][4] = {};
-          for (int m = from; m < 2; ++m) block_x(T, 16 * m, 16 * from, sh.A, 32 + 16 * l, 16 * m, lane, x);
-          block_t(T, 32 + 16 * to, 32 + 16 * l, lane, x, t);
-        }
+        float t[2][4] = {}, x[2][2][4] = {};
+#pragma unroll
+        for (int l = 0; l < 2; ++l)
+          if (l <= to) {
+            if (from == 0) block_x(T, 0, 0, sh.A, 16 * l, 0, lane, x[l]);
+            block_x(T, 16, 16 * from, sh.A, 16 * l, 16, lane, x[l]);
+          }
+#pragma unroll
+        for (int l = 0; l < 2; ++l)
+          if (l <= to) block_t(T, 32 + 16 * to, 32 + 16 * l, lane, x[l], t);
         store_block(T, 32 + 16 * to, 16 * from, lane, t);
       }
       fence_async_smem();
@@ -532,67 +721,73 @@ __global__ void __launch_bounds__(kGdnThreads, 1)
     }
   } else {
     // rows of the state: R, U, S, Y
-    const int w = warp >> 2, q4 = warp & 3, row = 32 * q4 + lane;
+    const int w = warp >> 2, q4 = warp & 3, row = 32 * q4 + lane, part = w >> 1, ww = w & 1;
     const uint32_t here = tm + ((uint32_t)(32 * q4) << 16);
     const bool have = row < a.R;
     const float nan = __int_as_float(0x7fffffff);
+    // A warp's 32 columns of the state in two halves of 16, in the order in which they are cut: the pieces of the first may
+    // lie over increments that have been read, not over the other half's.
+    const int at0 = 16 * ww, at1 = 16 - at0;
     float *const Sg = S + (size_t)row * kCols + 32 * w;
-    f2 s[16];
+    f2 s[2][8];
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      float4 v = f4zero();
-      if (pc.resume && have) v = *reinterpret_cast<const float4 *>(Sg + 4 * i);
-      s[2 * i] = pack2(v.x, v.y);
-      s[2 * i + 1] = pack2(v.z, v.w);
-    }
-    // pieces of 16 columns of the state: 8 columns of pairs hi, 8 lo
-    auto put_state = [&](int half) {
-      uint32_t o[16];
+    for (int half = 0; half < 2; ++half)
 #pragma unroll
-      for (int i = 0; i < 8; ++i) cut2(s[8 * half + i], o[i], o[8 + i]);
-      tm_st16(here + kColS + 32 * w + 16 * half, o);
+      for (int i = 0; i < 4; ++i) {
+        float4 v = f4zero();
+        if (pc.resume && have) v = *reinterpret_cast<const float4 *>(Sg + (half ? at1 : at0) + 4 * i);
+        s[half][2 * i] = pack2(v.x, v.y);
+        s[half][2 * i + 1] = pack2(v.z, v.w);
+      }
+    // 16 columns as three pieces of 8 columns of pairs
+    auto put = [&](uint32_t at, const f2 *v) {
+      uint32_t o[16], lo[8];
+#pragma unroll
+      for (int i = 0; i < 8; ++i) cut3(v[i], o[i], o[8 + i], lo[i]);
+      tm_st16(here + at, o);
+      tm_st8(here + at + 16, lo);
     };
-    put_state(0);
-    put_state(1);
+    const uint32_t piece0 = kColS + 48 * w + 24 * ww, piece1 = kColS + 48 * w + 24 - 24 * ww;
+    put(piece0, s[0]);
+    put(piece1, s[1]);
     tm_wait_st();
-    warp_arrive(sh.s_ready, lane);
-    const unsigned char *const vrow = sh.V[0][row >> 6] + 2 * (row & 7);
-    const int vchunk = (row & 63) >> 3;
-    float *yg = a.y + ((size_t)t0 * a.H + h) * a.R + row;
-    for (int c = 0; c < chunks; ++c) {
+    warp_arrive(sh.s_ready[part], lane);
+    const unsigned short *const vrow = reinterpret_cast<const unsigned short *>(sh.V[16 * w]) + row;
+    float *yg = a.y + ((size_t)(t0 + 16 * w) * a.H + h) * a.R + row;
+    const size_t ystep = (size_t)a.H * a.R;
+    int stage = 0;
+    for (int c = 0; c < chunks; ++c, yg += Q * ystep) {
       const int b = c & 1, valid = min(Q, ntok - c * Q);
       const Table &tab = sh.tab[b];
       wait(sh.full_t[b], c >> 1);
-      wait(sh.full_v[b], c >> 1);
+      wait(sh.full_v, c);
       const int tokens = tab.tokens;
-      {  // R = beta (v - rise K S^T)
-        uint32_t x[16];
-        wait(sh.ks_done, c);
-        tm_fence_after();
-        tm_ld16(here + kColR + 16 * w, x);
-        tm_wait_ld();
+      {  // R
         f2 r[8];
         f2 seen = pack2(0.f, 0.f);
-        const f2 zero = pack2(0.f, 0.f);
+        const f2 zero = seen;
 #pragma unroll
         for (int i = 0; i < 16; i += 4) {
-          const float4 g = *reinterpret_cast<const float4 *>(&tab.rise[16 * w + i]);
-          const float4 be = *reinterpret_cast<const float4 *>(&tab.beta[16 * w + i]);
-          float v[4];
+          const float4 f = *reinterpret_cast<const float4 *>(&tab.v[16 * w + i]);
+          uint32_t v[4];
 #pragma unroll
-          for (int k = 0; k < 4; ++k) {
-            const int t = 16 * w + i + k;
-            const unsigned short bits =
-                *reinterpret_cast<const unsigned short *>(vrow + 2 * kHalf * b + t * 128 + ((vchunk ^ (t & 7)) << 4));
-            v[k] = have ? __uint_as_float((uint32_t)bits << 16) : 0.f;
-          }
-          r[i / 2] = mul2(pack2(be.x, be.y), fma2(pack2(-g.x, -g.y), pack2(x[i], x[i + 1]), pack2(v[0], v[1])));
-          r[i / 2 + 1] = mul2(pack2(be.z, be.w), fma2(pack2(-g.z, -g.w), pack2(x[i + 2], x[i + 3]), pack2(v[2], v[3])));
+          for (int k = 0; k < 4; ++k) v[k] = (uint32_t)vrow[(i + k) * kCols] << 16;
+          r[i / 2] = mul2(pack2(f.x, f.y), pack2(v[0], v[1]));
+          r[i / 2 + 1] = mul2(pack2(f.z, f.w), pack2(v[2], v[3]));
+        }
+        uint32_t x[16];
+        wait(sh.ks_done[part], c);
+        tm_fence_after();
+        tm_ld16(here + kColR + 48 * part + 8 + 16 * ww, x);
+        tm_wait_ld();
+#pragma unroll
+        for (int i = 0; i < 16; i += 4) {
+          const float4 f = *reinterpret_cast<const float4 *>(&tab.k[16 * w + i]);
+          r[i / 2] = fma2(pack2(f.x, f.y), pack2(x[i], x[i + 1]), r[i / 2]);
+          r[i / 2 + 1] = fma2(pack2(f.z, f.w), pack2(x[i + 2], x[i + 3]), r[i / 2 + 1]);
           seen = fma2(r[i / 2], zero, fma2(r[i / 2 + 1], zero, seen));
         }
-        float lo, hi;
-        unpack2(seen, lo, hi);
-        if (tokens < 16 * w + 16 || !(lo + hi == 0.f)) {  // not all tokens count, or v holds values that are not finite
+        if (tokens < 16 * w + 16 || not_zero(seen)) {  // not all tokens count, or v holds values that are not finite
 #pragma unroll
           for (int i = 0; i < 8; ++i) {
             float e[2];
@@ -614,47 +809,56 @@ __global__ void __launch_bounds__(kGdnThreads, 1)
           atomicMin(&sh.first[row], c * Q + tokens);
           *(volatile int *)&sh.not_finite = 1;
         }
-#pragma unroll
-        for (int i = 0; i < 8; ++i) cut2(r[i], x[i], x[8 + i]);
-        tm_st16(here + kColR + 16 * w, x);
+        __syncwarp();
+        put(kColR + 24 * w, r);
         tm_wait_st();
-        warp_arrive(sh.r_ready, lane);
-        if (lane == 0) mbar_arrive(&sh.free_v[b]);
+        warp_arrive(sh.r_ready[part], lane);
+        if (lane == 0) {
+          mbar_arrive(&sh.free_v);
+          if (c > 0) {  // Y of the last chunk has left its stage
+            bulk_wait_read();
+            mbar_arrive(&sh.free_kq[stage == 0 ? kStages - 1 : stage - 1]);
+          }
+        }
+      }
+      float carry = tab.carry;
+      {  // U, and where it differs U as it counts at the chunk's end
+        uint32_t x[16];
+        f2 u[8];
+        wait(sh.u_done[part], c);
+        tm_fence_after();
+        tm_ld16(here + kColU + 48 * part + 8 + 16 * ww, x);
+        tm_wait_ld();
+        if (!tab.mild) {
+          if (part == 0) wait(sh.u_done[1], c);  // R of these tokens goes into U of the others
+#pragma unroll
+          for (int i = 0; i < 16; i += 4) {
+            const float4 f = *reinterpret_cast<const float4 *>(&tab.fall[16 * w + i]);
+            u[i / 2] = mul2(pack2(f.x, f.y), pack2(x[i], x[i + 1]));
+            u[i / 2 + 1] = mul2(pack2(f.z, f.w), pack2(x[i + 2], x[i + 3]));
+          }
+          put(kColR + 24 * w, u);
+        }
+#pragma unroll
+        for (int i = 0; i < 8; ++i) u[i] = pack2(x[2 * i], x[2 * i + 1]);
+        put(kColU + 24 * w, u);
+        tm_wait_st();
+        warp_arrive(sh.u_ready[part], lane);
       }
       f2 y[8];
-      {  // rise Q S^T, while U is on its way
+      {  // g Q S^T
         uint32_t x[16];
         wait(sh.qs_done, c);
         tm_fence_after();
         tm_ld16(here + kColY + 16 * w, x);
         tm_wait_ld();
-        const f2 scale = pack2(a.q_scale, a.q_scale);
+        warp_arrive(sh.y_taken, lane);
 #pragma unroll
         for (int i = 0; i < 16; i += 4) {
-          const float4 g = *reinterpret_cast<const float4 *>(&tab.rise[16 * w + i]);
-          y[i / 2] = mul2(mul2(scale, pack2(g.x, g.y)), pack2(x[i], x[i + 1]));
-          y[i / 2 + 1] = mul2(mul2(scale, pack2(g.z, g.w)), pack2(x[i + 2], x[i + 3]));
+          const float4 f = *reinterpret_cast<const float4 *>(&tab.q[16 * w + i]);
+          y[i / 2] = mul2(pack2(f.x, f.y), pack2(x[i], x[i + 1]));
+          y[i / 2 + 1] = mul2(pack2(f.z, f.w), pack2(x[i + 2], x[i + 3]));
         }
-      }
-      float carry = tab.carry;
-      {  // U, and U as it counts at the chunk's end
-        uint32_t x[16], o[16];
-        wait(sh.u_done, c);
-        tm_fence_after();
-        tm_ld16(here + kColU + 16 * w, x);
-        tm_wait_ld();
-#pragma unroll
-        for (int i = 0; i < 16; i += 4) {
-          const float4 g = *reinterpret_cast<const float4 *>(&tab.fall[16 * w + i]);
-          cut2(mul2(pack2(g.x, g.y), pack2(x[i], x[i + 1])), o[i / 2], o[8 + i / 2]);
-          cut2(mul2(pack2(g.z, g.w), pack2(x[i + 2], x[i + 3])), o[i / 2 + 1], o[8 + i / 2 + 1]);
-        }
-        tm_st16(here + kColR + 16 * w, o);
-#pragma unroll
-        for (int i = 0; i < 8; ++i) cut2(pack2(x[2 * i], x[2 * i + 1]), o[i], o[8 + i]);
-        tm_st16(here + kColU + 16 * w, o);
-        tm_wait_st();
-        warp_arrive(sh.u_ready, lane);
       }
       int first = 0x7fffffff;  // of this chunk's tokens, from where on the row is NaN
       if (*(volatile int *)&sh.not_finite) {
@@ -663,20 +867,20 @@ __global__ void __launch_bounds__(kGdnThreads, 1)
       }
       {
         const f2 cc = pack2(carry, carry);
-        wait(sh.d_done, c);
+        wait(sh.d_done[part], c);
         tm_fence_after();
 #pragma unroll
         for (int half = 0; half < 2; ++half) {
           uint32_t x[16];
-          tm_ld16(here + kColD + 32 * w + 16 * half, x);
+          tm_ld16(here + kColS + 96 * part + 16 + 32 * ww + (half ? at1 : at0), x);
           tm_wait_ld();
 #pragma unroll
-          for (int i = 0; i < 8; ++i) s[8 * half + i] = fma2(cc, s[8 * half + i], pack2(x[2 * i], x[2 * i + 1]));
-          if (c + 1 < chunks) put_state(half);
+          for (int i = 0; i < 8; ++i) s[half][i] = fma2(cc, s[half][i], pack2(x[2 * i], x[2 * i + 1]));
+          if (c + 1 < chunks) put(half ? piece1 : piece0, s[half]);
         }
         if (c + 1 < chunks) {
           tm_wait_st();
-          warp_arrive(sh.s_ready, lane);
+          warp_arrive(sh.s_ready[part], lane);
         }
       }
       {
@@ -686,28 +890,58 @@ __global__ void __launch_bounds__(kGdnThreads, 1)
         tm_ld16(here + kColY + 16 * w, x);
         tm_wait_ld();
         warp_arrive(sh.y_free, lane);
-        const f2 scale = pack2(a.q_scale, a.q_scale);
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          float e[2];
-          unpack2(fma2(scale, pack2(x[2 * i], x[2 * i + 1]), y[i]), e[0], e[1]);
+        for (int i = 0; i < 16; i += 4) {
+          const float4 f = *reinterpret_cast<const float4 *>(&tab.u[16 * w + i]);
+          y[i / 2] = fma2(pack2(f.x, f.y), pack2(x[i], x[i + 1]), y[i / 2]);
+          y[i / 2 + 1] = fma2(pack2(f.z, f.w), pack2(x[i + 2], x[i + 3]), y[i / 2 + 1]);
+        }
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&sh.free_t[b]);
+        if (valid >= 16 * w + 16 && __all_sync(0xffffffffu, first >= Q)) {
+          if (32 * q4 < a.R) {  // through the chunk's stage of k and q, which nobody reads any more
+            unsigned char *const out = sh.in[stage][0] + 2048 * warp;
 #pragma unroll
-          for (int k = 0; k < 2; ++k) {
-            const int t = 16 * w + 2 * i + k;
-            if (t >= first) e[k] = nan;
-            if (have && t < valid) yg[(size_t)(c * Q + t) * a.H * a.R] = e[k];
+            for (int i = 0; i < 8; ++i) {
+              float e[2];
+              unpack2(y[i], e[0], e[1]);
+              *reinterpret_cast<float *>(out + 256 * i + 4 * lane) = e[0];
+              *reinterpret_cast<float *>(out + 256 * i + 128 + 4 * lane) = e[1];
+            }
+            fence_async_smem();
+            __syncwarp();
+            if (lane == 0) {
+              tma_store_3d(&map_y, out, 32 * q4, h, t0 + c * Q + 16 * w);
+              bulk_commit();
+            }
+          }
+        } else if (have) {
+          float *at = yg;
+#pragma unroll
+          for (int i = 0; i < 8; ++i) {
+            float e[2];
+            unpack2(y[i], e[0], e[1]);
+#pragma unroll
+            for (int k = 0; k < 2; ++k, at += ystep) {
+              const int t = 16 * w + 2 * i + k;
+              if (t < valid) *at = t >= first ? nan : e[k];
+            }
           }
         }
+        if (++stage == kStages) stage = 0;
       }
     }
+    if (lane == 0) bulk_wait_read();
     if (have) {
 #pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        float4 v;
-        unpack2(s[2 * i], v.x, v.y);
-        unpack2(s[2 * i + 1], v.z, v.w);
-        *reinterpret_cast<float4 *>(Sg + 4 * i) = v;
-      }
+      for (int half = 0; half < 2; ++half)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          float4 v;
+          unpack2(s[half][2 * i], v.x, v.y);
+          unpack2(s[half][2 * i + 1], v.z, v.w);
+          *reinterpret_cast<float4 *>(Sg + (half ? at1 : at0) + 4 * i) = v;
+        }
     }
     tm_fence_before();
   }
@@ -730,7 +964,7 @@ cudaError_t launch_gdn_tc(const GdnScanArgs &s, const Prompts &pr, cudaStream_t 
   EncodeTiled fn;
   cudaError_t e = map_encoder(&fn);
   if (e != cudaSuccess) return e;
-  CUtensorMap mq, mk, mv;
+  CUtensorMap mq, mk, mv, my;
   const CUtensorMapDataType bf16 = CU_TENSOR_MAP_DATA_TYPE_BFLOAT16;
   const cuuint64_t sk[2] = {(cuuint64_t)s.Hk * kCols, (cuuint64_t)pr.total};
   const cuuint64_t tk[1] = {(cuuint64_t)s.Hk * kCols * 2};
@@ -739,11 +973,14 @@ cudaError_t launch_gdn_tc(const GdnScanArgs &s, const Prompts &pr, cudaStream_t 
   if (e == cudaSuccess) e = make_map(fn, &mk, bf16, s.k, 2, sk, tk, bk);
   const cuuint64_t sv[3] = {(cuuint64_t)s.R, (cuuint64_t)s.H, (cuuint64_t)pr.total};
   const cuuint64_t tv[2] = {(cuuint64_t)s.R * 2, (cuuint64_t)s.H * s.R * 2};
-  const cuuint32_t bv[3] = {64, 1, Q};
-  if (e == cudaSuccess) e = make_map(fn, &mv, bf16, s.v, 3, sv, tv, bv);
+  const cuuint32_t bv[3] = {kCols, 1, Q};
+  if (e == cudaSuccess) e = make_map(fn, &mv, bf16, s.v, 3, sv, tv, bv, CU_TENSOR_MAP_SWIZZLE_NONE);
+  const cuuint64_t ty[2] = {(cuuint64_t)s.R * 4, (cuuint64_t)s.H * s.R * 4};
+  const cuuint32_t by[3] = {32, 1, 16};
+  if (e == cudaSuccess) e = make_map(fn, &my, CU_TENSOR_MAP_DATA_TYPE_FLOAT32, s.y, 3, sv, ty, by, CU_TENSOR_MAP_SWIZZLE_NONE);
   if (e == cudaSuccess) e = cudaFuncSetAttribute(gdn_tc_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kGdnSmem);
   if (e != cudaSuccess) return e;
-  gdn_tc_kernel<<<(unsigned)pr.nseq * s.H, kGdnThreads, kGdnSmem, stream>>>(mq, mk, mv, a, pr);
+  gdn_tc_kernel<<<(unsigned)pr.nseq * s.H, kGdnThreads, kGdnSmem, stream>>>(mq, mk, mv, my, a, pr);
   return cudaGetLastError();
 }
 

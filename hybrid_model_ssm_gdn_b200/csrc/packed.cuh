@@ -42,4 +42,20 @@ __device__ __forceinline__ void cut2(f2 v, uint32_t &hi, uint32_t &lo) {
   lo = *reinterpret_cast<const uint32_t *>(&l);
 }
 
+// The three bf16 pieces of a pair, each to nearest, exact in all: 8 bits of what those before it left.  (12.8 issue cycles of
+// a scheduler; 16.2 with pieces that are masked off, since the masks' instructions are no cheaper than the conversions.)
+__device__ __forceinline__ void cut3(f2 v, uint32_t &hi, uint32_t &mid, uint32_t &lo) {
+  float a, b;
+  unpack2(v, a, b);
+  const __nv_bfloat162 h = __floats2bfloat162_rn(a, b);
+  hi = *reinterpret_cast<const uint32_t *>(&h);
+  const f2 left = sub2(v, pack2(hi << 16, hi & 0xffff0000u));
+  unpack2(left, a, b);
+  const __nv_bfloat162 m = __floats2bfloat162_rn(a, b);
+  mid = *reinterpret_cast<const uint32_t *>(&m);
+  unpack2(sub2(left, pack2(mid << 16, mid & 0xffff0000u)), a, b);
+  const __nv_bfloat162 l = __floats2bfloat162_rn(a, b);
+  lo = *reinterpret_cast<const uint32_t *>(&l);
+}
+
 }  // namespace rssm

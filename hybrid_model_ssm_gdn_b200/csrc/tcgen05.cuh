@@ -112,6 +112,35 @@ __device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint32_t b, uint3
       : "memory");
 }
 
+// The same issued under elect_one(): the compiler then knows that one thread issues and keeps the operands in uniform
+// registers, so that products take the tensor core's own time (128 x 64 x 16: 34 cycles, 64 with the predicate above and 45
+// in a branch on the lane's number).  Descriptors are one 64-bit word; whether to accumulate is known at compile time.
+__device__ __forceinline__ bool elect_one() {  // a whole warp; true in one of its threads
+  uint32_t r;
+  asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(r));
+  return r != 0;
+}
+__device__ __forceinline__ uint64_t wide_desc(uint32_t low) { return ((uint64_t)kTileDescHigh << 32) | low; }
+__device__ __forceinline__ void one_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t shape, bool accumulate) {
+  if (accumulate)
+    asm volatile("{\n\t.reg .pred p;\n\tsetp.eq.u32 p, 0, 0;\n\ttcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(
+                     d), "l"(a), "l"(b), "r"(shape) : "memory");
+  else
+    asm volatile("{\n\t.reg .pred p;\n\tsetp.ne.u32 p, 0, 0;\n\ttcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(
+                     d), "l"(a), "l"(b), "r"(shape) : "memory");
+}
+__device__ __forceinline__ void one_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t shape, bool accumulate) {
+  if (accumulate)
+    asm volatile("{\n\t.reg .pred p;\n\tsetp.eq.u32 p, 0, 0;\n\ttcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(
+                     d), "r"(a), "l"(b), "r"(shape) : "memory");
+  else
+    asm volatile("{\n\t.reg .pred p;\n\tsetp.ne.u32 p, 0, 0;\n\ttcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(
+                     d), "r"(a), "l"(b), "r"(shape) : "memory");
+}
+__device__ __forceinline__ void one_commit(uint64_t *bar) {
+  asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(smem_u32(bar)) : "memory");
+}
+
 // tiled TMA loads (no multicast); the innermost coordinate times the element size is a multiple of 16 bytes
 __device__ __forceinline__ void tma_load_2d(void *dst, const void *map, int x, int y, uint64_t *bar) {
   asm volatile(

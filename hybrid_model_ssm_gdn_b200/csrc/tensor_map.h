@@ -21,12 +21,14 @@ inline cudaError_t map_encoder(EncodeTiled *fn) {
   return cudaSuccess;
 }
 
-// rows of 128 bytes with the 128-byte swizzle; what lies outside the tensor reads as zero and is not written
+// tiles, unless told otherwise of rows of 128 bytes with the 128-byte swizzle; what lies outside the tensor reads as zero and
+// is not written
 inline cudaError_t make_map(EncodeTiled fn, CUtensorMap *map, CUtensorMapDataType type, const void *p, int dims,
-                            const cuuint64_t *size, const cuuint64_t *stride, const cuuint32_t *box) {
+                            const cuuint64_t *size, const cuuint64_t *stride, const cuuint32_t *box,
+                            CUtensorMapSwizzle swizzle = CU_TENSOR_MAP_SWIZZLE_128B) {
   const cuuint32_t one[3] = {1, 1, 1};
   const CUresult r = fn(map, type, dims, const_cast<void *>(p), size, stride, box, one,
-                        CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_128B,
+                        CU_TENSOR_MAP_INTERLEAVE_NONE, swizzle, CU_TENSOR_MAP_L2_PROMOTION_L2_128B,
                         CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
   return r == CUDA_SUCCESS ? cudaSuccess : cudaErrorInvalidValue;
 }

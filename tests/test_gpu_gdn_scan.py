@@ -235,7 +235,9 @@ def test_values_that_are_not_finite_reach_no_earlier_token(cuda_ok, dtype, H, Hk
 @pytest.mark.parametrize("key", ["q", "k", "alpha", "beta"])
 @pytest.mark.parametrize("lens", [(40, 1, 23), (300, 1, 260)])
 def test_other_inputs_that_are_not_finite_reach_no_earlier_token(cuda_ok, dtype, lens, key):
-    """NaN and infinities in k, alpha or beta: tokens before theirs and other prompts keep their bits; in q all others do."""
+    """NaN and infinities in k, alpha or beta: tokens before theirs and other prompts keep their bits; in q all others do.
+    Chunks may scale their tokens by the product of alpha up to their end, so with alpha the chunk's earlier tokens of that
+    head keep their values to the rounding of both runs."""
     offsets = packed(lens)
     total, n = offsets[-1], len(lens)
     g = on_gpu(make(38, dtype, total, 4, 2, 64, n, slow=8.0), dtype)
@@ -254,7 +256,14 @@ def test_other_inputs_that_are_not_finite_reach_no_earlier_token(cuda_ok, dtype,
                 hit = torch.zeros_like(y0, dtype=torch.bool)
                 end = t + 1 if key == "q" else offsets[i + 1]
                 hit[t:end, :heads] = True
+                if key == "alpha":
+                    near = torch.zeros_like(hit)
+                    near[offsets[i]:t, 0] = True
+                    assert torch.linalg.vector_norm((y0 - y1)[near]) <= 2 * tol(300) * torch.linalg.vector_norm(y0[near])
+                    hit |= near
+                    assert torch.isfinite(y1[near]).all()
                 assert torch.equal(y0[~hit], y1[~hit])
+                hit[:t] = False
                 assert not torch.isfinite(y1[hit]).any()
                 others = [s for s in range(n) if s != i]
                 assert torch.equal(S0[others], S1[others]) and torch.equal(S0[i, heads:], S1[i, heads:])
