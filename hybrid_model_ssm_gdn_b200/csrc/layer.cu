@@ -14,70 +14,104 @@ namespace {
 
 constexpr int kItems = 4;  // heads' vectors that 16 lanes have on their way at a time
 
-// 8 values as T, 16-byte aligned (32 for fp32)
-__device__ __forceinline__ void store8(float *p, const float (&v)[8]) {
-  *reinterpret_cast<float4 *>(p) = make_float4(v[0], v[1], v[2], v[3]);
-  *reinterpret_cast<float4 *>(p + 4) = make_float4(v[4], v[5], v[6], v[7]);
-}
 __device__ __forceinline__ uint32_t bf16_pair(float a, float b) {
   const __nv_bfloat162 h = __floats2bfloat162_rn(a, b);
   return *reinterpret_cast<const uint32_t *>(&h);
+}
+
+// Eight values as they lie in memory: loads of several are issued before the first is widened.
+template <typename T>
+struct Raw8;
+template <>
+struct Raw8<__nv_bfloat16> {
+  uint4 a;
+  __device__ __forceinline__ void load(const __nv_bfloat16 *p) { a = *reinterpret_cast<const uint4 *>(p); }
+  __device__ __forceinline__ void zero() { a = make_uint4(0, 0, 0, 0); }
+  __device__ __forceinline__ void wide(float (&v)[8]) const {
+    const uint32_t w[4] = {a.x, a.y, a.z, a.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      v[2 * i] = __uint_as_float(w[i] << 16);
+      v[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
+    }
+  }
+};
+template <>
+struct Raw8<float> {
+  float4 a, b;
+  __device__ __forceinline__ void load(const float *p) {
+    a = *reinterpret_cast<const float4 *>(p);
+    b = *reinterpret_cast<const float4 *>(p + 4);
+  }
+  __device__ __forceinline__ void zero() { a = b = make_float4(0.f, 0.f, 0.f, 0.f); }
+  __device__ __forceinline__ void wide(float (&v)[8]) const {
+    v[0] = a.x; v[1] = a.y; v[2] = a.z; v[3] = a.w;
+    v[4] = b.x; v[5] = b.y; v[6] = b.z; v[7] = b.w;
+  }
+};
+
+// 8 values as T, 16-byte aligned
+__device__ __forceinline__ void store8(float *p, const float (&v)[8]) {
+  *reinterpret_cast<float4 *>(p) = make_float4(v[0], v[1], v[2], v[3]);
+  *reinterpret_cast<float4 *>(p + 4) = make_float4(v[4], v[5], v[6], v[7]);
 }
 __device__ __forceinline__ void store8(__nv_bfloat16 *p, const float (&v)[8]) {
   *reinterpret_cast<uint4 *>(p) =
       make_uint4(bf16_pair(v[0], v[1]), bf16_pair(v[2], v[3]), bf16_pair(v[4], v[5]), bf16_pair(v[6], v[7]));
 }
 
-// Vectors: 16 lanes a head of 128, q / sqrt(sum q^2 + eps).  The blocks behind them: one thread a gate,
+// Vectors: 16 lanes a head of 128, q / sqrt(sum q^2 + eps); a block takes a.vector_rows rows of q or of k.  The blocks behind
+// them take a.gate_rows rows, one thread a gate:
 //   alpha = exp(-exp(A_log) softplus(a + bias)),  beta = 1 / (1 + exp(-b)).
 template <typename T>
-__global__ void __launch_bounds__(256) gdn_inputs_kernel(GdnInputsArgs a, int vector_blocks) {
-  if ((int)blockIdx.x >= vector_blocks) {
-    const long long n = (long long)a.rows * a.H;
-    const long long i = (long long)(blockIdx.x - vector_blocks) * 256 + threadIdx.x;
-    if (i >= n) return;
-    const int row = (int)(i / a.H), h = (int)(i % a.H);
-    const float z = to_f32(static_cast<const T *>(a.a)[row * a.stride_a + h]) + a.bias[h];
-    const float b = to_f32(static_cast<const T *>(a.b)[row * a.stride_b + h]);
-    const float softplus = fmaxf(z, 0.f) + log1pf(expf(-fabsf(z)));
-    // a NaN in z would be lost in the maximum
-    a.alpha[i] = expf(-expf(a.A_log[h]) * (z == z ? softplus : z));
-    a.beta[i] = 1.f / (1.f + expf(-b));
+__global__ void __launch_bounds__(256) gdn_inputs_kernel(GdnInputsArgs a, unsigned vector_blocks) {
+  if (blockIdx.x >= 2 * vector_blocks) {
+    const int row0 = (int)(blockIdx.x - 2 * vector_blocks) * a.gate_rows;
+    const int n = min(a.gate_rows, a.rows - row0) * a.H;
+    for (int i = threadIdx.x; i < n; i += 256) {
+      const int dr = (unsigned)i / (unsigned)a.H, h = i - dr * a.H;
+      const long long row = row0 + dr;
+      const float z = to_f32(static_cast<const T *>(a.a)[row * a.stride_a + h]) + a.bias[h];
+      const float b = to_f32(static_cast<const T *>(a.b)[row * a.stride_b + h]);
+      const float softplus = fmaxf(z, 0.f) + log1pf(expf(-fabsf(z)));
+      // a NaN in z would be lost in the maximum
+      a.alpha[row * a.H + h] = expf(-expf(a.A_log[h]) * (z == z ? softplus : z));
+      a.beta[row * a.H + h] = 1.f / (1.f + expf(-b));
+    }
     return;
   }
+  const bool key = blockIdx.x >= vector_blocks;
+  const int row0 = (int)(key ? blockIdx.x - vector_blocks : blockIdx.x) * a.vector_rows;
+  const int n = min(a.vector_rows, a.rows - row0) * a.Hk;
   const int l16 = threadIdx.x & 15, rep = a.out_heads / a.Hk;
-  const long long items = 2LL * a.rows * a.Hk, step = (long long)vector_blocks * 16;
-  for (long long first = (long long)blockIdx.x * 16 + (threadIdx.x >> 4); first - (threadIdx.x >> 4) < items; first += kItems * step) {
-    float v[kItems][8];
+  const T *in = static_cast<const T *>(key ? a.k : a.q) + 8 * l16;
+  T *out = static_cast<T *>(key ? a.k_out : a.q_out) + 8 * l16;
+  const long long stride = key ? a.stride_k : a.stride_q;
+  for (int first = 0; first < n; first += 16 * kItems) {
+    Raw8<T> raw[kItems];
+    int dr[kItems], h[kItems];
 #pragma unroll
     for (int j = 0; j < kItems; ++j) {
-      const long long e = first + j * step;
-      if (e < items) {
-        const long long rh = e >> 1;
-        const int row = (int)(rh / a.Hk), h = (int)(rh % a.Hk);
-        const T *src = static_cast<const T *>(e & 1 ? a.k : a.q) + row * (e & 1 ? a.stride_k : a.stride_q) + h * kCols;
-        load8(src + 8 * l16, v[j]);
-      } else {
-#pragma unroll
-        for (int i = 0; i < 8; ++i) v[j][i] = 0.f;
-      }
+      const int e = first + 16 * j + (threadIdx.x >> 4);
+      dr[j] = (unsigned)e / (unsigned)a.Hk;
+      h[j] = e - dr[j] * a.Hk;
+      raw[j].zero();
+      if (e < n) raw[j].load(in + (row0 + dr[j]) * stride + h[j] * kCols);
     }
 #pragma unroll
     for (int j = 0; j < kItems; ++j) {
-      float sum = 0.f;
+      float v[8], sum = 0.f;
+      raw[j].wide(v);
 #pragma unroll
-      for (int i = 0; i < 8; ++i) sum = fmaf(v[j][i], v[j][i], sum);
+      for (int i = 0; i < 8; ++i) sum = fmaf(v[i], v[i], sum);
 #pragma unroll
       for (int off = 8; off >= 1; off >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, off);
-      const float r = 1.f / sqrtf(sum + a.eps);
+      const float r = rsqrtf(sum + a.eps);
 #pragma unroll
-      for (int i = 0; i < 8; ++i) v[j][i] *= r;
-      const long long e = first + j * step;
-      if (e < items) {
-        const long long rh = e >> 1;
-        const int row = (int)(rh / a.Hk), h = (int)(rh % a.Hk);
-        T *dst = static_cast<T *>(e & 1 ? a.k_out : a.q_out) + ((size_t)row * a.out_heads + (size_t)h * rep) * kCols + 8 * l16;
-        for (int i = 0; i < rep; ++i) store8(dst + i * kCols, v[j]);
+      for (int i = 0; i < 8; ++i) v[i] *= r;
+      if (first + 16 * j + (int)(threadIdx.x >> 4) < n) {
+        T *dst = out + ((size_t)(row0 + dr[j]) * a.out_heads + (size_t)h[j] * rep) * kCols;
+        for (int i = 0; i < rep; ++i) store8(dst + i * kCols, v);
       }
     }
   }
@@ -111,26 +145,45 @@ __device__ __forceinline__ float team_sum(float v, float *words) {
   return warp_sum(v);
 }
 
-__device__ __forceinline__ float lanes_max(float v, int lanes) {
-  for (int off = lanes >> 1; off >= 1; off >>= 1) v = max_nan(v, __shfl_xor_sync(0xffffffffu, v, off));
+template <int kLanes>
+__device__ __forceinline__ float lanes_max(float v) {
+#pragma unroll
+  for (int off = kLanes >> 1; off >= 1; off >>= 1) v = max_nan(v, __shfl_xor_sync(0xffffffffu, v, off));
   return v;
 }
 
 template <bool kWarp>
 __device__ __forceinline__ float team_max(float v, float *words) {
-  v = lanes_max(v, 32);
+  v = lanes_max<32>(v);
   if (kWarp) return v;
   const int warps = blockDim.x >> 5;
   if ((threadIdx.x & 31) == 0) words[threadIdx.x >> 5] = v;
   __syncthreads();
   v = (int)(threadIdx.x & 31) < warps ? words[threadIdx.x & 31] : 0.f;
-  return lanes_max(v, 32);
+  return lanes_max<32>(v);
 }
 
-__device__ __forceinline__ void load_any(const void *p, size_t at, int dtype, float (&v)[8]) {
-  if (dtype == RSSM_BF16) load8(static_cast<const __nv_bfloat16 *>(p) + at, v);
-  else load8(static_cast<const float *>(p) + at, v);
-}
+// Eight values of a type known at run time: the loads do not wait for their widening
+struct RawAny {
+  uint4 a, b;
+  __device__ __forceinline__ void load(const void *p, size_t at, int dtype) {
+    const uint4 *from = reinterpret_cast<const uint4 *>(static_cast<const char *>(p) + at * (dtype == RSSM_BF16 ? 2 : 4));
+    a = from[0];
+    if (dtype != RSSM_BF16) b = from[1];
+  }
+  __device__ __forceinline__ void zero() { a = b = make_uint4(0, 0, 0, 0); }
+  __device__ __forceinline__ void wide(int dtype, float (&v)[8]) const {
+    if (dtype == RSSM_BF16) {
+      Raw8<__nv_bfloat16> r;
+      r.a = a;
+      r.wide(v);
+    } else {
+      const uint32_t w[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
+#pragma unroll
+      for (int i = 0; i < 8; ++i) v[i] = __uint_as_float(w[i]);
+    }
+  }
+};
 __device__ __forceinline__ void store_any(void *p, size_t at, int dtype, const float (&v)[8]) {
   if (dtype == RSSM_BF16) store8(static_cast<__nv_bfloat16 *>(p) + at, v);
   else store8(static_cast<float *>(p) + at, v);
@@ -149,59 +202,87 @@ __device__ __forceinline__ uint2 e4m3_codes(const float (&v)[8], float by) {
 }
 
 // the scale that maps `most` to 448 (a NaN stays one; not below the normal numbers, so that its inverse is finite)
-__device__ __forceinline__ float scale_of(float most) { return max_nan(most / 448.f, 1.17549435e-38f); }
+__device__ __forceinline__ float scale_of(float most) { return max_nan(most * (1.f / 448.f), 1.17549435e-38f); }
 
-template <bool kGated, bool kWarp, int NV>
-__global__ void __launch_bounds__(kWarp ? 256 : 1024) norm_kernel(NormArgs a) {
+// h silu(gate) = h z / (1 + e^-z).  e^-z = 2^(-z log2 e) takes the argument's rounding along, up to |z| 2^-23 of itself (1e-6
+// at z = -8, where silu is -3e-3; it fades for positive z); 2^x and the reciprocal add 2 units in the last place.  The
+// library's expf and __fdividef take 8 instructions a value more, of which the kernel has 30 in all: 100 us against 87 at 16384 x
+// 4096.  Past 2^126 the reciprocal is 0.
+template <typename T>
+__device__ __forceinline__ void times_silu(const Raw8<T> &gate, float (&h)[8]) {
+  float z[8];
+  gate.wide(z);
+#pragma unroll
+  for (int j = 0; j < 8; ++j) {
+    float e, r;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e) : "f"(z[j] * -1.442695041f));
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(1.f + e));
+    h[j] *= z[j] * r;
+  }
+}
+
+template <typename T, typename TG, bool kGated, bool kWarp, int NV>
+__global__ void __launch_bounds__(kWarp ? 256 : 512) norm_kernel(NormArgs a) {
   __shared__ NormShared sh;
   extern __shared__ float parts[];  // groups that are neither the row nor within a warp: sums of 8 columns, sums of groups
   const int team = kWarp ? 32 : blockDim.x, t = kWarp ? threadIdx.x & 31 : threadIdx.x;
   const long long row = kWarp ? (long long)blockIdx.x * 8 + (threadIdx.x >> 5) : blockIdx.x;
   if (kWarp && row >= a.rows) return;
   const int vecs = a.columns >> 3;
-  float h[NV][8], z[kGated ? NV : 1][8];
+  const T *x = static_cast<const T *>(a.x) + row * a.stride_x;
+  // 8 columns of this thread in round i; threads past the row's end read its last 8 once more and add nothing
+  auto at = [&](int i) { return 8 * min(i * team + t, vecs - 1); };
+  auto inside = [&](int i) { return i * team + t < vecs; };
+  float h[NV][8];
+  Raw8<T> in[NV];
+  Raw8<TG> gate[kGated ? NV : 1];
 #pragma unroll
-  for (int i = 0; i < NV; ++i) {
-    const int c = i * team + t;
-#pragma unroll
-    for (int j = 0; j < 8; ++j) h[i][j] = 0.f;
-    if (c < vecs) load_any(a.x, (size_t)row * a.stride_x + 8 * c, a.x_dtype, h[i]);
-  }
+  for (int i = 0; i < NV; ++i) in[i].load(x + at(i));
   if (kGated) {
+    const TG *g = static_cast<const TG *>(a.gate) + row * a.stride_gate;
+#pragma unroll
+    for (int i = 0; i < NV; ++i) gate[i].load(g + at(i));
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
-      const int c = i * team + t;
-#pragma unroll
-      for (int j = 0; j < 8; ++j) z[i][j] = 0.f;
-      if (c < vecs) load_any(a.gate, (size_t)row * a.stride_gate + 8 * c, a.gate_dtype, z[i]);
+      in[i].wide(h[i]);
+      if (!a.norm_first) times_silu(gate[i], h[i]);
     }
-#pragma unroll
-    for (int i = 0; i < NV; ++i)
-#pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        z[i][j] = z[i][j] / (1.f + expf(-z[i][j]));
-        if (!a.norm_first) h[i][j] *= z[i][j];
-      }
   } else if (a.residual) {
+    T *residual = static_cast<T *>(a.residual) + row * a.stride_residual;
+    Raw8<T> add[NV];
+#pragma unroll
+    for (int i = 0; i < NV; ++i) add[i].load(residual + at(i));
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
-      const int c = i * team + t;
-      if (c < vecs) {
-        float r[8];
-        load_any(a.residual, (size_t)row * a.stride_residual + 8 * c, a.x_dtype, r);
+      float r[8];
+      in[i].wide(h[i]);
+      add[i].wide(r);
 #pragma unroll
-        for (int j = 0; j < 8; ++j) h[i][j] += r[j];
-        // rounded once for the next addition; the norm below takes the sum itself
-        store_any(a.residual, (size_t)row * a.stride_residual + 8 * c, a.x_dtype, h[i]);
-      }
+      for (int j = 0; j < 8; ++j) h[i][j] += r[j];
+      // rounded once for the next addition; the norm below takes the sum itself
+      if (inside(i)) store8(residual + at(i), h[i]);
     }
+  } else {
+#pragma unroll
+    for (int i = 0; i < NV; ++i) in[i].wide(h[i]);
   }
+  RawAny weight[NV];
+  auto load_weight = [&]() {
+    const unsigned wc = a.weight_columns;
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+      const unsigned c = at(i);
+      weight[i].load(a.weight, wc == (unsigned)a.columns ? c : (wc & (wc - 1)) == 0 ? c & (wc - 1) : c % wc, a.weight_dtype);
+    }
+  };
+  if (kWarp) load_weight();  // on its way during the sums; a whole block's registers are better spent on another row
   float sq[NV];
 #pragma unroll
   for (int i = 0; i < NV; ++i) {
     sq[i] = 0.f;
 #pragma unroll
     for (int j = 0; j < 8; ++j) sq[i] = fmaf(h[i][j], h[i][j], sq[i]);
+    if (!inside(i)) sq[i] = 0.f;
   }
   const float inv_n = 1.f / (float)a.group;
   if (a.group == a.columns) {
@@ -209,14 +290,14 @@ __global__ void __launch_bounds__(kWarp ? 256 : 1024) norm_kernel(NormArgs a) {
 #pragma unroll
     for (int i = 1; i < NV; ++i) sum += sq[i];
     sum = team_sum<kWarp>(sum, sh.warp);
-    const float r = 1.f / sqrtf(sum * inv_n + a.eps);
+    const float r = rsqrtf(sum * inv_n + a.eps);
 #pragma unroll
     for (int i = 0; i < NV; ++i) sq[i] = r;
   } else if (a.group <= 256 && (a.group & (a.group - 1)) == 0) {
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
       for (int off = a.group >> 4; off >= 1; off >>= 1) sq[i] += __shfl_xor_sync(0xffffffffu, sq[i], off);
-      sq[i] = 1.f / sqrtf(sq[i] * inv_n + a.eps);
+      sq[i] = rsqrtf(sq[i] * inv_n + a.eps);
     }
   } else {
     float *part = kWarp ? parts + (threadIdx.x >> 5) * 2 * vecs : parts, *group = part + vecs;
@@ -229,24 +310,20 @@ __global__ void __launch_bounds__(kWarp ? 256 : 1024) norm_kernel(NormArgs a) {
       float sum = 0.f;
       for (int c = t & 31; c < per; c += 32) sum += part[g * per + c];
       sum = warp_sum(sum);
-      if ((t & 31) == 0) group[g] = 1.f / sqrtf(sum * inv_n + a.eps);
+      if ((t & 31) == 0) group[g] = rsqrtf(sum * inv_n + a.eps);
     }
     if (kWarp) __syncwarp(); else __syncthreads();
 #pragma unroll
     for (int i = 0; i < NV; ++i) sq[i] = i * team + t < vecs ? group[(i * team + t) / per] : 0.f;
   }
+  if (!kWarp) load_weight();
 #pragma unroll
   for (int i = 0; i < NV; ++i) {
-    const int c = i * team + t;
-    if (c < vecs) {
-      float w[8];
-      load_any(a.weight, a.weight_columns == a.columns ? 8 * c : 8 * c % a.weight_columns, a.weight_dtype, w);
+    float w[8];
+    weight[i].wide(a.weight_dtype, w);
 #pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        h[i][j] = h[i][j] * sq[i] * (a.offset + w[j]);
-        if (kGated && a.norm_first) h[i][j] *= z[i][j];
-      }
-    }
+    for (int j = 0; j < 8; ++j) h[i][j] = h[i][j] * sq[i] * (a.offset + w[j]);
+    if (kGated && a.norm_first) times_silu(gate[i], h[i]);
   }
   if (a.scale == RSSM_SCALE_NONE) {
 #pragma unroll
@@ -258,9 +335,9 @@ __global__ void __launch_bounds__(kWarp ? 256 : 1024) norm_kernel(NormArgs a) {
 #pragma unroll
   for (int i = 0; i < NV; ++i) {
     most[i] = 0.f;
-    if (i * team + t < vecs)
 #pragma unroll
-      for (int j = 0; j < 8; ++j) most[i] = max_nan(most[i], fabsf(h[i][j]));
+    for (int j = 0; j < 8; ++j) most[i] = max_nan(most[i], fabsf(h[i][j]));
+    if (!inside(i)) most[i] = 0.f;
   }
   float scale[NV];
   if (a.scale == RSSM_SCALE_ROW) {
@@ -275,7 +352,7 @@ __global__ void __launch_bounds__(kWarp ? 256 : 1024) norm_kernel(NormArgs a) {
     const int blocks = (vecs + 15) >> 4;
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
-      scale[i] = scale_of(lanes_max(most[i], 16));
+      scale[i] = scale_of(lanes_max<16>(most[i]));
       const int c = i * team + t;
       if ((c & 15) == 0 && c < vecs) a.scales[row * blocks + (c >> 4)] = scale[i];
     }
@@ -285,43 +362,53 @@ __global__ void __launch_bounds__(kWarp ? 256 : 1024) norm_kernel(NormArgs a) {
     const int c = i * team + t;
     if (c < vecs)
       *reinterpret_cast<uint2 *>(static_cast<unsigned char *>(a.out) + (size_t)row * a.columns + 8 * c) =
-          e4m3_codes(h[i], 1.f / scale[i]);
+          e4m3_codes(h[i], __fdividef(1.f, scale[i]));
   }
 }
 
-template <bool kGated, bool kWarp, int NV>
-cudaError_t launch_norm_as(const NormArgs &a, int threads, cudaStream_t stream) {
+template <typename T, typename TG, bool kGated, bool kWarp, int NV>
+cudaError_t launch_norm_as(const NormArgs &a, cudaStream_t stream) {
+  const int vecs = a.columns >> 3, threads = kWarp ? 256 : ((vecs + NV - 1) / NV + 31) / 32 * 32;
   const bool general = a.group != a.columns && (a.group > 256 || (a.group & (a.group - 1)));
-  const size_t smem = general ? (size_t)(kWarp ? 8 : 1) * 2 * (a.columns >> 3) * 4 : 0;
+  const size_t smem = general ? (size_t)(kWarp ? 8 : 1) * 2 * vecs * 4 : 0;
   const unsigned grid = kWarp ? (unsigned)((a.rows + 7) / 8) : (unsigned)a.rows;
-  norm_kernel<kGated, kWarp, NV><<<grid, kWarp ? 256 : threads, smem, stream>>>(a);
+  norm_kernel<T, TG, kGated, kWarp, NV><<<grid, threads, smem, stream>>>(a);
   return cudaGetLastError();
 }
 
-template <bool kGated>
+template <typename T, typename TG, bool kGated>
 cudaError_t launch_norm_type(const NormArgs &a, cudaStream_t stream) {
   const int vecs = a.columns >> 3;
-  if (vecs <= 32) return launch_norm_as<kGated, true, 1>(a, 0, stream);
-  if (vecs <= 64) return launch_norm_as<kGated, true, 2>(a, 0, stream);
-  if (vecs <= 128) return launch_norm_as<kGated, true, 4>(a, 0, stream);
-  auto threads = [&](int nv) { return ((vecs + nv - 1) / nv + 31) / 32 * 32; };
-  if (vecs <= 2048) return launch_norm_as<kGated, false, 2>(a, threads(2), stream);
-  return launch_norm_as<kGated, false, 4>(a, threads(4), stream);
+  if (vecs <= 32) return launch_norm_as<T, TG, kGated, true, 1>(a, stream);
+  if (vecs <= 64) return launch_norm_as<T, TG, kGated, true, 2>(a, stream);
+  if (vecs <= 128) return launch_norm_as<T, TG, kGated, true, 4>(a, stream);
+  constexpr int kFew = kGated ? 2 : 4;
+  if (vecs <= 512 * kFew) return launch_norm_as<T, TG, kGated, false, kFew>(a, stream);
+  return launch_norm_as<T, TG, kGated, false, 8>(a, stream);
 }
 
 }  // namespace
 
-cudaError_t launch_gdn_inputs(const GdnInputsArgs &a, int esz, int num_sms, cudaStream_t stream) {
-  const long long vectors = (2LL * a.rows * a.Hk + 15) / 16, gates = ((long long)a.rows * a.H + 255) / 256;
-  const long long full = (vectors + kItems - 1) / kItems;
-  const long long vb = vectors <= 8LL * num_sms ? vectors : full < 8LL * num_sms ? 8LL * num_sms : full;
-  if (esz == 2) gdn_inputs_kernel<__nv_bfloat16><<<(unsigned)(vb + gates), 256, 0, stream>>>(a, (int)vb);
-  else gdn_inputs_kernel<float><<<(unsigned)(vb + gates), 256, 0, stream>>>(a, (int)vb);
+cudaError_t launch_gdn_inputs(const GdnInputsArgs &args, int esz, int num_sms, cudaStream_t stream) {
+  GdnInputsArgs a = args;
+  // a row a block while that leaves the SMs with few blocks, otherwise as many as give every 16 lanes kItems vectors
+  a.vector_rows = a.rows <= 4 * num_sms ? 1 : max(1, 16 * kItems / a.Hk);
+  a.gate_rows = a.rows <= 4 * num_sms ? 1 : max(1, 1024 / a.H);
+  const unsigned vb = (unsigned)((a.rows + a.vector_rows - 1) / a.vector_rows);
+  const unsigned grid = 2 * vb + (unsigned)((a.rows + a.gate_rows - 1) / a.gate_rows);
+  if (esz == 2) gdn_inputs_kernel<__nv_bfloat16><<<grid, 256, 0, stream>>>(a, vb);
+  else gdn_inputs_kernel<float><<<grid, 256, 0, stream>>>(a, vb);
   return cudaGetLastError();
 }
 
 cudaError_t launch_norm(const NormArgs &a, bool gated, cudaStream_t stream) {
-  return gated ? launch_norm_type<true>(a, stream) : launch_norm_type<false>(a, stream);
+  using bf16 = __nv_bfloat16;
+  if (a.x_dtype == RSSM_BF16) {
+    if (!gated) return launch_norm_type<bf16, bf16, false>(a, stream);
+    return a.gate_dtype == RSSM_BF16 ? launch_norm_type<bf16, bf16, true>(a, stream) : launch_norm_type<bf16, float, true>(a, stream);
+  }
+  if (!gated) return launch_norm_type<float, float, false>(a, stream);
+  return a.gate_dtype == RSSM_BF16 ? launch_norm_type<float, bf16, true>(a, stream) : launch_norm_type<float, float, true>(a, stream);
 }
 
 }  // namespace rssm

@@ -13,6 +13,7 @@ struct GdnInputsArgs {
   float eps;
   void *q_out, *k_out;              // [rows][out_heads][128]
   float *alpha, *beta;              // [rows][H]
+  int vector_rows, gate_rows;       // rows of a block (the launch's to fill in)
 };
 cudaError_t launch_gdn_inputs(const GdnInputsArgs &a, int esz, int num_sms, cudaStream_t stream);
 
