@@ -4,8 +4,8 @@
 //   y_t = q_scale S_t q_t = q_scale (alpha_t S_{t-1} q_t + u (k_t . q_t))
 //
 // Both products of a token are taken from the state before it, so that one round of sums over a row's columns is all that
-// stands between two tokens.  A row of 128 fp32 lies in four lanes (two shuffles a sum), a warp carries 8 rows; k, q, v
-// come from shared memory, 16 tokens at a time with the next ones on their way.  fp32 throughout: inputs of 24 bits would
+// stands between two tokens.  A row of 128 fp32 lies in 4 or 16 lanes (two or four shuffles a sum); k, q, v come from shared
+// memory, 16 tokens at a time with the next ones on their way.  fp32 throughout: inputs of 24 bits would
 // need six bf16 products for each one of the chunk form.
 #include "prompt_kernels.h"
 #include "packed.cuh"
@@ -28,59 +28,83 @@ struct Stage {
   float4 g[kTok];  // alpha, beta, k . q
 };
 
-// this lane's 32 columns of a row of T in shared memory: runs of 16 bytes, 4 lanes side by side
+// this lane's 128 / L columns of a row of T in shared memory: runs of 16 bytes, L lanes side by side
 template <typename T>
 struct Columns;
 template <>
 struct Columns<float> {
   static constexpr int kRun = 4;
-  static __device__ __forceinline__ void load(const float *row, int l4, f2 (&o)[16]) {
+  template <int L>
+  static __device__ __forceinline__ void load(const float *row, int lane, f2 (&o)[64 / L]) {
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      const float4 v = *reinterpret_cast<const float4 *>(row + 4 * (l4 + 4 * i));
+    for (int i = 0; i < 32 / L; ++i) {
+      const float4 v = *reinterpret_cast<const float4 *>(row + 4 * (lane + L * i));
       o[2 * i] = pack2(v.x, v.y);
       o[2 * i + 1] = pack2(v.z, v.w);
     }
+  }
+  static __device__ __forceinline__ void quad(const float *row, int i, f2 (&o)[2]) {  // columns 4 i .. 4 i + 3
+    const float4 v = *reinterpret_cast<const float4 *>(row + 4 * i);
+    o[0] = pack2(v.x, v.y);
+    o[1] = pack2(v.z, v.w);
   }
 };
 template <>
 struct Columns<__nv_bfloat16> {
   static constexpr int kRun = 8;
-  static __device__ __forceinline__ void load(const __nv_bfloat16 *row, int l4, f2 (&o)[16]) {
+  template <int L>
+  static __device__ __forceinline__ void load(const __nv_bfloat16 *row, int lane, f2 (&o)[64 / L]) {
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const uint4 v = *reinterpret_cast<const uint4 *>(row + 8 * (l4 + 4 * i));
+    for (int i = 0; i < 16 / L; ++i) {
+      const uint4 v = *reinterpret_cast<const uint4 *>(row + 8 * (lane + L * i));
       o[4 * i] = pack2(v.x << 16, v.x & 0xffff0000u);
       o[4 * i + 1] = pack2(v.y << 16, v.y & 0xffff0000u);
       o[4 * i + 2] = pack2(v.z << 16, v.z & 0xffff0000u);
       o[4 * i + 3] = pack2(v.w << 16, v.w & 0xffff0000u);
     }
   }
+  static __device__ __forceinline__ void quad(const __nv_bfloat16 *row, int i, f2 (&o)[2]) {
+    const uint2 v = *reinterpret_cast<const uint2 *>(row + 4 * i);
+    o[0] = pack2(v.x << 16, v.x & 0xffff0000u);
+    o[1] = pack2(v.y << 16, v.y & 0xffff0000u);
+  }
 };
 
-__device__ __forceinline__ float sum4(f2 a, f2 b, f2 c, f2 d) {  // over the registers and a row's four lanes
+template <int N>
+__device__ __forceinline__ float sum_of(const f2 (&v)[4]) {  // of the first N pairs
   const f2 one = pack2(1.f, 1.f);
   float lo, hi;
-  unpack2(fma2(one, fma2(one, a, b), fma2(one, c, d)), lo, hi);
-  float v = lo + hi;
-  v += __shfl_xor_sync(0xffffffffu, v, 1);
-  return v + __shfl_xor_sync(0xffffffffu, v, 2);
+  unpack2(N == 2 ? fma2(one, v[0], v[1]) : fma2(one, fma2(one, v[0], v[1]), fma2(one, v[2], v[3])), lo, hi);
+  return lo + hi;
 }
 
-// R rows of head blockIdx.y from row blockIdx.z * R on
-template <typename T, int R>
-__global__ void __launch_bounds__(4 * R) gdn_scan_kernel(GdnScanArgs a, Prompts pr) {
+template <int L>
+__device__ __forceinline__ float lanes_sum(float v) {
+#pragma unroll
+  for (int off = 1; off < L; off <<= 1) v += __shfl_xor_sync(0xffffffffu, v, off);
+  return v;
+}
+
+// the first column of this lane's `i`-th four (of 32 / L)
+template <typename T, int L>
+__device__ __forceinline__ int four_at(int lane, int i) {
+  return Columns<T>::kRun == 4 ? 4 * (lane + L * i) : 8 * (lane + L * (i >> 1)) + 4 * (i & 1);
+}
+
+// R rows of head blockIdx.y from row blockIdx.z * R on, L lanes a row
+template <typename T, int R, int L>
+__global__ void __launch_bounds__(L * R) gdn_scan_kernel(GdnScanArgs a, Prompts pr) {
   __shared__ __align__(16) Stage<T, R> st[2];
   __shared__ PieceWord found;
-  constexpr int kThreads = 4 * R, kRun = Columns<T>::kRun, kShare = kThreads / kTok;
+  constexpr int kThreads = L * R, kWarps = kThreads / 32, kPairs = 64 / L;
   Piece pc;
   const int h = blockIdx.y, row0 = blockIdx.z * R;
   allow_next();
   if (find_piece(pr, blockIdx.x, pr.total + 1, pc, &found) != kPieceRun) return;
   const int len = pc.end - pc.begin;
   if (len == 0 && pc.resume) return;
-  const int tid = threadIdx.x, lane = tid & 31, l4 = lane & 3;
-  const int mine = tid >> 2;  // this lane's row within the block
+  const int tid = threadIdx.x, lane = tid & 31, l = lane & (L - 1);
+  const int mine = tid / L;  // this lane's row within the block
   const bool have = row0 + mine < a.R;
   const int hk = h / (a.H / a.Hk);
   const T *kg = static_cast<const T *>(a.k) + ((size_t)pc.begin * a.Hk + hk) * kCols;
@@ -111,13 +135,12 @@ __global__ void __launch_bounds__(4 * R) gdn_scan_kernel(GdnScanArgs a, Prompts 
   };
   if (len > 0) fetch(0, st[0]);
 
-  f2 s[16];
+  f2 s[kPairs];
   float *Sg = a.S + (((size_t)(a.by_prompt ? pc.seq : pc.slot) * a.H + h) * a.R + row0 + mine) * kCols;
 #pragma unroll
-  for (int i = 0; i < 8; ++i) {
+  for (int i = 0; i < kPairs / 2; ++i) {
     float4 v = f4zero();
-    const int col = kRun == 4 ? 4 * (l4 + 4 * i) : 8 * (l4 + 4 * (i >> 1)) + 4 * (i & 1);
-    if (pc.resume && have) v = *reinterpret_cast<const float4 *>(Sg + col);
+    if (pc.resume && have) v = *reinterpret_cast<const float4 *>(Sg + four_at<T, L>(l, i));
     s[2 * i] = pack2(v.x, v.y);
     s[2 * i + 1] = pack2(v.z, v.w);
   }
@@ -129,72 +152,102 @@ __global__ void __launch_bounds__(4 * R) gdn_scan_kernel(GdnScanArgs a, Prompts 
     asm volatile("cp.async.wait_group 0;" ::: "memory");
     __syncthreads();
     if (t0 + kTok < len) fetch(t0 + kTok, st[b ^ 1]);  // read last before the barrier above
-    {  // k . q of each token, by kShare neighbouring threads
-      const int t = tid / kShare, part = tid % kShare;
-      float v = 0.f;
+    // k . q of each token, a warp at a time
 #pragma unroll
-      for (int n = part; n < kCols; n += kShare) v = fmaf(to_f32(m.k[t][n]), to_f32(m.q[t][n]), v);
-#pragma unroll
-      for (int off = kShare / 2; off >= 1; off >>= 1) v += __shfl_xor_sync(0xffffffffu, v, off);
-      if (part == 0) m.g[t].z = v;
-      if (tid < kTok) {
-        m.g[tid].x = alpha_now;
-        m.g[tid].y = beta_now;
-      }
+    for (int j = 0; j < kTok; j += kWarps) {
+      const int t = j + (tid >> 5);
+      f2 k[2], q[2];
+      Columns<T>::quad(m.k[t], lane, k);
+      Columns<T>::quad(m.q[t], lane, q);
+      float lo, hi;
+      unpack2(fma2(k[0], q[0], mul2(k[1], q[1])), lo, hi);
+      lo = lanes_sum<32>(lo + hi);
+      if (lane == 0) m.g[t].z = lo;
+    }
+    if (tid < kTok) {
+      m.g[tid].x = alpha_now;
+      m.g[tid].y = beta_now;
     }
     __syncthreads();
     const int n = min(kTok, len - t0);
-#pragma unroll 2
+    f2 k[kPairs], q[kPairs];
+    constexpr bool kAhead = L > 4;  // registers for two tokens' k and q
+    if (kAhead) {
+      Columns<T>::template load<L>(m.k[0], l, k);
+      Columns<T>::template load<L>(m.q[0], l, q);
+    }
+    float4 g = m.g[0];
+    float v = to_f32(m.v[0][mine]);
+#pragma unroll 1
     for (int t = 0; t < n; ++t) {
-      const float4 g = m.g[t];
-      f2 k[16], q[16];
-      Columns<T>::load(m.k[t], l4, k);
-      Columns<T>::load(m.q[t], l4, q);
-      f2 p[4], w[4];
+      // the next token's inputs set out before this one's sums (the last of a stage reads itself again)
+      const int next = min(t + 1, kTok - 1);
+      f2 k2[kPairs], q2[kPairs], p[4], w[4];
+      if (kAhead) {
+        Columns<T>::template load<L>(m.k[next], l, k2);
+        Columns<T>::template load<L>(m.q[next], l, q2);
+      } else {
+        Columns<T>::template load<L>(m.k[t], l, k);
+        Columns<T>::template load<L>(m.q[t], l, q);
+      }
+      const float4 g2 = m.g[next];
+      const float v2 = to_f32(m.v[next][mine]);
+      constexpr int kSums = kPairs < 8 ? 2 : 4;
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
+      for (int i = 0; i < kSums; ++i) {
         p[i] = mul2(s[i], k[i]);
         w[i] = mul2(s[i], q[i]);
       }
 #pragma unroll
-      for (int i = 4; i < 16; ++i) {
-        p[i & 3] = fma2(s[i], k[i], p[i & 3]);
-        w[i & 3] = fma2(s[i], q[i], w[i & 3]);
+      for (int i = kSums; i < kPairs; ++i) {
+        p[i & (kSums - 1)] = fma2(s[i], k[i], p[i & (kSums - 1)]);
+        w[i & (kSums - 1)] = fma2(s[i], q[i], w[i & (kSums - 1)]);
       }
-      const float sk = sum4(p[0], p[1], p[2], p[3]), sq = sum4(w[0], w[1], w[2], w[3]);
-      const float u = g.y * fmaf(-g.x, sk, to_f32(m.v[t][mine]));
+      const float sk = lanes_sum<L>(sum_of<kSums>(p)), sq = lanes_sum<L>(sum_of<kSums>(w));
+      const float u = g.y * fmaf(-g.x, sk, v);
       const f2 uu = pack2(u, u), aa = pack2(g.x, g.x);
 #pragma unroll
-      for (int i = 0; i < 16; ++i) s[i] = fma2(uu, k[i], mul2(aa, s[i]));
-      if (l4 == 0 && have) yg[(size_t)(t0 + t) * a.H * a.R] = a.q_scale * fmaf(u, g.z, g.x * sq);
+      for (int i = 0; i < kPairs; ++i) s[i] = fma2(uu, k[i], mul2(aa, s[i]));
+      if (l == 0 && have) yg[(size_t)(t0 + t) * a.H * a.R] = a.q_scale * fmaf(u, g.z, g.x * sq);
+      if (kAhead) {
+#pragma unroll
+        for (int i = 0; i < kPairs; ++i) {
+          k[i] = k2[i];
+          q[i] = q2[i];
+        }
+      }
+      g = g2;
+      v = v2;
     }
     __syncthreads();  // g and the stage are read no more
   }
   if (have) {
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      const int col = kRun == 4 ? 4 * (l4 + 4 * i) : 8 * (l4 + 4 * (i >> 1)) + 4 * (i & 1);
+    for (int i = 0; i < kPairs / 2; ++i) {
       float4 v;
       unpack2(s[2 * i], v.x, v.y);
       unpack2(s[2 * i + 1], v.z, v.w);
-      *reinterpret_cast<float4 *>(Sg + col) = v;
+      *reinterpret_cast<float4 *>(Sg + four_at<T, L>(l, i)) = v;
     }
   }
 }
 
-template <typename T, int R>
+template <typename T, int R, int L>
 cudaError_t launch_rows(const GdnScanArgs &a, const Prompts &pr, cudaStream_t stream) {
-  gdn_scan_kernel<T, R><<<dim3(pr.nseq, a.H, (a.R + R - 1) / R), 4 * R, 0, stream>>>(a, pr);
+  gdn_scan_kernel<T, R, L><<<dim3(pr.nseq, a.H, (a.R + R - 1) / R), L * R, 0, stream>>>(a, pr);
   return cudaGetLastError();
 }
 
 template <typename T>
 cudaError_t launch_type(const GdnScanArgs &a, const Prompts &pr, int num_sms, cudaStream_t stream) {
-  // All rows a block share one staging of k and q; 8 rows, one warp, spread few heads and prompts over the SMs.
+  // All rows of a block share one staging of k and q, so many heads are best off with 64 rows a block, and 4 lanes a row need
+  // the fewest shuffles.  Few heads wait for each token's sums alone: 8 rows over 16 lanes put a warp on each quarter of an SM
+  // (fp32, us, 8 / 16 / 64 rows a block: 2 prompts of 150 tokens, 8 heads of 64 rows 39 / 53 / 79; 8 prompts 60 / 57 / 79;
+  // 8 of 32 heads of 128 rows 340 / 239 / 235; 32 of them 1287 / 858 / 789).
   const long long heads = (long long)pr.nseq * a.H;
-  if (heads >= 2LL * num_sms) return launch_rows<T, 64>(a, pr, stream);
-  if (heads * 4 >= num_sms) return launch_rows<T, 16>(a, pr, stream);
-  return launch_rows<T, 8>(a, pr, stream);
+  if (heads * ((a.R + 7) / 8) <= 2LL * num_sms) return launch_rows<T, 8, 16>(a, pr, stream);
+  if (heads < 2LL * num_sms) return launch_rows<T, 16, 4>(a, pr, stream);
+  return launch_rows<T, 64, 4>(a, pr, stream);
 }
 
 }  // namespace
