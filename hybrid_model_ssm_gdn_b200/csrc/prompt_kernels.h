@@ -49,7 +49,7 @@ struct GdnScanArgs {
 // token by token: fp32 inputs, prompts of a few tokens
 cudaError_t launch_gdn_scan(const GdnScanArgs &a, const Prompts &pr, int esz, int num_sms, cudaStream_t stream);
 // chunks on the tensor cores: bf16 inputs, total > 0
-cudaError_t launch_gdn_tc(const GdnScanArgs &a, const Prompts &pr, cudaStream_t stream);
+cudaError_t launch_gdn_tc(const GdnScanArgs &a, const Prompts &pr, int num_sms, cudaStream_t stream);
 // states of packed prompts [nseq][H][rows][128] from and to a GDN context's stored formats
 struct PromptStateArgs {
   int H, rows, hp_mode, read_mode;
