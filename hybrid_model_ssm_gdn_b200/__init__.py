@@ -560,8 +560,8 @@ def gdn_inputs(q, k, a, b, A_log, dt_bias, eps=1e-6, expand=False, out=None):
     strides = [_apart(t, n, lead, _count(inner), inner, dtype, device)
                for t, n, inner in ((q, "q", (Hk, 128)), (k, "k", (Hk, 128)), (a, "a", (H,)), (b, "b", (H,)))]
     if out is None:
-        out = (q.new_empty((*lead, heads, 128)), q.new_empty((*lead, heads, 128)),
-               q.new_empty((*lead, H), dtype=torch.float32), q.new_empty((*lead, H), dtype=torch.float32))
+        qk, gate = q.new_empty((*lead, heads, 128)), q.new_empty((*lead, H), dtype=torch.float32)
+        out = (qk, torch.empty_like(qk), gate, torch.empty_like(gate))  # half the time of a second new_empty
     else:
         for t, n, s, d in zip(out, ("q", "k", "alpha", "beta"), ((heads, 128), (heads, 128), (H,), (H,)),
                               (dtype, dtype, torch.float32, torch.float32), strict=True):
@@ -592,7 +592,7 @@ def _norm(x, weight, columns, group, eps, offset, out_dtype, scale, out, gate_dt
         kind, want = abi.F32, torch.float8_e4m3fn
         scales = lead if scale == "row" else (*lead, (columns + 127) // 128)
     if out is None:
-        y = x.new_empty(x.shape, dtype=want)
+        y = torch.empty_like(x) if want is x.dtype and x.is_contiguous() else x.new_empty(x.shape, dtype=want)
         got = y if scale is None else (y, x.new_empty(scales, dtype=torch.float32))
     else:
         got = out

@@ -1,12 +1,12 @@
 """The gated delta rule over packed prompts against the float64 oracle (needs a B200).
 
-Tolerance, per prompt and head, on the 2-norm of the error over the 2-norm of the result.  With unit keys, 0 <= beta <= 1
-and |alpha| <= 1 every token's map of the state is non-expanding, so an error made in one chunk of 64 tokens is carried on
-without growth, beside values of the size that it was made on.  Within a chunk a value passes the inverse, which reaches the tensor
-cores in two bf16 pieces (off by at most 2^-17 of itself), and three operands in three pieces (2^-24 each); fp32 sums of 64
-to 128 terms add 2^-24 a level and the blocks of the inverse, products of two-piece operands themselves, another 2^-17: at most
-2^-16.  Roundings of different chunks are independent, so that n chunks add up to sqrt(n) of it.  The fp32 kernel lies far below (2^-24 for each of some 24 steps of a
-token, tokens independent).
+Tolerance, per prompt and head, on the 2-norm of the error over the 2-norm of the result. With unit keys, 0 <= beta <= 1
+and |alpha| <= 1 every token's map of the state is non-expanding, so an error made in one chunk of 64 tokens is carried
+on without growth, beside values of the size that it was made on. Within a chunk a value passes the inverse, which
+reaches the tensor cores in two bf16 pieces (off by at most 2^-17 of itself), and three operands in three pieces (2^-24
+each); fp32 sums of 64 to 128 terms add 2^-24 a level and the blocks of the inverse, products of two-piece operands
+themselves, another 2^-17: at most 2^-16. Roundings of different chunks are independent, so that n chunks add up to
+sqrt(n) of it. The fp32 kernel lies far below (2^-24 for each of some 24 steps of a token, tokens independent).
 """
 
 import numpy as np
