@@ -17,6 +17,7 @@ Prompts and drafts around it: ``ReplaySSM.prefill`` / ``mamba2_scan``, ``ReplayS
 from __future__ import annotations
 
 import ctypes as C
+import functools
 
 import torch
 
@@ -544,65 +545,100 @@ def _count(shape):
     return n
 
 
+def _row_step(t, name, shape, lead, inner, width, dtype, device):
+    """``_apart`` behind a look for the usual case, a contiguous tensor."""
+    if t.shape == shape and t.dtype is dtype and t.get_device() == device and t.is_contiguous():
+        return width
+    return _apart(t, name, lead, width, inner, dtype, device)
+
+
+# What follows from sizes and types alone is worked out once for each (a decode step's calls are as long as their checks).
+@functools.lru_cache(maxsize=1024)
+def _inputs_plan(q_shape, a_shape, dtype, expand):
+    """(rows, heads of the output, sizes of one row, shapes of the vectors that come out and of the gates)"""
+    if len(q_shape) < 2 or len(a_shape) < 1:
+        raise ValueError("q and a: expected at least 2 dimensions and 1")
+    if dtype not in _DT:
+        raise ValueError(f"q: expected torch.float32 or torch.bfloat16, got {dtype}")
+    lead, Hk, H = q_shape[:-2], q_shape[-2], a_shape[-1]
+    if Hk < 1 or H < 1 or H % Hk:
+        raise ValueError(f"q: expected [...][heads that divide {H}][128], got {tuple(q_shape)}")
+    heads = H if expand else Hk
+    return lead, _count(lead), H, Hk, heads, torch.Size((*lead, Hk, 128)), torch.Size((*lead, H)), \
+        torch.Size((*lead, heads, 128))
+
+
 def gdn_inputs(q, k, a, b, A_log, dt_bias, eps=1e-6, expand=False, out=None):
     """Inputs of the gated delta rule from a layer's projections and convolution (rssm_gdn_inputs): q, k [...][Hk][128] and
     a, b [...][H] (bf16 or fp32; rows may lie apart), A_log, dt_bias fp32 [H], H a multiple of Hk -> (q, k, alpha, beta):
     q and k with length 1, [...][Hk][128], or with ``expand`` [...][H][128] as the decode calls take them; alpha =
     exp(-exp(A_log) softplus(a + dt_bias)), beta = sigmoid(b), fp32 [...][H]."""
-    if q.dim() < 2 or a.dim() < 1:
-        raise ValueError("q and a: expected at least 2 dimensions and 1")
-    dtype = _in_dtype(q, "q")
+    dtype = q.dtype
+    lead, rows, H, Hk, heads, in_shape, gate_shape, out_shape = _inputs_plan(q.shape, a.shape, dtype, bool(expand))
     device = _device(q, "q")
-    lead, Hk, H = q.shape[:-2], q.shape[-2], a.shape[-1]
-    if Hk < 1 or H < 1 or H % Hk:
-        raise ValueError(f"q: expected [...][heads that divide {H}][128], got {tuple(q.shape)}")
-    heads, rows = H if expand else Hk, _count(lead)
-    strides = [_apart(t, n, lead, _count(inner), inner, dtype, device)
-               for t, n, inner in ((q, "q", (Hk, 128)), (k, "k", (Hk, 128)), (a, "a", (H,)), (b, "b", (H,)))]
+    vec, row = 128 * Hk, (Hk, 128)
+    strides = (_row_step(q, "q", in_shape, lead, row, vec, dtype, device),
+               _row_step(k, "k", in_shape, lead, row, vec, dtype, device),
+               _row_step(a, "a", gate_shape, lead, (H,), H, dtype, device),
+               _row_step(b, "b", gate_shape, lead, (H,), H, dtype, device))
     if out is None:
-        qk, gate = q.new_empty((*lead, heads, 128)), q.new_empty((*lead, H), dtype=torch.float32)
+        qk = torch.empty_like(q) if heads == Hk and q.is_contiguous() else q.new_empty(out_shape)
+        gate = q.new_empty(gate_shape, dtype=torch.float32)
         out = (qk, torch.empty_like(qk), gate, torch.empty_like(gate))  # half the time of a second new_empty
     else:
-        for t, n, s, d in zip(out, ("q", "k", "alpha", "beta"), ((heads, 128), (heads, 128), (H,), (H,)),
+        for t, n, s, d in zip(out, ("q", "k", "alpha", "beta"), (out_shape, out_shape, gate_shape, gate_shape),
                               (dtype, dtype, torch.float32, torch.float32), strict=True):
-            _arr(t, d, "out " + n, (*lead, *s), device)
+            _arr(t, d, "out " + n, s, device)
     cfg = abi.GdnInputsConfig(rows, H, Hk, heads, _DT[dtype], eps, q.data_ptr(), k.data_ptr(), a.data_ptr(), b.data_ptr(),
                               *strides, _arr(A_log, torch.float32, "A_log", (H,), device),
                               _arr(dt_bias, torch.float32, "dt_bias", (H,), device))
-    abi.check(abi.load().rssm_gdn_inputs(C.byref(cfg), *[t.data_ptr() for t in out], _stream_of(device)), "rssm_gdn_inputs")
+    qo, ko, al, be = out
+    abi.check(abi.load().rssm_gdn_inputs(C.byref(cfg), qo.data_ptr(), ko.data_ptr(), al.data_ptr(), be.data_ptr(),
+                                         _stream_of(device)), "rssm_gdn_inputs")
     return out
 
 
 _SCALES = {None: abi.SCALE_NONE, "row": abi.SCALE_ROW, "block": abi.SCALE_BLOCK}
 
 
-def _norm(x, weight, columns, group, eps, offset, out_dtype, scale, out, gate_dtype, norm_first, device):
-    """(config, address of the weight, output, scales, and what the call returns) of a norm over the last dimension."""
+@functools.lru_cache(maxsize=1024)
+def _norm_plan(shape, x_dtype, weight_shape, weight_dtype, group, eps, offset, out_dtype, scale, gate_dtype, norm_first):
+    """(the call's config by reference, type of the output, shape of the scales or None, shape of the weight) of a norm over
+    the last dimension"""
+    columns, lead = shape[-1], shape[:-1]
+    group = group or columns
     if scale not in _SCALES:
         raise ValueError(f"scale: expected None, 'row' or 'block', got {scale!r}")
     if group < 1 or columns % group:
         raise ValueError(f"group: expected a divisor of {columns}, got {group}")
-    wcols = columns if weight.numel() == columns else group
-    lead = x.shape[:-1]
+    wcols = columns if _count(weight_shape) == columns else group
     if scale is None:
         if out_dtype not in _DT:
             raise ValueError(f"out_dtype: expected torch.float32 or torch.bfloat16, got {out_dtype}")
         kind, want, scales = _DT[out_dtype], out_dtype, None
     else:
         kind, want = abi.F32, torch.float8_e4m3fn
-        scales = lead if scale == "row" else (*lead, (columns + 127) // 128)
+        scales = lead if scale == "row" else torch.Size((*lead, (columns + 127) // 128))
+    if weight_dtype not in _DT:
+        raise ValueError(f"weight: expected torch.float32 or torch.bfloat16, got {weight_dtype}")
+    cfg = abi.NormConfig(_count(lead), columns, group, wcols, _DT[x_dtype], gate_dtype, _DT[weight_dtype], kind, _SCALES[scale],
+                         norm_first, eps, offset)
+    return C.byref(cfg), want, scales, torch.Size((wcols,))
+
+
+def _norm_out(x, want, scales, out, device):
+    """(output of x's shape, scales or None, and what the call returns)"""
     if out is None:
         y = torch.empty_like(x) if want is x.dtype and x.is_contiguous() else x.new_empty(x.shape, dtype=want)
-        got = y if scale is None else (y, x.new_empty(scales, dtype=torch.float32))
-    else:
-        got = out
-        _arr(out if scale is None else out[0], want, "out", x.shape, device)
-        if scale is not None:
-            _arr(out[1], torch.float32, "scales", scales, device)
-    y, s = (got, None) if scale is None else got
-    cfg = abi.NormConfig(_count(lead), columns, group, wcols, _DT[_in_dtype(x, "x")], gate_dtype,
-                         _DT[_in_dtype(weight, "weight")], kind, _SCALES[scale], norm_first, eps, offset)
-    return cfg, _arr(weight, weight.dtype, "weight", (wcols,), device), y.data_ptr(), _addr(s), got
+        if scales is None:
+            return y, None, y
+        s = x.new_empty(scales, dtype=torch.float32)
+        return y, s, (y, s)
+    y, s = (out, None) if scales is None else out
+    _arr(y, want, "out", x.shape, device)
+    if scales is not None:
+        _arr(s, torch.float32, "scales", scales, device)
+    return y, s, out
 
 
 def add_rmsnorm(x, weight, residual=None, eps=1e-6, offset=0.0, out_dtype=None, scale=None, out=None):
@@ -610,13 +646,16 @@ def add_rmsnorm(x, weight, residual=None, eps=1e-6, offset=0.0, out_dtype=None, 
     back to ``residual`` in place; x, residual [...][n] (bf16 or fp32; rows may lie apart), weight [n] -> h / rms(h) (offset +
     weight) in ``out_dtype`` (x's), or with ``scale`` "row" or "block" (of 128 columns) the pair (float8_e4m3fn, scales fp32
     [...] or [...][ceil(n/128)])."""
-    n, dtype = x.shape[-1], _in_dtype(x, "x")
+    shape, dtype = x.shape, _in_dtype(x, "x")
+    n, lead = shape[-1], shape[:-1]
     device = _device(x, "x")
-    lead = x.shape[:-1]
-    stride = _apart(x, "x", lead, n, (n,), dtype, device)
-    r_stride = 0 if residual is None else _apart(residual, "residual", lead, n, (n,), dtype, device)
-    cfg, w, y, s, got = _norm(x, weight, n, n, eps, offset, out_dtype or dtype, scale, out, 0, 0, device)
-    abi.check(abi.load().rssm_add_rmsnorm(C.byref(cfg), x.data_ptr(), stride, _addr(residual), r_stride, w, y, s,
+    stride = _row_step(x, "x", shape, lead, (n,), n, dtype, device)
+    r_stride = 0 if residual is None else _row_step(residual, "residual", shape, lead, (n,), n, dtype, device)
+    cfg, want, scales, w_shape = _norm_plan(shape, dtype, weight.shape, weight.dtype, 0, eps, offset, out_dtype or dtype,
+                                            scale, 0, 0)
+    y, s, got = _norm_out(x, want, scales, out, device)
+    abi.check(abi.load().rssm_add_rmsnorm(cfg, x.data_ptr(), stride, _addr(residual), r_stride,
+                                          _arr(weight, weight.dtype, "weight", w_shape, device), y.data_ptr(), _addr(s),
                                           _stream_of(device)), "rssm_add_rmsnorm")
     return got
 
@@ -625,15 +664,17 @@ def gated_rmsnorm(y, gate, weight, group=None, eps=1e-6, offset=0.0, norm_first=
     """The gated norm behind a layer (rssm_gated_rmsnorm): y [...][n], gate [...][n] (bf16 or fp32 each; rows may lie apart),
     weight [n], or [group] for all groups -> with s = silu(gate), the norm of each ``group`` columns (all) of y times s, or
     without ``norm_first`` of y s; in ``out_dtype`` (gate's) or in 8 bits as for ``add_rmsnorm``."""
-    n = y.shape[-1]
+    shape = y.shape
+    n, lead = shape[-1], shape[:-1]
     device = _device(y, "y")
-    lead = y.shape[:-1]
-    gate_dtype = _in_dtype(gate, "gate")
-    stride = _apart(y, "y", lead, n, (n,), _in_dtype(y, "y"), device)
-    g_stride = _apart(gate, "gate", lead, n, (n,), gate_dtype, device)
-    cfg, w, o, s, got = _norm(y, weight, n, group or n, eps, offset, out_dtype or gate_dtype, scale, out, _DT[gate_dtype],
-                              norm_first, device)
-    abi.check(abi.load().rssm_gated_rmsnorm(C.byref(cfg), y.data_ptr(), stride, gate.data_ptr(), g_stride, w, o, s,
+    dtype, gate_dtype = _in_dtype(y, "y"), _in_dtype(gate, "gate")
+    stride = _row_step(y, "y", shape, lead, (n,), n, dtype, device)
+    g_stride = _row_step(gate, "gate", shape, lead, (n,), n, gate_dtype, device)
+    cfg, want, scales, w_shape = _norm_plan(shape, dtype, weight.shape, weight.dtype, group, eps, offset, out_dtype or gate_dtype,
+                                            scale, _DT[gate_dtype], bool(norm_first))
+    o, s, got = _norm_out(gate if want is gate_dtype else y, want, scales, out, device)
+    abi.check(abi.load().rssm_gated_rmsnorm(cfg, y.data_ptr(), stride, gate.data_ptr(), g_stride,
+                                            _arr(weight, weight.dtype, "weight", w_shape, device), o.data_ptr(), _addr(s),
                                             _stream_of(device)), "rssm_gated_rmsnorm")
     return got
 
