@@ -647,6 +647,36 @@ rssm_status rssm_gdn_prefill(rssm_ctx *x, int qk_heads, const rssm_prompts *pr, 
 
 static bool dtype_ok(int d) { return d == RSSM_F32 || d == RSSM_BF16; }
 
+// whether [out, out + bytes) meets one of `rows` rows of `row` bytes that start `stride` bytes apart from `in`. Rows are
+// loaded ahead of the outputs before them, and by blocks other than the one that writes there
+static bool overlaps(const void *out, unsigned long long bytes, const void *in, long long rows, unsigned long long row,
+                     unsigned long long stride) {
+  const unsigned long long o = (uintptr_t)out, i = (uintptr_t)in;
+  if (o + bytes <= i) return false;
+  if (o < i) return true;
+  const unsigned long long r = (o - i) / stride;  // the last row that starts at or before `out`
+  if (r >= (unsigned long long)rows) return false;
+  return o < i + r * stride + row || (r + 1 < (unsigned long long)rows && o + bytes > i + (r + 1) * stride);
+}
+
+// a call's contiguous output, or the rows of an input
+struct Extent {
+  const void *at;
+  unsigned long long rows, row, stride;  // bytes
+};
+// whether one of the outputs meets an input or another output
+static bool outputs_meet(const Extent *outs, int n_outs, const Extent *ins, int n_ins) {
+  for (int o = 0; o < n_outs; ++o) {
+    const Extent &w = outs[o];
+    if (!w.at) continue;
+    for (int i = 0; i < n_ins; ++i)
+      if (ins[i].at && overlaps(w.at, w.row, ins[i].at, ins[i].rows, ins[i].row, ins[i].stride)) return true;
+    for (int i = 0; i < o; ++i)
+      if (outs[i].at && overlaps(w.at, w.row, outs[i].at, 1, outs[i].row, outs[i].row)) return true;
+  }
+  return false;
+}
+
 rssm_status rssm_gdn_inputs(const rssm_gdn_inputs_config *c, void *q_out, void *k_out, float *alpha, float *beta,
                             rssm_stream stream) {
   if (!c || !dtype_ok(c->in_dtype) || !(c->eps >= 0.f)) return RSSM_ERR_ARG;
@@ -663,6 +693,12 @@ rssm_status rssm_gdn_inputs(const rssm_gdn_inputs_config *c, void *q_out, void *
   if (!c->q || !c->k || !c->a || !c->b || !c->A_log || !c->bias || !q_out || !k_out || !alpha || !beta ||
       !aligned16(c->q) || !aligned16(c->k) || !aligned16(q_out) || !aligned16(k_out))
     return RSSM_ERR_ARG;
+  const unsigned long long rows = c->rows, esz = c->in_dtype == RSSM_BF16 ? 2 : 4;
+  const unsigned long long vecs = rows * c->out_heads * kCols * esz, gates = rows * c->nheads * 4;
+  const Extent outs[] = {{q_out, 1, vecs, vecs}, {k_out, 1, vecs, vecs}, {alpha, 1, gates, gates}, {beta, 1, gates, gates}};
+  const Extent ins[] = {{c->q, rows, vec * esz, c->q_stride * esz}, {c->k, rows, vec * esz, c->k_stride * esz},
+                        {c->a, rows, c->nheads * esz, c->a_stride * esz}, {c->b, rows, c->nheads * esz, c->b_stride * esz}};
+  if (outputs_meet(outs, 4, ins, 4)) return RSSM_ERR_ARG;
   GdnInputsArgs a{};
   a.rows = c->rows; a.H = c->nheads; a.Hk = c->qk_heads; a.out_heads = c->out_heads; a.eps = c->eps;
   a.q = c->q; a.k = c->k; a.a = c->a; a.b = c->b;
@@ -675,8 +711,20 @@ rssm_status rssm_gdn_inputs(const rssm_gdn_inputs_config *c, void *q_out, void *
   return e == cudaSuccess ? RSSM_OK : cuda_fail(e);
 }
 
-static rssm_status norm_args(const rssm_norm_config *c, bool gated, const void *x, long long x_stride, const void *weight,
-                             void *out, float *scales, NormArgs &a) {
+// whether rows of two inputs meet, rows of one wide matrix side by side not
+static bool rows_meet(const Extent &a, const Extent &b) {
+  const unsigned long long pa = (uintptr_t)a.at, pb = (uintptr_t)b.at;
+  const unsigned long long ea = pa + (a.rows - 1) * a.stride + a.row, eb = pb + (b.rows - 1) * b.stride + b.row;
+  if (ea <= pb || eb <= pa) return false;
+  if (a.stride != b.stride || a.row > a.stride || b.row > b.stride) return true;
+  const unsigned long long apart = pa < pb ? (pb - pa) % a.stride : a.stride - (pa - pb) % a.stride;  // from a's row to b's
+  return apart < a.row || apart + b.row > a.stride;
+}
+
+// other: the gate's rows, or the residual's
+static rssm_status norm_args(const rssm_norm_config *c, bool gated, const void *x, long long x_stride, const void *other,
+                             int other_dtype, long long other_stride, const void *weight, void *out, float *scales,
+                             NormArgs &a) {
   if (!c || !dtype_ok(c->x_dtype) || !dtype_ok(c->weight_dtype) || (gated && !dtype_ok(c->gate_dtype))) return RSSM_ERR_ARG;
   if (c->scale != RSSM_SCALE_NONE && c->scale != RSSM_SCALE_ROW && c->scale != RSSM_SCALE_BLOCK) return RSSM_ERR_ARG;
   if (c->scale == RSSM_SCALE_NONE && !dtype_ok(c->out_dtype)) return RSSM_ERR_ARG;
@@ -687,9 +735,22 @@ static rssm_status norm_args(const rssm_norm_config *c, bool gated, const void *
   if (!gated && (c->group != c->columns || c->weight_columns != c->columns)) return RSSM_ERR_SHAPE;
   if (c->rows > 0) {
     if (x_stride < c->columns || x_stride % 8 != 0) return RSSM_ERR_SHAPE;
+    if ((gated || other) && (other_stride < c->columns || other_stride % 8 != 0)) return RSSM_ERR_SHAPE;
+    if ((gated && !other) || (other && !aligned16(other))) return RSSM_ERR_ARG;
     if (!x || !weight || !out || !aligned16(x) || !aligned16(weight) || !aligned16(out) ||
         (c->scale != RSSM_SCALE_NONE && !scales))
       return RSSM_ERR_ARG;
+  }
+  if (c->rows > 0) {
+    auto size = [](int dtype) { return dtype == RSSM_BF16 ? 2ULL : 4ULL; };
+    const unsigned long long rows = c->rows, cols = c->columns;
+    const unsigned long long bytes = rows * cols * (c->scale == RSSM_SCALE_NONE ? size(c->out_dtype) : 1);
+    const unsigned long long marks = rows * (c->scale == RSSM_SCALE_ROW ? 1 : (cols + 127) / 128) * 4;
+    const Extent outs[] = {{out, 1, bytes, bytes}, {c->scale == RSSM_SCALE_NONE ? nullptr : scales, 1, marks, marks}};
+    const Extent ins[] = {{x, rows, cols * size(c->x_dtype), x_stride * size(c->x_dtype)},
+                          {other, rows, cols * size(other_dtype), other_stride * size(other_dtype)},
+                          {weight, 1, c->weight_columns * size(c->weight_dtype), c->weight_columns * size(c->weight_dtype)}};
+    if (outputs_meet(outs, 2, ins, 3)) return RSSM_ERR_ARG;
   }
   a.rows = c->rows; a.columns = c->columns; a.group = c->group; a.weight_columns = c->weight_columns;
   a.x_dtype = c->x_dtype; a.gate_dtype = c->gate_dtype; a.weight_dtype = c->weight_dtype; a.out_dtype = c->out_dtype;
@@ -701,10 +762,14 @@ static rssm_status norm_args(const rssm_norm_config *c, bool gated, const void *
 rssm_status rssm_add_rmsnorm(const rssm_norm_config *cfg, const void *x, long long x_stride, void *residual,
                              long long residual_stride, const void *weight, void *out, float *scales, rssm_stream stream) {
   NormArgs a{};
-  const rssm_status s = norm_args(cfg, false, x, x_stride, weight, out, scales, a);
+  if (!cfg) return RSSM_ERR_ARG;
+  const rssm_status s = norm_args(cfg, false, x, x_stride, residual, cfg->x_dtype, residual_stride, weight, out, scales, a);
   if (s != RSSM_OK || a.rows == 0) return s;
-  if (residual && (residual_stride < a.columns || residual_stride % 8 != 0)) return RSSM_ERR_SHAPE;
-  if (residual && !aligned16(residual)) return RSSM_ERR_ARG;
+  // h goes back while x is read: x itself, or apart from it
+  const unsigned long long esz = a.x_dtype == RSSM_BF16 ? 2 : 4, row = a.columns * esz;
+  const Extent to{residual, (unsigned long long)a.rows, row, residual_stride * esz};
+  const Extent from{x, (unsigned long long)a.rows, row, x_stride * esz};
+  if (residual && !(residual == x && (residual_stride == x_stride || a.rows == 1)) && rows_meet(to, from)) return RSSM_ERR_ARG;
   a.residual = residual; a.stride_residual = residual_stride;
   const cudaError_t e = launch_norm(a, false, reinterpret_cast<cudaStream_t>(stream));
   return e == cudaSuccess ? RSSM_OK : cuda_fail(e);
@@ -713,10 +778,9 @@ rssm_status rssm_add_rmsnorm(const rssm_norm_config *cfg, const void *x, long lo
 rssm_status rssm_gated_rmsnorm(const rssm_norm_config *cfg, const void *x, long long x_stride, const void *gate,
                                long long gate_stride, const void *weight, void *out, float *scales, rssm_stream stream) {
   NormArgs a{};
-  const rssm_status s = norm_args(cfg, true, x, x_stride, weight, out, scales, a);
+  if (!cfg) return RSSM_ERR_ARG;
+  const rssm_status s = norm_args(cfg, true, x, x_stride, gate, cfg->gate_dtype, gate_stride, weight, out, scales, a);
   if (s != RSSM_OK || a.rows == 0) return s;
-  if (gate_stride < a.columns || gate_stride % 8 != 0) return RSSM_ERR_SHAPE;
-  if (!gate || !aligned16(gate)) return RSSM_ERR_ARG;
   a.gate = gate; a.stride_gate = gate_stride;
   const cudaError_t e = launch_norm(a, true, reinterpret_cast<cudaStream_t>(stream));
   return e == cudaSuccess ? RSSM_OK : cuda_fail(e);
@@ -741,18 +805,6 @@ static rssm_status shortconv_validate(const rssm_shortconv_config *c, int tokens
 }
 
 static int shortconv_esize(const rssm_shortconv_config *c) { return c->in_dtype == RSSM_BF16 ? 2 : 4; }
-
-// whether [out, out + bytes) meets one of `rows` rows of `row` bytes that start `stride` bytes apart from `in`: tokens are
-// loaded ahead of the outputs before them, and a prompt's tiles read rows that are another block's
-static bool overlaps(const void *out, unsigned long long bytes, const void *in, long long rows, unsigned long long row,
-                     unsigned long long stride) {
-  const unsigned long long o = (uintptr_t)out, i = (uintptr_t)in;
-  if (o + bytes <= i) return false;
-  if (o < i) return true;
-  const unsigned long long r = (o - i) / stride;  // the last row that starts at or before `out`
-  if (r >= (unsigned long long)rows) return false;
-  return o < i + r * stride + row || (r + 1 < (unsigned long long)rows && o + bytes > i + (r + 1) * stride);
-}
 
 static rssm_status shortconv_args(const rssm_shortconv_config *c, void *hist, const int *cur, const void *in,
                                   long long in_stride, void *const out[3], long long rows, ShortConvArgs &a) {

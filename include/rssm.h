@@ -293,7 +293,8 @@ rssm_status rssm_shortconv_commit(const rssm_shortconv_config *cfg, int *cur, co
  * What the decode and prompt calls leave to a layer around them, on any number of token rows (a decode step's sequences,
  * a packed prompt's tokens).  The published layers' formulas; sums are fp32, each result is rounded once.
  * Strides count elements from one row to the next: rows may be slices of a wider projection; those of vectors start on
- * 16-byte boundaries.  Outputs are contiguous and overlap no input.  rows = 0 does nothing. */
+ * 16-byte boundaries.  Outputs are contiguous; one that overlaps an input or another is refused.  rows = 0
+ * does nothing. */
 
 /* Inputs of the gated delta rule, per row and head:
  *   q_out = q / sqrt(sum q^2 + eps), k_out likewise (in_dtype, [rows][out_heads][128]; out_heads = qk_heads, or nheads:
@@ -330,7 +331,8 @@ typedef struct {
 } rssm_norm_config;
 
 /* In front of a layer: h = x + residual (fp32), which goes back to residual, rounded once (the norm takes h before that).
- * residual may be NULL: h = x.  Takes cfg.group = cfg.weight_columns = columns. */
+ * residual may be NULL: h = x; its rows may be x itself or beside its rows, not across them.  Takes cfg.group =
+ * cfg.weight_columns = columns. */
 rssm_status rssm_add_rmsnorm(const rssm_norm_config *cfg, const void *x, long long x_stride, void *residual,
                              long long residual_stride, const void *weight, void *out, float *scales, rssm_stream stream);
 

@@ -150,6 +150,58 @@ def test_gated_rmsnorm(cuda_ok, n, group, shared, gate_dtype):
                 close_e4m3(*got, want, 128 if scale == "block" else None)
 
 
+def test_rows_side_by_side_and_in_place(cuda_ok):
+    """Input, residual and gate as slices of one wide matrix; x as its own residual; outputs over inputs are refused."""
+    r = np.random.default_rng(44)
+    wide = dev(values(r, BF, 9, 640), BF)
+    w = dev(values(r, BF, 200), BF)
+    x, res, z = wide[:, :200], wide[:, 200:400], wide[:, 400:600]
+    apart = [t.contiguous() for t in (x, res, z)]
+    want = add_rmsnorm(apart[0], w, apart[1])
+    assert torch.equal(add_rmsnorm(x, w, res), want) and torch.equal(wide[:, 200:400], apart[1])
+    assert torch.equal(wide[:, :200], apart[0]) and torch.equal(wide[:, 400:600], apart[2])
+    assert torch.equal(gated_rmsnorm(x, z, w, group=40), gated_rmsnorm(apart[0], apart[2], w, group=40))
+    twice = apart[0].clone()
+    want = add_rmsnorm(apart[0], w, res2 := apart[0].clone())
+    assert torch.equal(add_rmsnorm(twice, w, twice), want) and torch.equal(twice, res2)
+    for call in (lambda: add_rmsnorm(twice, w, out=twice), lambda: gated_rmsnorm(apart[0], twice, w, out=twice),
+                 lambda: add_rmsnorm(twice, w, res2, out=res2), lambda: add_rmsnorm(wide[:, :200], w, wide[:, 8:208])):
+        with pytest.raises(RuntimeError, match="RSSM_ERR_ARG"):
+            call()
+    q, a = dev(values(r, BF, 9, 2, 128), BF), dev(values(r, BF, 9, 4), BF)
+    A = torch.zeros(4, device="cuda")
+    out = (q, torch.empty_like(q), torch.empty(9, 4, device="cuda"), torch.empty(9, 4, device="cuda"))
+    with pytest.raises(RuntimeError, match="RSSM_ERR_ARG"):
+        gdn_inputs(q, q, a, a, A, A, out=out)
+
+
+@pytest.mark.parametrize("rows,n", [(2 ** 19 + 5, 8192), (2 ** 17 + 3, 32768)])
+def test_rows_past_32_bits(cuda_ok, rows, n):
+    """Matrices with more than 2^32 elements: the last rows are what they are in a small one."""
+    r = np.random.default_rng(45)
+    x, z, w = (dev(values(r, BF, *s), BF) for s in ((5, n), (5, n), (n,)))
+    big, gate = torch.empty(rows, n, dtype=BF, device="cuda"), torch.empty(rows, n, dtype=BF, device="cuda")
+    big[-5:], gate[-5:] = x, z
+    res, small = gate.clone(), z.clone()
+    out, scales = add_rmsnorm(big, w, res, scale="block")
+    want, s = add_rmsnorm(x, w, small, scale="block")
+    assert torch.equal(out[-5:].view(torch.uint8), want.view(torch.uint8)) and torch.equal(scales[-5:], s)
+    assert torch.equal(res[-5:], small)
+    del out, res
+    assert torch.equal(gated_rmsnorm(big, gate, w, group=64)[-5:], gated_rmsnorm(x, z, w, group=64))
+
+
+def test_inputs_past_32_bits(cuda_ok):
+    r = np.random.default_rng(46)
+    rows, H, Hk = 2 ** 21 + 77, 32, 16
+    q, a = dev(values(r, BF, 77, Hk, 128), BF), dev(values(r, BF, 77, H), BF)
+    A, bias = (torch.from_numpy(r.uniform(-1, 1, H).astype(np.float32)).cuda() for _ in range(2))
+    big, gates = torch.empty(rows, Hk, 128, dtype=BF, device="cuda"), torch.empty(rows, H, dtype=BF, device="cuda")
+    big[-77:], gates[-77:] = q, a
+    for got, want in zip(gdn_inputs(big, big, gates, gates, A, bias), gdn_inputs(q, q, a, a, A, bias)):
+        assert torch.equal(got[-77:], want)
+
+
 def test_norms_of_slices_and_own_outputs(cuda_ok):
     """Rows that lie apart, any leading dimensions, outputs of the caller, no rows at all."""
     r = np.random.default_rng(4)

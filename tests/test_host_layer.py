@@ -105,6 +105,36 @@ def test_norm_refusals(lib):
     assert gate(gate_dtype=2) == ARG and gate(z=None) == ARG and gate(z=C.c_void_p(8)) == ARG and gate(zs=63) == SHAPE
 
 
+def test_outputs_that_meet_inputs_are_refused(lib):
+    """Rows are read ahead of the outputs before them: no output may lie over an input or another output.  Every call here is
+    one that is refused, at addresses that nobody reads."""
+    M = 1 << 24
+    at = dict(x=M, r=2 * M, w=3 * M, out=4 * M, s=5 * M)
+    base = dict(rows=3, columns=64, group=64, weight_columns=64, x_dtype=1, gate_dtype=1, weight_dtype=1, out_dtype=1,
+                scale=0, norm_first=1, eps=1e-6, offset=0.0)
+
+    def call(f, xs=64, rs=64, scale=0, **kw):
+        p = {k: C.c_void_p(v) for k, v in {**at, **kw}.items()}
+        return f(C.byref(abi.NormConfig(**{**base, "scale": scale})), p["x"], xs, p["r"], rs, p["w"], p["out"], p["s"], None)
+
+    for f in (lib.rssm_add_rmsnorm, lib.rssm_gated_rmsnorm):
+        for name in ("x", "r", "w"):
+            assert call(f, out=at[name]) == ARG and call(f, out=at[name] - 3 * 128 + 16) == ARG
+        assert call(f, out=M + 2 * 128) == ARG  # the last row of x
+        assert call(f, xs=1024, out=M + 2 * 2048 + 112) == ARG
+        assert call(f, scale=1, s=M) == ARG and call(f, scale=2, s=4 * M + 128) == ARG and call(f, scale=1, out=2 * M + 256) == ARG
+    for r, xs, rs in ((M + 128, 64, 64), (M - 16, 64, 64), (M + 64, 128, 128), (M, 64, 128), (M - 64, 128, 128), (M + 256, 64, 72)):
+        assert call(lib.rssm_add_rmsnorm, r=r, xs=xs, rs=rs) == ARG, (r, xs, rs)
+
+    cfg_ = dict(rows=3, nheads=4, qk_heads=2, out_heads=2, in_dtype=abi.BF16, eps=1e-6, q=M, k=2 * M, a=3 * M, b=4 * M,
+                q_stride=256, k_stride=256, a_stride=4, b_stride=4, A_log=9 * M, bias=10 * M)
+    for i in range(4):
+        for where in (M, M + 2 * 512, 2 * M, 2 * M + 3 * 512 - 16, 3 * M + 16, 4 * M, *(m * M for m in (5, 6, 7, 8) if m != 5 + i)):
+            outs = [5 * M, 6 * M, 7 * M, 8 * M]
+            outs[i] = where
+            assert lib.rssm_gdn_inputs(C.byref(abi.GdnInputsConfig(**cfg_)), *map(C.c_void_p, outs), None) == ARG, (i, where)
+
+
 def test_binding_checks_shapes_and_devices():
     """Shapes and types are refused with ValueError, and tensors off the GPU before a pointer is taken from them."""
     t = torch.zeros
