@@ -385,11 +385,12 @@ cudaError_t launch_norm_type(const NormArgs &a, cudaStream_t stream) {
   // 27 / 29 against 39 / 39).  From there on a block a row, 8 columns a thread up to 1024 (65536 x 1024 84 / 78; a warp with 32
   // columns a lane 84 / 96), then 32, gated 16, so that sums and scales, which cost the same for any number of columns, are spread
   // over more (16384 x 4096 to E4M3, 8 / 16 / 32 columns a thread: 88 / 81 / 76; gated 119 / 107 / 117, where 32 leave too few
-  // registers for other rows).
+  // registers for other rows; 4096 x 16384 gated, 32 / 64: 123 / 156).
   if (vecs <= 32) return launch_norm_as<T, TG, kGated, true, 1>(a, stream);
   if (vecs <= 128) return launch_norm_as<T, TG, kGated, false, 1>(a, stream);
   constexpr int kFew = kGated ? 2 : 4;
   if (vecs <= 512 * kFew) return launch_norm_as<T, TG, kGated, false, kFew>(a, stream);
+  if (vecs <= 512 * 4) return launch_norm_as<T, TG, kGated, false, 4>(a, stream);
   return launch_norm_as<T, TG, kGated, false, 8>(a, stream);
 }
 
