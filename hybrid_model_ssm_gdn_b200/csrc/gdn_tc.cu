@@ -66,7 +66,7 @@ struct GdnShared {
   unsigned char in[kStages][4][kHalf];  // k, q of columns 0..63, k, q of columns 64..127; then Y on its way out
   __nv_bfloat16 V[Q][kCols];
   unsigned char T[2][2][kHalf], M[2][3][kHalf];  // pieces; row = token j
-  unsigned char A[2][kHalf / 2];  // blocks of A below the diagonal, see a_row
+  unsigned char A[2][kHalf / 2];  // blocks of A below the diagonal, see store_a
   float diag[4][16 * 20 + 16];  // blocks of A on the diagonal, [column][row]
   Table tab[2];
   float alpha[Q], prefix[Q], tot[4];
@@ -427,8 +427,9 @@ __global__ void __launch_bounds__(kGdnThreads, 1)
     }
   }
   if (tid == 0) {
-    uint64_t *one[] = {&sh.full_kq[0], &sh.full_kq[1], &sh.full_kq[2], &sh.full_v, &sh.ks_done[0], &sh.ks_done[1], &sh.qs_done, &sh.u_done[0],
-                       &sh.u_done[1], &sh.d_done[0], &sh.d_done[1], &sh.y_done, &sh.g_done, &sh.drained[0], &sh.drained[1]};
+    uint64_t *one[] = {&sh.full_kq[0], &sh.full_kq[1], &sh.full_kq[2], &sh.full_v, &sh.ks_done[0], &sh.ks_done[1],
+                       &sh.qs_done, &sh.u_done[0], &sh.u_done[1], &sh.d_done[0], &sh.d_done[1], &sh.y_done, &sh.g_done,
+                       &sh.drained[0], &sh.drained[1]};
     for (uint64_t *b : one) mbar_init(b, 1);
     uint64_t *prep[] = {&sh.full_t[0], &sh.full_t[1], &sh.g_free};
     for (uint64_t *b : prep) mbar_init(b, 4);
@@ -439,7 +440,7 @@ __global__ void __launch_bounds__(kGdnThreads, 1)
     for (uint64_t &b : sh.free_t) mbar_init(&b, kChain + 1);
     for (uint64_t &b : sh.full_unit) mbar_init(&b, 1);
     for (uint64_t &b : sh.free_unit) mbar_init(&b, kUnitReaders);
-    sh.abort = sh.not_finite = 0;
+    sh.abort = sh.not_finite = sh.slot = 0;
     fence_barrier_init();
   }
   if (tid < 256) sh.first[tid >> 7][tid & 127] = 0x7fffffff;
@@ -693,7 +694,8 @@ __global__ void __launch_bounds__(kGdnThreads, 1)
     float alpha_next = 1.f, beta_next = 0.f;
     Unit unit;
     int c = 0;  // chunk of all units
-    for (int i = 0; next_unit(i, unit); ++i) {
+    // The four warps go on or stop together: they meet at barriers of their own, and a block may be given up between their looks.
+    for (int i = 0; !prep_sync_or(!next_unit(i, unit)); ++i) {
       const int ntok = unit.tokens;
       const float *ag = a.alpha + (size_t)unit.begin * a.H + unit.head, *bg = a.beta + (size_t)unit.begin * a.H + unit.head;
       auto fetch = [&](int first) {
