@@ -598,6 +598,7 @@ rssm_status rssm_gdn_scan(const rssm_config *cfg, int qk_heads, const rssm_promp
   rssm_status s = gdn_scan_validate(cfg, qk_heads, false);
   if (s == RSSM_OK) s = prompts_validate(pr, cfg->batch);
   if (s != RSSM_OK) return s;
+  if ((long long)pr->nseq * cfg->nheads > 0x7fffffffLL) return RSSM_ERR_SHAPE;  // heads of prompts are counted in an int
   if (!S || !aligned16(S) || !gdn_scan_pointers(pr, tok, y)) return RSSM_ERR_ARG;
   int sms = 0;
   s = sm_count(&sms);
@@ -614,6 +615,7 @@ rssm_status rssm_gdn_prefill(rssm_ctx *x, int qk_heads, const rssm_prompts *pr, 
   rssm_status s = gdn_scan_validate(&c, qk_heads, true);
   if (s == RSSM_OK) s = prompts_validate(pr, c.batch);
   if (s != RSSM_OK) return s;
+  if ((long long)pr->nseq * c.nheads > 0x7fffffffLL) return RSSM_ERR_SHAPE;
   if (!gdn_scan_pointers(pr, tok, y)) return RSSM_ERR_ARG;
   const bool converted = gdn_converted(c);
   if (converted) {

@@ -44,6 +44,7 @@ constexpr int kGdnThreads = 24 * 32;
 constexpr int kUnits = 4;                                     // that the loading warp is ahead at most
 constexpr int kUnitReaders = 23;                              // all warps but the one that hands them out
 constexpr int kByLength = 64;
+constexpr int kMostInTurn = 4096;
 constexpr float kMild = 1.f / 65536.f;
 
 // Factors of a chunk's tokens in either form.
@@ -1156,7 +1157,8 @@ cudaError_t launch_gdn_tc(const GdnScanArgs &s, const Prompts &pr, int num_sms, 
   // Units in turn save a block's start and its end and bring the next state closer; one a block is what the hardware hands out
   // as blocks finish, and 3 % faster in a long prompt (32 heads of 128 rows, us, in turn / one a block: 48 prompts of 64 tokens
   // 136 / 170, of 256 347 / 365, of 512 638 / 631; 16 of 256 142 / 144, of 1024 470 / 441; 4 of 64, fewer units than SMs, 28 / 24).
-  if (a.units > num_sms && pr.total <= 256LL * pr.nseq) return run(gdn_tc_kernel<true>, num_sms);
+  // Not with many thousands of prompts: one warp looks through all slots for each unit, and the others' waits for it are bounded.
+  if (a.units > num_sms && pr.total <= 256LL * pr.nseq && pr.nseq <= kMostInTurn) return run(gdn_tc_kernel<true>, num_sms);
   return run(gdn_tc_kernel<false>, a.units);
 }
 

@@ -63,6 +63,31 @@ def test_units_in_turn_give_what_each_gives_alone(cuda_ok, nseq, H, P):
         same(states[b], start[b])
 
 
+def test_thousands_of_prompts_most_of_them_empty(cuda_ok):
+    """5000 prompts (a block a head of each) and 4000 (in turn) with tokens in every 40th: states of the others become zero, or
+    stay where they resume."""
+    for nseq in (5000, 4000):
+        lens = [0] * nseq
+        for i in range(0, nseq, 40):
+            lens[i] = 640 + i % 7
+        offsets, some = packed(lens), list(range(0, nseq, 40))
+        total = offsets[-1]
+        assert 16 * nseq <= total <= 256 * nseq
+        d = make(nseq, BF, 647, 2, 1, 8, 1)
+        g = on_gpu(d, BF)
+        rows = torch.cat([torch.arange(lens[i]) for i in some]).cuda()
+        S = g["S"].expand(nseq, -1, -1, -1).clone()
+        resume = [(i // 3) % 2 for i in range(nseq)]
+        y = gdn_scan(S, *(g[k][rows] for k in TOK), idx(offsets), idx(list(range(nseq))[::-1]), idx(resume, torch.uint8),
+                     q_scale=SCALE)
+        for i in (some[0], some[1], some[63], some[-1]):
+            compare({**d, **{k: d[k][:lens[i]] for k in TOK}}, [0, lens[i]], None, [resume[i]],
+                    S[nseq - 1 - i:nseq - i].cpu().numpy(), y[offsets[i]:offsets[i + 1]].cpu().numpy())
+        for i in range(1, nseq, 197):
+            if lens[i] == 0:
+                same(S[nseq - 1 - i], g["S"][0] if resume[i] else torch.zeros_like(g["S"][0]))
+
+
 @pytest.mark.parametrize("lens,H", [((150, 250), 4), ((100,) * 45, 4)])
 def test_a_load_that_never_comes_times_out_and_the_context_recovers(cuda_ok, monkeypatch, lens, H):
     """Every wait of the chunk kernel is bounded: with the second chunk's load withheld (and the bound shortened to about a

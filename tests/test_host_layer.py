@@ -44,6 +44,7 @@ def test_gdn_scan_refusals(lib):
     assert scan(pr=dict(offsets=None)) == ARG
     for bad in (dict(nseq=0), dict(nseq=5), dict(total=-1), dict(total=2 ** 30 + 1)):
         assert scan(pr=bad) == SHAPE, bad
+    assert scan(c=cfg(batch=2 ** 20, nheads=4096), pr=dict(nseq=2 ** 20)) == SHAPE
     assert scan(tok=None) == ARG
     for name in ("q", "k", "v", "alpha", "beta"):
         assert scan(tok=abi.Tokens(**{**dict(q=16, k=16, v=16, alpha=16, beta=16), name: None})) == ARG
