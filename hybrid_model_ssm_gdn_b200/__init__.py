@@ -561,7 +561,8 @@ def _row_step(t, name, shape, lead, inner, width, dtype, device):
     return _apart(t, name, lead, width, inner, dtype, device)
 
 
-# What follows from sizes and types alone is worked out once for each (a decode step's calls are as long as their checks).
+# What follows from sizes, types and numbers alone is worked out once for each (a decode step's calls are as long as their
+# checks).  Callers pass plain numbers: a tensor would be looked up by its identity, whatever it holds by then.
 @functools.lru_cache(maxsize=1024)
 def _inputs_plan(q_shape, a_shape, dtype, expand):
     """(leading sizes, rows, heads of v, of q, of the outputs, shape of q; shapes and strides of the gates and vectors out)"""
@@ -661,7 +662,8 @@ def add_rmsnorm(x, weight, residual=None, eps=1e-6, offset=0.0, out_dtype=None, 
     device = _device(x, "x")
     stride = _row_step(x, "x", shape, lead, (n,), n, dtype, device)
     r_stride = 0 if residual is None else _row_step(residual, "residual", shape, lead, (n,), n, dtype, device)
-    cfg, plan, w_shape = _norm_plan(shape, dtype, weight.shape, weight.dtype, 0, eps, offset, out_dtype or dtype, scale, 0, 0)
+    cfg, plan, w_shape = _norm_plan(shape, dtype, weight.shape, weight.dtype, 0, float(eps), float(offset), out_dtype or dtype,
+                                    scale, 0, 0)
     y, s, got = _norm_out(x, plan, out, device)
     abi.check(abi.load().rssm_add_rmsnorm(cfg, x.data_ptr(), stride, _addr(residual), r_stride,
                                           _arr(weight, weight.dtype, "weight", w_shape, device), y.data_ptr(), _addr(s),
@@ -679,8 +681,8 @@ def gated_rmsnorm(y, gate, weight, group=None, eps=1e-6, offset=0.0, norm_first=
     dtype, gate_dtype = _in_dtype(y, "y"), _in_dtype(gate, "gate")
     stride = _row_step(y, "y", shape, lead, (n,), n, dtype, device)
     g_stride = _row_step(gate, "gate", shape, lead, (n,), n, gate_dtype, device)
-    cfg, plan, w_shape = _norm_plan(shape, dtype, weight.shape, weight.dtype, group, eps, offset, out_dtype or gate_dtype, scale,
-                                    _DT[gate_dtype], bool(norm_first))
+    cfg, plan, w_shape = _norm_plan(shape, dtype, weight.shape, weight.dtype, group and int(group), float(eps), float(offset),
+                                    out_dtype or gate_dtype, scale, _DT[gate_dtype], bool(norm_first))
     o, s, got = _norm_out(y, plan, out, device)
     abi.check(abi.load().rssm_gated_rmsnorm(cfg, y.data_ptr(), stride, gate.data_ptr(), g_stride,
                                             _arr(weight, weight.dtype, "weight", w_shape, device), o.data_ptr(), _addr(s),
