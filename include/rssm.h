@@ -245,7 +245,8 @@ rssm_status rssm_gdn_scan_workspace(const rssm_config *cfg, int total, int nseq,
  *   work as for rssm_mamba2_scan.
  * From a value of v that is not finite on, its row's outputs in that prompt are not finite, nor its row of the state; from a
  * value of k, alpha or beta on, all of that head's; a value of q touches its own token's outputs alone.
- * alpha is any finite number; decays are products of it, so values beyond 1 can overflow as they do token by token. */
+ * alpha is any finite number; decays are products of it, so values beyond 1 can overflow as they do token by token (and from
+ * there on like values that are not finite).  With bf16 inputs, rows of v and S below about 1e-25 lose precision. */
 rssm_status rssm_gdn_scan(const rssm_config *cfg, int qk_heads, const rssm_prompts *pr, const rssm_tokens *tok, float *S,
                           float *y, void *work, size_t work_bytes, rssm_stream stream);
 
