@@ -16,9 +16,11 @@
 // within and between blocks of 16, never as a quotient, so that decays to nothing stay what they are; such chunks take 6 % more
 // (8191 tokens of 32 heads 655 -> 695 us).
 //
-// Precision.  q, k, v are bf16; S, R, U and M go into the products as three bf16 pieces each (24 bits), T as two, accumulated
-// in fp32: 7e-7 to 9e-7 of a norm off in all, against 5e-6 with two pieces of everything.  (I + A)^-1 is formed in fp32 on the
-// diagonal blocks of 16 and from there by products of blocks in two pieces with mma.sync.
+// Precision.  q, k, v are bf16; S, R, U, M and T go into the products as three bf16 pieces each (24 bits), accumulated in
+// fp32.  (I + A)^-1 is formed in fp32 on the diagonal blocks of 16 and from there by products of blocks in three pieces with
+// mma.sync.  512 tokens are 2e-7 (decays of 2^-60 a chunk) to 5.5e-7 (2^-1) of a norm off, whether keys are independent or alike
+// (mean cosines of 0 to 0.95, beta 0.5 to 1).  With T and the blocks' products in two pieces it was 1.3e-6 for independent
+// keys and 1.3e-5 for keys alike, for 3 to 9 % less time.
 //
 // What bounds it: the way of one chunk through S -> K S^T -> R -> U -> S, each step a product of 0.4 to 1 us and a pass of its
 // results through registers into pieces, 5.4 us a chunk in all with the preparation of the next chunk beside it (0.70 ms for
@@ -36,6 +38,7 @@ namespace {
 
 constexpr int Q = kGdnChunk;
 constexpr int kHalf = Q * 128;  // bytes of a tile: 64 rows of 64 bf16
+constexpr int kStepA = 52;      // floats from row to row of A: eight rows' 16-byte stores meet 32 different banks
 constexpr int kStages = 3;      // of q and k: one chunk in the chain of the state, one in front of it, one on its way
 // Tensor memory.  K S^T, U and the increment of S are cut where they lie: a warp's 16 (32) columns of results become 24 (48)
 // of pieces in a range of its own, so results stand in the middle of the two ranges that they share.
@@ -68,9 +71,9 @@ struct Unit {
 struct GdnShared {
   unsigned char in[kStages][4][kHalf];  // k, q of columns 0..63, k, q of columns 64..127; then Y on its way out
   __nv_bfloat16 V[Q][kCols];
-  unsigned char T[2][2][kHalf], M[2][3][kHalf];  // pieces; row = token j
-  unsigned char A[2][kHalf / 2];  // blocks of A below the diagonal, see store_a
-  float diag[4][16 * 20 + 16];  // blocks of A on the diagonal, [column][row]
+  unsigned char T[2][3][kHalf], M[2][3][kHalf];  // pieces; row = token j
+  float A[32 * kStepA];           // blocks of A below the diagonal, see store_a
+  __align__(16) float diag[4][16 * 20 + 16];  // blocks of A on the diagonal, [column][row]; then X, see block_x
   Table tab[2];
   float alpha[Q], prefix[Q], tot[4];
   int first[2][128];  // per row of the state, the first token of the unit (odd ones, even ones) whose v is not finite
@@ -145,52 +148,71 @@ __device__ __forceinline__ unsigned char *at_tile(unsigned char *tile, int row, 
   return tile + row * 128 + (((col >> 3) ^ (row & 7)) << 4);
 }
 
-// operands of m16n8k16 from a block of 16 x 16 of a tile at (row, col): as the left operand, as the left one transposed, and
-// as the right one of two tiles of 8 columns whose columns are the block's rows
-__device__ __forceinline__ void load_left(unsigned char *tile, int row, int col, int lane, uint32_t (&f)[4]) {
-  ldmatrix_x4(at_tile(tile, row + (lane & 15), col + 8 * (lane >> 4)), f[0], f[1], f[2], f[3]);
+// operands of m16n8k16: a block of 16 x 16 of a tile at (row, col) as the left operand, and as the left one transposed, in three
+// pieces
+__device__ __forceinline__ void load_left(unsigned char (*T)[kHalf], int row, int col, int lane, uint32_t (&f)[3][4]) {
+#pragma unroll
+  for (int p = 0; p < 3; ++p)
+    ldmatrix_x4(at_tile(T[p], row + (lane & 15), col + 8 * (lane >> 4)), f[p][0], f[p][1], f[p][2], f[p][3]);
 }
-__device__ __forceinline__ void load_left_t(unsigned char *tile, int row, int col, int lane, uint32_t (&f)[4]) {
-  ldmatrix_x4_trans(at_tile(tile, row + (lane & 7) + 8 * (lane >> 4), col + (lane & 8)), f[0], f[1], f[2], f[3]);
+__device__ __forceinline__ void load_left_t(unsigned char (*T)[kHalf], int row, int col, int lane, uint32_t (&f)[3][4]) {
+#pragma unroll
+  for (int p = 0; p < 3; ++p)
+    ldmatrix_x4_trans(at_tile(T[p], row + (lane & 7) + 8 * (lane >> 4), col + (lane & 8)), f[p][0], f[p][1], f[p][2], f[p][3]);
 }
-__device__ __forceinline__ void load_right(unsigned char *tile, int row, int col, int lane, uint32_t (&f)[4]) {
-  ldmatrix_x4(at_tile(tile, row + (lane & 7) + 8 * (lane >> 4), col + (lane & 8)), f[0], f[1], f[2], f[3]);
-}
-__device__ __forceinline__ void mma(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
-  mma_16816(d, a[0], a[1], a[2], a[3], b0, b1);
+// d += a b for 16 columns, the right operand words of fp32 values that are cut here: the products above 2^-24 of the result, as
+// four sums of three that do not wait for one another
+__device__ __forceinline__ void mma3(float (&d)[2][4], const uint32_t (&a)[3][4], const f2 (&b)[2][2]) {
+  uint32_t p[2][3][2];
+  float small[2][4] = {};
+#pragma unroll
+  for (int n = 0; n < 2; ++n)
+#pragma unroll
+    for (int k = 0; k < 2; ++k) cut3(b[n][k], p[n][0][k], p[n][1][k], p[n][2][k]);
+  auto both = [&](float (&to)[2][4], int i, int k) {
+#pragma unroll
+    for (int n = 0; n < 2; ++n) mma_16816(to[n], a[i][0], a[i][1], a[i][2], a[i][3], p[n][k][0], p[n][k][1]);
+  };
+  both(small, 2, 0);
+  both(d, 1, 0);
+  both(small, 0, 2);
+  both(d, 0, 1);
+  both(small, 1, 1);
+  both(d, 0, 0);
+#pragma unroll
+  for (int n = 0; n < 2; ++n)
+#pragma unroll
+    for (int i = 0; i < 4; ++i) d[n][i] += small[n][i];
 }
 
-// X^T (+)= Z^T B^T for blocks of 16 x 16, Z at (zr, zc) of T and B at (br, bc) of A, in two pieces each; x[n]: columns 8 n ..
-__device__ __forceinline__ void block_x(unsigned char (*T)[kHalf], int zr, int zc, unsigned char (*A)[kHalf / 2], int br, int bc,
-                                        int lane, float (&x)[2][4]) {
-  uint32_t zh[4], zl[4], bh[4], bl[4];
-  load_left_t(T[0], zr, zc, lane, zh);
-  load_left_t(T[1], zr, zc, lane, zl);
-  load_right(A[0], br, bc, lane, bh);
-  load_right(A[1], br, bc, lane, bl);
+// X^T (+)= Z^T B^T for blocks of 16 x 16, Z at (zr, zc) of T and B at (br, bc) of A; x[n]: columns 8 n ..
+__device__ __forceinline__ void block_x(unsigned char (*T)[kHalf], int zr, int zc, const float *A, int br, int bc, int lane,
+                                        float (&x)[2][4]) {
+  uint32_t z[3][4];
+  f2 b[2][2];
+  load_left_t(T, zr, zc, lane, z);
 #pragma unroll
-  for (int n = 0; n < 2; ++n) {
-    mma(x[n], zh, bl[2 * n], bl[2 * n + 1]);
-    mma(x[n], zl, bh[2 * n], bh[2 * n + 1]);
-    mma(x[n], zh, bh[2 * n], bh[2 * n + 1]);
-  }
+  for (int n = 0; n < 2; ++n)  // columns of B^T are rows of B
+#pragma unroll
+    for (int k = 0; k < 2; ++k) {
+      const float2 v = *reinterpret_cast<const float2 *>(A + (br + 8 * n + (lane >> 2)) * kStepA + bc + 8 * k + 2 * (lane & 3));
+      b[n][k] = pack2(v.x, v.y);
+    }
+  mma3(x, z, b);
 }
-// T block (+)= W X for W at (wr, wc) of T and X from block_x
-__device__ __forceinline__ void block_t(unsigned char (*T)[kHalf], int wr, int wc, int lane, const float (&x)[2][4],
+// the accumulators of X^T as the right operand of a product with X
+__device__ __forceinline__ void turn_x(const float (&x)[2][4], f2 (&b)[2][2]) {
+#pragma unroll
+  for (int n = 0; n < 2; ++n)
+#pragma unroll
+    for (int k = 0; k < 2; ++k) b[n][k] = pack2(x[k][2 * n], x[k][2 * n + 1]);
+}
+// T block (+)= W X for W at (wr, wc) of T
+__device__ __forceinline__ void block_t(unsigned char (*T)[kHalf], int wr, int wc, int lane, const f2 (&x)[2][2],
                                         float (&t)[2][4]) {
-  uint32_t wh[4], wl[4], h[2][2], l[2][2];
-  load_left(T[0], wr, wc, lane, wh);
-  load_left(T[1], wr, wc, lane, wl);
-#pragma unroll
-  for (int n = 0; n < 2; ++n)  // the accumulators of X^T are the right operand of W X
-#pragma unroll
-    for (int k = 0; k < 2; ++k) split_bf16x2(x[k][2 * n], x[k][2 * n + 1], h[n][k], l[n][k]);
-#pragma unroll
-  for (int n = 0; n < 2; ++n) {
-    mma(t[n], wh, l[n][0], l[n][1]);
-    mma(t[n], wl, h[n][0], h[n][1]);
-    mma(t[n], wh, h[n][0], h[n][1]);
-  }
+  uint32_t w[3][4];
+  load_left(T, wr, wc, lane, w);
+  mma3(t, w, x);
 }
 __device__ __forceinline__ void store_block(unsigned char (*T)[kHalf], int row, int col, int lane, const float (&t)[2][4]) {
   const int g = lane >> 2, p = 2 * (lane & 3);
@@ -198,10 +220,10 @@ __device__ __forceinline__ void store_block(unsigned char (*T)[kHalf], int row, 
   for (int n = 0; n < 2; ++n)
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
-      uint32_t h, l;
-      split_bf16x2(-t[n][2 * i], -t[n][2 * i + 1], h, l);
-      *reinterpret_cast<uint32_t *>(at_tile(T[0], row + g + 8 * i, col + 8 * n) + 2 * p) = h;
-      *reinterpret_cast<uint32_t *>(at_tile(T[1], row + g + 8 * i, col + 8 * n) + 2 * p) = l;
+      uint32_t c[3];
+      cut3(pack2(-t[n][2 * i], -t[n][2 * i + 1]), c[0], c[1], c[2]);
+#pragma unroll
+      for (int k = 0; k < 3; ++k) *reinterpret_cast<uint32_t *>(at_tile(T[k], row + g + 8 * i, col + 8 * n) + 2 * p) = c[k];
     }
 }
 
@@ -253,21 +275,17 @@ struct PrepRow {
   float f[4];        // product of alpha from the end of an earlier block to this token
 };
 
-// Where A is held, in tiles of 32 rows: the block of 32 x 32 below the diagonal at columns 0..31, and the two of 16 x 16
-// within the diagonal blocks of 32 at columns 32..47.
+// Where A is held, in 32 rows: the block of 32 x 32 below the diagonal at columns 0..31, and the two of 16 x 16 within the
+// diagonal blocks of 32 at columns 32..47.
 __device__ __forceinline__ void store_a(GdnShared &sh, const PrepRow &r, int blk, const f2 (&v)[8]) {
   const int row = blk < 2 * r.upper ? r.j - 32 : 16 * r.upper + r.jj, col = blk < 2 * r.upper ? 16 * blk : 32;
+  if (blk >= r.bj) return;
 #pragma unroll
-  for (int i = 0; i < 2; ++i) {
-    uint4 p0, p1;
-    cut2(v[4 * i], p0.x, p1.x);
-    cut2(v[4 * i + 1], p0.y, p1.y);
-    cut2(v[4 * i + 2], p0.z, p1.z);
-    cut2(v[4 * i + 3], p0.w, p1.w);
-    if (blk < r.bj) {
-      *reinterpret_cast<uint4 *>(at_tile(sh.A[0], row, col + 8 * i)) = p0;
-      *reinterpret_cast<uint4 *>(at_tile(sh.A[1], row, col + 8 * i)) = p1;
-    }
+  for (int i = 0; i < 4; ++i) {
+    float4 e;
+    unpack2(v[2 * i], e.x, e.y);
+    unpack2(v[2 * i + 1], e.z, e.w);
+    *reinterpret_cast<float4 *>(&sh.A[row * kStepA + col + 4 * i]) = e;
   }
 }
 __device__ __forceinline__ void store_m(unsigned char (*M)[kHalf], const PrepRow &r, int blk, const f2 (&v)[8]) {
@@ -411,6 +429,26 @@ __device__ __noinline__ int prep_careful(GdnShared &sh, PrepRow r, bool odd, boo
     for (int blk = 0; blk < r.bj; ++blk) store_a(sh, r, blk, zero);
   }
   return bad;
+}
+
+// Of 16 tokens of U from `first` on (of the unit's from `at` on), what grew past fp32's range becomes 0 and its row ends there: it
+// must not meet the zeros that M has for earlier tokens.  A whole warp.
+__device__ __noinline__ void clear_u(GdnShared &sh, uint32_t taddr, int first, int tokens, int at, int *bad_from) {
+  uint32_t x[16];
+  tm_ld16(taddr, x);
+  tm_wait_ld();
+#pragma unroll
+  for (int i = 0; i < 16; ++i)
+    if (!(fabsf(__uint_as_float(x[i])) < __int_as_float(0x7f800000))) {
+      if (first + i < tokens) {
+        atomicMin(bad_from, at + first + i);
+        *(volatile int *)&sh.not_finite = 1;
+      }
+      x[i] = 0;
+    }
+  __syncwarp();
+  tm_st16(taddr, x);
+  tm_wait_st();
 }
 
 // kMany: the block takes units in turn, otherwise one.
@@ -596,7 +634,7 @@ __global__ void __launch_bounds__(kGdnThreads, 1)
         for (int left = __shfl_sync(0xffffffffu, unit.tokens, 0); left > 0; left -= Q, ++c) {
           const int b = c & 1;
           const uint64_t k0 = wide_desc(dk + s * kStage), q0 = k0 + (kHalf >> 4), kn = wide_desc(dkn + s * kStage);
-          const uint64_t T = wide_desc(dT + b * 2 * kPiece), M = wide_desc(dM + b * 3 * kPiece);
+          const uint64_t T = wide_desc(dT + b * 3 * kPiece), M = wide_desc(dM + b * 3 * kPiece);
           wait.warp(sh.full_kq[s], turn);
 #pragma unroll
           for (int part = 0; part < 2; ++part) {  // K S^T: halves of S as they come, the last ones by halves of the tokens
@@ -638,7 +676,8 @@ __global__ void __launch_bounds__(kGdnThreads, 1)
               for (int k = 0; k < 2 * half + 2; ++k) {  // pieces of R by pieces of T; the others are below 2^-24
                 const uint32_t r = td + kColR + 24 * k, u = td + kColU + 48 * half + 8;
                 const uint64_t t = T + half * kRows + 2 * k;
-                one_ts(u, r + 8, t + kPiece, half_q, k > 0);
+                one_ts(u, r, t + 2 * kPiece, half_q, k > 0);
+                one_ts(u, r + 8, t + kPiece, half_q, true);
                 one_ts(u, r + 16, t, half_q, true);
                 one_ts(u, r, t + kPiece, half_q, true);
                 one_ts(u, r + 8, t, half_q, true);
@@ -705,7 +744,7 @@ __global__ void __launch_bounds__(kGdnThreads, 1)
     r.gram = tm + ((uint32_t)(32 * pw) << 16) + kColG;
     const int j = r.j, bj = r.bj, jj = r.jj;
     const bool of_k = r.of_k;
-    for (int i = p; i < 2 * 2 * kHalf / 16; i += 128)  // blocks above the diagonal stay zero
+    for (int i = p; i < 2 * 3 * kHalf / 16; i += 128)  // blocks above the diagonal stay zero
       reinterpret_cast<uint4 *>(sh.T[0][0])[i] = make_uint4(0, 0, 0, 0);
     for (int i = p; i < 2 * 3 * kHalf / 16; i += 128) reinterpret_cast<uint4 *>(sh.M[0][0])[i] = make_uint4(0, 0, 0, 0);
     float alpha_next = 1.f, beta_next = 0.f;
@@ -813,35 +852,49 @@ __global__ void __launch_bounds__(kGdnThreads, 1)
               if (l + 3 > i) t[l + 3] = fmaf(-v.w, t[i], t[l + 3]);
             }
           }
-          const int lo = lane >> 4;  // lanes 0..15 write the first pieces, the others the second
+          const int lo = lane >> 4;  // lanes 0..15 write the first pieces, the others the second; each the third of 8 rows
+          auto put_t = [&](int piece, int i, __nv_bfloat16 v) {
+            *reinterpret_cast<__nv_bfloat16 *>(at_tile(T[piece], 16 * pw + i, 16 * pw + (col & 8)) + 2 * (col & 7)) = v;
+          };
+          auto left_of = [](float v) { return v - __bfloat162float(__float2bfloat16_rn(v)); };
 #pragma unroll
-          for (int i = 0; i < 16; ++i) {
-            const __nv_bfloat16 hi = __float2bfloat16_rn(t[i]);
-            const __nv_bfloat16 v = lo ? __float2bfloat16_rn(t[i] - __bfloat162float(hi)) : hi;
-            *reinterpret_cast<__nv_bfloat16 *>(at_tile(T[lo], 16 * pw + i, 16 * pw + (col & 8)) + 2 * (col & 7)) = v;
-          }
+          for (int i = 0; i < 16; ++i) put_t(lo, i, __float2bfloat16_rn(lo ? left_of(t[i]) : t[i]));
+#pragma unroll
+          for (int i = 0; i < 8; ++i) put_t(2, 8 * lo + i, __float2bfloat16_rn(left_of(left_of(lo ? t[8 + i] : t[i]))));
         }
         prep_sync();
         if (!(pw & 1)) {  // T10 = -T11 A10 T00 in both blocks of 32
           const int r0 = 16 * pw;
           float x[2][4] = {}, t[2][4] = {};
+          f2 right[2][2];
           block_x(T, r0, r0, sh.A, r0 >> 1, 32, lane, x);
-          block_t(T, r0 + 16, r0 + 16, lane, x, t);
+          turn_x(x, right);
+          block_t(T, r0 + 16, r0 + 16, lane, right, t);
           store_block(T, r0 + 16, r0, lane, t);
         }
         prep_sync();
-        {  // the same of the whole: block (32 + 16 to, 16 from)
+        {  // the same of the whole: rows 16 l of X = A T00 at columns 16 from, one a warp, and block (32 + 16 to, 16 from) of T
           const int to = pw >> 1, from = pw & 1;
-          float t[2][4] = {}, x[2][2][4] = {};
+          float t[2][4] = {}, x[2][4] = {};
+          f2 right[2][2];
+          if (from == 0) block_x(T, 0, 0, sh.A, 16 * to, 0, lane, x);
+          block_x(T, 16, 16 * from, sh.A, 16 * to, 16, lane, x);
+          turn_x(x, right);
+          ulonglong2 *const held = reinterpret_cast<ulonglong2 *>(sh.diag[0]);  // the blocks on the diagonal are done with
+#pragma unroll
+          for (int n = 0; n < 2; ++n) held[(2 * pw + n) * 32 + lane] = make_ulonglong2(right[n][0].v, right[n][1].v);
+          prep_sync();
 #pragma unroll
           for (int l = 0; l < 2; ++l)
             if (l <= to) {
-              if (from == 0) block_x(T, 0, 0, sh.A, 16 * l, 0, lane, x[l]);
-              block_x(T, 16, 16 * from, sh.A, 16 * l, 16, lane, x[l]);
-            }
 #pragma unroll
-          for (int l = 0; l < 2; ++l)
-            if (l <= to) block_t(T, 32 + 16 * to, 32 + 16 * l, lane, x[l], t);
+              for (int n = 0; n < 2; ++n) {
+                const ulonglong2 v = held[(2 * (2 * l + from) + n) * 32 + lane];
+                right[n][0].v = v.x;
+                right[n][1].v = v.y;
+              }
+              block_t(T, 32 + 16 * to, 32 + 16 * l, lane, right, t);
+            }
           store_block(T, 32 + 16 * to, 16 * from, lane, t);
         }
         fence_async_smem();
@@ -1019,22 +1072,15 @@ __global__ void __launch_bounds__(kGdnThreads, 1)
           tm_fence_after();
           tm_ld16(here + kColU + 48 * part + 8 + 16 * ww, x);
           tm_wait_ld();
-          f2 seen = pack2(0.f, 0.f);
-          const f2 zero = seen;
+          f2 seen[2] = {};
+          const f2 zero = seen[0];
 #pragma unroll
-          for (int i = 0; i < 8; ++i) seen = fma2(pack2(x[2 * i], x[2 * i + 1]), zero, seen);
-          if (not_zero(seen)) {  // what grew past fp32 must not meet the zeros of earlier tokens' M
-#pragma unroll
-            for (int i = 0; i < 16; ++i)
-              if (!(fabsf(__uint_as_float(x[i])) < __int_as_float(0x7f800000))) {
-                if (16 * w + i < tokens) {
-                  atomicMin(bad_from, at + 16 * w + i);
-                  *(volatile int *)&sh.not_finite = 1;
-                }
-                x[i] = 0;
-              }
+          for (int i = 0; i < 8; ++i) seen[i & 1] = fma2(pack2(x[2 * i], x[2 * i + 1]), zero, seen[i & 1]);
+          if (__any_sync(0xffffffffu, not_zero(fma2(seen[0], zero, seen[1])))) {
+            clear_u(sh, here + kColU + 48 * part + 8 + 16 * ww, 16 * w, tokens, at, bad_from);
+            tm_ld16(here + kColU + 48 * part + 8 + 16 * ww, x);
+            tm_wait_ld();
           }
-          __syncwarp();
           if (!tab.mild) {
             if (part == 0) wait(sh.u_done[1], c);  // R of these tokens goes into U of the others
 #pragma unroll
