@@ -206,24 +206,37 @@ __device__ __forceinline__ uint2 e4m3_codes(const float (&v)[8], float by) {
 // the scale that maps `most` to 448 (a NaN stays one; not below the normal numbers, so that its inverse is finite)
 __device__ __forceinline__ float scale_of(float most) { return max_nan(most * (1.f / 448.f), 1.17549435e-38f); }
 
-// h silu(gate) = h z / (1 + e^-z).  e^-z = 2^(-z log2 e) takes the argument's rounding along, up to |z| 2^-23 of itself (1e-6
-// at z = -8, where silu is -3e-3; it fades for positive z); 2^x and the reciprocal add 2 units in the last place.  The
-// library's expf and __fdividef take 8 instructions a value more, of which the kernel has 30 in all: 100 us against 87 at 16384 x
-// 4096.  Past 2^126 the reciprocal is 0.
-template <typename T>
+// h silu(gate) = h z / (1 + e^-z).  For bf16 gates and outputs of 16 or 8 bits e^-z = 2^(-z log2 e) takes the argument's rounding
+// along, up to |z| 2^-23 of itself (1e-6 at z = -8, where silu is -3e-3; it fades for positive z); 2^x and the reciprocal add
+// 2 units in the last place.  The library's expf and __fdividef take 8 instructions a value more, of which the kernel has 30 in
+// all: 100 us against 87 at 16384 x 4096.  Past e^-z = 2^126 (z < -87.3) the reciprocal is 0, where silu is below 2^-119.
+// Otherwise (kFine) to within 2^-20 of the value down to its last bits: with h = 2^(-|z| log2 e / 2), whose argument's rounding is
+// given back to first order, silu is z / (1 + h^2) for z > 0 and z h^2 / (1 + h^2) for z < 0, which stays in the normal range as
+// long as the result has bits.
+template <bool kFine, typename T>
 __device__ __forceinline__ void times_silu(const Raw8<T> &gate, float (&h)[8]) {
+  constexpr float kL = 1.4426950408889634f, kRest = (float)(1.4426950408889634 - (double)kL), kLn2 = 0.69314718f;
   float z[8];
   gate.wide(z);
 #pragma unroll
   for (int j = 0; j < 8; ++j) {
     float e, r;
-    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e) : "f"(z[j] * -1.442695041f));
-    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(1.f + e));
-    h[j] *= z[j] * r;
+    if constexpr (kFine) {
+      const float a = fminf(fabsf(z[j]), 1e6f), t = a * (-0.5f * kL);
+      asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e) : "f"(t));
+      e = fmaf(e * kLn2, fmaf(a, -0.5f * kRest, fmaf(a, -0.5f * kL, -t)), e);
+      asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(fmaf(e, e, 1.f)));
+      const float q = z[j] * r;
+      h[j] *= z[j] < 0.f ? q * e * e : q;
+    } else {
+      asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e) : "f"(z[j] * -kL));
+      asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(1.f + e));
+      h[j] *= z[j] * r;
+    }
   }
 }
 
-template <typename T, typename TG, bool kGated, bool kWarp, int NV>
+template <typename T, typename TG, bool kGated, bool kFine, bool kWarp, int NV>
 __global__ void __launch_bounds__(kWarp ? 256 : 512) norm_kernel(NormArgs a) {
   __shared__ NormShared sh;
   extern __shared__ float parts[];  // groups that are neither the row nor within a warp: sums of 8 columns, sums of groups
@@ -247,7 +260,7 @@ __global__ void __launch_bounds__(kWarp ? 256 : 512) norm_kernel(NormArgs a) {
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
       in[i].wide(h[i]);
-      if (!a.norm_first) times_silu(gate[i], h[i]);
+      if (!a.norm_first) times_silu<kFine>(gate[i], h[i]);
     }
   } else if (a.residual) {
     T *residual = static_cast<T *>(a.residual) + row * a.stride_residual;
@@ -325,7 +338,7 @@ __global__ void __launch_bounds__(kWarp ? 256 : 512) norm_kernel(NormArgs a) {
     weight[i].wide(a.weight_dtype, w);
 #pragma unroll
     for (int j = 0; j < 8; ++j) h[i][j] = h[i][j] * sq[i] * (a.offset + w[j]);
-    if (kGated && a.norm_first) times_silu(gate[i], h[i]);
+    if (kGated && a.norm_first) times_silu<kFine>(gate[i], h[i]);
   }
   if (a.scale == RSSM_SCALE_NONE) {
 #pragma unroll
@@ -368,17 +381,17 @@ __global__ void __launch_bounds__(kWarp ? 256 : 512) norm_kernel(NormArgs a) {
   }
 }
 
-template <typename T, typename TG, bool kGated, bool kWarp, int NV>
+template <typename T, typename TG, bool kGated, bool kFine, bool kWarp, int NV>
 cudaError_t launch_norm_as(const NormArgs &a, cudaStream_t stream) {
   const int vecs = a.columns >> 3, threads = kWarp ? 256 : ((vecs + NV - 1) / NV + 31) / 32 * 32;
   const bool general = a.group != a.columns && (a.group > 256 || (a.group & (a.group - 1)));
   const size_t smem = general ? (size_t)(kWarp ? 8 : 1) * 2 * vecs * 4 : 0;
   const unsigned grid = kWarp ? (unsigned)((a.rows + 7) / 8) : (unsigned)a.rows;
-  norm_kernel<T, TG, kGated, kWarp, NV><<<grid, threads, smem, stream>>>(a);
+  norm_kernel<T, TG, kGated, kFine, kWarp, NV><<<grid, threads, smem, stream>>>(a);
   return cudaGetLastError();
 }
 
-template <typename T, typename TG, bool kGated>
+template <typename T, typename TG, bool kGated, bool kFine>
 cudaError_t launch_norm_type(const NormArgs &a, cudaStream_t stream) {
   const int vecs = a.columns >> 3;
   // Rows of up to 256 columns: a warp each (bf16 with a residual / gated, us: 131072 x 128 37 / 45, as blocks 74 / 74; 65536 x 256
@@ -386,12 +399,12 @@ cudaError_t launch_norm_type(const NormArgs &a, cudaStream_t stream) {
   // columns a lane 84 / 96), then 32, gated 16, so that sums and scales, which cost the same for any number of columns, are spread
   // over more (16384 x 4096 to E4M3, 8 / 16 / 32 columns a thread: 88 / 81 / 76; gated 119 / 107 / 117, where 32 leave too few
   // registers for other rows; 4096 x 16384 gated, 32 / 64: 123 / 156).
-  if (vecs <= 32) return launch_norm_as<T, TG, kGated, true, 1>(a, stream);
-  if (vecs <= 128) return launch_norm_as<T, TG, kGated, false, 1>(a, stream);
+  if (vecs <= 32) return launch_norm_as<T, TG, kGated, kFine, true, 1>(a, stream);
+  if (vecs <= 128) return launch_norm_as<T, TG, kGated, kFine, false, 1>(a, stream);
   constexpr int kFew = kGated ? 2 : 4;
-  if (vecs <= 512 * kFew) return launch_norm_as<T, TG, kGated, false, kFew>(a, stream);
-  if (vecs <= 512 * 4) return launch_norm_as<T, TG, kGated, false, 4>(a, stream);
-  return launch_norm_as<T, TG, kGated, false, 8>(a, stream);
+  if (vecs <= 512 * kFew) return launch_norm_as<T, TG, kGated, kFine, false, kFew>(a, stream);
+  if (vecs <= 512 * 4) return launch_norm_as<T, TG, kGated, kFine, false, 4>(a, stream);
+  return launch_norm_as<T, TG, kGated, kFine, false, 8>(a, stream);
 }
 
 }  // namespace
@@ -409,14 +422,17 @@ cudaError_t launch_gdn_inputs(const GdnInputsArgs &args, int esz, int num_sms, c
   return cudaGetLastError();
 }
 
-cudaError_t launch_norm(const NormArgs &a, bool gated, cudaStream_t stream) {
+template <typename T>
+cudaError_t launch_norm_in(const NormArgs &a, bool gated, cudaStream_t stream) {
   using bf16 = __nv_bfloat16;
-  if (a.x_dtype == RSSM_BF16) {
-    if (!gated) return launch_norm_type<bf16, bf16, false>(a, stream);
-    return a.gate_dtype == RSSM_BF16 ? launch_norm_type<bf16, bf16, true>(a, stream) : launch_norm_type<bf16, float, true>(a, stream);
-  }
-  if (!gated) return launch_norm_type<float, float, false>(a, stream);
-  return a.gate_dtype == RSSM_BF16 ? launch_norm_type<float, bf16, true>(a, stream) : launch_norm_type<float, float, true>(a, stream);
+  if (!gated) return launch_norm_type<T, T, false, false>(a, stream);
+  if (a.gate_dtype != RSSM_BF16) return launch_norm_type<T, float, true, true>(a, stream);
+  if (a.scale == RSSM_SCALE_NONE && a.out_dtype != RSSM_BF16) return launch_norm_type<T, bf16, true, true>(a, stream);
+  return launch_norm_type<T, bf16, true, false>(a, stream);
+}
+
+cudaError_t launch_norm(const NormArgs &a, bool gated, cudaStream_t stream) {
+  return a.x_dtype == RSSM_BF16 ? launch_norm_in<__nv_bfloat16>(a, gated, stream) : launch_norm_in<float>(a, gated, stream);
 }
 
 }  // namespace rssm

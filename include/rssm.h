@@ -337,7 +337,8 @@ typedef struct {
 rssm_status rssm_add_rmsnorm(const rssm_norm_config *cfg, const void *x, long long x_stride, void *residual,
                              long long residual_stride, const void *weight, void *out, float *scales, rssm_stream stream);
 
-/* Behind a layer: with s = gate / (1 + exp(-gate)), the norm of x times s (norm_first), or the norm of (x s). */
+/* Behind a layer: with s = gate / (1 + exp(-gate)), the norm of x times s (norm_first), or the norm of (x s).  With bf16 gates
+ * and outputs of 16 or 8 bits, s below 2^-119 (gate < -87.3) may be 0; otherwise it keeps fp32's precision down to its last bits. */
 rssm_status rssm_gated_rmsnorm(const rssm_norm_config *cfg, const void *x, long long x_stride, const void *gate,
                                long long gate_stride, const void *weight, void *out, float *scales, rssm_stream stream);
 
