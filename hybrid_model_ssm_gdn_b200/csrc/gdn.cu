@@ -1045,16 +1045,16 @@ __global__ void __launch_bounds__(kGdnThreads, 1) gdn_replay_kernel(GArgs a) {
 #pragma unroll
               for (int c = 0; c < 8; ++c) {
                 const float4 pa = va ? *srow(ra, c ^ odd) : f4zero(), pb = vb ? *srow(rb, c ^ odd) : f4zero();
-                bmx[c] = fmaxf(fmaxf(fabsf(pa.x), fabsf(pa.y)), fmaxf(fabsf(pa.z), fabsf(pa.w)));
-                bmx[8 + c] = fmaxf(fmaxf(fabsf(pb.x), fabsf(pb.y)), fmaxf(fabsf(pb.z), fabsf(pb.w)));
+                bmx[c] = max_nan(max_nan(fabsf(pa.x), fabsf(pa.y)), max_nan(fabsf(pa.z), fabsf(pa.w)));
+                bmx[8 + c] = max_nan(max_nan(fabsf(pb.x), fabsf(pb.y)), max_nan(fabsf(pb.z), fabsf(pb.w)));
               }
               float w8[8], w4[4];
 #pragma unroll
               for (int k = 0; k < 8; ++k)
-                w8[k] = fmaxf(b0 ? bmx[k + 8] : bmx[k], __shfl_xor_sync(0xffffffffu, b0 ? bmx[k] : bmx[k + 8], 1));
+                w8[k] = max_nan(b0 ? bmx[k + 8] : bmx[k], __shfl_xor_sync(0xffffffffu, b0 ? bmx[k] : bmx[k + 8], 1));
 #pragma unroll
               for (int k = 0; k < 4; ++k)
-                w4[k] = fmaxf(b1 ? w8[k + 4] : w8[k], __shfl_xor_sync(0xffffffffu, b1 ? w8[k] : w8[k + 4], 2));
+                w4[k] = max_nan(b1 ? w8[k + 4] : w8[k], __shfl_xor_sync(0xffffffffu, b1 ? w8[k] : w8[k + 4], 2));
               float dq[4], rq[4];
               uint32_t scw = 0u;
 #pragma unroll
@@ -1186,10 +1186,10 @@ __global__ void __launch_bounds__(kGdnThreads, 1) gdn_replay_kernel(GArgs a) {
 #pragma unroll
                   for (int c = 0; c < 8; ++c) {
                     unsigned int *cc = cm + ((c + lane) & 7) * 4;
-                    atomicMax(cc, __float_as_uint(fabsf(sv[c].x)));
-                    atomicMax(cc + 1, __float_as_uint(fabsf(sv[c].y)));
-                    atomicMax(cc + 2, __float_as_uint(fabsf(sv[c].z)));
-                    atomicMax(cc + 3, __float_as_uint(fabsf(sv[c].w)));
+                    atomicMax(cc, __float_as_uint(fmaxf(fabsf(sv[c].x), 0.f)));  // a NaN left out
+                    atomicMax(cc + 1, __float_as_uint(fmaxf(fabsf(sv[c].y), 0.f)));
+                    atomicMax(cc + 2, __float_as_uint(fmaxf(fabsf(sv[c].z), 0.f)));
+                    atomicMax(cc + 3, __float_as_uint(fmaxf(fabsf(sv[c].w), 0.f)));
                   }
                 }
                 unsigned int *cz = cmx + ((fd + 1) % 3) * kCmSlotWords;
@@ -1285,10 +1285,10 @@ __global__ void __launch_bounds__(kGdnThreads, 1) gdn_replay_kernel(GArgs a) {
 #pragma unroll
                 for (int c = 0; c < 8; ++c) {
                   const float4 k4 = *reinterpret_cast<const float4 *>(kr + ((c + lane) & 7) * 4);
-                  sv[c].x = k4.x > 0.f ? __fdiv_rn(sv[c].x, k4.x) : 0.f;
-                  sv[c].y = k4.y > 0.f ? __fdiv_rn(sv[c].y, k4.y) : 0.f;
-                  sv[c].z = k4.z > 0.f ? __fdiv_rn(sv[c].z, k4.z) : 0.f;
-                  sv[c].w = k4.w > 0.f ? __fdiv_rn(sv[c].w, k4.w) : 0.f;
+                  sv[c].x = k4.x > 0.f ? __fdiv_rn(sv[c].x, k4.x) : 0.f * sv[c].x;
+                  sv[c].y = k4.y > 0.f ? __fdiv_rn(sv[c].y, k4.y) : 0.f * sv[c].y;
+                  sv[c].z = k4.z > 0.f ? __fdiv_rn(sv[c].z, k4.z) : 0.f * sv[c].z;
+                  sv[c].w = k4.w > 0.f ? __fdiv_rn(sv[c].w, k4.w) : 0.f * sv[c].w;
                 }
               }
               if (live) {
@@ -1297,8 +1297,8 @@ __global__ void __launch_bounds__(kGdnThreads, 1) gdn_replay_kernel(GArgs a) {
 #pragma unroll
                 for (int c = 0; c < 8; ++c) {
                   const int ch = (c + lane) & 7;
-                  const float mq = fmaxf(fmaxf(fabsf(sv[c].x), fabsf(sv[c].y)), fmaxf(fabsf(sv[c].z), fabsf(sv[c].w)));
-                  if (ch < 4) bam0 = fmaxf(bam0, mq); else bam1 = fmaxf(bam1, mq);
+                  const float mq = max_nan(max_nan(fabsf(sv[c].x), fabsf(sv[c].y)), max_nan(fabsf(sv[c].z), fabsf(sv[c].w)));
+                  if (ch < 4) bam0 = max_nan(bam0, mq); else bam1 = max_nan(bam1, mq);
                 }
                 float db0, db1;
                 const uint32_t sc0 = fp4d ? nvfp4d_block_scale(bam0, &db0) : nvfp4_block_scale(bam0, g, &db0);

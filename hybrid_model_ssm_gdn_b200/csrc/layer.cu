@@ -7,6 +7,7 @@
 #include <cuda_fp8.h>
 
 #include "layer_kernels.h"
+#include "lowprec.cuh"
 
 namespace rssm {
 
@@ -120,12 +121,6 @@ __global__ void __launch_bounds__(256) gdn_inputs_kernel(GdnInputsArgs a, unsign
 }
 
 // ------------------------------------------------------------------------------------------ norms
-
-__device__ __forceinline__ float max_nan(float a, float b) {  // NaN if either is
-  float r;
-  asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
-  return r;
-}
 
 constexpr int kMaxWarps = 32;
 

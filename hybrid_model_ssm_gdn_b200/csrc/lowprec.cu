@@ -10,7 +10,9 @@ namespace rssm {
 
 namespace {
 
-// Tile t of a head's fp32 state `head` [rows_per_head][128] into the stored formats of unit (sequence, head).
+// Tile t of a head's fp32 state `head` [rows_per_head][128] into the stored formats of unit (sequence, head).  kPrompt: the state
+// that a prompt left, where what is not finite becomes NaN in every format but fp32.
+template <bool kPrompt>
 __device__ __forceinline__ void store_tile(const float *head, size_t unit, int t, uint32_t epoch, void *hp, float *hs,
                                            int hp_mode, unsigned char *rq, unsigned char *rs, float *rg,
                                            unsigned char *rc, int read_mode, int rows_per_head,
@@ -22,9 +24,13 @@ __device__ __forceinline__ void store_tile(const float *head, size_t unit, int t
   const int rowg = kFp4Rows * t + row;
   const float *src = head + (size_t)rowg * kCols;
   __shared__ float red[64];
+  auto value = [&](int c) {
+    const float v = src[c];
+    return kPrompt && !(fabsf(v) < __int_as_float(0x7f800000)) ? __int_as_float(0x7fffffff) : v;
+  };
   float am = 0.f;
   if (live)
-    for (int c = 0; c < kCols; ++c) am = fmaxf(am, fabsf(src[c]));
+    for (int c = 0; c < kCols; ++c) am = fmaxf(am, fabsf(value(c)));
   // tile maximum (FP8 checkpoint scale, NVFP4 tile scale)
   red[row] = am;
   __syncthreads();
@@ -40,10 +46,10 @@ __device__ __forceinline__ void store_tile(const float *head, size_t unit, int t
         const uint32_t elem = (uint32_t)(rowg * kCols + c);
         const uint4 rw = philox4x32_10(make_uint4((uint32_t)unit, epoch, elem >> 2, 0u), (uint32_t)seed,
                                        (uint32_t)(seed >> 32));
-        dst[c] = (unsigned char)fp8_sr_code(__fdiv_rn(src[c], s8), rw.x);
-        dst[c + 1] = (unsigned char)fp8_sr_code(__fdiv_rn(src[c + 1], s8), rw.y);
-        dst[c + 2] = (unsigned char)fp8_sr_code(__fdiv_rn(src[c + 2], s8), rw.z);
-        dst[c + 3] = (unsigned char)fp8_sr_code(__fdiv_rn(src[c + 3], s8), rw.w);
+        dst[c] = (unsigned char)fp8_sr_code(__fdiv_rn(value(c), s8), rw.x);
+        dst[c + 1] = (unsigned char)fp8_sr_code(__fdiv_rn(value(c + 1), s8), rw.y);
+        dst[c + 2] = (unsigned char)fp8_sr_code(__fdiv_rn(value(c + 2), s8), rw.z);
+        dst[c + 3] = (unsigned char)fp8_sr_code(__fdiv_rn(value(c + 3), s8), rw.w);
       }
     } else if (hp_mode == RSSM_HP_F32) {
       float *dst = reinterpret_cast<float *>(hp) + (unit * rows_per_head + rowg) * kCols;
@@ -54,10 +60,10 @@ __device__ __forceinline__ void store_tile(const float *head, size_t unit, int t
         const uint32_t elem = (uint32_t)(rowg * kCols + c);
         const uint4 rw = philox4x32_10(make_uint4((uint32_t)unit, epoch, elem >> 2, 0u), (uint32_t)seed,
                                        (uint32_t)(seed >> 32));
-        dst[c] = fp16_sr(src[c], rw.x);
-        dst[c + 1] = fp16_sr(src[c + 1], rw.y);
-        dst[c + 2] = fp16_sr(src[c + 2], rw.z);
-        dst[c + 3] = fp16_sr(src[c + 3], rw.w);
+        dst[c] = fp16_sr(value(c), rw.x);
+        dst[c + 1] = fp16_sr(value(c + 1), rw.y);
+        dst[c + 2] = fp16_sr(value(c + 2), rw.z);
+        dst[c + 3] = fp16_sr(value(c + 3), rw.w);
       }
     }
   }
@@ -71,7 +77,7 @@ __device__ __forceinline__ void store_tile(const float *head, size_t unit, int t
     for (int q = row; q < kFp4Rows / 16 * kCols; q += kFp4Rows) cmax[q / kCols][q % kCols] = 0u;
     __syncthreads();
     if (live)
-      for (int c = 0; c < kCols; ++c) atomicMax(&cmax[row >> 4][c], __float_as_uint(fabsf(src[c])));
+      for (int c = 0; c < kCols; ++c) atomicMax(&cmax[row >> 4][c], __float_as_uint(fmaxf(fabsf(value(c)), 0.f)));
     __syncthreads();
     const int ngr = (rows_per_head + 15) / 16, ngr_t = (rows + 15) / 16;
     for (int q = row; q < ngr_t * kCols; q += kFp4Rows) {
@@ -87,8 +93,8 @@ __device__ __forceinline__ void store_tile(const float *head, size_t unit, int t
       float xv[16], bam = 0.f;
       for (int c = 0; c < 16; ++c) {
         const float k = kr[blk * 16 + c];
-        xv[c] = k > 0.f ? __fdiv_rn(src[blk * 16 + c], k) : 0.f;
-        bam = fmaxf(bam, fabsf(xv[c]));
+        xv[c] = k > 0.f ? __fdiv_rn(value(blk * 16 + c), k) : 0.f * value(blk * 16 + c);
+        bam = max_nan(bam, fabsf(xv[c]));
       }
       float d_b;
       rs[(unit * rows_per_head + rowg) * (kCols / 16) + blk] = (unsigned char)nvfp4d_block_scale(bam, &d_b);
@@ -102,11 +108,11 @@ __device__ __forceinline__ void store_tile(const float *head, size_t unit, int t
   if (!live) return;
   for (int blk = 0; blk < kCols / 16; ++blk) {
     float bam = 0.f;
-    for (int c = 0; c < 16; ++c) bam = fmaxf(bam, fabsf(src[blk * 16 + c]));
+    for (int c = 0; c < 16; ++c) bam = max_nan(bam, fabsf(value(blk * 16 + c)));
     float d_b;
     rs[(unit * rows_per_head + rowg) * (kCols / 16) + blk] = (unsigned char)nvfp4_block_scale(bam, g, &d_b);
     for (int c = 0; c < 16; c += 2) {
-      const uint32_t lo = nvfp4_code(src[blk * 16 + c], d_b), hi = nvfp4_code(src[blk * 16 + c + 1], d_b);
+      const uint32_t lo = nvfp4_code(value(blk * 16 + c), d_b), hi = nvfp4_code(value(blk * 16 + c + 1), d_b);
       rq[(unit * rows_per_head + rowg) * (kCols / 2) + (blk * 16 + c) / 2] = (unsigned char)(lo | (hi << 4));
     }
   }
@@ -117,7 +123,7 @@ __global__ void store_state_kernel(const float *S, void *hp, float *hs, int hp_m
                                    unsigned long long seed) {
   const int nrb = (rows_per_head + kFp4Rows - 1) / kFp4Rows;
   const size_t unit = blockIdx.x / nrb;
-  store_tile(S + unit * rows_per_head * kCols, unit, blockIdx.x % nrb, 0u, hp, hs, hp_mode, rq, rs, rg, rc, read_mode,
+  store_tile<false>(S + unit * rows_per_head * kCols, unit, blockIdx.x % nrb, 0u, hp, hs, hp_mode, rq, rs, rg, rc, read_mode,
              rows_per_head, seed);
 }
 
@@ -175,7 +181,7 @@ __global__ void __launch_bounds__(kFp4Rows) prompt_state_kernel(PromptStateArgs 
   const size_t unit = (size_t)pc.slot * a.H + h;
   if (kStore) {
     if (pc.resume && pc.end == pc.begin) return;  // an empty prompt leaves its sequence as it is
-    store_tile(head, unit, t, (uint32_t)pr.meta[pc.slot].y + 1u, a.hp, a.hs, a.hp_mode, a.rq, a.rs, a.rg, a.rc,
+    store_tile<true>(head, unit, t, (uint32_t)pr.meta[pc.slot].y + 1u, a.hp, a.hs, a.hp_mode, a.rq, a.rs, a.rg, a.rc,
                a.read_mode, a.rows, a.seed);
   } else if (pc.resume) {
     widen_tile(head, unit, t, a.hp, a.hs, a.hp_mode, a.rq, a.rs, a.rg, a.read_mode, a.rows);

@@ -22,6 +22,8 @@
 //   per column and group of 16 rows c = E4M3(amax_group / (6 g)), step k = c g;
 //   x' = x / k (0 where k = 0); per row block s_b = E4M3(amax_b(x') / (6 * 2^-8)),
 //   d_b = s_b * 2^-8; code = sign(x') | E2M1(|x'| / d_b); value = (E2M1 * d_b) * k.
+// * NaN stays NaN and keeps to its row: E4M3 code 0x7F, fp16 NaN, in NVFP4 the scale code 0x7F of its block of 16 columns.
+//   Maxima of tiles and column groups leave it out.  States of prompts count infinities as NaN; elsewhere they saturate.
 // * Random words: Philox4x32-10 (Salmon, Moraes, Dror & Shaw, SC'11), counter
 //   (sequence*H + head, epoch written, element/4, 0), key = the 64-bit seed; element e
 //   uses output word e % 4.
@@ -35,6 +37,12 @@
 namespace rssm {
 
 constexpr int kFp4Rows = 64;  // rows of one NVFP4 tile (one row block of a head's state)
+
+__device__ __forceinline__ float max_nan(float a, float b) {  // NaN if either is
+  float r;
+  asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
+  return r;
+}
 
 __device__ __forceinline__ uint4 philox4x32_10(uint4 c, uint32_t k0, uint32_t k1) {
 #pragma unroll
@@ -96,6 +104,7 @@ __device__ __forceinline__ uint32_t fp8_sr_code(float y, uint32_t r) {
     return code | (sign << 7);
   }
   const uint32_t mant = bits & 0x7FFFFFu;
+  if (E == 255 && mant) return 0x7Fu;
   const uint32_t M = E ? (mant | 0x800000u) : mant;  // |y| = M * 2^(Eeff - 150)
   const int Eeff = E ? E : 1;
   const int s = max(20, 141 - Eeff);                  // fp32 bits below the E4M3 spacing
@@ -125,6 +134,7 @@ __device__ __forceinline__ uint32_t fp8_sr_code(float y, uint32_t r) {
 
 __device__ __forceinline__ float e4m3_signed_value(uint32_t code) {
   const uint32_t ef = (code >> 3) & 0xFu, m = code & 7u;
+  if ((code & 0x7Fu) == 0x7Fu) return __int_as_float(0x7fffffff);
   const float mag = ef == 0 ? ldexpf((float)m, -9) : ldexpf((float)(8u + m), (int)ef - 10);
   return (code & 0x80u) ? -mag : mag;
 }
@@ -157,6 +167,7 @@ __device__ __forceinline__ float4 e2m1x4_to_float4(uint32_t w) {  // four codes,
 
 __device__ __forceinline__ float e4m3_value(uint32_t code) {
   const uint32_t ef = (code >> 3) & 0xFu, m = code & 7u;
+  if ((code & 0x7Fu) == 0x7Fu) return __int_as_float(0x7fffffff);
   return ef == 0 ? ldexpf((float)m, -9) : ldexpf((float)(8u + m), (int)ef - 10);
 }
 

@@ -251,7 +251,8 @@ rssm_status rssm_gdn_scan(const rssm_config *cfg, int qk_heads, const rssm_promp
                           float *y, void *work, size_t work_bytes, rssm_stream stream);
 
 /* The same on a context, as rssm_mamba2_prefill: the states become the sequences' checkpoints in the context's formats
- * (stochastic rounding takes the words of the sequence's new epoch), with their read copies. */
+ * (stochastic rounding takes the words of the sequence's new epoch), with their read copies.  Rows of the state that are not
+ * finite are NaN in every format and copy, and stay NaN through later steps; they do not touch their tile's scales. */
 rssm_status rssm_gdn_prefill(rssm_ctx *ctx, int qk_heads, const rssm_prompts *pr, const rssm_tokens *tok, float *y,
                              void *work, size_t work_bytes, rssm_stream stream);
 
