@@ -84,7 +84,7 @@ struct GdnShared {
   uint64_t s_ready[2], r_ready[2], u_ready[2], y_taken, y_free, full_unit[kUnits], free_unit[kUnits];
   uint32_t tmem;
   int abort, not_finite, bad;
-  int slot;  // of the unit handed out last
+  int slot;  // of the unit whose state is on the chip: what a wait that runs out reports, for units end in turn
 };
 constexpr int kGdnSmem = (int)sizeof(GdnShared);
 static_assert(kGdnSmem <= 227 * 1024, "shared memory of a block");
@@ -99,7 +99,7 @@ struct GdnTcArgs {
   float *y;                 // [total][H][R]
   int *err;                 // may be null
   long long wait_cycles;
-  int withhold;             // test hook: no block loads k and q of this chunk (-1: off)
+  int withhold;             // test hook: no block loads v of this chunk of a prompt (-1: off)
 };
 
 struct Waiter {
@@ -532,6 +532,7 @@ __global__ void __launch_bounds__(kGdnThreads, 1)
         u.begin = pr.off[u.seq];
         u.tokens = pr.off[u.seq + 1] - u.begin;
         u.slot = pr.slots ? pr.slots[u.seq] : u.seq;
+        if (lane == 0 && n == 0) *(volatile int *)&sh.slot = u.slot;  // the first to come
         u.resume = pr.resume ? pr.resume[u.seq] : 0;
         bool skip = __any_sync(0xffffffffu, refused(pr, u.seq, u.slot, u.resume, lane, 32));
         if (!skip && u.tokens == 0) {
@@ -543,7 +544,6 @@ __global__ void __launch_bounds__(kGdnThreads, 1)
         if (skip && kMany) continue;
         more = !skip;
       }
-      if (lane == 0) sh.slot = u.slot;
       if (!more) u.tokens = 0;
       if (kMany && n >= kUnits) wait.warp(sh.free_unit[n % kUnits], n / kUnits - 1);
       if (__any_sync(0xffffffffu, *(volatile int *)&sh.abort)) break;
@@ -557,7 +557,7 @@ __global__ void __launch_bounds__(kGdnThreads, 1)
         for (int c = 0; c < chunks; ++c) {
           const int t = u.begin + c * Q;
           if (asked >= kStages) wait(sh.free_kq[s], turn - 1);
-          if (*(volatile int *)&sh.abort || c == a.withhold) {
+          if (*(volatile int *)&sh.abort) {
             more = false;
             break;
           }
@@ -581,17 +581,21 @@ __global__ void __launch_bounds__(kGdnThreads, 1)
   } else if (warp == kWarpLoadV) {
     Unit u;
     int asked = 0;
-    for (int i = 0; next_unit(i, u); ++i) {
+    bool more = true;
+    for (int i = 0; more && next_unit(i, u); ++i) {
       if (lane == 0) {
         for (int t = 0; t < u.tokens; t += Q) {
           if (asked > 0) wait(sh.free_v, asked - 1);
-          if (*(volatile int *)&sh.abort) break;
+          if (*(volatile int *)&sh.abort || t / Q == a.withhold) {
+            more = false;
+            break;
+          }
           mbar_arrive_expect_tx(&sh.full_v, 2 * kHalf);
           tma_load_3d(sh.V, &map_v, 0, u.head, u.begin + t, &sh.full_v);
           ++asked;
         }
       }
-      __syncwarp();
+      more = __all_sync(0xffffffffu, more);
     }
     if (lane == 0 && asked) mbar_wait(&sh.full_v, (asked - 1) & 1, wait.ws);
     __syncwarp();
@@ -993,6 +997,7 @@ __global__ void __launch_bounds__(kGdnThreads, 1)
       tm_wait_st();
       warp_arrive(sh.s_ready[part], lane);
       const Unit &unit = sh.unit[number % kUnits];
+      if (tid == 0) *(volatile int *)&sh.slot = unit.slot;
       const int ntok = unit.tokens;
       int *const bad_from = &sh.first[number & 1][row];
       float *yg = a.y + ((size_t)(unit.begin + 16 * w) * a.H + unit.head) * a.R + row;

@@ -44,7 +44,7 @@ struct GdnScanArgs {
   float *y;                         // [total][H][R]
   int *err;                         // error word, may be null
   long long wait_cycles;            // bound of the tensor-core kernel's waits
-  int withhold;                     // test hook: no block loads k of this chunk (-1: off)
+  int withhold;                     // test hook: no block loads v of this chunk (-1: off)
 };
 // token by token: fp32 inputs, prompts of a few tokens
 cudaError_t launch_gdn_scan(const GdnScanArgs &a, const Prompts &pr, int esz, int num_sms, cudaStream_t stream);

@@ -165,3 +165,31 @@ def test_rows_past_32_bits(cuda_ok, dtype, H, total, nseq, n):
         same(y[:n], y[-n:])
         same(S[0], S[-1])
     compare(d, [0, n], None, [1], S[-1:].cpu().numpy(), y[-n:].cpu().numpy())
+
+
+@pytest.mark.parametrize("long", [5, 40, 99, 180])
+def test_a_timeout_names_the_sequence_that_waited(cuda_ok, monkeypatch, long):
+    """Blocks that take heads and prompts in turn, of which one prompt alone has a second chunk, which is not loaded: whatever the
+    blocks have taken on in the meantime, behind it or to their ends, the context reports the slot of that prompt. Prompts of
+    other blocks have their results."""
+    n, H = 200, 4
+    lens = [20] * n
+    lens[long] = 100
+    offsets = packed(lens)
+    d = make(61, BF, offsets[-1], H, 2, 64, n)
+    slots = [(i + n - long + 150) % n for i in range(n)]  # the long one's is 150; lower ones come before and behind it
+    assert slots[long] == 150 and min(slots[long + 1:] + slots[:long]) == 0
+    assert n * H > 4 * torch.cuda.get_device_properties(0).multi_processor_count and offsets[-1] <= 256 * n
+    g = on_gpu(d, BF)
+    monkeypatch.setenv("RSSM_WAIT_CYCLES", "2000000")
+    monkeypatch.setenv("RSSM_WITHHOLD_TILE", "1")
+    layer = context(d, BF, n)
+    monkeypatch.delenv("RSSM_WITHHOLD_TILE")
+    monkeypatch.delenv("RSSM_WAIT_CYCLES")
+    y = torch.full((offsets[-1], H, 64), 7.0, device="cuda")
+    layer.gdn_prefill(*tokens(g), idx(offsets), idx(slots), y=y)
+    assert layer.get_error() == (abi.DEV_TIMEOUT, 150)
+    assert torch.isnan(y[offsets[long]:offsets[long + 1]]).all()
+    want = scan(dict(g, S=g["S"].clone()), offsets)
+    fine = torch.isfinite(y)
+    assert fine.float().mean() > 0.9 and torch.equal(y[fine], want[fine])
