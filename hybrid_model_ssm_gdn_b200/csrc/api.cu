@@ -699,8 +699,9 @@ rssm_status rssm_gdn_inputs(const rssm_gdn_inputs_config *c, void *q_out, void *
   const unsigned long long vecs = rows * c->out_heads * kCols * esz, gates = rows * c->nheads * 4;
   const Extent outs[] = {{q_out, 1, vecs, vecs}, {k_out, 1, vecs, vecs}, {alpha, 1, gates, gates}, {beta, 1, gates, gates}};
   const Extent ins[] = {{c->q, rows, vec * esz, c->q_stride * esz}, {c->k, rows, vec * esz, c->k_stride * esz},
-                        {c->a, rows, c->nheads * esz, c->a_stride * esz}, {c->b, rows, c->nheads * esz, c->b_stride * esz}};
-  if (outputs_meet(outs, 4, ins, 4)) return RSSM_ERR_ARG;
+                        {c->a, rows, c->nheads * esz, c->a_stride * esz}, {c->b, rows, c->nheads * esz, c->b_stride * esz},
+                        {c->A_log, 1, c->nheads * 4ULL, c->nheads * 4ULL}, {c->bias, 1, c->nheads * 4ULL, c->nheads * 4ULL}};
+  if (outputs_meet(outs, 4, ins, 6)) return RSSM_ERR_ARG;
   GdnInputsArgs a{};
   a.rows = c->rows; a.H = c->nheads; a.Hk = c->qk_heads; a.out_heads = c->out_heads; a.eps = c->eps;
   a.q = c->q; a.k = c->k; a.a = c->a; a.b = c->b;
@@ -772,6 +773,9 @@ rssm_status rssm_add_rmsnorm(const rssm_norm_config *cfg, const void *x, long lo
   const Extent to{residual, (unsigned long long)a.rows, row, residual_stride * esz};
   const Extent from{x, (unsigned long long)a.rows, row, x_stride * esz};
   if (residual && !(residual == x && (residual_stride == x_stride || a.rows == 1)) && rows_meet(to, from)) return RSSM_ERR_ARG;
+  // blocks read the weight after others have stored their h
+  const unsigned long long w = a.columns * (a.weight_dtype == RSSM_BF16 ? 2ULL : 4ULL);
+  if (residual && overlaps(weight, w, residual, a.rows, row, to.stride)) return RSSM_ERR_ARG;
   a.residual = residual; a.stride_residual = residual_stride;
   const cudaError_t e = launch_norm(a, false, reinterpret_cast<cudaStream_t>(stream));
   return e == cudaSuccess ? RSSM_OK : cuda_fail(e);

@@ -333,8 +333,8 @@ typedef struct {
 } rssm_norm_config;
 
 /* In front of a layer: h = x + residual (fp32), which goes back to residual, rounded once (the norm takes h before that).
- * residual may be NULL: h = x; its rows may be x itself or beside its rows, not across them.  Takes cfg.group =
- * cfg.weight_columns = columns. */
+ * residual may be NULL: h = x; its rows may be x itself or beside its rows, not across them nor over the weight.  Takes
+ * cfg.group = cfg.weight_columns = columns. */
 rssm_status rssm_add_rmsnorm(const rssm_norm_config *cfg, const void *x, long long x_stride, void *residual,
                              long long residual_stride, const void *weight, void *out, float *scales, rssm_stream stream);
 

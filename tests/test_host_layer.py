@@ -136,6 +136,32 @@ def test_outputs_that_meet_inputs_are_refused(lib):
             assert lib.rssm_gdn_inputs(C.byref(abi.GdnInputsConfig(**cfg_)), *map(C.c_void_p, outs), None) == ARG, (i, where)
 
 
+def test_outputs_over_parameters_are_refused(lib):
+    """A_log and bias under each output of the inputs, and the weight under the residual, whose h goes back while other rows
+    read it; at addresses that nobody reads, as above."""
+    M = 1 << 24
+    cfg_ = dict(rows=3, nheads=4, qk_heads=2, out_heads=2, in_dtype=abi.BF16, eps=1e-6, q=M, k=2 * M, a=3 * M, b=4 * M,
+                q_stride=256, k_stride=256, a_stride=4, b_stride=4, A_log=9 * M, bias=10 * M)
+    for i in range(4):
+        size = 3 * 512 if i < 2 else 48  # bytes of the output
+        for at in (9 * M, 10 * M):
+            for where in (at, at - size + 16):
+                outs = [5 * M, 6 * M, 7 * M, 8 * M]
+                outs[i] = where
+                assert lib.rssm_gdn_inputs(C.byref(abi.GdnInputsConfig(**cfg_)), *map(C.c_void_p, outs), None) == ARG, (i, where)
+
+    for dtype, esz in ((abi.BF16, 2), (abi.F32, 4)):
+        base = dict(rows=3, columns=64, group=64, weight_columns=64, x_dtype=abi.BF16, weight_dtype=dtype, out_dtype=abi.BF16,
+                    eps=1e-6)
+
+        def add(r, rs, w):
+            return lib.rssm_add_rmsnorm(C.byref(abi.NormConfig(**base)), M, 64, r, rs, w, 4 * M, None, None)
+
+        for rs in (64, 72, 1024):
+            for w in (2 * M, 2 * M + 2 * rs * 2, 2 * M + 2 * rs * 2 + 112, 2 * M - 64 * esz + 16):
+                assert add(2 * M, rs, w) == ARG, (rs, w - 2 * M)
+
+
 def test_binding_checks_shapes_and_devices():
     """Shapes and types are refused with ValueError, and tensors off the GPU before a pointer is taken from them."""
     t = torch.zeros
