@@ -685,8 +685,8 @@ rssm_status rssm_gdn_inputs(const rssm_gdn_inputs_config *c, void *q_out, void *
   if (c->rows < 0 || c->rows > (1 << 30) || c->nheads < 1 || c->nheads > 65535 || c->qk_heads < 1 ||
       c->nheads % c->qk_heads != 0 || (c->out_heads != c->qk_heads && c->out_heads != c->nheads))
     return RSSM_ERR_SHAPE;
-  // blocks of the launch: a block takes 16 vectors or 256 gates
-  if (((long long)c->rows * c->qk_heads >> 3) + ((long long)c->rows * c->nheads >> 8) > 0x7ffffff0LL) return RSSM_ERR_SHAPE;
+  // (cut for few rows it has three blocks a row, of at most four rows an SM)
+  if (cut_inputs(c->rows, c->nheads, c->qk_heads, false).blocks > 0x7fffffffLL) return RSSM_ERR_SHAPE;
   if (c->rows == 0) return RSSM_OK;
   const long long vec = (long long)c->qk_heads * kCols;
   if (c->q_stride < vec || c->k_stride < vec || c->q_stride % 8 != 0 || c->k_stride % 8 != 0 || c->a_stride < c->nheads ||

@@ -15,7 +15,7 @@ namespace {
 
 // ------------------------------------------------------------------------------------------ inputs of the gated delta rule
 
-constexpr int kItems = 4;  // heads' vectors that 16 lanes have on their way at a time
+constexpr int kItems = kInputItems;
 
 __device__ __forceinline__ uint32_t bf16_pair(float a, float b) {
   const __nv_bfloat162 h = __floats2bfloat162_rn(a, b);
@@ -406,12 +406,10 @@ cudaError_t launch_norm_type(const NormArgs &a, cudaStream_t stream) {
 
 cudaError_t launch_gdn_inputs(const GdnInputsArgs &args, int esz, int num_sms, cudaStream_t stream) {
   GdnInputsArgs a = args;
-  // a row a block while that leaves the SMs with few blocks (64 rows of 16 heads: 6.1 us, with several rows a block 8.2),
-  // otherwise as many as give every 16 lanes kItems vectors
-  a.vector_rows = a.rows <= 4 * num_sms ? 1 : max(1, 16 * kItems / a.Hk);
-  a.gate_rows = a.rows <= 4 * num_sms ? 1 : max(1, 1024 / a.H);
-  const unsigned vb = (unsigned)((a.rows + a.vector_rows - 1) / a.vector_rows);
-  const unsigned grid = 2 * vb + (unsigned)((a.rows + a.gate_rows - 1) / a.gate_rows);
+  const InputsCut cut = cut_inputs(a.rows, a.H, a.Hk, a.rows <= 4 * num_sms);
+  a.vector_rows = cut.vectors;
+  a.gate_rows = cut.gates;
+  const unsigned vb = (unsigned)(((long long)a.rows + a.vector_rows - 1) / a.vector_rows), grid = (unsigned)cut.blocks;
   if (esz == 2) gdn_inputs_kernel<__nv_bfloat16><<<grid, 256, 0, stream>>>(a, vb);
   else gdn_inputs_kernel<float><<<grid, 256, 0, stream>>>(a, vb);
   return cudaGetLastError();

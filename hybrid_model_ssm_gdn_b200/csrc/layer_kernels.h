@@ -15,6 +15,20 @@ struct GdnInputsArgs {
   float *alpha, *beta;              // [rows][H]
   int vector_rows, gate_rows;       // rows of a block (the launch's to fill in)
 };
+// How the launch is cut: blocks of `vectors` rows of q or of k, then blocks of `gates` rows.  A row a block while that leaves the
+// SMs with few of them (64 rows of 16 heads: 6.1 us, with several rows a block 8.2), otherwise as many as give every 16 lanes
+// kInputItems vectors.
+constexpr int kInputItems = 4;  // heads' vectors that 16 lanes have on their way at a time
+struct InputsCut {
+  int vectors, gates;
+  long long blocks;
+};
+inline InputsCut cut_inputs(int rows, int H, int Hk, bool few) {
+  auto most = [&](int n) { return few || n < 1 ? 1 : n; };
+  InputsCut c{most(16 * kInputItems / Hk), most(1024 / H), 0};
+  c.blocks = 2 * (((long long)rows + c.vectors - 1) / c.vectors) + ((long long)rows + c.gates - 1) / c.gates;
+  return c;
+}
 cudaError_t launch_gdn_inputs(const GdnInputsArgs &a, int esz, int num_sms, cudaStream_t stream);
 
 struct NormArgs {

@@ -136,6 +136,17 @@ def test_outputs_that_meet_inputs_are_refused(lib):
             assert lib.rssm_gdn_inputs(C.byref(abi.GdnInputsConfig(**cfg_)), *map(C.c_void_p, outs), None) == ARG, (i, where)
 
 
+def test_inputs_of_more_blocks_than_a_launch_has_are_refused(lib):
+    """Rows and heads whose blocks, as the launch is cut (64 / qk_heads rows of vectors, 1024 / nheads of gates, at least one),
+    pass 2^31 - 1."""
+    p, most = C.c_void_p(16), 1 << 30
+    for hk, h in ((64, 64), (33, 33), (40, 1200), (50, 65500)):
+        blocks = 2 * -(-most // max(1, 64 // hk)) + -(-most // max(1, 1024 // h))
+        c = abi.GdnInputsConfig(rows=most, nheads=h, qk_heads=hk, out_heads=hk, in_dtype=abi.BF16, eps=1e-6, q=16, k=16, a=2, b=2,
+                                q_stride=128 * hk, k_stride=128 * hk, a_stride=h, b_stride=h, A_log=4, bias=4)
+        assert blocks > 2 ** 31 - 1 and lib.rssm_gdn_inputs(C.byref(c), p, p, p, p, None) == SHAPE, (hk, h)
+
+
 def test_outputs_over_parameters_are_refused(lib):
     """A_log and bias under each output of the inputs, and the weight under the residual, whose h goes back while other rows
     read it; at addresses that nobody reads, as above."""
