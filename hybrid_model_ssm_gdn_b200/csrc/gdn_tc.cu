@@ -75,7 +75,7 @@ struct GdnShared {
   float A[32 * kStepA];           // blocks of A below the diagonal, see store_a
   __align__(16) float diag[4][16 * 20 + 16];  // blocks of A on the diagonal, [column][row]; then X, see block_x
   Table tab[2];
-  float alpha[Q], prefix[Q], tot[4];
+  float alpha[2][Q], prefix[2][Q], fall[2][Q], tot[2][4];  // products within a token's block of 16: up to it, and behind it
   int first[2][128];  // per row of the state, the first token of the unit (odd ones, even ones) whose v is not finite
   Unit unit[kUnits];
   int order[kByLength];  // prompts by length
@@ -304,23 +304,54 @@ __device__ __forceinline__ void store_m(unsigned char (*M)[kHalf], const PrepRow
   }
 }
 
-// Without decays: A = beta_j G, M = G up to the diagonal.  Returns a sum that is not 0 where a value of k or beta that
-// this row uses, or that lies in its block, is not finite.  What rows before it take is finite: they take nothing behind
-// them, and M is selected up to the diagonal.
-__device__ __forceinline__ f2 prep_mild(GdnShared &sh, const PrepRow &r, unsigned char (*M)[kHalf]) {
-  f2 seen = pack2(0.f, 0.f);
-  const f2 zero = seen, by = pack2(r.by, r.by);
+// The factors of a row of the Gram matrix and a block of columns: by_j, with decays by_j D_ji up to the diagonal.
+__device__ __forceinline__ void row_factors(const GdnShared &sh, const PrepRow &r, bool strong, int b, int blk, f2 (&e)[8]) {
+  if (!strong) {
 #pragma unroll
-  for (int blk = 0; blk < 4; ++blk) {
-    if (blk > 2 * r.upper + 1) break;  // (above the diagonal of both blocks that this warp's rows lie in)
+    for (int i = 0; i < 8; ++i) e[i] = pack2(r.by, r.by);
+    return;
+  }
+  const float f = r.by * (blk == 0 ? r.f[0] : blk == 1 ? r.f[1] : r.f[2]);
+  if (blk < 2 * r.upper) {  // before the blocks of all of this warp's rows
+    const f2 ff = pack2(f, f);
+#pragma unroll
+    for (int i = 0; i < 16; i += 4) {
+      const float4 a4 = *reinterpret_cast<const float4 *>(&sh.fall[b][16 * blk + i]);
+      e[i / 2] = mul2(ff, pack2(a4.x, a4.y));
+      e[i / 2 + 1] = mul2(ff, pack2(a4.z, a4.w));
+    }
+    return;
+  }
+  const int last = blk == r.bj ? r.jj : 15;  // factors behind the row's token do not count
+  float d = blk < r.bj ? f : r.by;
+#pragma unroll
+  for (int i = 12; i >= 0; i -= 4) {
+    const float4 a4 = *reinterpret_cast<const float4 *>(&sh.alpha[b][16 * blk + i]);
+    const float d3 = d, d2 = d3 * (i + 3 <= last ? a4.w : 1.f), d1 = d2 * (i + 2 <= last ? a4.z : 1.f),
+                d0 = d1 * (i + 1 <= last ? a4.y : 1.f);
+    e[i / 2 + 1] = pack2(d2, d3);
+    e[i / 2] = pack2(d0, d1);
+    d = d0 * (i <= last ? a4.x : 1.f);
+  }
+}
+
+// Rows of A = beta_j D G, or of M = D G up to the diagonal; D is left out in the form without decays.  Returns a sum that is not 0
+// where a value of k or beta that this row of A uses, or that lies in its block, is not finite.  What rows before it take is
+// finite: they take nothing behind them, and M is selected up to the diagonal.
+__device__ __forceinline__ f2 prep_rows(GdnShared &sh, const PrepRow &r, bool strong, unsigned char (*M)[kHalf], int b) {
+  f2 seen = pack2(0.f, 0.f);
+  const f2 zero = seen;
+#pragma unroll 1
+  for (int blk = 0; blk < 2 * r.upper + 2; ++blk) {
     uint32_t G[16];
     f2 v[8];
     tm_ld16(r.gram + 16 * blk, G);
+    row_factors(sh, r, strong, b, blk, v);
     tm_wait_ld();
     if (r.of_k) {
 #pragma unroll
       for (int i = 0; i < 8; ++i) {
-        v[i] = mul2(by, pack2(G[2 * i], G[2 * i + 1]));
+        v[i] = mul2(v[i], pack2(G[2 * i], G[2 * i + 1]));
         seen = fma2(v[i], zero, seen);
       }
       if (blk == r.bj) {
@@ -332,56 +363,15 @@ __device__ __forceinline__ f2 prep_mild(GdnShared &sh, const PrepRow &r, unsigne
           sh.diag[r.bj][40 * i + 20 + r.jj] = e1;
         }
       }
-      if (blk <= 2 * r.upper) store_a(sh, r, blk, v);
-    } else {
-      const int most = blk < r.bj ? 15 : r.jj;  // last column of this row (rows above the block are not stored)
-#pragma unroll
-      for (int i = 0; i < 8; ++i)
-        v[i] = blk < 2 * r.upper ? pack2(G[2 * i], G[2 * i + 1])
-                                 : pack2(2 * i <= most ? G[2 * i] : 0u, 2 * i + 1 <= most ? G[2 * i + 1] : 0u);
-      store_m(M, r, blk, v);
-    }
-  }
-  return seen;
-}
-
-// With decays: A = beta_j D G, M = D G; see prep_mild.
-__device__ __noinline__ f2 prep_strong(GdnShared &sh, PrepRow r, unsigned char (*M)[kHalf]) {
-  f2 seen = pack2(0.f, 0.f);
-  const f2 zero = seen;
-#pragma unroll 1
-  for (int blk = 0; blk < 2 * r.upper + 2; ++blk) {
-    uint32_t G[16];
-    f2 v[8];
-    tm_ld16(r.gram + 16 * blk, G);
-    const int own = blk == r.bj ? r.jj : -1;  // column of the diagonal in this block
-    const int most = blk < r.bj ? 15 : own;
-    const float f = blk == 0 ? r.f[0] : blk == 1 ? r.f[1] : blk == 2 ? r.f[2] : 0.f;
-    float d = r.by * f, e[16];
-    tm_wait_ld();
-#pragma unroll
-    for (int i = 12; i >= 0; i -= 4) {
-      const float4 a4 = *reinterpret_cast<const float4 *>(&sh.alpha[16 * blk + i]);
-      const float al[4] = {a4.x, a4.y, a4.z, a4.w};
-#pragma unroll
-      for (int k = 3; k >= 0; --k) {
-        if (i + k == own) d = r.by;
-        e[i + k] = r.of_k || i + k <= most ? d * __uint_as_float(G[i + k]) : 0.f;
-        d *= al[k];
-      }
-    }
-#pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      v[i] = pack2(e[2 * i], e[2 * i + 1]);
-      seen = fma2(v[i], zero, seen);
-    }
-    if (r.of_k) {
-      if (blk == r.bj) {
-#pragma unroll
-        for (int i = 0; i < 16; ++i) sh.diag[r.bj][20 * i + r.jj] = e[i];
-      }
       store_a(sh, r, blk, v);
     } else {
+      if (blk >= 2 * r.upper) {
+        const int most = blk < r.bj ? 15 : r.jj;  // last column of this row (rows above the block are not stored)
+#pragma unroll
+        for (int i = 0; i < 16; ++i) G[i] = i <= most ? G[i] : 0u;
+      }
+#pragma unroll
+      for (int i = 0; i < 8; ++i) v[i] = mul2(v[i], pack2(G[2 * i], G[2 * i + 1]));
       store_m(M, r, blk, v);
     }
   }
@@ -395,27 +385,22 @@ __device__ __forceinline__ bool not_zero(f2 v) {
 // Some value of the chunk is not finite.  From the first token on whose k, alpha or beta is not (k_j . k_j is not, if k_j is
 // not), or whose products of alpha pass fp32's range, the tokens change nothing; the state warps write NaN for them.  Rows
 // before it have used none of them.  Returns that token, or the number of tokens.
-__device__ __noinline__ int prep_careful(GdnShared &sh, PrepRow r, bool odd, bool strong, int valid) {
-  uint32_t G[2][16];
-  tm_ld16(r.gram + 32 * r.upper, G[0]);
-  tm_ld16(r.gram + 32 * r.upper + 16, G[1]);
-  tm_wait_ld();
+__device__ __noinline__ int prep_careful(GdnShared &sh, PrepRow r, bool odd, bool strong, int b, int valid) {
   float own = r.by;
-#pragma unroll
-  for (int i = 0; i < 16; ++i)
-    if (i == r.jj) own = fmaf(__uint_as_float(r.bj & 1 ? G[1][i] : G[0][i]), 0.f, own);
-  if (strong) {  // the row of A before its diagonal, as in prep_strong
 #pragma unroll 1
-    for (int blk = 0; blk < 2 * r.upper + 2; ++blk) {
-      tm_ld16(r.gram + 16 * blk, G[0]);
-      tm_wait_ld();
-      float d = r.by * (blk == 0 ? r.f[0] : blk == 1 ? r.f[1] : blk == 2 ? r.f[2] : 0.f);
+  for (int blk = 0; blk < 2 * r.upper + 2; ++blk) {
+    uint32_t G[16];
+    f2 e[8];
+    tm_ld16(r.gram + 16 * blk, G);
+    row_factors(sh, r, strong, b, blk, e);
+    tm_wait_ld();
 #pragma unroll
-      for (int i = 15; i >= 0; --i) {
-        if (blk == r.bj && i == r.jj) d = r.by;
-        else if (blk < r.bj || (blk == r.bj && i < r.jj)) own = fmaf(d * __uint_as_float(G[0][i]), 0.f, own);
-        d *= sh.alpha[16 * blk + i];
-      }
+    for (int i = 0; i < 16; ++i) {
+      float e0, e1;
+      unpack2(e[i / 2], e0, e1);
+      if (blk == r.bj && i == r.jj) own = fmaf(__uint_as_float(G[i]), 0.f, own);
+      else if (strong && (blk < r.bj || (blk == r.bj && i < r.jj)))
+        own = fmaf((i & 1 ? e1 : e0) * __uint_as_float(G[i]), 0.f, own);
     }
   }
   if (threadIdx.x == 32 * kWarpPrep) sh.bad = valid;
@@ -757,118 +742,128 @@ __global__ void __launch_bounds__(kGdnThreads, 1)
     // The four warps go on or stop together: they meet at barriers of their own, and a block may be given up between their looks.
     for (int i = 0; !prep_sync_or(!next_unit(i, unit)); ++i) {
       const int ntok = unit.tokens;
-      const float *ag = a.alpha + (size_t)unit.begin * a.H + unit.head, *bg = a.beta + (size_t)unit.begin * a.H + unit.head;
+      size_t next = ((size_t)unit.begin + j) * a.H + unit.head;  // this thread's token of the next chunk
       auto fetch = [&](int first) {
-        const int t = first + j;
         alpha_next = 1.f;
         beta_next = 0.f;  // a token behind the end changes nothing
-        if (of_k && t < ntok) {
-          alpha_next = ag[(size_t)t * a.H];
-          beta_next = bg[(size_t)t * a.H];
+        if (of_k && first + j < ntok) {
+          alpha_next = a.alpha[next];
+          beta_next = a.beta[next];
         }
+        next += (size_t)Q * a.H;
       };
       fetch(0);
-      for (int at = 0; at < ntok; at += Q, ++c) {
-        const int b = c & 1, valid = min(Q, ntok - at);
-        const bool odd = !(fabsf(alpha_next) < __int_as_float(0x7f800000));
-        const float al = odd ? 1.f : alpha_next, be = beta_next;  // (the chunk ends before an odd one)
-        if (at + Q < ntok) fetch(at + Q);
-        float up = al, down = al;  // products within the block of 16: up to this token, and behind it
-        if (of_k) {
+      // What follows from alpha alone is worked out a chunk ahead, by two warps while the others form the first blocks of T.
+      float up = 1.f, down = 1.f, be = 0.f;  // products within the block of 16: up to this token, and behind it; beta
+      bool odd = false;                      // alpha is not finite (the chunk ends before it)
+      for (int at = -Q; at < ntok; at += Q) {
+        const int b = c & 1;
+        unsigned char(*const T)[kHalf] = sh.T[b];
+        if (at >= 0) {
+          const int valid = min(Q, ntok - at);
+          if (valid < Q) {  // rows of k that belong to other prompts must not reach the state, whatever they hold
+            wait(sh.full_kq[c % kStages], c / kStages);
+            for (int i = p + valid * 8; i < Q * 8; i += 128) {
+              *reinterpret_cast<uint4 *>(sh.in[c % kStages][0] + 16 * i) = make_uint4(0, 0, 0, 0);
+              *reinterpret_cast<uint4 *>(sh.in[c % kStages][2] + 16 * i) = make_uint4(0, 0, 0, 0);
+            }
+          }
+          const bool grows = prep_sync_or(!(fabsf(up) <= 1.f && fabsf(down) <= 1.f));
+          if (c > 1) wait(sh.free_t[b], (c >> 1) - 1);
+          const float tot[4] = {sh.tot[b][0], sh.tot[b][1], sh.tot[b][2], sh.tot[b][3]};
+          const float carry = (tot[0] * tot[1]) * (tot[2] * tot[3]);
+          const bool strong = grows || !(fabsf(carry) >= kMild);  // otherwise f_j = carry / (product up to j) >= carry
+          Table &tab = sh.tab[b];
+          r.by = of_k ? be : 1.f;
+          r.f[3] = 0.f;
+          {
+            float run = sh.prefix[b][j];
 #pragma unroll
-          for (int off = 1; off < 16; off <<= 1) {
-            const float u = __shfl_up_sync(0xffffffffu, up, off, 16), d = __shfl_down_sync(0xffffffffu, down, off, 16);
-            if (jj >= off) up *= u;
-            if (jj + off < 16) down *= d;
+            for (int i = 2; i >= 0; --i) {
+              r.f[i] = i < bj ? run : 0.f;
+              if (i < bj) run *= tot[i];
+            }
           }
-          down = __shfl_down_sync(0xffffffffu, down, 1, 16);
-          if (jj == 15) {
-            down = 1.f;
-            sh.tot[bj] = up;
-          }
-          sh.alpha[j] = al;
-          sh.prefix[j] = up;
-        }
-        if (valid < Q) {  // rows of k that belong to other prompts must not reach the state, whatever they hold
-          wait(sh.full_kq[c % kStages], c / kStages);
-          for (int i = p + valid * 8; i < Q * 8; i += 128) {
-            *reinterpret_cast<uint4 *>(sh.in[c % kStages][0] + 16 * i) = make_uint4(0, 0, 0, 0);
-            *reinterpret_cast<uint4 *>(sh.in[c % kStages][2] + 16 * i) = make_uint4(0, 0, 0, 0);
-          }
-        }
-        const bool grows = prep_sync_or(!(fabsf(up) <= 1.f && fabsf(down) <= 1.f));
-        if (c > 1) wait(sh.free_t[b], (c >> 1) - 1);
-        const float tot[4] = {sh.tot[0], sh.tot[1], sh.tot[2], sh.tot[3]};
-        const float carry = (tot[0] * tot[1]) * (tot[2] * tot[3]);
-        const bool strong = grows || !(fabsf(carry) >= kMild);  // otherwise f_j = carry / (product up to j) >= carry
-        Table &tab = sh.tab[b];
-        r.by = of_k ? be : 1.f;
-        r.f[3] = 0.f;
-        {
-          float run = sh.prefix[j];
+          if (of_k) {
+            float rise = up, fall = down;
 #pragma unroll
-          for (int i = 2; i >= 0; --i) {
-            r.f[i] = i < bj ? run : 0.f;
-            if (i < bj) run *= tot[i];
+            for (int i = 0; i < 4; ++i) {
+              if (i < bj) rise *= tot[i];
+              if (i > bj) fall *= tot[i];
+            }
+            tab.v[j] = strong ? be : be * fall;
+            tab.k[j] = strong ? -be * rise : -be * carry;
+            tab.q[j] = a.q_scale * rise;
+            tab.u[j] = strong ? a.q_scale : a.q_scale / fall;
+            tab.fall[j] = fall;
+            if (j == 0) {
+              tab.carry = carry;
+              tab.mild = !strong;
+            }
           }
-        }
-        int tokens = valid;
-        wait(sh.g_done, c);
-        tm_fence_after();
-        const f2 seen = strong ? prep_strong(sh, r, sh.M[b]) : prep_mild(sh, r, sh.M[b]);
-        if (prep_sync_or(of_k && (odd || not_zero(seen)))) {
-          tokens = prep_careful(sh, r, odd, strong, valid);
+          int tokens = valid;
+          wait(sh.g_done, c);
+          tm_fence_after();
+          const f2 seen = prep_rows(sh, r, strong, sh.M[b], b);
+          if (prep_sync_or(of_k && (odd || not_zero(seen)))) {
+            tokens = prep_careful(sh, r, odd, strong, b, valid);
+            prep_sync();
+          }
+          if (of_k && j == 0) tab.tokens = tokens;
+          warp_arrive(sh.g_free, lane);
+          {  // blocks on the diagonal by substitution, one a warp, lane = column
+            const int col = lane & 15;
+            float t[16];
+#pragma unroll
+            for (int i = 0; i < 16; ++i) t[i] = col == i ? 1.f : 0.f;
+#pragma unroll
+            for (int i = 0; i < 15; ++i) {  // t_i is known: off it goes from the rows below
+#pragma unroll
+              for (int l = (i + 1) & ~3; l < 16; l += 4) {
+                const float4 v = *reinterpret_cast<const float4 *>(&sh.diag[pw][20 * i + l]);
+                if (l > i) t[l] = fmaf(-v.x, t[i], t[l]);
+                if (l + 1 > i) t[l + 1] = fmaf(-v.y, t[i], t[l + 1]);
+                if (l + 2 > i) t[l + 2] = fmaf(-v.z, t[i], t[l + 2]);
+                if (l + 3 > i) t[l + 3] = fmaf(-v.w, t[i], t[l + 3]);
+              }
+            }
+            const int lo = lane >> 4;  // lanes 0..15 write the first pieces, the others the second; each the third of 8 rows
+            auto put_t = [&](int piece, int i, __nv_bfloat16 v) {
+              *reinterpret_cast<__nv_bfloat16 *>(at_tile(T[piece], 16 * pw + i, 16 * pw + (col & 8)) + 2 * (col & 7)) = v;
+            };
+            auto left_of = [](float v) { return v - __bfloat162float(__float2bfloat16_rn(v)); };
+#pragma unroll
+            for (int i = 0; i < 16; ++i) put_t(lo, i, __float2bfloat16_rn(lo ? left_of(t[i]) : t[i]));
+#pragma unroll
+            for (int i = 0; i < 8; ++i) put_t(2, 8 * lo + i, __float2bfloat16_rn(left_of(left_of(lo ? t[8 + i] : t[i]))));
+          }
           prep_sync();
         }
         if (of_k) {
-          float rise = up, fall = down;
+          if (at + Q < ntok) {
+            const int to = at < 0 ? b : b ^ 1;
+            odd = !(fabsf(alpha_next) < __int_as_float(0x7f800000));
+            const float al = odd ? 1.f : alpha_next;
+            be = beta_next;
+            fetch(at + 2 * Q);
+            up = down = al;
 #pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            if (i < bj) rise *= tot[i];
-            if (i > bj) fall *= tot[i];
-          }
-          tab.v[j] = strong ? be : be * fall;
-          tab.k[j] = strong ? -be * rise : -be * carry;
-          tab.q[j] = a.q_scale * rise;
-          tab.u[j] = strong ? a.q_scale : a.q_scale / fall;
-          tab.fall[j] = fall;
-          if (j == 0) {
-            tab.carry = carry;
-            tab.tokens = tokens;
-            tab.mild = !strong;
-          }
-        }
-        warp_arrive(sh.g_free, lane);
-        unsigned char(*const T)[kHalf] = sh.T[b];
-        {  // blocks on the diagonal by substitution, one a warp, lane = column
-          const int col = lane & 15;
-          float t[16];
-#pragma unroll
-          for (int i = 0; i < 16; ++i) t[i] = col == i ? 1.f : 0.f;
-#pragma unroll
-          for (int i = 0; i < 15; ++i) {  // t_i is known: off it goes from the rows below
-#pragma unroll
-            for (int l = (i + 1) & ~3; l < 16; l += 4) {
-              const float4 v = *reinterpret_cast<const float4 *>(&sh.diag[pw][20 * i + l]);
-              if (l > i) t[l] = fmaf(-v.x, t[i], t[l]);
-              if (l + 1 > i) t[l + 1] = fmaf(-v.y, t[i], t[l + 1]);
-              if (l + 2 > i) t[l + 2] = fmaf(-v.z, t[i], t[l + 2]);
-              if (l + 3 > i) t[l + 3] = fmaf(-v.w, t[i], t[l + 3]);
+            for (int off = 1; off < 16; off <<= 1) {
+              const float u = __shfl_up_sync(0xffffffffu, up, off, 16), d = __shfl_down_sync(0xffffffffu, down, off, 16);
+              if (jj >= off) up *= u;
+              if (jj + off < 16) down *= d;
             }
+            down = __shfl_down_sync(0xffffffffu, down, 1, 16);
+            if (jj == 15) {
+              down = 1.f;
+              sh.tot[to][bj] = up;
+            }
+            sh.alpha[to][j] = al;
+            sh.prefix[to][j] = up;
+            sh.fall[to][j] = down;
           }
-          const int lo = lane >> 4;  // lanes 0..15 write the first pieces, the others the second; each the third of 8 rows
-          auto put_t = [&](int piece, int i, __nv_bfloat16 v) {
-            *reinterpret_cast<__nv_bfloat16 *>(at_tile(T[piece], 16 * pw + i, 16 * pw + (col & 8)) + 2 * (col & 7)) = v;
-          };
-          auto left_of = [](float v) { return v - __bfloat162float(__float2bfloat16_rn(v)); };
-#pragma unroll
-          for (int i = 0; i < 16; ++i) put_t(lo, i, __float2bfloat16_rn(lo ? left_of(t[i]) : t[i]));
-#pragma unroll
-          for (int i = 0; i < 8; ++i) put_t(2, 8 * lo + i, __float2bfloat16_rn(left_of(left_of(lo ? t[8 + i] : t[i]))));
-        }
-        prep_sync();
-        if (!(pw & 1)) {  // T10 = -T11 A10 T00 in both blocks of 32
-          const int r0 = 16 * pw;
+        } else if (at >= 0) {  // T10 = -T11 A10 T00 in both blocks of 32
+          const int r0 = 32 * (pw & 1);
           float x[2][4] = {}, t[2][4] = {};
           f2 right[2][2];
           block_x(T, r0, r0, sh.A, r0 >> 1, 32, lane, x);
@@ -876,6 +871,7 @@ __global__ void __launch_bounds__(kGdnThreads, 1)
           block_t(T, r0 + 16, r0 + 16, lane, right, t);
           store_block(T, r0 + 16, r0, lane, t);
         }
+        if (at < 0) continue;
         prep_sync();
         {  // the same of the whole: rows 16 l of X = A T00 at columns 16 from, one a warp, and block (32 + 16 to, 16 from) of T
           const int to = pw >> 1, from = pw & 1;
@@ -904,6 +900,7 @@ __global__ void __launch_bounds__(kGdnThreads, 1)
         fence_async_smem();
         __syncwarp();
         if (lane == 0) mbar_arrive(&sh.full_t[b]);
+        ++c;
       }
     }
   } else {
