@@ -569,8 +569,9 @@ static rssm_status run_gdn_scan(const rssm_config &c, int qk_heads, const Prompt
   a.q = tok->q; a.k = tok->k; a.v = tok->v; a.alpha = tok->alpha; a.beta = tok->beta; a.S = S; a.y = y;
   a.err = err; a.wait_cycles = wait_cycles; a.withhold = withhold;
   // On the tensor cores a chunk costs the same however few of its 64 tokens there are; token by token the time grows with them
-  // (32 heads of 128 rows, us, tokens / chunks: 256 prompts of 12 tokens 569 / 576, of 15 651 / 576; 48 of 12 112 / 129, of 16
-  // 135 / 129; 4 of 16 22 / 26, of 32 32 / 27).
+  // (32 heads of 128 rows, us, tokens / chunks: 256 prompts of 12 tokens 571 / 602, of 15 653 / 604; 48 of 12 116 / 135, of 16
+  // 137 / 135; 4 of 16 23 / 26, of 32 35 / 27).  The host does not know the lengths: one long prompt among many of a token or two
+  // goes token by token, too, and takes eight times as long there (8000 tokens beside 600 of one 5.3 ms, alone 0.64).
   const bool chunks = c.in_dtype == RSSM_BF16 && p.total >= 16LL * p.nseq;
   cudaError_t e = chunks ? launch_gdn_tc(a, p, num_sms, st) : launch_gdn_scan(a, p, esize(c), num_sms, st);
   if (e == cudaSuccess && p.refused_nan && p.total > 0) e = launch_refuse(p, y, c.nheads * c.headdim, num_sms, st);

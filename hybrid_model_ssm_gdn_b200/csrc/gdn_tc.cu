@@ -13,20 +13,22 @@
 // (diag(f) V - g_Q K S^T) = diag(f) of the R above,  Y = q_scale diag(1 / f) (g_Q Q S^T + M U),  S <- g_Q S + U^T K: one cut
 // of U serves both products.  f lies in 2^-24 .. 1, so nothing overflows that would not without it, and values down to 2^-85
 // keep their 24 bits in the pieces of f U (the last one's resolution is 2^-133).  Otherwise ("strong") D is formed from products
-// within and between blocks of 16, never as a quotient, so that decays to nothing stay what they are; such chunks take 6 % more
-// (8191 tokens of 32 heads 655 -> 695 us).
+// within and between blocks of 16, never as a quotient, so that decays to nothing stay what they are; such chunks take 9 % more
+// (8191 tokens of 32 heads 667 -> 730 us).
 //
 // Precision.  q, k, v are bf16; S, R, U, M and T go into the products as three bf16 pieces each (24 bits), accumulated in
 // fp32.  (I + A)^-1 is formed in fp32 on the diagonal blocks of 16 and from there by products of blocks in three pieces with
 // mma.sync.  512 tokens are 2e-7 (decays of 2^-60 a chunk) to 5.5e-7 (2^-1) of a norm off, whether keys are independent or alike
 // (mean cosines of 0 to 0.95, beta 0.5 to 1).  With T and the blocks' products in two pieces it was 1.3e-6 for independent
-// keys and 1.3e-5 for keys alike, for 3 to 9 % less time.
+// keys and 1.3e-5 for keys alike, for 3 to 5 % less time in one long prompt.
 //
-// What bounds it: the way of one chunk through S -> K S^T -> R -> U -> S, each step a product of 0.4 to 1 us and a pass of its
-// results through registers into pieces, 5.4 us a chunk in all with the preparation of the next chunk beside it (0.70 ms for
-// 8191 tokens of 32 heads, where 32 SMs work; 0.48 ms for 8 prompts of 16384 tokens, where the longest prompt stands for
-// 0.38).  The tensor cores are busy a quarter of that.  Rows of the state split over more blocks, and more warps for the
-// preparation and for Y, took as long or longer: the steps wait for one another, not for issue slots.
+// What bounds it: two chains of a chunk that are about as long, some 5.2 us (5.7 with strong decays) for few blocks. The state's:
+// S -> K S^T -> R -> U -> S, each step a product of 0.4 to 1 us and a pass of its results through registers into pieces. Beside it
+// the next chunk's preparation: the rows of A and M, the inverse's blocks one after another, 120 mma.sync of three pieces; the state
+// waits for it 0.3 to 0.7 us of a chunk. 8191 tokens of 32 heads take 0.75 ms, on 32 SMs; 16384 tokens of 8 prompts 0.44 to 0.62 ms by
+// their lengths. The tensor cores are busy a quarter of that. Rows of the state split over more blocks, and more warps for the
+// preparation and for Y, took as long or longer: the steps wait for one another, and instructions for their way to the SM, so
+// that the preparation's loops stay rolled (unrolled, 405 -> 475 us for 8 prompts of 2048).
 #include "prompt_kernels.h"
 #include "packed.cuh"
 #include "tcgen05.cuh"
@@ -1235,8 +1237,8 @@ cudaError_t launch_gdn_tc(const GdnScanArgs &s, const Prompts &pr, int num_sms, 
     return cudaGetLastError();
   };
   // Units in turn save a block's start and its end and bring the next state closer; one a block is what the hardware hands out
-  // as blocks finish, and 3 % faster in a long prompt (32 heads of 128 rows, us, in turn / one a block: 48 prompts of 64 tokens
-  // 136 / 170, of 256 347 / 365, of 512 638 / 631; 16 of 256 142 / 144, of 1024 470 / 441; 4 of 64, fewer units than SMs, 28 / 24).
+  // as blocks finish, and 7 % faster in a long prompt (32 heads of 128 rows, us, in turn / one a block: 48 prompts of 64 tokens
+  // 137 / 178, of 256 331 / 373, of 512 602 / 633; 16 of 256 142 / 146, of 1024 479 / 447; 4 of 64, fewer units than SMs, 28 / 24).
   // Not with many thousands of prompts: one warp looks through all slots for each unit, and the others' waits for it are bounded.
   if (a.units > num_sms && pr.total <= 256LL * pr.nseq && pr.nseq <= kMostInTurn) return run(gdn_tc_kernel<true>, num_sms);
   return run(gdn_tc_kernel<false>, a.units);
