@@ -8,7 +8,7 @@
 // A block carries one head along one prompt; lanes of tensor memory are rows of the state (d_v), so R, U and Y are held
 // transposed, and S stays on the chip.
 //
-// Two forms.  Where the products of alpha never pass 1 and the chunk's stays above 2^-24 (a "mild" chunk), the decays leave
+// Two forms.  Where no product of alpha from an end of a block of 16 on passes 1 and the chunk's is 2^-24 or more ("mild"), they leave
 // the matrices: with f_j = g_Q / g_j,  A_ji = [i < j] beta_j (k_j . k_i),  M_ji = [i <= j] (q_j . k_i),  R = diag(beta)
 // (diag(f) V - g_Q K S^T) = diag(f) of the R above,  Y = q_scale diag(1 / f) (g_Q Q S^T + M U),  S <- g_Q S + U^T K: one cut
 // of U serves both products.  f lies in 2^-24 .. 1, so nothing overflows that would not without it, and values down to 2^-85

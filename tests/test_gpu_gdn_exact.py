@@ -56,3 +56,21 @@ def test_keys_alike(cuda_ok, dtype, cosine, decay, lens):
             for what, got, want in (("y", y_got[part, h], y[part, h]), ("S", S_got[i, h], S[i, h])):
                 off = np.linalg.norm(got - want) / np.linalg.norm(want)
                 assert off <= bound(dtype, m, cosine), f"{what} of prompt {i}, head {h}: {off:.2e}"
+
+
+@pytest.mark.parametrize("dtype", [BF, F32])
+@pytest.mark.parametrize("n", [64, 128])
+def test_outputs_of_a_held_state(cuda_ok, dtype, n):
+    """A state that prompts hardly change, under weak writes of small values: outputs are its products with the queries, so that
+    they are as exact as the form in which it is read."""
+    r = np.random.default_rng(82)
+    d = make(83, dtype, n, 2, 1, 128, 1, slow=100.0)
+    d["S"] = r.standard_normal(d["S"].shape).astype(np.float32)
+    d["v"] = round_to_dtype((d["v"] * 1e-3).astype(np.float32), "bf16" if dtype == BF else "f32")
+    d["beta"] = r.uniform(0, 0.01, (n, 2)).astype(np.float32)
+    S, y = oracle_scan(**d, offsets=[0, n], resume=[1], q_scale=SCALE)
+    g = on_gpu(d, dtype)
+    y_got = scan(g, [0, n], resume=[1]).double().cpu().numpy()
+    for h in range(2):
+        assert np.linalg.norm(y_got[:, h] - y[:, h]) <= bound(dtype, n, 0.0) * np.linalg.norm(y[:, h])
+        assert np.linalg.norm(g["S"].double().cpu().numpy()[0, h] - S[0, h]) <= bound(dtype, n, 0.0) * np.linalg.norm(S[0, h])
